@@ -467,6 +467,151 @@ moe_status_t moe_post_permute(const moe_problem_t* p, const void* rows,
                               void* stream);
 
 /* ---------------------------------------------------------------------------------------- */
+/* Around the routed experts: the projection that makes the router logits (and the dense      */
+/* products beside the experts), the norms and the residual around the layer, and the training */
+/* of the router.  No source page has these operators; the formulas here define them.         */
+/* Tensors start on 16-byte boundaries (MOE_ERR_INVALID_ARG otherwise).                        */
+/* ---------------------------------------------------------------------------------------- */
+
+/* Activation of moe_linear, applied to the f32 product plus bias z. */
+typedef enum {
+  MOE_LINEAR_NONE = 0,
+  MOE_LINEAR_SILU = 1,      /* z / (1 + e^-z) */
+  MOE_LINEAR_GELU_TANH = 2, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  MOE_LINEAR_RELU2 = 3      /* max(z, 0)^2 */
+} moe_linear_act_t;
+
+typedef struct {
+  int32_t T;          /* rows of x, residual and out; >= 0 */
+  int32_t N;          /* output columns; any >= 1 */
+  int32_t K;          /* reduction length; a multiple of 8 (MOE_ERR_UNSUPPORTED otherwise) */
+  int32_t dtype;      /* moe_dtype_t of x, w, bias and a 16-bit out */
+  int32_t activation; /* moe_linear_act_t */
+  int32_t out_f32;    /* nonzero: out and residual are f32 (router logits for moe_route) */
+} moe_linear_t;
+
+/*
+ * moe_linear -- out[t, n] = round( act( sum_k x[t, k] w[n, k] + bias[n] ) + residual[t, n] )
+ * with f32 accumulation and one rounding to out's type.
+ *   x [T, K], w [N, K], bias [N] or NULL: dtype; residual [T, N] or NULL and out [T, N]: dtype,
+ *   or f32 with out_f32.  out may be the residual itself; it overlaps no other input.
+ *   workspace  moe_linear_workspace_size(g) bytes (its status word records a wait that gave up).
+ * The same call gives the same bits (sums in a fixed order, no atomics).
+ */
+size_t moe_linear_workspace_size(const moe_linear_t* g);
+moe_status_t moe_linear(const moe_linear_t* g, const void* x, const void* w, const void* bias,
+                        const void* residual, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* How the gate of moe_block_norm_fwd is broadcast. */
+typedef enum {
+  MOE_GATE_NONE = 0,    /* 1 */
+  MOE_GATE_CHANNEL = 1, /* [H] */
+  MOE_GATE_TOKEN = 2,   /* [T] */
+  MOE_GATE_ELEMENT = 3  /* [T, H] */
+} moe_gate_t;
+
+typedef struct {
+  int32_t T;            /* rows, >= 0 */
+  int32_t H;            /* row length; a multiple of 8, at most 16384 */
+  int32_t dtype;        /* moe_dtype_t of every tensor */
+  int32_t gate;         /* moe_gate_t */
+  int32_t post_norm;    /* nonzero: the branch is normed before it joins the stream */
+  int32_t pre_norm;     /* nonzero: the norm in front of the next block is computed too */
+  float residual_scale; /* a */
+  float weight_offset;  /* o: 0, or 1 for zero-centred norm weights */
+  float eps;            /* added to the mean square, >= 0 */
+} moe_block_norm_t;
+
+/*
+ * moe_block_norm_fwd -- what stands between two blocks, in one pass over the rows:
+ *   u = branch * ry * (o + post_weight),  ry = 1/sqrt(mean(branch^2) + eps)   (post_norm)
+ *   u = branch                                                                (otherwise)
+ *   stream = a * residual + gate * u
+ *   normed = stream * rr * (o + pre_weight),  rr = 1/sqrt(mean(stream^2) + eps)   (pre_norm)
+ * in f32 (normed comes from the stream before its rounding), each output rounded once.
+ *   branch [T, H]; residual [T, H] or NULL (0); gate as p->gate says (NULL iff MOE_GATE_NONE);
+ *   post_weight, pre_weight [H] or NULL (the factor o + weight is then 1);
+ *   stream_out [T, H] or NULL; normed_out [T, H] iff pre_norm.
+ *   stream_out may be the residual or the branch itself; outputs overlap nothing else.
+ */
+moe_status_t moe_block_norm_fwd(const moe_block_norm_t* p, const void* branch,
+                                const void* residual, const void* gate, const void* post_weight,
+                                const void* pre_weight, void* stream_out, void* normed_out,
+                                void* stream);
+
+/*
+ * moe_block_norm_bwd -- the gradients of moe_block_norm_fwd for the same inputs (nothing is
+ * saved by the forward: the statistics and the stream are computed again from branch and
+ * residual).  With D = d_stream plus what d_normed sends back through the pre norm:
+ *   d_residual = a D;  d_gate = D u, summed over what the gate is broadcast over;
+ *   d_branch = gate D sent back through the post norm;
+ *   d_post_weight = sum_t gate D branch ry;  d_pre_weight = sum_t d_normed stream rr.
+ *   d_stream [T, H] or NULL (0); d_normed [T, H] iff pre_norm; inputs as in the forward;
+ *   every output may be NULL (not wanted); d_gate, d_post_weight and d_pre_weight have the
+ *   shapes of their inputs and need those inputs.  Sums over tokens are f32, in an order that
+ *   depends on p and the GPU alone; every output is rounded once.  With T = 0 the gradients
+ *   summed over tokens are 0.
+ *   d_residual may be d_stream and d_branch may be d_normed; outputs overlap nothing else.
+ *   workspace  moe_block_norm_bwd_workspace_size(p) bytes.
+ */
+size_t moe_block_norm_bwd_workspace_size(const moe_block_norm_t* p);
+moe_status_t moe_block_norm_bwd(const moe_block_norm_t* p, const void* d_stream,
+                                const void* d_normed, const void* branch, const void* residual,
+                                const void* gate, const void* post_weight,
+                                const void* pre_weight, void* d_branch, void* d_residual,
+                                void* d_gate, void* d_post_weight, void* d_pre_weight,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_balance_loss_fwd -- per-expert counts and the balance loss of each sequence, averaged over
+ * the sequences.  Sequence s holds the tokens [seq_offsets[s], seq_offsets[s+1]); a token whose
+ * ids are all -1 is padding and takes no part; T_s tokens of s are left, and n sequences have any:
+ *   counts[s, e]   = routes of the sequence's tokens to expert e (an id of -1 is no route)
+ *   prob_sum[s, e] = sum over its tokens of p_te; p_t = softmax(x_t) for MOE_SOFTMAX, and
+ *                    sigmoid(x_t) / sum_e sigmoid(x_te) for MOE_SIGMOID; a row of -inf alone
+ *                    has p = 0
+ *   coef[s, e]     = coeff * E * counts[s, e] / (n * top_k * T_s^2)  (0 for an empty sequence)
+ *   loss           = sum_s sum_e coef[s, e] * prob_sum[s, e]
+ * The counts carry no gradient: d loss / d p_te = coef[s(t), e], which moe_router_bwd takes.
+ *   p: T, E, top_k and scoring are used (the router's selection options are not); the ids are
+ *   those of all E experts (an expert-parallel shard is MOE_ERR_UNSUPPORTED).
+ *   gating_output [T, E] f32; topk_ids [T, top_k] int32; seq_offsets [n_seq + 1] int32, device,
+ *   non-decreasing in [0, T] (NULL: one sequence of all T tokens, n_seq = 1); n_seq <= 2^20;
+ *   loss [1] f32, counts [n_seq, E] int32, live_tokens [n_seq] int32 (T_s), prob_sum and coef
+ *   [n_seq, E] f32: all out, written in full.  Sums are f32 in a fixed order.
+ *   workspace  moe_balance_loss_workspace_size(p, n_seq) bytes.  An id outside [-1, E) counts as
+ *              -1 and sets MOE_ERR_BAD_EXPERT_ID in its status word; offsets that decrease or
+ *              leave [0, T] set MOE_ERR_INVALID_ARG there (the outputs are then not valid).
+ */
+size_t moe_balance_loss_workspace_size(const moe_problem_t* p, int32_t n_seq);
+moe_status_t moe_balance_loss_fwd(const moe_problem_t* p, int32_t n_seq, float coeff,
+                                  const float* gating_output, const int32_t* topk_ids,
+                                  const int32_t* seq_offsets, float* loss, int32_t* counts,
+                                  int32_t* live_tokens, float* prob_sum, float* coef,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_router_bwd -- the gradient of the router logits from the balance loss and from the route
+ * weights that moe_route returned:
+ *   d_gating_output[t, :] = d_loss * sum_e coef[s(t), e] dp_te/dx_t
+ *                           + sum_j d_topk_weights[t, j] dw_tj/dx_t
+ * with w_tj = routed_scaling_factor * score_j (/ the sum of the selected scores, renormalize),
+ * score = softmax(x) or sigmoid(x), and the selection held fixed.  An id of -1 (or outside
+ * [0, E)) is not part of the selection; a padding token's row is 0, and so is the first term of
+ * a token outside every sequence.  An expert that a token names twice counts twice.
+ *   p: T, E, top_k, scoring, renormalize and routed_scaling_factor are used.
+ *   gating_output [T, E] f32, topk_ids [T, top_k] int32; d_topk_weights [T, top_k] f32 or NULL
+ *   (0); coef [n_seq, E] f32 from moe_balance_loss_fwd or NULL (no balance term); seq_offsets as
+ *   there; d_loss [1] f32, device, or NULL (1); d_gating_output [T, E] f32 out, written in full;
+ *   it may be gating_output itself.
+ */
+moe_status_t moe_router_bwd(const moe_problem_t* p, int32_t n_seq, const float* gating_output,
+                            const int32_t* topk_ids, const float* d_topk_weights,
+                            const float* coef, const int32_t* seq_offsets, const float* d_loss,
+                            float* d_gating_output, void* stream);
+
+/* ---------------------------------------------------------------------------------------- */
 /* Status.                                                                                    */
 /* ---------------------------------------------------------------------------------------- */
 

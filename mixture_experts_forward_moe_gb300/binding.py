@@ -24,6 +24,9 @@ _DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 _SCORING = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}
 # moe_activation_t: the two gated forms keep 2F rows per expert in w_gate_up, ReLU2 keeps F.
 _ACTIVATIONS = {"silu": 0, "gelu_tanh": 1, "relu2": 2}
+# moe_linear_act_t and moe_gate_t.
+_LINEAR_ACTS = {"none": 0, "silu": 1, "gelu_tanh": 2, "relu2": 3}
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = 0, 1, 2, 3
 
 
 def gate_up_rows(activation: str, F: int) -> int:
@@ -43,7 +46,9 @@ EXPORTED = (
     "moe_gemm2_w4a16", "moe_nvfp4_pack", "moe_nvfp4_packed_bytes", "moe_pre_permute",
     "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_post_permute",
     "moe_grouped_gemm_fp8", "moe_host_staging_bytes", "fused_moe_fwd_host",
-    "fused_moe_fwd_w4a16_host",
+    "fused_moe_fwd_w4a16_host", "moe_linear_workspace_size", "moe_linear", "moe_block_norm_fwd",
+    "moe_block_norm_bwd_workspace_size", "moe_block_norm_bwd", "moe_balance_loss_workspace_size",
+    "moe_balance_loss_fwd", "moe_router_bwd",
 )
 
 
@@ -64,6 +69,22 @@ class GroupedGemm(ctypes.Structure):
         ("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
         ("max_m", ctypes.c_int32), ("rows", ctypes.c_int64), ("dtype", ctypes.c_int32),
         ("activation", ctypes.c_int32), ("out_f32", ctypes.c_int32),
+    ]
+
+
+class Linear(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("out_f32", ctypes.c_int32),
+    ]
+
+
+class BlockNorm(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("gate", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32),
+        ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float),
+        ("eps", ctypes.c_float),
     ]
 
 
@@ -141,6 +162,21 @@ def lib():
                 getattr(L, fn).restype = ctypes.c_int
             L.moe_nvfp4_packed_bytes.restype = i64
             L.moe_nvfp4_packed_bytes.argtypes = [i64, i32, i32]
+            PL, PN = ctypes.POINTER(Linear), ctypes.POINTER(BlockNorm)
+            L.moe_linear_workspace_size.restype = sz
+            L.moe_linear_workspace_size.argtypes = [PL]
+            L.moe_linear.argtypes = [PL, P, P, P, P, P, P, sz, P]
+            L.moe_block_norm_fwd.argtypes = [PN] + [P] * 8
+            L.moe_block_norm_bwd_workspace_size.restype = sz
+            L.moe_block_norm_bwd_workspace_size.argtypes = [PN]
+            L.moe_block_norm_bwd.argtypes = [PN] + [P] * 13 + [sz, P]
+            L.moe_balance_loss_workspace_size.restype = sz
+            L.moe_balance_loss_workspace_size.argtypes = [PP, i32]
+            L.moe_balance_loss_fwd.argtypes = [PP, i32, ctypes.c_float] + [P] * 9 + [sz, P]
+            L.moe_router_bwd.argtypes = [PP, i32] + [P] * 8
+            for fn in ("moe_linear", "moe_block_norm_fwd", "moe_block_norm_bwd",
+                       "moe_balance_loss_fwd", "moe_router_bwd"):
+                getattr(L, fn).restype = ctypes.c_int
             for fn in ("fused_moe_fwd", "moe_route", "moe_align_sort", "moe_gemm1_swiglu",
                        "moe_gemm2", "moe_combine", "moe_shared_expert_fwd",
                        "moe_get_device_status", "moe_workspace_init", "fused_moe_fwd_w4a16",
@@ -784,4 +820,237 @@ def moe_grouped_gemm_fp8(a, a_scale, b, b_scale, layout_metadata, out=None, work
                                       _p(layout_metadata), _p(out), _p(workspace),
                                       workspace.numel(), _stream(stream)),
            "moe_grouped_gemm_fp8")
+    return out
+
+
+# ------------------------------------------------------------------ around the routed experts
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _CallStream:
+    """The stream of a call, current while its outputs and scratch are allocated, so that torch's
+    allocator reuses their memory in that stream's order."""
+
+    def __init__(self, stream, device):
+        self.device = device
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self._ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+    @property
+    def handle(self):
+        return self.stream.cuda_stream
+
+    def workspace(self, nbytes):
+        """Scratch of this stream: calls on other streams may run at the same time.  A captured
+        call gets its own, which lives in the graph's memory."""
+        if torch.cuda.is_current_stream_capturing():
+            return new_workspace(nbytes, self.device)
+        key = (str(self.device), threading.get_ident(), self.handle)
+        ws = _ws_cache.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = _ws_cache[key] = new_workspace(nbytes, self.device)
+        return ws
+
+
+def call_workspace(device=None, stream=None) -> torch.Tensor:
+    """The workspace that the calls below share on `stream` when none is given (its status word:
+    get_device_status)."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    with _CallStream(stream, device) as c:
+        return c.workspace(256)
+
+
+def moe_linear(x, w, bias=None, activation="none", residual=None, out_dtype=None, out=None,
+               workspace=None, stream=None):
+    """act(x w^T + bias) + residual (include/moe.h: moe_linear).  x [T, K] and w [N, K] in bf16 or
+    f16, bias [N] in their type; residual and the result [T, N] in `out_dtype`: x's (default) or
+    float32.  ``activation``: "none", "silu", "gelu_tanh" or "relu2".  `out` may be the residual."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must have two dimensions")
+    T, K = x.shape
+    N = w.shape[0]
+    dt = x.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    if activation not in _LINEAR_ACTS:
+        raise ValueError(f"unsupported activation {activation}")
+    odt = dt if out_dtype is None else out_dtype
+    if odt not in (dt, torch.float32):
+        raise ValueError(f"out_dtype must be {dt} or torch.float32, got {odt}")
+    _need(x, "x")
+    _need(w, "w", dt, (N, K))
+    if bias is not None:
+        _need(bias, "bias", dt, (N,))
+    if residual is not None:
+        _need(residual, "residual", odt, (T, N))
+    g = Linear(T, N, K, _DTYPES[dt], _LINEAR_ACTS[activation], odt == torch.float32)
+    with _CallStream(stream, x.device) as c:
+        if out is None:
+            out = torch.empty((T, N), dtype=odt, device=x.device)
+        else:
+            _need(out, "out", odt, (T, N))
+        if workspace is None:
+            workspace = c.workspace(256)
+        _check(lib().moe_linear(ctypes.byref(g), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
+                                _ptr(out), _ptr(workspace), workspace.numel(), c.handle),
+               "moe_linear")
+    return out
+
+
+def _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
+                residual_scale, weight_offset, eps) -> BlockNorm:
+    if branch.dim() != 2:
+        raise ValueError("branch must have two dimensions")
+    T, H = branch.shape
+    dt = branch.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    _need(branch, "branch")
+    if residual is not None:
+        _need(residual, "residual", dt, (T, H))
+    kind = GATE_NONE
+    if gate is not None:
+        shape = tuple(gate.shape)
+        # a gate of T = H values is per channel; [T, 1] is always per token
+        if shape == (H,):
+            kind = GATE_CHANNEL
+        elif shape in ((T,), (T, 1)):
+            kind = GATE_TOKEN
+        else:
+            kind = GATE_ELEMENT
+            shape = (T, H)
+        _need(gate, "gate", dt, shape)
+    if post_weight is not None:
+        _need(post_weight, "post_weight", dt, (H,))
+    if pre_weight is not None:
+        _need(pre_weight, "pre_weight", dt, (H,))
+    return BlockNorm(T, H, _DTYPES[dt], kind, bool(post_norm), bool(pre_norm), residual_scale,
+                     weight_offset, eps)
+
+
+def moe_block_norm(branch, residual=None, gate=None, post_weight=None, pre_weight=None,
+                   post_norm=True, pre_norm=True, residual_scale=1.0, weight_offset=0.0, eps=1e-6,
+                   stream_out=None, want_stream=True, stream=None):
+    """What stands between two blocks (include/moe.h: moe_block_norm_fwd): the norm of `branch`
+    (post_norm), times `gate` ([H] per channel, [T] or [T, 1] per token, [T, H]), plus
+    residual_scale * residual, and the norm of that for the next block (pre_norm).  Returns
+    (stream, normed), None for what is not computed (want_stream, pre_norm)."""
+    p = _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
+                    residual_scale, weight_offset, eps)
+    normed = None
+    with _CallStream(stream, branch.device) as c:
+        if stream_out is not None:
+            _need(stream_out, "stream_out", branch.dtype, branch.shape)
+        elif want_stream:
+            stream_out = torch.empty_like(branch)
+        if pre_norm:
+            normed = torch.empty_like(branch)
+        _check(lib().moe_block_norm_fwd(ctypes.byref(p), _ptr(branch), _ptr(residual), _ptr(gate),
+                                        _ptr(post_weight), _ptr(pre_weight), _ptr(stream_out),
+                                        _ptr(normed), c.handle), "moe_block_norm_fwd")
+    return stream_out, normed
+
+
+def moe_block_norm_bwd(d_stream, d_normed, branch, residual=None, gate=None, post_weight=None,
+                       pre_weight=None, post_norm=True, pre_norm=True, residual_scale=1.0,
+                       weight_offset=0.0, eps=1e-6, workspace=None, stream=None):
+    """The gradients of moe_block_norm (include/moe.h: moe_block_norm_bwd) for the same inputs and
+    options; d_stream may be None, d_normed is None without pre_norm.  Returns a dict of d_branch
+    and, where there is such an input, d_residual, d_gate, d_post_weight and d_pre_weight."""
+    p = _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
+                    residual_scale, weight_offset, eps)
+    if d_stream is not None:
+        _need(d_stream, "d_stream", branch.dtype, branch.shape)
+    if (d_normed is not None) != bool(pre_norm):
+        raise ValueError("d_normed goes with pre_norm")
+    if d_normed is not None:
+        _need(d_normed, "d_normed", branch.dtype, branch.shape)
+    with _CallStream(stream, branch.device) as c:
+        nbytes = lib().moe_block_norm_bwd_workspace_size(ctypes.byref(p))
+        if workspace is None:
+            workspace = c.workspace(nbytes)
+        ins = dict(d_branch=branch, d_residual=residual, d_gate=gate, d_post_weight=post_weight,
+                   d_pre_weight=pre_weight)
+        out = {k: torch.empty_like(v) for k, v in ins.items() if v is not None}
+        _check(lib().moe_block_norm_bwd(
+            ctypes.byref(p), _ptr(d_stream), _ptr(d_normed), _ptr(branch), _ptr(residual),
+            _ptr(gate), _ptr(post_weight), _ptr(pre_weight), *[_ptr(out.get(k)) for k in ins],
+            _ptr(workspace), workspace.numel(), c.handle), "moe_block_norm_bwd")
+    return out
+
+
+def _router_args(gating_output, topk_ids, seq_offsets):
+    if gating_output.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("gating_output and topk_ids must have two dimensions")
+    T, E = gating_output.shape
+    k = topk_ids.shape[1]
+    _need(gating_output, "gating_output", torch.float32)
+    _need(topk_ids, "topk_ids", torch.int32, (T, k))
+    n_seq = 1
+    if seq_offsets is not None:
+        _need(seq_offsets, "seq_offsets", torch.int32)
+        n_seq = seq_offsets.numel() - 1
+        if seq_offsets.dim() != 1 or n_seq < 1:
+            raise ValueError("seq_offsets must hold n_seq + 1 offsets")
+    return T, E, k, n_seq
+
+
+def moe_balance_loss(gating_output, topk_ids, coeff, scoring_func="softmax", seq_offsets=None,
+                     workspace=None, stream=None):
+    """Per-expert counts and the balance loss of ragged sequences (include/moe.h:
+    moe_balance_loss_fwd).  Returns a dict of loss [1] and, per sequence, counts [n_seq, E] int32,
+    live_tokens [n_seq] int32, prob_sum and coef [n_seq, E]; coef is what moe_router_bwd takes."""
+    T, E, k, n = _router_args(gating_output, topk_ids, seq_offsets)
+    prob = make_problem(T, 8, E, 8, k, torch.bfloat16, scoring_func)
+    dev = gating_output.device
+    with _CallStream(stream, dev) as c:
+        if workspace is None:
+            workspace = c.workspace(lib().moe_balance_loss_workspace_size(ctypes.byref(prob), n))
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        counts = torch.empty((n, E), dtype=torch.int32, device=dev)
+        live = torch.empty(n, dtype=torch.int32, device=dev)
+        prob_sum = torch.empty((n, E), dtype=torch.float32, device=dev)
+        coef = torch.empty((n, E), dtype=torch.float32, device=dev)
+        _check(lib().moe_balance_loss_fwd(
+            ctypes.byref(prob), n, coeff, _ptr(gating_output), _ptr(topk_ids), _ptr(seq_offsets),
+            _ptr(loss), _ptr(counts), _ptr(live), _ptr(prob_sum), _ptr(coef), _ptr(workspace),
+            workspace.numel(), c.handle), "moe_balance_loss_fwd")
+    return dict(loss=loss, counts=counts, live_tokens=live, prob_sum=prob_sum, coef=coef)
+
+
+def moe_router_bwd(gating_output, topk_ids, d_topk_weights=None, coef=None, d_loss=None,
+                   seq_offsets=None, scoring_func="softmax", renormalize=True,
+                   routed_scaling_factor=1.0, out=None, stream=None):
+    """The gradient of the router logits (include/moe.h: moe_router_bwd) from d_topk_weights
+    [T, top_k] (of moe_route's weights) and from the balance loss: `coef` of moe_balance_loss
+    times d_loss (a device scalar, 1 when None).  Returns d_gating_output [T, E] f32."""
+    T, E, k, n = _router_args(gating_output, topk_ids, seq_offsets)
+    if d_topk_weights is not None:
+        _need(d_topk_weights, "d_topk_weights", torch.float32, (T, k))
+    if coef is not None:
+        _need(coef, "coef", torch.float32, (n, E))
+    if d_loss is not None:
+        _need(d_loss, "d_loss", torch.float32)
+        if d_loss.numel() != 1:
+            raise ValueError("d_loss must hold one value")
+    prob = make_problem(T, 8, E, 8, k, torch.bfloat16, scoring_func, renormalize,
+                        routed_scaling_factor=routed_scaling_factor)
+    with _CallStream(stream, gating_output.device) as c:
+        if out is None:
+            out = torch.empty_like(gating_output)
+        else:
+            _need(out, "out", torch.float32, (T, E))
+        _check(lib().moe_router_bwd(ctypes.byref(prob), n, _ptr(gating_output), _ptr(topk_ids),
+                                    _ptr(d_topk_weights), _ptr(coef), _ptr(seq_offsets),
+                                    _ptr(d_loss), _ptr(out), c.handle), "moe_router_bwd")
     return out
