@@ -6,6 +6,7 @@ fallback: if the library cannot be loaded the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -824,50 +825,50 @@ def moe_grouped_gemm_fp8(a, a_scale, b, b_scale, layout_metadata, out=None, work
 
 
 # ------------------------------------------------------------------ around the routed experts
+# These calls are short beside their host time, so the checks below compare first and build a
+# message (through _need) only when something does not fit.
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _CallStream:
-    """The stream of a call, current while its outputs and scratch are allocated, so that torch's
-    allocator reuses their memory in that stream's order."""
+def _fits(t, name, dtype, shape):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape)
 
-    def __init__(self, stream, device):
-        self.device = device
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self._ctx = None if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
+def _handle(stream, device):
+    """The cudaStream_t of a call on `device`."""
+    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+            else stream.cuda_stream)
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
 
-    @property
-    def handle(self):
-        return self.stream.cuda_stream
+def _on(stream):
+    """Makes `stream` current while a call allocates, so that torch's allocator reuses the memory
+    in that stream's order."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
-    def workspace(self, nbytes):
-        """Scratch of this stream: calls on other streams may run at the same time.  A captured
-        call gets its own, which lives in the graph's memory."""
-        if torch.cuda.is_current_stream_capturing():
-            return new_workspace(nbytes, self.device)
-        key = (str(self.device), threading.get_ident(), self.handle)
-        ws = _ws_cache.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = _ws_cache[key] = new_workspace(nbytes, self.device)
-        return ws
+
+def _scratch(nbytes, device, handle):
+    """Workspace of a call on the stream `handle` (current): one per stream and host thread, since
+    calls on other streams may run at the same time.  A captured call gets its own, which lives in
+    the graph's memory."""
+    if torch.cuda.is_current_stream_capturing():
+        return new_workspace(nbytes, device)
+    key = (device, threading.get_ident(), handle)
+    ws = _ws_cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _ws_cache[key] = new_workspace(nbytes, device)
+    return ws
 
 
 def call_workspace(device=None, stream=None) -> torch.Tensor:
-    """The workspace that the calls below share on `stream` when none is given (its status word:
+    """The workspace that the calls below use on `stream` when none is given (its status word:
     get_device_status)."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    with _CallStream(stream, device) as c:
-        return c.workspace(256)
+    if device is None or device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _on(stream):
+        return _scratch(256, device, _handle(stream, device))
 
 
 def moe_linear(x, w, bias=None, activation="none", residual=None, out_dtype=None, out=None,
@@ -880,30 +881,37 @@ def moe_linear(x, w, bias=None, activation="none", residual=None, out_dtype=None
     T, K = x.shape
     N = w.shape[0]
     dt = x.dtype
-    if dt not in _DTYPES:
+    code = _DTYPES.get(dt)
+    if code is None:
         raise ValueError(f"unsupported dtype {dt}")
-    if activation not in _LINEAR_ACTS:
+    act = _LINEAR_ACTS.get(activation)
+    if act is None:
         raise ValueError(f"unsupported activation {activation}")
     odt = dt if out_dtype is None else out_dtype
-    if odt not in (dt, torch.float32):
+    if odt is not dt and odt is not torch.float32:
         raise ValueError(f"out_dtype must be {dt} or torch.float32, got {odt}")
-    _need(x, "x")
-    _need(w, "w", dt, (N, K))
+    _fits(x, "x", dt, (T, K))
+    _fits(w, "w", dt, (N, K))
     if bias is not None:
-        _need(bias, "bias", dt, (N,))
+        _fits(bias, "bias", dt, (N,))
     if residual is not None:
-        _need(residual, "residual", odt, (T, N))
-    g = Linear(T, N, K, _DTYPES[dt], _LINEAR_ACTS[activation], odt == torch.float32)
-    with _CallStream(stream, x.device) as c:
-        if out is None:
-            out = torch.empty((T, N), dtype=odt, device=x.device)
-        else:
-            _need(out, "out", odt, (T, N))
-        if workspace is None:
-            workspace = c.workspace(256)
-        _check(lib().moe_linear(ctypes.byref(g), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
-                                _ptr(out), _ptr(workspace), workspace.numel(), c.handle),
-               "moe_linear")
+        _fits(residual, "residual", odt, (T, N))
+    if out is not None:
+        _fits(out, "out", odt, (T, N))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_linear(x, w, bias, activation, residual, out_dtype, out, workspace)
+    dev = x.device
+    s = _handle(None, dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=odt, device=dev)
+    if workspace is None:
+        workspace = _scratch(256, dev, s)
+    g = Linear(T, N, K, code, act, odt is torch.float32)
+    rc = lib().moe_linear(ctypes.byref(g), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
+                          out.data_ptr(), workspace.data_ptr(), workspace.numel(), s)
+    if rc:
+        _check(rc, "moe_linear")
     return out
 
 
@@ -913,28 +921,29 @@ def _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_
         raise ValueError("branch must have two dimensions")
     T, H = branch.shape
     dt = branch.dtype
-    if dt not in _DTYPES:
+    code = _DTYPES.get(dt)
+    if code is None:
         raise ValueError(f"unsupported dtype {dt}")
-    _need(branch, "branch")
+    _fits(branch, "branch", dt, (T, H))
     if residual is not None:
-        _need(residual, "residual", dt, (T, H))
+        _fits(residual, "residual", dt, (T, H))
     kind = GATE_NONE
     if gate is not None:
-        shape = tuple(gate.shape)
+        shape = gate.shape
         # a gate of T = H values is per channel; [T, 1] is always per token
         if shape == (H,):
             kind = GATE_CHANNEL
-        elif shape in ((T,), (T, 1)):
+        elif shape == (T,) or shape == (T, 1):
             kind = GATE_TOKEN
         else:
             kind = GATE_ELEMENT
             shape = (T, H)
-        _need(gate, "gate", dt, shape)
+        _fits(gate, "gate", dt, shape)
     if post_weight is not None:
-        _need(post_weight, "post_weight", dt, (H,))
+        _fits(post_weight, "post_weight", dt, (H,))
     if pre_weight is not None:
-        _need(pre_weight, "pre_weight", dt, (H,))
-    return BlockNorm(T, H, _DTYPES[dt], kind, bool(post_norm), bool(pre_norm), residual_scale,
+        _fits(pre_weight, "pre_weight", dt, (H,))
+    return BlockNorm(T, H, code, kind, bool(post_norm), bool(pre_norm), residual_scale,
                      weight_offset, eps)
 
 
@@ -944,20 +953,24 @@ def moe_block_norm(branch, residual=None, gate=None, post_weight=None, pre_weigh
     """What stands between two blocks (include/moe.h: moe_block_norm_fwd): the norm of `branch`
     (post_norm), times `gate` ([H] per channel, [T] or [T, 1] per token, [T, H]), plus
     residual_scale * residual, and the norm of that for the next block (pre_norm).  Returns
-    (stream, normed), None for what is not computed (want_stream, pre_norm)."""
+    (stream, normed), None for what is not computed (want_stream, pre_norm).  `stream_out` may be
+    the residual or the branch."""
     p = _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
                     residual_scale, weight_offset, eps)
+    if stream_out is not None:
+        _fits(stream_out, "stream_out", branch.dtype, branch.shape)
     normed = None
-    with _CallStream(stream, branch.device) as c:
-        if stream_out is not None:
-            _need(stream_out, "stream_out", branch.dtype, branch.shape)
-        elif want_stream:
+    with _on(stream):
+        if stream_out is None and want_stream:
             stream_out = torch.empty_like(branch)
         if pre_norm:
             normed = torch.empty_like(branch)
-        _check(lib().moe_block_norm_fwd(ctypes.byref(p), _ptr(branch), _ptr(residual), _ptr(gate),
-                                        _ptr(post_weight), _ptr(pre_weight), _ptr(stream_out),
-                                        _ptr(normed), c.handle), "moe_block_norm_fwd")
+        rc = lib().moe_block_norm_fwd(ctypes.byref(p), branch.data_ptr(), _ptr(residual),
+                                      _ptr(gate), _ptr(post_weight), _ptr(pre_weight),
+                                      _ptr(stream_out), _ptr(normed),
+                                      _handle(stream, branch.device))
+    if rc:
+        _check(rc, "moe_block_norm_fwd")
     return stream_out, normed
 
 
@@ -970,62 +983,87 @@ def moe_block_norm_bwd(d_stream, d_normed, branch, residual=None, gate=None, pos
     p = _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
                     residual_scale, weight_offset, eps)
     if d_stream is not None:
-        _need(d_stream, "d_stream", branch.dtype, branch.shape)
+        _fits(d_stream, "d_stream", branch.dtype, branch.shape)
     if (d_normed is not None) != bool(pre_norm):
         raise ValueError("d_normed goes with pre_norm")
     if d_normed is not None:
-        _need(d_normed, "d_normed", branch.dtype, branch.shape)
-    with _CallStream(stream, branch.device) as c:
-        nbytes = lib().moe_block_norm_bwd_workspace_size(ctypes.byref(p))
+        _fits(d_normed, "d_normed", branch.dtype, branch.shape)
+    L = lib()
+    empty = torch.empty_like
+    with _on(stream):
+        s = _handle(stream, branch.device)
         if workspace is None:
-            workspace = c.workspace(nbytes)
-        ins = dict(d_branch=branch, d_residual=residual, d_gate=gate, d_post_weight=post_weight,
-                   d_pre_weight=pre_weight)
-        out = {k: torch.empty_like(v) for k, v in ins.items() if v is not None}
-        _check(lib().moe_block_norm_bwd(
-            ctypes.byref(p), _ptr(d_stream), _ptr(d_normed), _ptr(branch), _ptr(residual),
-            _ptr(gate), _ptr(post_weight), _ptr(pre_weight), *[_ptr(out.get(k)) for k in ins],
-            _ptr(workspace), workspace.numel(), c.handle), "moe_block_norm_bwd")
+            workspace = _scratch(L.moe_block_norm_bwd_workspace_size(ctypes.byref(p)),
+                                 branch.device, s)
+        out = {"d_branch": empty(branch)}
+        if residual is not None:
+            out["d_residual"] = empty(residual)
+        if gate is not None:
+            out["d_gate"] = empty(gate)
+        if post_weight is not None:
+            out["d_post_weight"] = empty(post_weight)
+        if pre_weight is not None:
+            out["d_pre_weight"] = empty(pre_weight)
+        get = out.get
+        rc = L.moe_block_norm_bwd(
+            ctypes.byref(p), _ptr(d_stream), _ptr(d_normed), branch.data_ptr(), _ptr(residual),
+            _ptr(gate), _ptr(post_weight), _ptr(pre_weight), out["d_branch"].data_ptr(),
+            _ptr(get("d_residual")), _ptr(get("d_gate")), _ptr(get("d_post_weight")),
+            _ptr(get("d_pre_weight")), workspace.data_ptr(), workspace.numel(), s)
+    if rc:
+        _check(rc, "moe_block_norm_bwd")
     return out
 
 
-def _router_args(gating_output, topk_ids, seq_offsets):
+def _router_args(gating_output, topk_ids, seq_offsets, scoring_func, renormalize, factor):
     if gating_output.dim() != 2 or topk_ids.dim() != 2:
         raise ValueError("gating_output and topk_ids must have two dimensions")
+    scoring = _SCORING.get(scoring_func)
+    if scoring is None:
+        raise ValueError(f"unsupported scoring_func {scoring_func}")
     T, E = gating_output.shape
     k = topk_ids.shape[1]
-    _need(gating_output, "gating_output", torch.float32)
-    _need(topk_ids, "topk_ids", torch.int32, (T, k))
+    _fits(gating_output, "gating_output", torch.float32, (T, E))
+    _fits(topk_ids, "topk_ids", torch.int32, (T, k))
     n_seq = 1
     if seq_offsets is not None:
-        _need(seq_offsets, "seq_offsets", torch.int32)
         n_seq = seq_offsets.numel() - 1
         if seq_offsets.dim() != 1 or n_seq < 1:
             raise ValueError("seq_offsets must hold n_seq + 1 offsets")
-    return T, E, k, n_seq
+        _fits(seq_offsets, "seq_offsets", torch.int32, (n_seq + 1,))
+    p = MoeProblem(T, 8, E, 8, k, MOE_BF16, scoring, bool(renormalize), 0, 0, factor)
+    return p, T, E, k, n_seq
 
 
 def moe_balance_loss(gating_output, topk_ids, coeff, scoring_func="softmax", seq_offsets=None,
                      workspace=None, stream=None):
     """Per-expert counts and the balance loss of ragged sequences (include/moe.h:
     moe_balance_loss_fwd).  Returns a dict of loss [1] and, per sequence, counts [n_seq, E] int32,
-    live_tokens [n_seq] int32, prob_sum and coef [n_seq, E]; coef is what moe_router_bwd takes."""
-    T, E, k, n = _router_args(gating_output, topk_ids, seq_offsets)
-    prob = make_problem(T, 8, E, 8, k, torch.bfloat16, scoring_func)
+    live_tokens [n_seq] int32, prob_sum and coef [n_seq, E]; coef is what moe_router_bwd takes.
+    The results are views of one allocation."""
+    p, _, E, _, n = _router_args(gating_output, topk_ids, seq_offsets, scoring_func, True, 1.0)
     dev = gating_output.device
-    with _CallStream(stream, dev) as c:
+    L = lib()
+    with _on(stream):
+        s = _handle(stream, dev)
         if workspace is None:
-            workspace = c.workspace(lib().moe_balance_loss_workspace_size(ctypes.byref(prob), n))
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
-        counts = torch.empty((n, E), dtype=torch.int32, device=dev)
-        live = torch.empty(n, dtype=torch.int32, device=dev)
-        prob_sum = torch.empty((n, E), dtype=torch.float32, device=dev)
-        coef = torch.empty((n, E), dtype=torch.float32, device=dev)
-        _check(lib().moe_balance_loss_fwd(
-            ctypes.byref(prob), n, coeff, _ptr(gating_output), _ptr(topk_ids), _ptr(seq_offsets),
-            _ptr(loss), _ptr(counts), _ptr(live), _ptr(prob_sum), _ptr(coef), _ptr(workspace),
-            workspace.numel(), c.handle), "moe_balance_loss_fwd")
-    return dict(loss=loss, counts=counts, live_tokens=live, prob_sum=prob_sum, coef=coef)
+            workspace = _scratch(L.moe_balance_loss_workspace_size(ctypes.byref(p), n), dev, s)
+        # [prob_sum | coef | loss, then counts | live_tokens], each on a 16-byte boundary
+        table = (n * E + 3) // 4 * 4
+        f32 = torch.empty(3 * table + 4 + n, dtype=torch.float32, device=dev)
+        at = f32.data_ptr()
+        rc = L.moe_balance_loss_fwd(
+            ctypes.byref(p), n, coeff, gating_output.data_ptr(), topk_ids.data_ptr(),
+            _ptr(seq_offsets), at + 8 * table, at + 8 * table + 16, at + 12 * table + 16, at,
+            at + 4 * table, workspace.data_ptr(), workspace.numel(), s)
+    if rc:
+        _check(rc, "moe_balance_loss_fwd")
+    i32 = f32.view(torch.int32)
+    return {"loss": f32[2 * table:2 * table + 1],
+            "counts": i32.as_strided((n, E), (E, 1), 2 * table + 4),
+            "live_tokens": i32.as_strided((n,), (1,), 3 * table + 4),
+            "prob_sum": f32.as_strided((n, E), (E, 1), 0),
+            "coef": f32.as_strided((n, E), (E, 1), table)}
 
 
 def moe_router_bwd(gating_output, topk_ids, d_topk_weights=None, coef=None, d_loss=None,
@@ -1034,23 +1072,25 @@ def moe_router_bwd(gating_output, topk_ids, d_topk_weights=None, coef=None, d_lo
     """The gradient of the router logits (include/moe.h: moe_router_bwd) from d_topk_weights
     [T, top_k] (of moe_route's weights) and from the balance loss: `coef` of moe_balance_loss
     times d_loss (a device scalar, 1 when None).  Returns d_gating_output [T, E] f32."""
-    T, E, k, n = _router_args(gating_output, topk_ids, seq_offsets)
+    p, T, E, k, n = _router_args(gating_output, topk_ids, seq_offsets, scoring_func, renormalize,
+                                 routed_scaling_factor)
     if d_topk_weights is not None:
-        _need(d_topk_weights, "d_topk_weights", torch.float32, (T, k))
+        _fits(d_topk_weights, "d_topk_weights", torch.float32, (T, k))
     if coef is not None:
-        _need(coef, "coef", torch.float32, (n, E))
+        _fits(coef, "coef", torch.float32, (n, E))
     if d_loss is not None:
-        _need(d_loss, "d_loss", torch.float32)
         if d_loss.numel() != 1:
             raise ValueError("d_loss must hold one value")
-    prob = make_problem(T, 8, E, 8, k, torch.bfloat16, scoring_func, renormalize,
-                        routed_scaling_factor=routed_scaling_factor)
-    with _CallStream(stream, gating_output.device) as c:
+        _need(d_loss, "d_loss", torch.float32)
+    if out is not None:
+        _fits(out, "out", torch.float32, (T, E))
+    with _on(stream):
         if out is None:
             out = torch.empty_like(gating_output)
-        else:
-            _need(out, "out", torch.float32, (T, E))
-        _check(lib().moe_router_bwd(ctypes.byref(prob), n, _ptr(gating_output), _ptr(topk_ids),
-                                    _ptr(d_topk_weights), _ptr(coef), _ptr(seq_offsets),
-                                    _ptr(d_loss), _ptr(out), c.handle), "moe_router_bwd")
+        rc = lib().moe_router_bwd(ctypes.byref(p), n, gating_output.data_ptr(),
+                                  topk_ids.data_ptr(), _ptr(d_topk_weights), _ptr(coef),
+                                  _ptr(seq_offsets), _ptr(d_loss), out.data_ptr(),
+                                  _handle(stream, gating_output.device))
+    if rc:
+        _check(rc, "moe_router_bwd")
     return out
