@@ -18,6 +18,57 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
+// True in one lane of a converged warp.  The producer and issuer loops below run in all lanes and
+// only their asynchronous instructions are elected: stage, phase and addresses then stay
+// warp-uniform, as those instructions need their operands.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// mbar_try_wait may suspend the thread for a while; this only looks.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A bounded wait (as mbar_wait: false once `limit_ns` has passed or another role gave up, at the
+// first look with a limit of 0) that reads the timer every 64 polls.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         uint64_t limit_ns, int* status) {
+  if (limit_ns == 0) {
+    if (mbar_test_wait(bar, parity)) return true;
+  } else {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if ((it & 63) != 0) continue;
+      if (*abort) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0)
+        t0 = t;
+      else if (t - t0 > limit_ns)
+        break;
+    }
+  }
+  *abort = 1;
+  if (status) atomicCAS(status, 0, (int)MOE_ERR_TIMEOUT);
+  return false;
+}
+
 struct LinArgs {
   int T, N, K;
   int act, out_f32;
@@ -27,6 +78,42 @@ struct LinArgs {
   int* status;
   uint64_t limit_ns;
 };
+
+// Position in a ring of `stages` barriers.  A look at a barrier takes over a hundred cycles to
+// come back even when its phase is over, so the next stage's is looked at (`ready`) before the
+// current stage's copies or MMAs are issued; only if it was not over yet is it waited for.
+struct Ring {
+  uint64_t* bars;
+  int stages, stage;
+  uint32_t parity;
+  bool ready;
+  __device__ __forceinline__ Ring(uint64_t* b, int n, uint32_t p)
+      : bars(b), stages(n), stage(0), parity(p), ready(false) {}
+  __device__ __forceinline__ uint64_t* bar() const { return bars + stage; }
+  __device__ __forceinline__ void next() {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+    ready = mbar_test_wait(bars + stage, parity);
+  }
+};
+
+// After a wait gave up: copies of the last `stages` of `issued` stages, or MMAs, land (one
+// bounded budget) before the CTA goes on to leave.
+constexpr uint64_t kDrainNs = 1000000000ull;
+__device__ __forceinline__ void land_copies(uint64_t* full_bar, int issued, int stages) {
+  const uint64_t t = global_timer_ns();
+  const int n = issued < stages ? issued : stages;
+  for (int i = issued - n; i < issued; ++i)
+    while (!mbar_try_wait(&full_bar[i % stages], (uint32_t)((i / stages) & 1)))
+      if (global_timer_ns() - t > kDrainNs) break;
+}
+__device__ __forceinline__ void land_mmas(uint64_t* bar) {
+  const uint64_t t = global_timer_ns();
+  while (!mbar_try_wait(bar, 0))
+    if (global_timer_ns() - t > kDrainNs) break;
+}
 
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
@@ -61,34 +148,6 @@ __device__ __forceinline__ void finish(const LinArgs& p, float z, int t, int n) 
   }
 }
 
-// Sixteen consecutive rows of x (t ... t+15, the first `live` of them) for one output column: all
-// residuals are asked for before the first is needed.
-template <typename T>
-__device__ __forceinline__ void finish16(const LinArgs& p, float (&z)[16], int t, int live,
-                                         int n) {
-  const float b = p.bias ? DT<T>::to_f(static_cast<const T*>(p.bias)[n]) : 0.0f;
-  const int64_t o = (int64_t)t * p.N + n;
-  float r[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    r[j] = 0.0f;
-    if (p.res && j < live)
-      r[j] = p.out_f32 ? static_cast<const float*>(p.res)[o + (int64_t)j * p.N]
-                       : DT<T>::to_f(static_cast<const T*>(p.res)[o + (int64_t)j * p.N]);
-  }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (j >= live) break;
-    float v = z[j] + b;
-    if (p.act != MOE_LINEAR_NONE) v = activate(v, p.act);
-    if (p.res) v += r[j];
-    if (p.out_f32)
-      static_cast<float*>(p.out)[o + (int64_t)j * p.N] = v;
-    else
-      static_cast<T*>(p.out)[o + (int64_t)j * p.N] = DT<T>::from_f(v);
-  }
-}
-
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -98,38 +157,149 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-// Adds the `split` parts of a tile of 128 weight rows by `cols` rows of x, in their order, and
-// finishes this CTA's share (the `part`-th of `split`).  Part s lies at `base` of the cluster's
-// CTA s * stride + first, as [column][128 rows].
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Eight consecutive outputs of row t from their f32 sums; n is a multiple of 8, `bias` holds the
+// biases of the columns.  With N a multiple of 8 they are whole vectors; otherwise one by one.
 template <typename T>
+struct Finish {
+  const LinArgs& p;
+  int n;
+  bool vec;
+  float bias[8];
+  __device__ __forceinline__ Finish(const LinArgs& a, int col) : p(a), n(col) {
+    vec = (a.N & 7) == 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      bias[j] = a.bias && n + j < a.N ? DT<T>::to_f(static_cast<const T*>(a.bias)[n + j]) : 0.0f;
+  }
+  // The residual, asked for before the sums are there.
+  __device__ __forceinline__ void residual(int t, float (&r)[8]) const {
+    const int64_t o = (int64_t)t * p.N + n;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = 0.0f;
+    if (!p.res || n >= p.N) return;
+    if (vec && p.out_f32) {
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.res) + o);
+      const float4 a = src[0], b = src[1];
+      r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
+      r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+    } else if (vec) {
+      unpack<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.res) + o), r);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j < p.N)
+          r[j] = p.out_f32 ? static_cast<const float*>(p.res)[o + j]
+                           : DT<T>::to_f(static_cast<const T*>(p.res)[o + j]);
+    }
+  }
+  __device__ __forceinline__ void store(int t, float (&z)[8], const float (&r)[8]) const {
+    if (n >= p.N) return;
+    const int64_t o = (int64_t)t * p.N + n;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] += bias[j];
+    if (p.act != MOE_LINEAR_NONE)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = activate(z[j], p.act);
+    if (p.res)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] += r[j];
+    if (vec && p.out_f32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
+      dst[0] = make_float4(z[0], z[1], z[2], z[3]);
+      dst[1] = make_float4(z[4], z[5], z[6], z[7]);
+    } else if (vec) {
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + o) = pack<T>(z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (n + j >= p.N) break;
+        if (p.out_f32)
+          static_cast<float*>(p.out)[o + j] = z[j];
+        else
+          static_cast<T*>(p.out)[o + j] = DT<T>::from_f(z[j]);
+      }
+    }
+  }
+};
+
+// The f32 sums of a tile lie in shared memory as [column][128 weight rows] at `base`, in kSplit
+// parts of K that belong to the cluster's CTAs s * stride + first.  This CTA (part `part`) adds
+// the parts of its share of the columns [0, cols), in their order, and finishes the outputs of
+// the rows t0 ... of x: sixteen threads take the 128 consecutive outputs of a row.  A peer's
+// shared memory takes most of a microsecond to answer, so all parts are asked for at once.
+template <typename T, int kSplit>
+__device__ __forceinline__ void join_parts(const LinArgs& p, uint32_t base, int cols, int n0,
+                                           int t0, int part, uint32_t stride, uint32_t first) {
+  const int c1 = cols * (part + 1) / kSplit;
+  const int g = threadIdx.x & 15;
+  const Finish<T> f(p, n0 + g * 8);
+  constexpr int kCols = kSplit <= 2 ? 4 : (kSplit <= 4 ? 2 : 1);  // rows of x at a time
+  const int step = (int)blockDim.x / 16;
+  for (int c = cols * part / kSplit + (int)(threadIdx.x >> 4); c < c1; c += kCols * step) {
+    float4 v[kCols][kSplit][2];
+    float r[kCols][8];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const int ci = c + i * step < c1 ? c + i * step : c;
+      const uint32_t at = base + (uint32_t)((ci * kSlab + g * 8) * 4);
+#pragma unroll
+      for (int s = 0; s < kSplit; ++s) {
+        if (kSplit > 1) {
+          const uint32_t a = cluster_map(at, (uint32_t)s * stride + first);
+          v[i][s][0] = ld_cluster_f4(a);
+          v[i][s][1] = ld_cluster_f4(a + 16);
+        } else {
+          v[i][s][0] = ld_shared_f4(at);
+          v[i][s][1] = ld_shared_f4(at + 16);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCols; ++i)
+      if (c + i * step < c1) f.residual(t0 + c + i * step, r[i]);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      if (c + i * step >= c1) break;
+      float4 a = v[i][0][0], b = v[i][0][1];
+#pragma unroll
+      for (int s = 1; s < kSplit; ++s) {
+        a.x += v[i][s][0].x, a.y += v[i][s][0].y, a.z += v[i][s][0].z, a.w += v[i][s][0].w;
+        b.x += v[i][s][1].x, b.y += v[i][s][1].y, b.z += v[i][s][1].z, b.w += v[i][s][1].w;
+      }
+      float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      f.store(t0 + c + i * step, z, r[i]);
+    }
+  }
+}
+template <typename T, int kMaxSplit>
 __device__ __forceinline__ void join(const LinArgs& p, uint32_t base, int cols, int n0, int t0,
                                      int part, int split, uint32_t stride, uint32_t first) {
-  // four rows of one column per item
-  const int items = cols * (kSlab / 4);
-  const int i0 = (int)((int64_t)items * part / split);
-  const int i1 = (int)((int64_t)items * (part + 1) / split);
-  for (int i = i0 + (int)threadIdx.x; i < i1; i += (int)blockDim.x) {
-    float4 v[8];
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-      if (s < split)
-        v[s] = ld_cluster_f4(cluster_map(base + (uint32_t)i * 16u, (uint32_t)s * stride + first));
-    float4 z = v[0];
-#pragma unroll
-    for (int s = 1; s < 8; ++s)
-      if (s < split) {
-        z.x += v[s].x;
-        z.y += v[s].y;
-        z.z += v[s].z;
-        z.w += v[s].w;
-      }
-    const int t = t0 + i / (kSlab / 4);
-    const int n = n0 + (i % (kSlab / 4)) * 4;
-    if (n < p.N) finish<T>(p, z.x, t, n);
-    if (n + 1 < p.N) finish<T>(p, z.y, t, n + 1);
-    if (n + 2 < p.N) finish<T>(p, z.z, t, n + 2);
-    if (n + 3 < p.N) finish<T>(p, z.w, t, n + 3);
+  if (split == 1) return join_parts<T, 1>(p, base, cols, n0, t0, part, stride, first);
+  if (split == 2) return join_parts<T, 2>(p, base, cols, n0, t0, part, stride, first);
+  if (split == 3) return join_parts<T, 3>(p, base, cols, n0, t0, part, stride, first);
+  if (split == 4) return join_parts<T, 4>(p, base, cols, n0, t0, part, stride, first);
+  if constexpr (kMaxSplit > 4) {
+    if (split == 5) return join_parts<T, 5>(p, base, cols, n0, t0, part, stride, first);
+    if (split == 6) return join_parts<T, 6>(p, base, cols, n0, t0, part, stride, first);
+    if (split == 7) return join_parts<T, 7>(p, base, cols, n0, t0, part, stride, first);
+    return join_parts<T, 8>(p, base, cols, n0, t0, part, stride, first);
   }
+}
+
+// Cluster barrier after which a CTA may leave: it orders nothing but the peers' finished reads
+// (cluster_sync's release would first wait for this CTA's global stores).
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::
+                   : "memory");
 }
 
 // ---- few rows: weights streamed once through the CUDA cores -----------------------------------
@@ -190,8 +360,8 @@ __global__ void __launch_bounds__(kGemvWarps * 32)
 // The tensor cores add to an accumulator with truncation, so its error grows with the number of
 // additions: the 64-k blocks go round kAccs accumulators, which the epilogue adds.
 constexpr int kMmaThreads = 192;
-constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kAccs = 4;
+constexpr int kMaxStages = 12;
 
 template <int BN>
 struct Shape {
@@ -210,18 +380,18 @@ struct Shape {
 template <typename T, int BN>
 __global__ void __launch_bounds__(kMmaThreads)
     mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-               const LinArgs p, int split) {
+               const LinArgs p, int split, int stages) {
   using S = Shape<BN>;
   extern __shared__ uint8_t dsmem[];
-  __shared__ __align__(8) uint64_t full_bar[S::kStages];
-  __shared__ __align__(8) uint64_t empty_bar[S::kStages];
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages];
+  __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
   __shared__ __align__(8) uint64_t done_bar;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   // the same offset in every CTA of the cluster: the join reads the peers' tiles there
   const uint32_t raw = smem_u32(dsmem);
   uint8_t* smem = dsmem + ((1024u - (raw & 1023u)) & 1023u);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort_flag = &s_abort;
   const int rank = split > 1 ? (int)cluster_ctarank() : 0;
   const int tile = blockIdx.x / split;
@@ -233,88 +403,76 @@ __global__ void __launch_bounds__(kMmaThreads)
   const int kb1 = (int)((int64_t)num_kb * (rank + 1) / split);
   const int cols = p.T - t0 < BN ? p.T - t0 : BN;  // live columns
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 1);
+  auto load = [&](int kb, int stage) {
+    uint8_t* st = smem + stage * S::kStageBytes;
+    mbar_arrive_expect_tx(&full_bar[stage], S::kStageBytes);
+    tma_load_2d(st, &tmW, &full_bar[stage], kb * kBlockK, n0);
+    tma_load_2d(st + S::kABytes, &tmX, &full_bar[stage], kb * kBlockK, t0);
+  };
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < stages; ++s) {
+        mbar_init(&full_bar[s], 1);
+        mbar_init(&empty_bar[s], 1);
+      }
+      mbar_init(&done_bar, 1);
+      s_abort = 0;
+      fence_mbar_init();
     }
-    mbar_init(&done_bar, 1);
-    s_abort = 0;
-    fence_mbar_init();
-    prefetch_tensormap(&tmW);
-    prefetch_tensormap(&tmX);
-  }
-  if (warp == 1) {
+  } else if (warp == 1) {
     tmem_alloc(&s_tmem, S::kTmemCols);
     tmem_relinquish();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.limit_ns, p.status)) break;
-        uint8_t* st = smem + stage * S::kStageBytes;
-        mbar_arrive_expect_tx(&full_bar[stage], S::kStageBytes);
-        tma_load_2d(st, &tmW, &full_bar[stage], kb * kBlockK, n0);
-        tma_load_2d(st + S::kABytes, &tmX, &full_bar[stage], kb * kBlockK, t0);
-        ++issued;
-        if (++stage == S::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+    if (elect_one()) {
+      Ring r(empty_bar, stages, 1u);
+      int kb = kb0;
+      for (; kb < kb1; ++kb) {
+        if (!r.ready && !wait_bar(r.bar(), r.parity, abort_flag, p.limit_ns, p.status)) break;
+        const int stage = r.stage;
+        r.next();
+        load(kb, stage);
       }
-      if (*abort_flag) {  // let the copies in flight land before the CTA goes away
-        const uint64_t t = global_timer_ns();
-        const int n = issued < S::kStages ? issued : S::kStages;
-        for (int i = issued - n; i < issued; ++i)
-          while (!mbar_try_wait(&full_bar[i % S::kStages], (uint32_t)((i / S::kStages) & 1)))
-            if (global_timer_ns() - t > kDrainNs) break;
-      }
+      if (*abort_flag) land_copies(full_bar, kb - kb0, stages);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
+    if (elect_one()) {
+      Ring r(full_bar, stages, 0u);
       const uint32_t base = smem_u32(smem);
       const uint32_t idesc = idesc_f16_m128(BN, DT<T>::kIsBF16);
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.limit_ns, p.status)) break;
+        if (!r.ready && !wait_bar(r.bar(), r.parity, abort_flag, p.limit_ns, p.status)) break;
         tc_fence_after();
-        const uint32_t sa = base + (uint32_t)(stage * S::kStageBytes);
+        const uint32_t sa = base + (uint32_t)(r.stage * S::kStageBytes);
         const uint32_t sb = sa + (uint32_t)S::kABytes;
+        const uint32_t d = tmem + (uint32_t)((kb - kb0) % kAccs * BN);
+        uint64_t* empty = &empty_bar[r.stage];
+        r.next();
 #pragma unroll
         for (int k = 0; k < kBlockK / 16; ++k)
-          umma_f16(tmem + (uint32_t)((kb - kb0) % kAccs * BN), sw128_kmajor_desc(sa + k * 32),
-                   sw128_kmajor_desc(sb + k * 32), idesc, (kb - kb0 >= kAccs || k > 0) ? 1u : 0u);
-        umma_commit(&empty_bar[stage]);
-        if (++stage == S::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+          umma_f16(d, sw128_kmajor_desc(sa + k * 32), sw128_kmajor_desc(sb + k * 32), idesc,
+                   (kb - kb0 >= kAccs || k > 0) ? 1u : 0u);
+        umma_commit(empty);
       }
       // done_bar flips when every MMA issued has completed; on an abort that is all that is left
       umma_commit(&done_bar);
-      if (*abort_flag) {
-        const uint64_t t = global_timer_ns();
-        while (!mbar_try_wait(&done_bar, 0))
-          if (global_timer_ns() - t > kDrainNs) break;
-      }
+      if (*abort_flag) land_mmas(&done_bar);
     }
   } else {
-    const bool ok = mbar_wait(&done_bar, 0, abort_flag, p.limit_ns, p.status);
+    const bool ok =
+        __all_sync(kAll, wait_bar(&done_bar, 0, abort_flag, p.limit_ns, p.status));
     tc_fence_after();
     const int q = warp & 3;
     const int row = q * 32 + lane;
     const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
-    __syncwarp();
-    if (__all_sync(kAll, ok)) {
-      float* part = reinterpret_cast<float*>(smem);
+    if (ok) {
+      float* stash = reinterpret_cast<float*>(smem);
       const int accs = kb1 - kb0 < kAccs ? kb1 - kb0 : kAccs;
       for (int c0 = 0; c0 < cols; c0 += 16) {
         float v[16];
@@ -325,25 +483,20 @@ __global__ void __launch_bounds__(kMmaThreads)
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] += u[j];
         }
-        if (split > 1) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) part[(c0 + j) * kSlab + row] = v[j];
-        } else if (n0 + row < p.N) {
-          finish16<T>(p, v, t0 + c0, cols - c0, n0 + row);
-        }
+        for (int j = 0; j < 16; ++j) stash[(c0 + j) * kSlab + row] = v[j];
       }
     }
   }
   __syncwarp();
   tc_fence_before();
-  if (split > 1) {
+  if (split > 1)
     cluster_sync();
-    join<T>(p, smem_u32(smem), cols, n0, t0, rank, split, 1u, 0u);
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while a peer may still read its part
-  } else {
+  else
     __syncthreads();
-  }
+  join<T, 8>(p, smem_u32(smem), cols, n0, t0, rank, split, 1u, 0u);
+  __syncwarp();
+  if (split > 1) cluster_leave();  // a peer may still read this CTA's part
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
@@ -363,28 +516,61 @@ __global__ void __launch_bounds__(kMmaThreads)
 // and the epilogue warps add the finished one to sums in registers, rounded to nearest (the
 // tensor cores truncate; a chain over all of K would cost several bits).
 constexpr int kDrainKb = 8;
+constexpr int kJoinCols = 128;  // columns whose sums are in shared memory at a time (64 KB)
+
+// TMEM address of the lanes that an epilogue warp may read.
+__device__ __forceinline__ uint32_t tmem_lane(uint32_t tmem, int warp) {
+  return tmem + ((uint32_t)((warp & 3) * 32) << 16);
+}
+// Columns [from, from + min(cols, kJoinCols)) of a warp's accumulator rows, to shared memory.
+__device__ __forceinline__ void stash_cols(uint32_t tb, int from, float* stash, int row,
+                                           int cols) {
+  for (int c0 = 0; c0 < cols && c0 < kJoinCols; c0 += 16) {
+    float v[16];
+    tmem_ld_x16(tb + (uint32_t)(from + c0), v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) stash[(c0 + j) * kSlab + row] = v[j];
+  }
+}
 
 template <int BN, bool kF32>
 struct PairShape {
+  // 64-k blocks per stage: at BN = 128 the four MMAs of one block take less time than a stage's
+  // waits and arrivals
+  static constexpr int kKps = BN == 128 ? 2 : 1;
+  static constexpr int kPerSm = BN == 128 ? 1 : 2;
   static constexpr int kABytes = kSlab * kBlockK * 2;
   static constexpr int kBBytes = BN / 2 * kBlockK * 2;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 3 : 4;
+  static constexpr int kBlockBytes = kABytes + kBBytes;
+  static constexpr int kStageBytes = kKps * kBlockBytes;
+  static constexpr int kStages = BN == 128 ? 4 : 3;
   static constexpr int kSmem = kStages * kStageBytes + 1024;
   static constexpr int kBufs = kF32 ? 2 : 1;
   static constexpr int kTmemCols = kBufs * BN;
-  static_assert(2 * (kSmem + 2048) <= 228 * 1024 && kTmemCols <= 256, "two CTAs per SM");
-  static_assert(!kF32 || BN == 128, "the sums of a row stay in registers");
+  static_assert(kPerSm * (kSmem + 2048) <= 228 * 1024 && kPerSm * kTmemCols <= 512, "per SM");
+  static_assert(kJoinCols * kSlab * 4 <= kStages * kStageBytes, "the sums of a tile");
+  static_assert(!kF32 || (BN == 128 && kDrainKb % kKps == 0), "the sums of a row stay in registers");
 };
 
+// Arrives on the barrier at this offset of both CTAs of the pair when the MMAs issued so far
+// have completed.
+__device__ __forceinline__ void umma_commit_both(uint32_t bar, uint32_t even) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)(3u << even))
+      : "memory");
+}
+
 template <typename T, int BN, bool kF32>
-__global__ void __launch_bounds__(kMmaThreads, 2)
+__global__ void __launch_bounds__(kMmaThreads, PairShape<BN, kF32>::kPerSm)
     pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const LinArgs p, int split) {
   using S = PairShape<BN, kF32>;
+  constexpr int stages = S::kStages;
   extern __shared__ uint8_t dsmem[];
-  __shared__ __align__(8) uint64_t full_bar[S::kStages];
-  __shared__ __align__(8) uint64_t empty_bar[S::kStages];
+  __shared__ __align__(8) uint64_t full_bar[stages];
+  __shared__ __align__(8) uint64_t empty_bar[stages];
   __shared__ __align__(8) uint64_t tfull_bar[S::kBufs];
   __shared__ __align__(8) uint64_t tempty_bar[S::kBufs];
   __shared__ __align__(8) uint64_t drain_bar;
@@ -392,7 +578,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   __shared__ int s_abort;
   const uint32_t raw = smem_u32(dsmem);
   uint8_t* smem = dsmem + ((1024u - (raw & 1023u)) & 1023u);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort_flag = &s_abort;
   const uint32_t rank = cluster_ctarank();
   const uint32_t side = rank & 1u, even = rank & ~1u;
@@ -407,23 +593,22 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   const int cols = p.T - t0 < BN ? p.T - t0 : BN;
   const int chunk = kF32 ? kDrainKb : kb1 - kb0;  // blocks of one accumulator pass
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      // the even CTA's stage is full when its copies and, by the forwarder, the odd CTA's landed
-      mbar_init(&full_bar[s], side == 0 ? 2 : 1);
-      mbar_init(&empty_bar[s], 1);
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < stages; ++s) {
+        // the even CTA's stage is full when its copies and, by the forwarder, the odd CTA's landed
+        mbar_init(&full_bar[s], side == 0 ? 2 : 1);
+        mbar_init(&empty_bar[s], 1);
+      }
+      for (int b = 0; b < S::kBufs; ++b) {
+        mbar_init(&tfull_bar[b], 1);
+        mbar_init(&tempty_bar[b], 8);  // an arrival per epilogue warp of both CTAs
+      }
+      mbar_init(&drain_bar, 1);
+      s_abort = 0;
+      fence_mbar_init();
     }
-    for (int b = 0; b < S::kBufs; ++b) {
-      mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], 8);  // an arrival per epilogue warp of both CTAs
-    }
-    mbar_init(&drain_bar, 1);
-    s_abort = 0;
-    fence_mbar_init();
-    prefetch_tensormap(&tmW);
-    prefetch_tensormap(&tmX);
-  }
-  if (warp == 1) {
+  } else if (warp == 1) {
     tmem_alloc_pair(&s_tmem, S::kTmemCols);
     tmem_relinquish_pair();
   }
@@ -432,86 +617,85 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  bool got = false;  // this epilogue warp saw its accumulator
   const uint32_t peer_abort = cluster_map(smem_u32(&s_abort), rank ^ 1u);
+  // by one thread; on giving up the peer CTA is told too
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_wait(bar, parity, abort_flag, p.limit_ns, p.status)) return true;
+    if (wait_bar(bar, parity, abort_flag, p.limit_ns, p.status)) return true;
     st_cluster_u32(peer_abort, 1u);
     return false;
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
+    if (elect_one()) {
+      Ring r(empty_bar, stages, 1u);
+      int issued = 0;
       const int tx = t0 + (int)side * (BN / 2);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait(&empty_bar[stage], phase ^ 1u)) break;
-        uint8_t* st = smem + stage * S::kStageBytes;
-        mbar_arrive_expect_tx(&full_bar[stage], S::kStageBytes);
-        tma_load_2d(st, &tmW, &full_bar[stage], kb * kBlockK, n0);
-        tma_load_2d(st + S::kABytes, &tmX, &full_bar[stage], kb * kBlockK, tx);
-        ++issued;
-        if (++stage == S::kStages) {
-          stage = 0;
-          phase ^= 1u;
+      for (int kb = kb0; kb < kb1; kb += S::kKps) {
+        if (!r.ready && !wait(r.bar(), r.parity)) break;
+        uint8_t* st = smem + r.stage * S::kStageBytes;
+        uint64_t* full = &full_bar[r.stage];
+        r.next();
+        const int n = kb1 - kb < S::kKps ? kb1 - kb : S::kKps;
+        mbar_arrive_expect_tx(full, (uint32_t)(n * S::kBlockBytes));
+#pragma unroll
+        for (int j = 0; j < S::kKps; ++j) {
+          if (j >= n) break;
+          uint8_t* at = st + j * S::kBlockBytes;
+          tma_load_2d(at, &tmW, full, (kb + j) * kBlockK, n0);
+          tma_load_2d(at + S::kABytes, &tmX, full, (kb + j) * kBlockK, tx);
         }
+        ++issued;
       }
-      if (*abort_flag) {  // let the copies in flight land (one budget for all)
-        const uint64_t t = global_timer_ns();
-        const int n = issued < S::kStages ? issued : S::kStages;
-        for (int i = issued - n; i < issued; ++i)
-          while (!mbar_try_wait(&full_bar[i % S::kStages], (uint32_t)((i / S::kStages) & 1)))
-            if (global_timer_ns() - t > kDrainNs) break;
-      }
+      if (*abort_flag) land_copies(full_bar, issued, stages);
     }
   } else if (warp == 1 && side != 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait(&full_bar[stage], phase)) break;
-        mbar_arrive_cluster(cluster_map(smem_u32(&full_bar[stage]), even));
-        if (++stage == S::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+    if (elect_one()) {
+      Ring r(full_bar, stages, 0u);
+      const uint32_t to = cluster_map(smem_u32(full_bar), even);
+      for (int kb = kb0; kb < kb1; kb += S::kKps) {
+        if (!r.ready && !wait(r.bar(), r.parity)) break;
+        mbar_arrive_cluster(to + (uint32_t)r.stage * 8u);
+        r.next();
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
+    if (elect_one()) {
+      Ring r(full_bar, stages, 0u);
+      int buf = 0;
+      uint32_t buf_phase = 0;
       bool ok = true;
       const uint32_t base = smem_u32(smem);
       const uint32_t idesc = idesc_f16(256, BN, DT<T>::kIsBF16);
-      const uint32_t odd = even | 1u;
+      const uint32_t empty_own = smem_u32(empty_bar), tfull_own = smem_u32(tfull_bar);
       for (int kc = kb0; kc < kb1 && ok; kc += chunk) {
         if (kF32 && !wait(&tempty_bar[buf], buf_phase ^ 1u)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * BN);
         const int ke = kc + chunk < kb1 ? kc + chunk : kb1;
-        for (int kb = kc; kb < ke; ++kb) {
-          if (!wait(&full_bar[stage], phase)) {
+        for (int kb = kc; kb < ke; kb += S::kKps) {
+          if (!r.ready && !wait(r.bar(), r.parity)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + (uint32_t)(stage * S::kStageBytes);
-          const uint32_t sb = sa + (uint32_t)S::kABytes;
+          const uint32_t st = base + (uint32_t)(r.stage * S::kStageBytes);
+          const uint32_t at = (uint32_t)r.stage * 8u;
+          r.next();
 #pragma unroll
-          for (int k = 0; k < kBlockK / 16; ++k)
-            umma_f16_pair(d, sw128_kmajor_desc(sa + k * 32), sw128_kmajor_desc(sb + k * 32), idesc,
-                          (kb > kc || k > 0) ? 1u : 0u);
-          umma_commit_pair(smem_u32(&empty_bar[stage]));
-          umma_commit_pair(cluster_map(smem_u32(&empty_bar[stage]), odd));
-          if (++stage == S::kStages) {
-            stage = 0;
-            phase ^= 1u;
+          for (int j = 0; j < S::kKps; ++j) {
+            if (kb + j >= ke) break;
+            const uint32_t sa = st + (uint32_t)(j * S::kBlockBytes);
+            const uint32_t sb = sa + (uint32_t)S::kABytes;
+#pragma unroll
+            for (int k = 0; k < kBlockK / 16; ++k)
+              umma_f16_pair(d, sw128_kmajor_desc(sa + k * 32), sw128_kmajor_desc(sb + k * 32),
+                            idesc, (kb > kc || j > 0 || k > 0) ? 1u : 0u);
           }
+          umma_commit_both(empty_own + at, even);
         }
         if (!ok) break;
-        umma_commit_pair(smem_u32(&tfull_bar[buf]));
-        umma_commit_pair(cluster_map(smem_u32(&tfull_bar[buf]), odd));
+        umma_commit_both(tfull_own + (uint32_t)buf * 8u, even);
         if (++buf == S::kBufs) {
           buf = 0;
           buf_phase ^= 1u;
@@ -519,14 +703,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       }
       // every MMA issued has completed once drain_bar flips
       umma_commit_pair(smem_u32(&drain_bar));
-      const uint64_t t = global_timer_ns();
-      while (!mbar_try_wait(&drain_bar, 0))
-        if (global_timer_ns() - t > kDrainNs) break;
+      land_mmas(&drain_bar);
     }
   } else {
-    const int q = warp & 3;
-    const int row = q * 32 + lane;
-    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t tb = tmem_lane(tmem, warp);
     float* stash = reinterpret_cast<float*>(smem);
     if constexpr (kF32) {
       float acc[BN] = {};
@@ -555,41 +736,38 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       }
       if (ok) {
 #pragma unroll
-        for (int c = 0; c < BN; ++c) {
-          if (c < cols) {
-            if (split > 1)
-              stash[c * kSlab + row] = acc[c];
-            else if (n0 + row < p.N)
-              finish<T>(p, acc[c], t0 + c, n0 + row);
-          }
-        }
+        for (int c = 0; c < BN; ++c)
+          if (c < cols) stash[c * kSlab + row] = acc[c];
       }
     } else {
-      const bool ok = wait(&tfull_bar[0], 0);
+      got = __all_sync(kAll, wait(&tfull_bar[0], 0));
       tc_fence_after();
-      __syncwarp();
-      if (__all_sync(kAll, ok)) {
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-          float v[16];
-          tmem_ld_x16(tb + (uint32_t)c0, v);
-          if (split > 1) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) stash[(c0 + j) * kSlab + row] = v[j];
-          } else if (n0 + row < p.N) {
-            finish16<T>(p, v, t0 + c0, cols - c0, n0 + row);
-          }
-        }
-      }
+      if (got) stash_cols(tb, 0, stash, row, cols);
     }
   }
   __syncwarp();
   tc_fence_before();
+  // Both CTAs of a pair are past their MMAs here, and the parts of a split are in place.
   cluster_sync();
-  if (split > 1) {
-    join<T>(p, smem_u32(smem), cols, n0, t0, part, split, 2u, side);
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while a peer may still read its part
+  tc_fence_after();
+  join<T, 4>(p, smem_u32(smem), cols < kJoinCols ? cols : kJoinCols, n0, t0, part, split, 2u, side);
+  if constexpr (BN > kJoinCols) {  // not split: the second half by the CTA alone
+    if (cols > kJoinCols) {
+      __syncthreads();
+      if (warp >= 2 && got) stash_cols(tmem_lane(tmem, warp), kJoinCols,
+                                       reinterpret_cast<float*>(smem), (warp & 3) * 32 + lane,
+                                       cols - kJoinCols);
+      __syncwarp();
+      tc_fence_before();
+      __syncthreads();
+      join_parts<T, 1>(p, smem_u32(smem), cols - kJoinCols, n0, t0 + kJoinCols, 0, 2u, side);
+    }
   }
+  __syncwarp();
+  if (split > 1)
+    cluster_leave();  // a peer may still read this CTA's part
+  else
+    __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, S::kTmemCols);
@@ -613,10 +791,10 @@ cudaError_t set_smem_limit(int bytes) {
   return result[dev];
 }
 
-template <auto Kernel>
+template <auto Kernel, typename... Rest>
 cudaError_t launch_tiles(const LinArgs& p, int dtype, const void* x, const void* w, int box_x,
-                         int smem, int64_t ctas, int cluster, int split, cudaStream_t s) {
-  const cudaError_t e = set_smem_limit<Kernel>(smem);
+                         int smem, int64_t ctas, int cluster, cudaStream_t s, Rest... rest) {
+  const cudaError_t e = set_smem_limit<Kernel>(227 * 1024 - 1024);
   if (e != cudaSuccess) return e;
   CUtensorMap tmW, tmX;
   if (!make_map16(&tmW, dtype, w, (uint64_t)p.K, (uint64_t)p.N, kSlab) ||
@@ -635,7 +813,7 @@ cudaError_t launch_tiles(const LinArgs& p, int dtype, const void* x, const void*
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, Kernel, tmW, tmX, p, split);
+  return cudaLaunchKernelEx(&cfg, Kernel, tmW, tmX, p, rest...);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -645,13 +823,17 @@ cudaError_t launch_mma(const LinArgs& p, int dtype, const void* x, const void* w
                        cudaStream_t s) {
   const int64_t tiles = ceil_div(p.N, kSlab) * ceil_div(p.T, BN);
   const int num_kb = (p.K + kBlockK - 1) / kBlockK;
-  // Split K while the tiles leave SM slots empty and each part keeps at least four 64-k blocks.
+  // Split K while two CTAs per SM take the parts and each keeps at least seven 64-k blocks.
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= (int64_t)num_sms() * Shape<BN>::kPerSm &&
-         num_kb >= split * 2 * 4)
-    split *= 2;
-  return launch_tiles<mma_kernel<T, BN>>(p, dtype, x, w, BN, Shape<BN>::kSmem, tiles * split,
-                                         split, split, s);
+  while (split < 8 && tiles * (split + 1) <= (int64_t)num_sms() * 2 && num_kb >= (split + 1) * 7)
+    ++split;
+  // Alone on its SM a CTA takes all the shared memory for stages.
+  int stages = Shape<BN>::kStages;
+  if (tiles * split <= num_sms()) stages = 225 * 1024 / Shape<BN>::kStageBytes;
+  if (stages > kMaxStages) stages = kMaxStages;
+  return launch_tiles<mma_kernel<T, BN>>(p, dtype, x, w, BN,
+                                         stages * Shape<BN>::kStageBytes + 1024, tiles * split,
+                                         split, s, split, stages);
 }
 
 template <typename T, int BN, bool kF32>
@@ -661,10 +843,10 @@ cudaError_t launch_pair(const LinArgs& p, int dtype, const void* x, const void* 
   const int num_kb = (p.K + kBlockK - 1) / kBlockK;
   int split = 1;
   if (BN == 128)  // a part of a 256-column tile does not fit beside a second CTA
-    while (split < 4 && tiles * split * 2 <= num_sms() && num_kb >= split * 2 * 4) split *= 2;
+    while (split < 4 && tiles * (split + 1) * 2 <= num_sms() && num_kb >= (split + 1) * 7) ++split;
   return launch_tiles<pair_kernel<T, BN, kF32>>(p, dtype, x, w, BN / 2,
                                                 PairShape<BN, kF32>::kSmem, tiles * split * 2,
-                                                2 * split, split, s);
+                                                2 * split, s, split);
 }
 
 template <typename T>
