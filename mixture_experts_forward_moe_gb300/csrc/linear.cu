@@ -369,7 +369,6 @@ struct Shape {
   static constexpr int kABytes = kSlab * kBlockK * 2;
   static constexpr int kBBytes = BN * kBlockK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kSmem = kStages * kStageBytes + 1024;
   static constexpr int kTmemCols = kAccs * BN;
   // CTAs that fit an SM (228 KB of shared memory, 512 TMEM columns)
   static constexpr int kPerSm = BN <= 32 ? 3 : 2;

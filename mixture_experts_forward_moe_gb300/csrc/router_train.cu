@@ -2,10 +2,12 @@
 // moe_router_bwd): per-expert counts, the balance loss over ragged sequences, and the gradient of
 // the logits from that loss and from the route weights.
 //
-// One warp per token, expert e in lane e % 32, as in the router itself.
+// One warp per token, its row of logits spread over the lanes, as in the router itself.
+#include <limits.h>
 #include <math.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace gb300moe {
 
@@ -25,45 +27,108 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// A token's unnormalised probabilities, safe at both ends of the range: softmax shifts by the
-// largest logit m.  sigmoid(x) / sum sigmoid is unchanged when every sigmoid is multiplied by
-// e^-b; with b = min(m, 0) the largest stays near 1 where plain sigmoids would underflow.
-// A row of -inf alone gives zeros.
-struct Shift {
-  float b;   // subtracted in the exponent
-  float eb;  // e^b (sigmoid)
-};
-__device__ __forceinline__ Shift row_shift(float m, int scoring) {
-  Shift s;
-  s.b = m == -INFINITY ? 0.0f : (scoring == MOE_SOFTMAX ? m : fminf(m, 0.0f));
-  s.eb = scoring == MOE_SOFTMAX ? 1.0f : expf(s.b);
-  return s;
+// Sum / maximum over the `width` lanes (a power of two) that start at a multiple of it.
+__device__ __forceinline__ float group_sum(float v, int width) {
+  for (int off = width >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+  return v;
 }
-// e: the shifted score; om: 1 - sigmoid(x) (1 for softmax).
-__device__ __forceinline__ void score(float x, const Shift& s, int scoring, float& e, float& om) {
-  if (scoring == MOE_SOFTMAX) {
-    e = expf(x - s.b);
-    om = 1.0f;
-  } else if (x >= 0.0f) {
-    const float t = expf(-x);
-    e = __frcp_rn(1.0f + t);
-    om = t * e;
-  } else {
-    const float t = expf(x - s.b);
-    om = __frcp_rn(fmaf(t, s.eb, 1.0f));
-    e = t * om;
-  }
+__device__ __forceinline__ float group_max(float v, int width) {
+  for (int off = width >> 1; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
+  return v;
 }
-__device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 
-// First sequence s with seq_offsets[s + 1] > t (n_seq when there is none).
-__device__ __forceinline__ int seq_of(const int32_t* off, int n_seq, int t) {
-  int lo = 0, hi = n_seq;
+// A row of E logits (or coefficients) in a warp: lane l holds the VEC consecutive experts from
+// (l + 32 i) VEC on, i < N.  VEC is 4 when E is a multiple of 4 (rows are then whole 16-byte
+// vectors), else 1.
+template <int VEC, int N>
+struct Row {
+  float v[N][VEC];
+  __device__ __forceinline__ void load(const float* row, int E, int lane, float fill) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = (lane + 32 * i) * VEC;
+      if constexpr (VEC == 4) {
+        float4 x = make_float4(fill, fill, fill, fill);
+        if (e < E) x = *reinterpret_cast<const float4*>(row + e);
+        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+      } else {
+        v[i][0] = e < E ? row[e] : fill;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* row, int E, int lane) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = (lane + 32 * i) * VEC;
+      if (e >= E) continue;
+      if constexpr (VEC == 4)
+        *reinterpret_cast<float4*>(row + e) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+      else
+        row[e] = v[i][0];
+    }
+  }
+};
+#define EACH(i, j)                  \
+  _Pragma("unroll") for (int i = 0; i < N; ++i) _Pragma("unroll") for (int j = 0; j < VEC; ++j)
+
+// Sigmoid s and 1 - s, both to f32 precision at either end.
+__device__ __forceinline__ void sigmoid2(float x, float& s, float& om) {
+  const float t = expf(-fabsf(x));
+  const float d = __fdividef(1.0f, 1.0f + t);
+  s = x >= 0.0f ? d : t * d;
+  om = x >= 0.0f ? t * d : d;
+}
+// Below this sum of sigmoids every logit is under -57, where sigmoid(x) is e^x to all of f32's
+// digits: the row (or selection) is then shifted by its largest logit, as a softmax is, instead
+// of underflowing.
+constexpr float kTinySum = 1e-25f;
+
+// Scores of a row, proportional to its probabilities: e^(x - max), or sigmoid(x) (shifted as said
+// above); `om` is 1 - sigmoid (1 for softmax).  Returns 1 / the row's sum, 0 for a row of -inf
+// alone (a sum of NaN stays one).
+template <int VEC, int N>
+__device__ __forceinline__ float row_scores(Row<VEC, N>& x, Row<VEC, N>& om, int scoring) {
+  float sum = 0.0f;
+  if (scoring == MOE_SIGMOID) {
+    Row<VEC, N> s;
+    EACH(i, j) {
+      sigmoid2(x.v[i][j], s.v[i][j], om.v[i][j]);
+      sum += s.v[i][j];
+    }
+    sum = warp_sum(sum);
+    if (!__any_sync(kAll, sum < kTinySum)) {
+      x = s;
+      return __fdividef(1.0f, sum);
+    }
+    sum = 0.0f;
+  }
+  float m = -INFINITY;
+  EACH(i, j) m = fmaxf(m, x.v[i][j]);
+  m = warp_max(m);
+  if (m == -INFINITY) m = 0.0f;
+  EACH(i, j) {
+    x.v[i][j] = expf(x.v[i][j] - m);
+    om.v[i][j] = 1.0f;
+    sum += x.v[i][j];
+  }
+  sum = warp_sum(sum);
+  return sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+}
+
+// First sequence s with seq_offsets[s + 1] > t (n_seq when there is none).  Lane l holds
+// `mine` = seq_offsets[l + 1] (or INT_MAX past the end), which answers for the first 32.
+__device__ __forceinline__ int seq_of(const int32_t* off, int n_seq, int t, int mine) {
+  const int first = __popc(__ballot_sync(kAll, mine <= t));
+  if (first < 32 || n_seq <= 32) return first < n_seq ? first : n_seq;
+  int lo = 32, hi = n_seq;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (off[mid + 1] > t) hi = mid; else lo = mid + 1;
   }
   return lo;
+}
+__device__ __forceinline__ int my_offset(const int32_t* off, int n_seq, int lane) {
+  return off && lane < n_seq ? off[lane + 1] : INT_MAX;
 }
 __device__ __forceinline__ int clamp_i(int v, int lo, int hi) {
   return v < lo ? lo : (v > hi ? hi : v);
@@ -80,69 +145,61 @@ struct Records {
   int32_t* live;   // [n_rec]
 };
 
-template <int VPL>
+template <int VEC, int N>
 __global__ void __launch_bounds__(kWarps * 32)
     balance_chunk_kernel(int T, int E, int K, int n_seq, int scoring, int chunk,
                          const float* __restrict__ x, const int32_t* __restrict__ ids,
                          const int32_t* __restrict__ off, const Records rec, int* status) {
   extern __shared__ uint8_t dyn[];
-  float* s_prob = reinterpret_cast<float*>(dyn);                // [kWarps][E]
-  int* s_count = reinterpret_cast<int*>(s_prob + kWarps * E);   // [E]
+  const int pitch = (E + 3) & ~3;
+  float* s_prob = reinterpret_cast<float*>(dyn);                   // [kWarps][pitch]
+  int* s_count = reinterpret_cast<int*>(s_prob + kWarps * pitch);  // [E]
   __shared__ int s_live;
+  pdl_trigger();  // the second pass waits for this grid before it reads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = blockIdx.x * chunk;
   const int c1 = T - c0 < chunk ? T : c0 + chunk;
   bool bad = false;
   int t0 = c0;
-  for (int s = off ? seq_of(off, n_seq, c0) : 0; s < n_seq && t0 < c1; ++s) {
+  for (int s = off ? seq_of(off, n_seq, c0, my_offset(off, n_seq, lane)) : 0;
+       s < n_seq && t0 < c1; ++s) {
     if (off) t0 = max(t0, off[s]);
     const int t1 = off ? min(c1, off[s + 1]) : c1;
     if (t1 <= t0) continue;
     for (int e = threadIdx.x; e < E; e += blockDim.x) s_count[e] = 0;
     if (threadIdx.x == 0) s_live = 0;
     __syncthreads();
-    float acc[VPL] = {};
+    Row<VEC, N> acc = {};
     int live = 0;
+    // the next token's row and ids are on their way while this one's are worked on
+    Row<VEC, N> next;
+    int next_id = -1;
+    auto fetch = [&](int t) {
+      if (t >= t1) return;
+      next.load(x + (size_t)t * E, E, lane, -INFINITY);
+      next_id = lane < K ? ids[(size_t)t * K + lane] : -1;
+    };
+    fetch(t0 + warp);
     for (int t = t0 + warp; t < t1; t += kWarps) {
-      const int id = lane < K ? ids[(size_t)t * K + lane] : -1;
+      Row<VEC, N> v = next, om;
+      const int id = next_id;
+      fetch(t + kWarps);
       const bool on = id >= 0 && id < E;
       bad |= id < -1 || id >= E;
       if (!__any_sync(kAll, on)) continue;
       ++live;
       if (on) atomicAdd(&s_count[id], 1);
-      const float* row = x + (size_t)t * E;
-      float v[VPL];
-      float m = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = e < E ? row[e] : -INFINITY;
-        m = fmaxf(m, v[i]);
-      }
-      const Shift sh = row_shift(warp_max(m), scoring);
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        float om;
-        score(v[i], sh, scoring, v[i], om);
-        sum += v[i];
-      }
-      const float inv = inverse(warp_sum(sum));
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+      const float inv = row_scores(v, om, scoring);
+      EACH(i, j) acc.v[i][j] = fmaf(v.v[i][j], inv, acc.v[i][j]);
     }
     if (lane == 0 && live) atomicAdd(&s_live, live);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E) s_prob[warp * E + e] = acc[i];
-    }
+    acc.store(s_prob + warp * pitch, E, lane);
     __syncthreads();
     const size_t r = (size_t)blockIdx.x + s;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
       float p = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) p += s_prob[w * E + e];
+      for (int w = 0; w < kWarps; ++w) p += s_prob[w * pitch + e];
       rec.prob[r * E + e] = p;
       rec.count[r * E + e] = s_count[e];
     }
@@ -166,10 +223,9 @@ __global__ void __launch_bounds__(kFinE * kFinC)
                          float* __restrict__ coef, float* part, int* ticket, int* status) {
   __shared__ float s_p[kFinC][kFinE];
   __shared__ int s_c[kFinC][kFinE];
-  __shared__ int s_live, s_nlive, s_last;
+  __shared__ int s_live[kFinC], s_seqs[kFinC];
+  __shared__ int s_last;
   const int tid = threadIdx.y * kFinE + threadIdx.x;
-  if (tid == 0) s_live = s_nlive = 0;
-  __syncthreads();
   // The chunks of sequence s are [first, last]; empty when it has no tokens.
   auto range = [&](int s, int& first, int& last) {
     const int a = off ? clamp_i(off[s], 0, T) : 0;
@@ -177,56 +233,64 @@ __global__ void __launch_bounds__(kFinE * kFinC)
     first = a / chunk;
     last = b > a ? (b - 1) / chunk : first - 1;
   };
-  int n = 0;
+  const int e = blockIdx.x * kFinE + threadIdx.x;
+  pdl_wait();
+  // Sequences with live tokens.
+  int seqs = 0;
   for (int s = tid; s < n_seq; s += kFinE * kFinC) {
     int c, last;
     range(s, c, last);
     bool any = false;
     for (; c <= last && !any; ++c) any = rec.live[(size_t)c + s] > 0;
-    n += any;
+    seqs += any;
     if (off && blockIdx.x == 0 && blockIdx.y == 0 &&
         (off[s] < 0 || off[s + 1] < off[s] || off[s + 1] > T))
       set_status(status, MOE_ERR_INVALID_ARG);
   }
-  if (n) atomicAdd(&s_nlive, n);
   float loss_part = 0.0f;
-  const int e = blockIdx.x * kFinE + threadIdx.x;
   for (int s = blockIdx.y; s < n_seq; s += gridDim.y) {
     int first, last;
     range(s, first, last);
     int live = 0;
     for (int c = first + tid; c <= last; c += kFinE * kFinC) live += rec.live[(size_t)c + s];
-    if (live) atomicAdd(&s_live, live);
     float p = 0.0f;
     int cnt = 0;
     if (e < E)
-#pragma unroll 4
-      for (int c = first + threadIdx.y; c <= last; c += kFinC) {
+#pragma unroll 8
+      for (int c = first + (int)threadIdx.y; c <= last; c += kFinC) {
         const size_t r = ((size_t)c + s) * E + e;
         p += rec.prob[r];
         cnt += rec.count[r];
       }
+    live = __reduce_add_sync(kAll, live);
+    const int n = __reduce_add_sync(kAll, seqs);
     s_p[threadIdx.y][threadIdx.x] = p;
     s_c[threadIdx.y][threadIdx.x] = cnt;
+    if (threadIdx.x == 0) {
+      s_live[threadIdx.y] = live;
+      s_seqs[threadIdx.y] = n;
+    }
     __syncthreads();
-    if (threadIdx.y == 0 && e < E) {
+    if (threadIdx.y == 0) {
+      const int T_all = __reduce_add_sync(kAll, s_live[threadIdx.x]);
+      const int n_all = __reduce_add_sync(kAll, s_seqs[threadIdx.x]);
 #pragma unroll
       for (int y = 1; y < kFinC; ++y) {
         p += s_p[y][threadIdx.x];
         cnt += s_c[y][threadIdx.x];
       }
-      const float T_s = (float)max(s_live, 1);
-      const float w = (float)cnt * (coeff * (float)E) / ((float)max(s_nlive, 1) * (float)K) / T_s /
-                      T_s;
-      const size_t o = (size_t)s * E + e;
-      counts[o] = cnt;
-      prob_sum[o] = p;
-      coef[o] = w;
-      loss_part = fmaf(w, p, loss_part);
-      if (blockIdx.x == 0 && threadIdx.x == 0) live_out[s] = s_live;
+      if (e < E) {
+        const float T_s = (float)max(T_all, 1);
+        const float w =
+            (float)cnt * (coeff * (float)E) / ((float)max(n_all, 1) * (float)K) / T_s / T_s;
+        const size_t o = (size_t)s * E + e;
+        counts[o] = cnt;
+        prob_sum[o] = p;
+        coef[o] = w;
+        loss_part = fmaf(w, p, loss_part);
+      }
+      if (blockIdx.x == 0 && threadIdx.x == 0) live_out[s] = T_all;
     }
-    __syncthreads();
-    if (tid == 0) s_live = 0;
     __syncthreads();
   }
   const int n_parts = gridDim.x * gridDim.y;
@@ -252,7 +316,11 @@ __global__ void __launch_bounds__(kFinE * kFinC)
 }
 
 // ---- gradient of the logits --------------------------------------------------------------------
-template <int VPL>
+//   d x_j = (1 - s_j) (p_j (c_j - sum_i c_i p_i - A) + q_j)
+// with c the loss' coefficients, q the route weights' terms of the selected experts and A what
+// softmax weights without renormalisation take from every expert (1 - s_j is 1 for softmax).
+// The q of a token meet the row in shared memory.
+template <int VEC, int N>
 __global__ void __launch_bounds__(kWarps * 32)
     router_bwd_kernel(int T, int E, int K, int n_seq, int scoring, int renorm, float rsf,
                       const float* x, const int32_t* __restrict__ ids,
@@ -261,67 +329,92 @@ __global__ void __launch_bounds__(kWarps * 32)
                       float* out) {
   extern __shared__ uint8_t dyn[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* s_row = reinterpret_cast<float*>(dyn) + warp * E;  // this warp's route terms, by expert
-  for (int e = lane; e < E; e += 32) s_row[e] = 0.0f;
+  const int pitch = (E + 3) & ~3;
+  float* s_row = reinterpret_cast<float*>(dyn) + warp * pitch;  // this warp's q, by expert
+  for (int e = lane; e < pitch; e += 32) s_row[e] = 0.0f;
   __syncwarp();
   const float scale = d_loss ? *d_loss : 1.0f;
-  for (int t = blockIdx.x * kWarps + warp; t < T; t += gridDim.x * kWarps) {
-    const int id = lane < K ? ids[(size_t)t * K + lane] : -1;
+  const int mine = my_offset(off, n_seq, lane);
+  int width = 1;  // lanes that hold a token's routes
+  while (width < K) width <<= 1;
+  const int stride = gridDim.x * kWarps;
+  // the next token's row, ids and weights are on their way while this one's are worked on
+  Row<VEC, N> next;
+  int next_id = -1;
+  float next_g = 0.0f;
+  auto fetch = [&](int t) {
+    if (t >= T) return;
+    next.load(x + (size_t)t * E, E, lane, -INFINITY);
+    next_id = lane < K ? ids[(size_t)t * K + lane] : -1;
+    next_g = dw && lane < K ? dw[(size_t)t * K + lane] : 0.0f;
+  };
+  fetch(blockIdx.x * kWarps + warp);
+  for (int t = blockIdx.x * kWarps + warp; t < T; t += stride) {
+    Row<VEC, N> v = next, om;
+    const int id = next_id;
+    const float g0 = next_g;
     const bool on = id >= 0 && id < E;
-    const float* row = x + (size_t)t * E;
+    const float xs = on && dw ? x[(size_t)t * E + id] : -INFINITY;
+    // x may be out: the rows that are fetched ahead are this warp's own, written later
+    fetch(t + stride);
     float* dst = out + (size_t)t * E;
     if (!__any_sync(kAll, on)) {
-      for (int e = lane; e < E; e += 32) dst[e] = 0.0f;
+      const Row<VEC, N> zero = {};
+      zero.store(dst, E, lane);
       continue;
     }
-    float v[VPL], om[VPL];
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = e < E ? row[e] : -INFINITY;
-      m = fmaxf(m, v[i]);
-    }
-    const Shift sh = row_shift(warp_max(m), scoring);
     const float* c = nullptr;
     if (coef) {
       if (!off) {
         c = coef;
       } else {
-        const int s = seq_of(off, n_seq, t);
+        const int s = seq_of(off, n_seq, t, mine);
         if (s < n_seq && off[s] <= t) c = coef + (size_t)s * E;
       }
     }
-    float sum = 0.0f, csum = 0.0f, cc[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      score(v[i], sh, scoring, v[i], om[i]);
-      cc[i] = c && e < E ? c[e] * scale : 0.0f;
-      sum += v[i];
-      csum = fmaf(cc[i], v[i], csum);
+    Row<VEC, N> cc = {};
+    if (c) cc.load(c, E, lane, 0.0f);
+    const float inv = row_scores(v, om, scoring);
+    float mean_c = 0.0f;
+    if (c) {
+      EACH(i, j) mean_c = fmaf(cc.v[i][j], v.v[i][j], mean_c);
+      mean_c = warp_sum(mean_c) * inv;
     }
-    const float inv = inverse(warp_sum(sum));
-    const float mean_c = warp_sum(csum) * inv;
-    // The route weights' term of each selected expert, up to the factor 1 - sigmoid.
-    float all = 0.0f;  // softmax over all experts: p_j times this is subtracted
+    float all = 0.0f;
     if (dw) {
-      const float xs = on ? row[id] : -INFINITY;
-      const float g = on ? dw[(size_t)t * K + lane] * rsf : 0.0f;
-      float es, oms, q;
-      if (renorm) {
-        // shifted by the selection's own largest logit: it may lie far below the row's
-        score(xs, row_shift(warp_max(xs), scoring), scoring, es, oms);
-        const float w = es * inverse(warp_sum(es));
-        q = w * (g - warp_sum(w * g));
-      } else {
-        score(xs, sh, scoring, es, oms);
-        if (scoring == MOE_SOFTMAX) {
-          q = es * inv * g;
-          all = warp_sum(q);
+      const float g = on ? g0 * rsf : 0.0f;
+      float q;
+      if (scoring == MOE_SIGMOID) {
+        float s, unused;
+        sigmoid2(xs, s, unused);
+        if (renorm) {
+          float sum = group_sum(s, width);
+          // (decided by the lanes that hold the routes, for all lanes: the others' sums are 0)
+          if (__shfl_sync(kAll, sum, 0) < kTinySum) {
+            const float m = group_max(xs, width);
+            s = m == -INFINITY ? 0.0f : expf(xs - m);
+            sum = group_sum(s, width);
+          }
+          const float w = sum == 0.0f ? 0.0f : __fdividef(s, sum);
+          q = w * (g - group_sum(w * g, width));
         } else {
-          q = es * sh.eb * g;  // the sigmoid itself: the shift undone
+          q = s * g;
         }
+      } else if (renorm) {
+        const float m = group_max(xs, width);
+        const float s = m == -INFINITY ? 0.0f : expf(xs - m);
+        const float sum = group_sum(s, width);
+        const float w = sum == 0.0f ? 0.0f : __fdividef(s, sum);
+        q = w * (g - group_sum(w * g, width));
+      } else {
+        // the row's scores are in their owners' registers
+        v.store(s_row, E, lane);
+        __syncwarp();
+        q = on ? s_row[id] * inv * g : 0.0f;
+        all = warp_sum(q);
+        __syncwarp();
+        for (int e = lane; e < pitch; e += 32) s_row[e] = 0.0f;
+        __syncwarp();
       }
       // An expert named twice gets the sum of its routes, in route order, from the first.
       const unsigned same = __match_any_sync(kAll, on ? id : -1 - lane);
@@ -334,34 +427,35 @@ __global__ void __launch_bounds__(kWarps * 32)
         }
       }
       if (on && (int)__ffs(same) - 1 == lane) s_row[id] = tot;
+      __syncwarp();
+      Row<VEC, N> qr;
+      qr.load(s_row, E, lane, 0.0f);
+      EACH(i, j) v.v[i][j] = (v.v[i][j] * inv * (cc.v[i][j] * scale - mean_c * scale - all) +
+                              qr.v[i][j]) * om.v[i][j];
+      __syncwarp();
+      if (on) s_row[id] = 0.0f;
+      __syncwarp();
+    } else {
+      EACH(i, j) v.v[i][j] = v.v[i][j] * inv * scale * (cc.v[i][j] - mean_c) * om.v[i][j];
     }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E) {
-        const float p = v[i] * inv;
-        float d = p * (cc[i] - mean_c - all);
-        if (dw) d += s_row[e];
-        dst[e] = d * om[i];
-      }
-    }
-    __syncwarp();
-    if (dw && on) s_row[id] = 0.0f;
-    __syncwarp();
+    v.store(dst, E, lane);
   }
 }
 
-constexpr int kBalanceChunk = 64;
+// CTAs of the first pass: four on each of a GB300's 152 SMs.
+constexpr int kChunkCtas = 608;
 
 // Workspace of the balance loss past its header: the records and the parts of the loss.
 struct BalanceLayout {
-  int n_chunks, e_tiles, seq_ctas;
+  int chunk, n_chunks, e_tiles, seq_ctas;
   size_t prob, count, live, part, total;
 };
 BalanceLayout balance_layout(int T, int E, int n_seq) {
   BalanceLayout L;
-  L.n_chunks = (T + kBalanceChunk - 1) / kBalanceChunk;
+  // a token per warp at least
+  L.chunk = ((T + kChunkCtas - 1) / kChunkCtas + kWarps - 1) / kWarps * kWarps;
+  if (L.chunk < kWarps) L.chunk = kWarps;
+  L.n_chunks = (T + L.chunk - 1) / L.chunk;
   L.e_tiles = (E + kFinE - 1) / kFinE;
   L.seq_ctas = n_seq < 512 ? n_seq : 512;
   size_t o = kHeaderBytes;
@@ -383,17 +477,20 @@ BalanceLayout balance_layout(int T, int E, int n_seq) {
 
 size_t balance_workspace_bytes(int T, int E, int n_seq) { return balance_layout(T, E, n_seq).total; }
 
-// CALL(values per lane) for E experts.
-#define ROUTER_VPL(E, CALL)            \
-  [&]() -> cudaError_t {               \
-    const int need_ = ((E) + 31) / 32; \
-    if (need_ <= 1) return CALL(1);    \
-    if (need_ <= 2) return CALL(2);    \
-    if (need_ <= 4) return CALL(4);    \
-    if (need_ <= 8) return CALL(8);    \
-    if (need_ <= 12) return CALL(12);  \
-    if (need_ <= 16) return CALL(16);  \
-    return CALL(32);                   \
+// CALL(VEC, N) for rows of E values.
+#define ROUTER_ROW(E, CALL)                     \
+  [&]() -> cudaError_t {                        \
+    const int e_ = (E);                         \
+    if (e_ % 4 == 0) {                          \
+      if (e_ <= 128) return CALL(4, 1);         \
+      if (e_ <= 256) return CALL(4, 2);         \
+      if (e_ <= 384) return CALL(4, 3);         \
+      if (e_ <= 512) return CALL(4, 4);         \
+      return CALL(4, 8);                        \
+    }                                           \
+    if (e_ <= 64) return CALL(1, 2);            \
+    if (e_ <= 256) return CALL(1, 8);           \
+    return CALL(1, 32);                         \
   }()
 
 cudaError_t launch_balance_loss(const moe_problem_t& p, int n_seq, float coeff, const float* x,
@@ -409,16 +506,16 @@ cudaError_t launch_balance_loss(const moe_problem_t& p, int n_seq, float coeff, 
   int* status = reinterpret_cast<int*>(ws);
   int* ticket = reinterpret_cast<int*>(ws + kTicketOffset);
   if (p.T > 0) {
-    const size_t smem = (size_t)(kWarps + 1) * p.E * 4;
-#define CHUNK_(V)                                                                             \
-  launch_k(balance_chunk_kernel<V>, dim3(L.n_chunks), dim3(kWarps * 32), smem, s, false, p.T, \
-           p.E, p.top_k, n_seq, p.scoring, kBalanceChunk, x, ids, off, rec, status)
-    const cudaError_t e = ROUTER_VPL(p.E, CHUNK_);
+    const size_t smem = (size_t)(kWarps + 1) * (p.E + 3) * 4;
+#define CHUNK_(V, N)                                                                             \
+  launch_k(balance_chunk_kernel<V, N>, dim3(L.n_chunks), dim3(kWarps * 32), smem, s, false, p.T, \
+           p.E, p.top_k, n_seq, p.scoring, L.chunk, x, ids, off, rec, status)
+    const cudaError_t e = ROUTER_ROW(p.E, CHUNK_);
 #undef CHUNK_
     if (e != cudaSuccess) return e;
   }
   return launch_k(balance_final_kernel, dim3(L.e_tiles, L.seq_ctas), dim3(kFinE, kFinC), 0, s,
-                  false, p.T, p.E, p.top_k, n_seq, kBalanceChunk, coeff, off, rec, loss, counts,
+                  p.T > 0, p.T, p.E, p.top_k, n_seq, L.chunk, coeff, off, rec, loss, counts,
                   live, prob_sum, coef, reinterpret_cast<float*>(ws + L.part), ticket, status);
 }
 
@@ -429,12 +526,12 @@ cudaError_t launch_router_bwd(const moe_problem_t& p, int n_seq, const float* x,
   if (p.T == 0) return cudaSuccess;
   const int need = (p.T + kWarps - 1) / kWarps;
   const int most = num_sms() * 8;
-  const size_t smem = (size_t)kWarps * p.E * 4;
-#define BWD_(V)                                                                                \
-  launch_k(router_bwd_kernel<V>, dim3(need < most ? need : most), dim3(kWarps * 32), smem, s, \
+  const size_t smem = (size_t)kWarps * (p.E + 3) * 4;
+#define BWD_(V, N)                                                                                \
+  launch_k(router_bwd_kernel<V, N>, dim3(need < most ? need : most), dim3(kWarps * 32), smem, s, \
            false, p.T, p.E, p.top_k, n_seq, p.scoring, p.renormalize, p.routed_scaling_factor, \
            x, ids, dw, coef, off, d_loss, out)
-  return ROUTER_VPL(p.E, BWD_);
+  return ROUTER_ROW(p.E, BWD_);
 #undef BWD_
 }
 
