@@ -1,41 +1,27 @@
 // block_norm.cu -- the norm, gate and residual between two blocks (include/moe.h:
 // moe_block_norm_fwd, moe_block_norm_bwd).
 //
-//   u = y ry (o + wq), r = a x + g u, h = r rr (o + wp);  ry, rr = 1/sqrt(mean square + eps)
+//   u = y ry q, r = a x + g u, h = r rr w;  ry, rr = 1/sqrt(mean square + eps), q = o + wq, w = o + wp
 //
-// A row is held in registers (16-bit, eight elements per 16-byte vector) by one CTA: both means
-// need the whole row, and r needs ry first, so a row is read once and its two reductions run
-// over the CTA.  Everything between load and store is f32.
+// Both means need the whole row, so a row is read once and stays with the threads that read it
+// (a "group"); its reductions run over the group.  Everything between load and store is f32.
+//   row kernel    forward of few rows, where latency counts: one CTA per row
+//   group kernels persistent, one CTA per SM with as many groups as fit: while one group waits
+//                 for a reduction or for memory another one computes.  Each thread copies its own
+//                 vectors of its next row to shared memory (cp.async) while it works on the
+//                 current one: nobody else reads them, so no barrier orders them.  The
+//                 per-channel vectors lie in shared memory once per CTA.
+#include <mutex>
+
 #include "vec16.cuh"
+#include "ptx.cuh"
 
 namespace gb300moe {
 
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-
-// Sums of N values over the CTA, the same bits in every thread: shuffles within a warp, then
-// each warp adds the warps' sums in the same butterfly.  One barrier; `buf` may be written again
-// only after another one.
-template <int N>
-__device__ __forceinline__ void cta_sum(float (&v)[N], float (*buf)[32], int n_warps) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kAll, v[i], off);
-  if (n_warps == 1) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) buf[i][warp] = v[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < n_warps ? buf[i][lane] : 0.0f;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kAll, v[i], off);
-}
+constexpr int kPairs = kVec / 2;
 
 struct NormArgs {
   int T, H, n_vec;  // n_vec = H / 8
@@ -44,269 +30,573 @@ struct NormArgs {
   const uint4 *y, *x, *g, *wq, *wp;
 };
 
-// The gate of vector v of row t.
-template <typename T>
-__device__ __forceinline__ void load_gate(const NormArgs& p, int t, int v, float (&g)[kVec]) {
-  if (p.gate == MOE_GATE_CHANNEL) {
-    unpack<T>(__ldg(p.g + v), g);
-  } else if (p.gate == MOE_GATE_ELEMENT) {
-    unpack<T>(__ldg(p.g + (size_t)t * p.n_vec + v), g);
-  } else {
-    const float s =
-        p.gate == MOE_GATE_TOKEN ? DT<T>::to_f(reinterpret_cast<const T*>(p.g)[t]) : 1.0f;
+struct NormGrads {
+  const uint4 *dr, *dh;
+  uint4 *dy, *dx, *dg;  // dg: element gate only
+  void* dg_token;       // token gate
+  float* part;          // [gridDim.x][n_cols][H] per-channel partial sums
+  int col_a, col_p;     // which of the n_cols sums are A and P (below), -1: not wanted
+  int n_cols;
+};
+// Per-channel sums over the rows: P = sum dh rhat, and A = sum c D yhat with c the gate where it
+// varies by row and 1 otherwise.  d_pre_weight = P; with a gate per channel d_gate = q A and
+// d_post_weight = g A, else d_post_weight = A.
+
+// Sums of N values over a group of `warps` warps, the same bits in every thread: shuffles within
+// a warp, then each warp adds the warps' sums in the same butterfly.  Consecutive calls of a
+// group use the two halves of `buf` in turn: a half is written again only behind the barrier of
+// the call between.
+template <int N>
+struct GroupSum {
+  float (*buf)[N][32];  // [2][N][the CTA's warps]
+  int warps, warp, lane, bar, threads;
+  int base = 0;  // the group's first warp in the CTA
+  int turn = 0;
+  __device__ __forceinline__ void operator()(float (&v)[N], int n = N) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) g[i] = s;
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < n) v[i] += __shfl_xor_sync(kAll, v[i], off);
+    if (warps == 1) return;
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < n) buf[turn][i][base + warp] = v[i];
+    named_bar_sync(bar, threads);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) v[i] = lane < warps ? buf[turn][i][base + lane] : 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < n) v[i] += __shfl_xor_sync(kAll, v[i], off);
+    turn ^= 1;
   }
+};
+
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// A norm weight's factor o + w (1 without a weight).
 template <typename T>
-__device__ __forceinline__ void load_weight(const uint4* w, float o, int v, float (&f)[kVec]) {
-  if (w) {
-    unpack<T>(__ldg(w + v), f);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) f[i] += o;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) f[i] = 1.0f;
-  }
+__device__ __forceinline__ float token_gate(const NormArgs& p, int t) {
+  return DT<T>::to_f(reinterpret_cast<const T*>(p.g)[t]);
 }
 
+// ---- forward, one CTA per row -----------------------------------------------------------------
 template <typename T, int VPT>
-__global__ void __launch_bounds__(512)
-    block_norm_fwd_kernel(const NormArgs p, uint4* r_out, uint4* h_out) {
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512)
+    norm_row_kernel(const NormArgs p, uint4* r_out, uint4* h_out) {
   __shared__ float s_red[2][1][32];
-  const int n_warps = blockDim.x >> 5;
   const int t = blockIdx.x;
   const size_t row = (size_t)t * p.n_vec;
-  float r[VPT][kVec];
-  uint4 xv[VPT];
-  float ss[1] = {0.0f};
+  GroupSum<1> sum{s_red, (int)blockDim.x >> 5, (int)threadIdx.x >> 5, (int)threadIdx.x & 31, 0,
+                  (int)blockDim.x};
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 yv[VPT], xv[VPT], gv[VPT], qv[VPT], wv[VPT];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
+  for (int i = 0; i < VPT; ++i) {  // everything is asked for before anything is needed
     const int v = threadIdx.x + i * blockDim.x;
-    uint4 yv = make_uint4(0, 0, 0, 0);
-    xv[i] = make_uint4(0, 0, 0, 0);
-    if (v < p.n_vec) {
-      yv = p.y[row + v];
-      if (p.x) xv[i] = p.x[row + v];
-    }
-    unpack<T>(yv, r[i]);
+    const bool in = v < p.n_vec;
+    yv[i] = in ? p.y[row + v] : zero;
+    xv[i] = in && p.x ? p.x[row + v] : zero;
+    gv[i] = zero;
+    if (in && p.gate == MOE_GATE_CHANNEL) gv[i] = __ldg(p.g + v);
+    if (in && p.gate == MOE_GATE_ELEMENT) gv[i] = __ldg(p.g + row + v);
+    qv[i] = in && p.wq ? __ldg(p.wq + v) : zero;
+    wv[i] = in && p.wp ? __ldg(p.wp + v) : zero;
   }
+  const F2 gt = f2(p.gate == MOE_GATE_TOKEN ? token_gate<T>(p, t) : 1.0f);
+  const F2 oq = f2(p.wq ? p.o : 1.0f), ow = f2(p.wp ? p.o : 1.0f), a = f2(p.x ? p.a : 0.0f);
+  F2 r[VPT][kPairs];
+  float ss[1] = {0.0f};
   float ry = 1.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) unpack<T>(yv[i], r[i]);
   if (p.post) {
+    F2 s = f2(0.0f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) ss[0] = fmaf(r[i][j], r[i][j], ss[0]);
-    cta_sum<1>(ss, s_red[0], n_warps);
+      for (int j = 0; j < kPairs; ++j) s = f2_fma(r[i][j], r[i][j], s);
+    ss[0] = f2_sum(s);
+    sum(ss);
     ry = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
   }
-  ss[0] = 0.0f;
+  F2 s = f2(0.0f);
+  const F2 ry2 = f2(ry);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
-    if (v < p.n_vec) {
-      float f[kVec], x[kVec];
-      if (p.post) {
-        load_weight<T>(p.wq, p.o, v, f);
+    F2 f[kPairs], x[kPairs];
+    if (p.post) {
+      unpack<T>(qv[i], f);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) r[i][j] = r[i][j] * ry * f[j];
-      }
-      load_gate<T>(p, t, v, f);
-      unpack<T>(xv[i], x);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        r[i][j] *= f[j];
-        if (p.x) r[i][j] = fmaf(p.a, x[j], r[i][j]);
-        ss[0] = fmaf(r[i][j], r[i][j], ss[0]);
-      }
-      if (r_out) r_out[row + v] = pack<T>(r[i]);
+      for (int j = 0; j < kPairs; ++j) r[i][j] = r[i][j] * ry2 * (f[j] + oq);
     }
+    if (p.gate == MOE_GATE_CHANNEL || p.gate == MOE_GATE_ELEMENT) {
+      unpack<T>(gv[i], f);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) r[i][j] = r[i][j] * f[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) r[i][j] = r[i][j] * gt;
+    }
+    unpack<T>(xv[i], x);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      if (p.x) r[i][j] = f2_fma(a, x[j], r[i][j]);
+      s = f2_fma(r[i][j], r[i][j], s);
+    }
+    if (r_out && v < p.n_vec) r_out[row + v] = pack<T>(r[i]);
   }
   if (!p.pre) return;
-  cta_sum<1>(ss, s_red[1], n_warps);
-  const float rr = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+  ss[0] = f2_sum(s);
+  sum(ss);
+  const F2 rr = f2(rsqrtf(fmaf(ss[0], p.inv_h, p.eps)));
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
-    if (v < p.n_vec) {
-      float f[kVec];
-      load_weight<T>(p.wp, p.o, v, f);
+    F2 f[kPairs];
+    unpack<T>(wv[i], f);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) f[j] *= r[i][j] * rr;
-      h_out[row + v] = pack<T>(f);
-    }
+    for (int j = 0; j < kPairs; ++j) f[j] = (f[j] + ow) * (r[i][j] * rr);
+    if (v < p.n_vec) h_out[row + v] = pack<T>(f);
   }
 }
 
-struct NormGrads {
-  const uint4 *dr, *dh;
-  uint4 *dy, *dx, *dg;      // dg: element gate only
-  void* dg_token;           // token gate
-  float* part;              // [gridDim.x][n_cols][H] per-channel partial sums
-  int col_g, col_q, col_p;  // which of the n_cols sums is d_gate, d_post_weight, d_pre_weight
-  int n_cols;
+// ---- group kernels -----------------------------------------------------------------------------
+// Shared memory: [3][n_vec] the per-channel gate, post and pre weights (zero where there is
+// none), then per group kBufs row buffers of n_vec vectors.
+struct GroupShape {
+  int threads;  // of a group
+  int groups;
+  size_t smem;
 };
 
-// One row at a time per CTA, grid-strided; the per-channel sums stay in the threads that own the
-// channels and go to `part` at the end, one row of partial sums per CTA.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512)
-    block_norm_bwd_kernel(const NormArgs p, const NormGrads q) {
-  __shared__ float s_red[3][2][32];
-  const int n_warps = blockDim.x >> 5;
-  float acc_g[VPT][kVec] = {}, acc_q[VPT][kVec] = {}, acc_p[VPT][kVec] = {};
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const size_t row = (size_t)t * p.n_vec;
-    float y[VPT][kVec], d[VPT][kVec], r[VPT][kVec];
-    uint4 dhv[VPT];
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    float s1[1] = {0.0f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      const bool in = v < p.n_vec;
-      unpack<T>(in ? p.y[row + v] : zero, y[i]);
-      unpack<T>(in && q.dr ? q.dr[row + v] : zero, d[i]);
-      unpack<T>(in && p.x ? p.x[row + v] : zero, r[i]);
-      dhv[i] = in && p.pre ? q.dh[row + v] : zero;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) s1[0] = fmaf(y[i][j], y[i][j], s1[0]);
-    }
-    float ry = 1.0f;
-    if (p.post) {
-      cta_sum<1>(s1, s_red[0], n_warps);
-      ry = rsqrtf(fmaf(s1[0], p.inv_h, p.eps));
-    }
-    if (p.pre) {
-      float s2[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v < p.n_vec) {
-          float f[kVec], g[kVec], dn[kVec], wp[kVec];
-          load_weight<T>(p.post ? p.wq : nullptr, p.o, v, f);
-          load_gate<T>(p, t, v, g);
-          unpack<T>(dhv[i], dn);
-          load_weight<T>(p.wp, p.o, v, wp);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            r[i][j] = fmaf(p.a, r[i][j], g[j] * (y[i][j] * ry * f[j]));
-            s2[0] = fmaf(r[i][j], r[i][j], s2[0]);
-            s2[1] = fmaf(r[i][j], dn[j] * wp[j], s2[1]);
-          }
-        }
-      }
-      cta_sum<2>(s2, s_red[1], n_warps);
-      const float rr = rsqrtf(fmaf(s2[0], p.inv_h, p.eps));
-      const float c = s2[1] * rr * rr * p.inv_h;  // mean(dh wp' rhat) rr
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v < p.n_vec) {
-          float dn[kVec], wp[kVec];
-          unpack<T>(dhv[i], dn);
-          load_weight<T>(p.wp, p.o, v, wp);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            d[i][j] = fmaf(rr, dn[j] * wp[j] - c * r[i][j], d[i][j]);
-            acc_p[i][j] = fmaf(dn[j], r[i][j] * rr, acc_p[i][j]);
-          }
-        }
-      }
-    }
-    // d = D; the residual's and the gate's gradients, and the branch's (r holds it from here).
-    float s3[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < p.n_vec) {
-        float f[kVec], g[kVec], w[kVec];
-        load_weight<T>(p.post ? p.wq : nullptr, p.o, v, w);
-        load_gate<T>(p, t, v, g);
-        if (q.dx) {
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) f[j] = p.a * d[i][j];
-          q.dx[row + v] = pack<T>(f);
-        }
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float yh = y[i][j] * ry;
-          f[j] = d[i][j] * (yh * w[j]);  // D u
-          s3[1] += f[j];
-          acc_g[i][j] += f[j];
-          const float du = d[i][j] * g[j];
-          acc_q[i][j] = fmaf(du, yh, acc_q[i][j]);
-          r[i][j] = du * w[j];
-          s3[0] = fmaf(r[i][j], yh, s3[0]);
-          y[i][j] = yh;
-        }
-        if (q.dg) q.dg[row + v] = pack<T>(f);
-      }
-    }
-    cta_sum<2>(s3, s_red[2], n_warps);
-    if (q.dg_token && threadIdx.x == 0)
-      reinterpret_cast<T*>(q.dg_token)[t] = DT<T>::from_f(s3[1]);
-    const float c = p.post ? s3[0] * p.inv_h : 0.0f;
-    if (q.dy) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v < p.n_vec) {
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) r[i][j] = ry * fmaf(-c, y[i][j], r[i][j]);
-          q.dy[row + v] = pack<T>(r[i]);
-        }
-      }
-    }
-    __syncthreads();  // s_red is written again by the next row
+// What a group thread knows of its place.
+template <int N>
+struct Place {
+  int g, tid;
+  GroupSum<N> sum;
+  __device__ __forceinline__ Place(int threads, float (*red)[N][32]) {
+    g = threadIdx.x / threads;
+    tid = threadIdx.x - g * threads;
+    sum.buf = red;
+    sum.base = g * (threads >> 5);
+    sum.warps = threads >> 5;
+    sum.warp = tid >> 5;
+    sum.lane = tid & 31;
+    sum.bar = 1 + g;
+    sum.threads = threads;
   }
-  auto put = [&](int col, const float (&acc)[VPT][kVec]) {
-    if (col < 0) return;
-    float4* dst =
-        reinterpret_cast<float4*>(q.part + ((size_t)blockIdx.x * q.n_cols + col) * p.H);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < p.n_vec) {
-        dst[2 * v] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        dst[2 * v + 1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-      }
-    }
-  };
-  put(q.col_g, acc_g);
-  put(q.col_q, acc_q);
-  put(q.col_p, acc_p);
+};
+
+// kWide: rows too long for the per-channel vectors to lie in shared memory beside them.
+template <bool kWide>
+__device__ __forceinline__ uint4 chan(const uint4* global, const uint4* shared, int v) {
+  if constexpr (kWide) return global ? __ldg(global + v) : make_uint4(0, 0, 0, 0);
+  return shared[v];
 }
 
-// out[col][h] = sum over the CTAs' partial rows, in a fixed order: thread (x, y) adds rows
-// y, y + 8, ... of one channel, and the eight sums are added in order.
-constexpr int kRedX = 32, kRedY = 8;
+template <bool kWide>
+__device__ __forceinline__ void load_channel(const NormArgs& p, uint4* s) {
+  if constexpr (kWide) return;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int v = threadIdx.x; v < p.n_vec; v += blockDim.x) {
+    s[v] = p.gate == MOE_GATE_CHANNEL ? p.g[v] : zero;
+    s[p.n_vec + v] = p.wq ? p.wq[v] : zero;
+    s[2 * p.n_vec + v] = p.wp ? p.wp[v] : zero;
+  }
+}
+
+constexpr int kMaxGroups = 28;   // groups of one warp need no barrier; others are at most 14
+constexpr int kGroupCta = 896;   // threads of a forward CTA: 72 registers each
+// Threads of a backward CTA, 168 registers each: the two per-channel sums and D of two rows of 7168
+// take three quarters of the register file, which leaves room to compute only in few threads
+// with many vectors each.
+constexpr int kBwdCta = 384;
+
+// The product of the gate per channel or element and the post weight, c q (token gate apart).
+template <typename T, int GATE>
+__device__ __forceinline__ void gate_weight(const uint4& gv, const uint4& qv, F2 oq,
+                                            F2 (&gw)[kPairs]) {
+  unpack<T>(qv, gw);
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) gw[j] = gw[j] + oq;
+  if constexpr (GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_ELEMENT) {
+    F2 g[kPairs];
+    unpack<T>(gv, g);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) gw[j] = gw[j] * g[j];
+  }
+}
+
+template <typename T, int VPT, int GATE, bool kWide>
+__global__ void __launch_bounds__(kWide ? 512 : kGroupCta, 1)
+    norm_group_kernel(const NormArgs p, const GroupShape shape, uint4* r_out, uint4* h_out) {
+  constexpr int kTensors = GATE == MOE_GATE_ELEMENT ? 3 : 2;  // y, x, gate
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ float s_red[2][1][32];
+  uint4* s_chan = reinterpret_cast<uint4*>(dyn);
+  Place<1> me(shape.threads, s_red);
+  // [2 rows][tensor][n_vec] of this group
+  uint4* buf = s_chan + (kWide ? 0 : 3 * p.n_vec) + (size_t)me.g * 2 * kTensors * p.n_vec;
+  load_channel<kWide>(p, s_chan);
+  __syncthreads();
+  const int step = gridDim.x * shape.groups;
+  auto fetch = [&](int t, int half) {
+    if (t < p.T) {
+      const size_t row = (size_t)t * p.n_vec;
+      uint4* b = buf + half * kTensors * p.n_vec;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = me.tid + i * shape.threads;
+        if (v >= p.n_vec) continue;
+        copy_async(b + v, p.y + row + v);
+        if (p.x) copy_async(b + p.n_vec + v, p.x + row + v);
+        if constexpr (GATE == MOE_GATE_ELEMENT)
+          copy_async(b + 2 * p.n_vec + v, p.g + row + v);
+      }
+    }
+    copy_commit();
+  };
+  const F2 oq = f2(p.wq ? p.o : 1.0f), ow = f2(p.wp ? p.o : 1.0f), a = f2(p.a);
+  const uint4* cg = GATE == MOE_GATE_CHANNEL ? p.g : nullptr;
+  const int t0 = blockIdx.x + me.g * gridDim.x;
+  fetch(t0, 0);
+  int half = 0;
+  for (int t = t0; t < p.T; t += step, half ^= 1) {
+    fetch(t + step, half ^ 1);
+    copy_wait<1>();
+    const size_t row = (size_t)t * p.n_vec;
+    const uint4* b = buf + half * kTensors * p.n_vec;
+    F2 r[VPT][kPairs];
+    float ss[1];
+    float scale = GATE == MOE_GATE_TOKEN ? token_gate<T>(p, t) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me.tid + i * shape.threads;
+      unpack<T>(v < p.n_vec ? b[v] : make_uint4(0, 0, 0, 0), r[i]);
+    }
+    if (p.post) {
+      F2 s = f2(0.0f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) s = f2_fma(r[i][j], r[i][j], s);
+      ss[0] = f2_sum(s);
+      me.sum(ss);
+      scale *= rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+    }
+    F2 s = f2(0.0f);
+    const F2 sc = f2(scale);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me.tid + i * shape.threads;
+      if (v >= p.n_vec) continue;
+      F2 gw[kPairs], x[kPairs];
+      gate_weight<T, GATE>(GATE == MOE_GATE_ELEMENT ? b[2 * p.n_vec + v] : chan<kWide>(cg, s_chan, v),
+                           chan<kWide>(p.wq, s_chan + p.n_vec, v), oq, gw);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) r[i][j] = r[i][j] * sc * gw[j];
+      if (p.x) {
+        unpack<T>(b[p.n_vec + v], x);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) r[i][j] = f2_fma(a, x[j], r[i][j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) s = f2_fma(r[i][j], r[i][j], s);
+      if (r_out) r_out[row + v] = pack<T>(r[i]);
+    }
+    if (p.pre) {
+      ss[0] = f2_sum(s);
+      me.sum(ss);
+      const F2 rr = f2(rsqrtf(fmaf(ss[0], p.inv_h, p.eps)));
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = me.tid + i * shape.threads;
+        if (v >= p.n_vec) continue;
+        F2 f[kPairs];
+        unpack<T>(chan<kWide>(p.wp, s_chan + 2 * p.n_vec, v), f);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) f[j] = (f[j] + ow) * (r[i][j] * rr);
+        h_out[row + v] = pack<T>(f);
+      }
+    }
+  }
+  copy_wait<0>();
+}
+
+// D = dr + rr (dh w - rhat mean(dh w rhat));  dx = a D;  dg = D u;
+// dy = ry (g D q - yhat mean(g D q yhat)).  r is computed again from y and x.
+template <typename T, int VPT, int GATE, bool kWide>
+__global__ void __launch_bounds__(kBwdCta, 1)
+    norm_group_bwd_kernel(const NormArgs p, const NormGrads q, const GroupShape shape) {
+  constexpr int kTensors = GATE == MOE_GATE_ELEMENT ? 5 : 4;  // y, x, dr, dh, gate
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ float s_red[2][2][32];
+  uint4* s_chan = reinterpret_cast<uint4*>(dyn);
+  Place<2> me(shape.threads, s_red);
+  uint4* rows = s_chan + (kWide ? 0 : 3 * p.n_vec);
+  uint4* buf = rows + (size_t)me.g * (kTensors + 1) * p.n_vec;
+  // y has two buffers: the last step of a row reads it while the next row is on its way
+  uint4* y_cur = buf;
+  uint4* y_next = buf + kTensors * p.n_vec;
+  load_channel<kWide>(p, s_chan);
+  // what is not there stays zero
+  for (int v = threadIdx.x; v < shape.groups * (kTensors + 1) * p.n_vec; v += blockDim.x)
+    rows[v] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const int step = gridDim.x * shape.groups;
+  auto fetch = [&](int t) {
+    if (t < p.T) {
+      const size_t row = (size_t)t * p.n_vec;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = me.tid + i * shape.threads;
+        if (v >= p.n_vec) continue;
+        copy_async(y_next + v, p.y + row + v);
+        if (p.x) copy_async(buf + p.n_vec + v, p.x + row + v);
+        if (q.dr) copy_async(buf + 2 * p.n_vec + v, q.dr + row + v);
+        if (p.pre) copy_async(buf + 3 * p.n_vec + v, q.dh + row + v);
+        if constexpr (GATE == MOE_GATE_ELEMENT)
+          copy_async(buf + 4 * p.n_vec + v, p.g + row + v);
+      }
+    }
+    copy_commit();
+  };
+  const F2 oq = f2(p.wq ? p.o : 1.0f), ow = f2(p.wp ? p.o : 1.0f), a = f2(p.a);
+  const uint4* cg = GATE == MOE_GATE_CHANNEL ? p.g : nullptr;
+  F2 sum_a[VPT][kPairs], sum_p[VPT][kPairs];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) sum_a[i][j] = sum_p[i][j] = f2(0.0f);
+  const int t0 = blockIdx.x + me.g * gridDim.x;
+  fetch(t0);
+  for (int t = t0; t < p.T; t += step) {
+    copy_wait<0>();
+    uint4* const y_row = y_next;
+    y_next = y_cur;
+    y_cur = y_row;
+    const size_t row = (size_t)t * p.n_vec;
+    const float gt = GATE == MOE_GATE_TOKEN ? token_gate<T>(p, t) : 1.0f;
+    F2 d[VPT][kPairs];  // r, then D
+    float ss[2] = {0.0f, 0.0f};
+    float ry = 1.0f;
+    if (p.post) {
+      F2 s = f2(0.0f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = me.tid + i * shape.threads;
+        if (v >= p.n_vec) continue;
+        F2 y[kPairs];
+        unpack<T>(y_row[v], y);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) s = f2_fma(y[j], y[j], s);
+      }
+      ss[0] = f2_sum(s);
+      me.sum(ss, 1);
+      ry = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+    }
+    const F2 sc = f2(ry * gt);
+    float rr = 0.0f, c = 0.0f;  // D = dr + rr dh w - c r
+    if (p.pre) {
+      F2 s0 = f2(0.0f), s1 = f2(0.0f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = me.tid + i * shape.threads;
+        if (v >= p.n_vec) continue;
+        F2 y[kPairs], x[kPairs], dn[kPairs], w[kPairs];
+        unpack<T>(y_row[v], y);
+        gate_weight<T, GATE>(GATE == MOE_GATE_ELEMENT ? buf[4 * p.n_vec + v] : chan<kWide>(cg, s_chan, v),
+                             chan<kWide>(p.wq, s_chan + p.n_vec, v), oq, w);
+        unpack<T>(buf[p.n_vec + v], x);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) d[i][j] = f2_fma(a, x[j], y[j] * sc * w[j]);
+        unpack<T>(buf[3 * p.n_vec + v], dn);
+        unpack<T>(chan<kWide>(p.wp, s_chan + 2 * p.n_vec, v), w);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          s0 = f2_fma(d[i][j], d[i][j], s0);
+          s1 = f2_fma(d[i][j], dn[j] * (w[j] + ow), s1);
+        }
+      }
+      ss[0] = f2_sum(s0);
+      ss[1] = f2_sum(s1);
+      me.sum(ss);
+      rr = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+      c = -ss[1] * rr * rr * rr * p.inv_h;
+    }
+    const F2 rr2 = f2(rr), c2 = f2(c), ry2 = f2(ry), gt2 = f2(gt);
+    F2 s = f2(0.0f);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me.tid + i * shape.threads;
+      if (v >= p.n_vec) continue;
+      F2 f[kPairs], y[kPairs];
+      unpack<T>(buf[2 * p.n_vec + v], f);
+      if (p.pre) {
+        F2 dn[kPairs], w[kPairs];
+        unpack<T>(buf[3 * p.n_vec + v], dn);
+        unpack<T>(chan<kWide>(p.wp, s_chan + 2 * p.n_vec, v), w);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          sum_p[i][j] = f2_fma(dn[j], d[i][j] * rr2, sum_p[i][j]);
+          d[i][j] = f2_fma(rr2, dn[j] * (w[j] + ow), f2_fma(c2, d[i][j], f[j]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) d[i][j] = f[j];
+      }
+      if (q.dx) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) f[j] = a * d[i][j];
+        q.dx[row + v] = pack<T>(f);
+      }
+      unpack<T>(y_row[v], y);
+      if constexpr (GATE == MOE_GATE_ELEMENT) {
+        F2 g[kPairs], w[kPairs];
+        unpack<T>(buf[4 * p.n_vec + v], g);
+        unpack<T>(chan<kWide>(p.wq, s_chan + p.n_vec, v), w);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const F2 e = d[i][j] * (y[j] * ry2);
+          f[j] = e * (w[j] + oq);  // D u
+          const F2 ge = g[j] * e;
+          sum_a[i][j] = sum_a[i][j] + ge;
+          s = f2_fma(ge, w[j] + oq, s);
+          d[i][j] = d[i][j] * (g[j] * (w[j] + oq));
+        }
+        if (q.dg) q.dg[row + v] = pack<T>(f);
+      } else {
+        gate_weight<T, GATE>(chan<kWide>(cg, s_chan, v),
+                             chan<kWide>(p.wq, s_chan + p.n_vec, v), oq, f);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const F2 e = d[i][j] * (y[j] * ry2);
+          if constexpr (GATE == MOE_GATE_TOKEN)
+            sum_a[i][j] = f2_fma(gt2, e, sum_a[i][j]);
+          else
+            sum_a[i][j] = sum_a[i][j] + e;
+          s = f2_fma(e, f[j], s);
+          d[i][j] = d[i][j] * f[j];
+        }
+      }
+    }
+    fetch(t + step);  // this row's buffers have been read
+    if (p.post || GATE == MOE_GATE_TOKEN) {
+      ss[0] = f2_sum(s);
+      me.sum(ss, 1);
+      if (GATE == MOE_GATE_TOKEN && q.dg_token && me.tid == 0)
+        reinterpret_cast<T*>(q.dg_token)[t] = DT<T>::from_f(ss[0]);
+    }
+    if (q.dy) {  // d = D c q here
+      const F2 k1 = f2(ry * gt);
+      const F2 k2 = f2(p.post ? -ss[0] * gt * p.inv_h * ry * ry : 0.0f);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = me.tid + i * shape.threads;
+        if (v >= p.n_vec) continue;
+        F2 y[kPairs];
+        unpack<T>(y_row[v], y);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) y[j] = f2_fma(k2, y[j], k1 * d[i][j]);
+        q.dy[row + v] = pack<T>(y);
+      }
+    }
+  }
+  copy_wait<0>();
+  if (q.n_cols == 0) return;
+  // The groups' sums meet in the row buffers (as large as two f32 rows per group) and are added in
+  // the order of the groups.
+  __syncthreads();
+  float4* s_sum = reinterpret_cast<float4*>(rows);  // [groups][2][2 n_vec]
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = me.tid + i * shape.threads;
+    if (v >= p.n_vec) continue;
+    float4* at = s_sum + (size_t)me.g * 4 * p.n_vec + 2 * v;
+    const float2 a0 = f2_get(sum_a[i][0]), a1 = f2_get(sum_a[i][1]), a2 = f2_get(sum_a[i][2]),
+                 a3 = f2_get(sum_a[i][3]);
+    at[0] = make_float4(a0.x, a0.y, a1.x, a1.y);
+    at[1] = make_float4(a2.x, a2.y, a3.x, a3.y);
+    at += 2 * p.n_vec;
+    const float2 p0 = f2_get(sum_p[i][0]), p1 = f2_get(sum_p[i][1]), p2 = f2_get(sum_p[i][2]),
+                 p3 = f2_get(sum_p[i][3]);
+    at[0] = make_float4(p0.x, p0.y, p1.x, p1.y);
+    at[1] = make_float4(p2.x, p2.y, p3.x, p3.y);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int col = k == 0 ? q.col_a : q.col_p;
+    if (col < 0) continue;
+    float4* dst = reinterpret_cast<float4*>(q.part + ((size_t)blockIdx.x * q.n_cols + col) * p.H);
+    for (int v = threadIdx.x; v < 2 * p.n_vec; v += blockDim.x) {
+      float4 s = s_sum[(size_t)k * 2 * p.n_vec + v];
+      for (int g = 1; g < shape.groups; ++g) {
+        const float4 o = s_sum[(size_t)(2 * g + k) * 2 * p.n_vec + v];
+        s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+      }
+      dst[v] = s;
+    }
+  }
+}
+
+// Sums over the CTAs' partial rows, in a fixed order: thread (x, y) adds rows y, y + 16, ... of
+// one channel, and the sixteen sums are added in order.
+constexpr int kRedX = 32, kRedY = 16;
 struct RedOut {
-  void* out[3];
+  void *g, *q, *p;      // d_gate per channel, d_post_weight, d_pre_weight (or null)
+  const void *gate, *wq;  // per-channel gate (or null) and post weight (or null)
+  float o;
+  int col_a, col_p;
 };
 template <typename T>
 __global__ void __launch_bounds__(kRedX * kRedY)
-    block_norm_reduce_kernel(const float* __restrict__ part, int rows, int n_cols, int H,
-                             const RedOut o) {
+    norm_reduce_kernel(const float* __restrict__ part, int rows, int n_cols, int H,
+                       const RedOut o) {
   __shared__ float s[kRedY][kRedX];
+  pdl_wait();
   const int h = blockIdx.x * kRedX + threadIdx.x;
   const int col = blockIdx.y;
   float a = 0.0f;
   if (h < H)
-#pragma unroll 4
+#pragma unroll 8
     for (int c = threadIdx.y; c < rows; c += kRedY)
       a += part[((size_t)c * n_cols + col) * H + h];
   s[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
-  if (threadIdx.y == 0 && h < H) {
+  if (threadIdx.y != 0 || h >= H) return;
 #pragma unroll
-    for (int y = 1; y < kRedY; ++y) a += s[y][threadIdx.x];
-    reinterpret_cast<T*>(o.out[col])[h] = DT<T>::from_f(a);
+  for (int y = 1; y < kRedY; ++y) a += s[y][threadIdx.x];
+  if (col == o.col_p) {
+    static_cast<T*>(o.p)[h] = DT<T>::from_f(a);
+    return;
+  }
+  if (o.g) {
+    const float w = o.wq ? o.o + DT<T>::to_f(static_cast<const T*>(o.wq)[h]) : 1.0f;
+    static_cast<T*>(o.g)[h] = DT<T>::from_f(a * w);
+  }
+  if (o.q) {
+    const float g = o.gate ? DT<T>::to_f(static_cast<const T*>(o.gate)[h]) : 1.0f;
+    static_cast<T*>(o.q)[h] = DT<T>::from_f(a * g);
   }
 }
 
+// ---- host side ---------------------------------------------------------------------------------
 NormArgs norm_args(const moe_block_norm_t& b, const void* branch, const void* residual,
                    const void* gate, const void* wq, const void* wp) {
   NormArgs p;
@@ -333,19 +623,87 @@ int threads_for(int n_vec, int vpt) {
   return (n + 31) / 32 * 32;
 }
 
+constexpr int kSmemMax = 220 * 1024;  // leaves room for the static arrays
+
+// As many groups as the threads, the barriers and the shared memory allow; `chans` per-channel
+// vectors lie beside the groups' `bufs` row buffers.
+GroupShape group_shape(const NormArgs& p, int vpt, int most, int chans, int bufs) {
+  GroupShape s;
+  s.threads = threads_for(p.n_vec, vpt);
+  s.groups = most / s.threads;
+  if (s.threads > 32 && s.groups > 14) s.groups = 14;
+  if (s.groups > kMaxGroups) s.groups = kMaxGroups;
+  const int row = p.n_vec * 16;
+  const int fit = (kSmemMax - chans * row) / (bufs * row);
+  if (s.groups > fit) s.groups = fit;
+  s.smem = (size_t)(chans + s.groups * bufs) * row;
+  return s;
+}
+
+template <auto Kernel, typename... Args>
+cudaError_t launch_group(const GroupShape& s, int ctas, cudaStream_t stream, Args... args) {
+  static cudaError_t result[64];
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (s.groups < 1) return cudaErrorInvalidConfiguration;
+  std::call_once(once[dev], [dev] {
+    result[dev] =
+        cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  });
+  if (result[dev] != cudaSuccess) return result[dev];
+  return launch_k(Kernel, dim3(ctas), dim3(s.threads * s.groups), s.smem, stream, false, args...);
+}
+
+// Forward: two vectors per thread up to rows of 7168, so that a CTA holds two groups or more;
+// four beyond.
+bool fwd_wide(const NormArgs& p) { return threads_for(p.n_vec, 2) > kGroupCta / 2; }
+GroupShape fwd_shape(const NormArgs& p) {
+  const int bufs = p.gate == MOE_GATE_ELEMENT ? 6 : 4;
+  return fwd_wide(p) ? group_shape(p, 4, 512, 0, bufs) : group_shape(p, 2, kGroupCta, 3, bufs);
+}
+template <typename T, int GATE>
+cudaError_t fwd_groups(const NormArgs& p, uint4* r, uint4* h, cudaStream_t s) {
+  const GroupShape g = fwd_shape(p);
+  const int ctas = p.T < num_sms() ? p.T : num_sms();
+  return fwd_wide(p)
+             ? launch_group<norm_group_kernel<T, 4, GATE, true>>(g, ctas, s, p, g, r, h)
+             : launch_group<norm_group_kernel<T, 2, GATE, false>>(g, ctas, s, p, g, r, h);
+}
+
 template <typename T>
 cudaError_t fwd_typed(const NormArgs& p, void* r, void* h, cudaStream_t s) {
   uint4* ro = static_cast<uint4*>(r);
   uint4* ho = static_cast<uint4*>(h);
-  const dim3 grid(p.T);
-  if (p.n_vec <= 256)
-    return launch_k(block_norm_fwd_kernel<T, 1>, grid, dim3(threads_for(p.n_vec, 1)), 0, s,
-                    false, p, ro, ho);
-  if (p.n_vec <= 1024)
-    return launch_k(block_norm_fwd_kernel<T, 2>, grid, dim3(threads_for(p.n_vec, 2)), 0, s,
-                    false, p, ro, ho);
-  return launch_k(block_norm_fwd_kernel<T, 4>, grid, dim3(threads_for(p.n_vec, 4)), 0, s, false,
-                  p, ro, ho);
+  // A row per CTA while every group of the other kernel would get two rows or fewer.
+  if ((int64_t)p.T <= 2ll * num_sms() * fwd_shape(p).groups) {
+    const dim3 grid(p.T);
+    if (p.n_vec <= 1024)
+      return launch_k(norm_row_kernel<T, 1>, grid, dim3(threads_for(p.n_vec, 1)), 0, s, false, p,
+                      ro, ho);
+    return launch_k(norm_row_kernel<T, 4>, grid, dim3(threads_for(p.n_vec, 4)), 0, s, false, p,
+                    ro, ho);
+  }
+  switch (p.gate) {
+    case MOE_GATE_CHANNEL: return fwd_groups<T, MOE_GATE_CHANNEL>(p, ro, ho, s);
+    case MOE_GATE_TOKEN: return fwd_groups<T, MOE_GATE_TOKEN>(p, ro, ho, s);
+    case MOE_GATE_ELEMENT: return fwd_groups<T, MOE_GATE_ELEMENT>(p, ro, ho, s);
+    default: return fwd_groups<T, MOE_GATE_NONE>(p, ro, ho, s);
+  }
+}
+
+// Backward: five vectors per thread (two groups up to rows of 7680) while the per-channel vectors
+// fit beside the rows; six beyond.
+template <typename T, int GATE>
+cudaError_t bwd_groups(const NormArgs& p, const NormGrads& q, int ctas, cudaStream_t s) {
+  const int bufs = GATE == MOE_GATE_ELEMENT ? 6 : 5;
+  const GroupShape g = group_shape(p, 5, kBwdCta, 3, bufs);
+  if (g.groups >= 1)
+    return launch_group<norm_group_bwd_kernel<T, 5, GATE, false>>(g, ctas, s, p, q, g);
+  const GroupShape w = group_shape(p, 6, kBwdCta, 0, bufs);
+  return launch_group<norm_group_bwd_kernel<T, 6, GATE, true>>(w, ctas, s, p, q, w);
 }
 
 template <typename T>
@@ -353,16 +711,16 @@ cudaError_t bwd_typed(const NormArgs& p, const NormGrads& q, int ctas, const Red
                       cudaStream_t s) {
   if (p.T > 0) {
     cudaError_t e;
-    if (p.n_vec <= 1024)
-      e = launch_k(block_norm_bwd_kernel<T, 1>, dim3(ctas), dim3(threads_for(p.n_vec, 1)), 0, s,
-                   false, p, q);
-    else
-      e = launch_k(block_norm_bwd_kernel<T, 4>, dim3(ctas), dim3(threads_for(p.n_vec, 4)), 0, s,
-                   false, p, q);
+    switch (p.gate) {
+      case MOE_GATE_CHANNEL: e = bwd_groups<T, MOE_GATE_CHANNEL>(p, q, ctas, s); break;
+      case MOE_GATE_TOKEN: e = bwd_groups<T, MOE_GATE_TOKEN>(p, q, ctas, s); break;
+      case MOE_GATE_ELEMENT: e = bwd_groups<T, MOE_GATE_ELEMENT>(p, q, ctas, s); break;
+      default: e = bwd_groups<T, MOE_GATE_NONE>(p, q, ctas, s);
+    }
     if (e != cudaSuccess) return e;
   }
   if (q.n_cols == 0) return cudaSuccess;
-  return launch_k(block_norm_reduce_kernel<T>, dim3((p.H + kRedX - 1) / kRedX, q.n_cols),
+  return launch_k(norm_reduce_kernel<T>, dim3((p.H + kRedX - 1) / kRedX, q.n_cols),
                   dim3(kRedX, kRedY), 0, s, false, (const float*)q.part, ctas, q.n_cols, p.H,
                   red);
 }
@@ -395,14 +753,16 @@ cudaError_t launch_block_norm_bwd(const moe_block_norm_t& b, const void* dr, con
   q.dg_token = b.gate == MOE_GATE_TOKEN ? dg : nullptr;
   q.part = part;
   RedOut red = {};
-  auto col = [&](void* out) {
-    if (!out) return -1;
-    red.out[q.n_cols] = out;
-    return q.n_cols++;
-  };
-  q.col_g = col(b.gate == MOE_GATE_CHANNEL ? dg : nullptr);
-  q.col_q = col(dwq);
-  q.col_p = col(dwp);
+  red.g = b.gate == MOE_GATE_CHANNEL ? dg : nullptr;
+  red.q = dwq;
+  red.p = dwp;
+  red.gate = b.gate == MOE_GATE_CHANNEL ? gate : nullptr;
+  red.wq = wq;
+  red.o = b.weight_offset;
+  q.col_a = red.g || red.q ? q.n_cols++ : -1;
+  q.col_p = red.p ? q.n_cols++ : -1;
+  red.col_a = q.col_a;
+  red.col_p = q.col_p;
   const int ctas = block_norm_bwd_ctas(b.T);
   return b.dtype == MOE_BF16 ? bwd_typed<__nv_bfloat16>(p, q, ctas, red, s)
                              : bwd_typed<__half>(p, q, ctas, red, s);
