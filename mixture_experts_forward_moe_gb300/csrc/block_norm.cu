@@ -42,8 +42,8 @@ struct NormGrads {
 // varies by row and 1 otherwise.  d_pre_weight = P; with a gate per channel d_gate = q A and
 // d_post_weight = g A, else d_post_weight = A.
 
-// Sums of N values over a group of `warps` warps, the same bits in every thread: shuffles within
-// a warp, then each warp adds the warps' sums in the same butterfly.  Consecutive calls of a
+// Sums of N (one or two) values over a group of `warps` warps, the same bits in every thread:
+// shuffles within a warp, then each warp adds the warps' sums in the same way.  Consecutive calls of a
 // group use the two halves of `buf` in turn: a half is written again only behind the barrier of
 // the call between.
 template <int N>
@@ -52,26 +52,34 @@ struct GroupSum {
   int warps, warp, lane, bar, threads;
   int base = 0;  // the group's first warp in the CTA
   int turn = 0;
+  // Over the warp.  Of two values each half warp takes one after the first exchange, so that they
+  // cost one shuffle more than one; lane 0 then holds the first, lane 16 the second.
+  __device__ __forceinline__ float over_warp(const float (&v)[N], int n) const {
+    float x = v[0];
+    if (N == 2 && n == 2) {
+      const bool low = lane < 16;
+      x = (low ? v[0] : v[N - 1]) + __shfl_xor_sync(kAll, low ? v[N - 1] : v[0], 16);
+    } else {
+      x += __shfl_xor_sync(kAll, x, 16);
+    }
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
+    return x;
+  }
   __device__ __forceinline__ void operator()(float (&v)[N], int n = N) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < n) v[i] += __shfl_xor_sync(kAll, v[i], off);
-    if (warps == 1) return;
-    if (lane == 0)
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < n) buf[turn][i][base + warp] = v[i];
+    const float x = over_warp(v, n);
+    if (warps == 1) {
+      v[0] = __shfl_sync(kAll, x, 0);
+      if (N == 2 && n == 2) v[N - 1] = __shfl_sync(kAll, x, 16);
+      return;
+    }
+    if ((lane & 15) == 0 && (lane >> 4) < n) buf[turn][N == 2 ? lane >> 4 : 0][base + warp] = x;
     named_bar_sync(bar, threads);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < n) v[i] = lane < warps ? buf[turn][i][base + lane] : 0.0f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < n) v[i] += __shfl_xor_sync(kAll, v[i], off);
+    for (int i = 0; i < N; ++i) v[i] = i < n && lane < warps ? buf[turn][i][base + lane] : 0.0f;
+    const float y = over_warp(v, n);
+    v[0] = __shfl_sync(kAll, y, 0);
+    if (N == 2 && n == 2) v[N - 1] = __shfl_sync(kAll, y, 16);
     turn ^= 1;
   }
 };
@@ -176,8 +184,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512)
 }
 
 // ---- group kernels -----------------------------------------------------------------------------
-// Shared memory: [3][n_vec] the per-channel gate, post and pre weights (zero where there is
-// none), then per group kBufs row buffers of n_vec vectors.
+// Shared memory: the per-channel vectors (kChanRows rows of 16-bit values in size), then each
+// group's row buffers of n_vec vectors.
+constexpr int kChanRows = 4;
 struct GroupShape {
   int threads;  // of a group
   int groups;
@@ -202,57 +211,90 @@ struct Place {
   }
 };
 
-// kWide: rows too long for the per-channel vectors to lie in shared memory beside them.
-template <bool kWide>
-__device__ __forceinline__ uint4 chan(const uint4* global, const uint4* shared, int v) {
-  if constexpr (kWide) return global ? __ldg(global + v) : make_uint4(0, 0, 0, 0);
-  return shared[v];
-}
-
-template <bool kWide>
-__device__ __forceinline__ void load_channel(const NormArgs& p, uint4* s) {
-  if constexpr (kWide) return;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int v = threadIdx.x; v < p.n_vec; v += blockDim.x) {
-    s[v] = p.gate == MOE_GATE_CHANNEL ? p.g[v] : zero;
-    s[p.n_vec + v] = p.wq ? p.wq[v] : zero;
-    s[2 * p.n_vec + v] = p.wp ? p.wp[v] : zero;
+// What multiplies a row channel by channel: c q (the gate per channel, if it is one, times the
+// post weight's factor) and w (the pre weight's), f32.  They are made once per CTA in shared
+// memory, [2][H]; kWide: the rows leave no room for that, so they are made where they are needed.
+template <typename T, bool kWide>
+struct Channels {
+  const uint4 *g, *wq, *wp;
+  F2 oq, ow;
+  const F2* shared;
+  int n_vec;
+  __device__ __forceinline__ Channels(const NormArgs& p, void* s)
+      : g(p.gate == MOE_GATE_CHANNEL ? p.g : nullptr), wq(p.wq), wp(p.wp),
+        oq(f2(p.wq ? p.o : 1.0f)), ow(f2(p.wp ? p.o : 1.0f)), shared(static_cast<F2*>(s)),
+        n_vec(p.n_vec) {
+    if constexpr (kWide) return;
+    F2* to = static_cast<F2*>(s);
+    for (int v = threadIdx.x; v < n_vec; v += blockDim.x) {
+      F2 a[kPairs], b[kPairs];
+      make_post(v, a);
+      make_pre(v, b);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        to[at(0, v, j)] = a[j];
+        to[at(1, v, j)] = b[j];
+      }
+    }
   }
-}
+  __device__ __forceinline__ void make_post(int v, F2 (&f)[kPairs]) const {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) f[j] = oq;
+    if (wq) {
+      unpack<T>(__ldg(wq + v), f);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) f[j] = f[j] + oq;
+    }
+    if (g) {
+      F2 x[kPairs];
+      unpack<T>(__ldg(g + v), x);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) f[j] = f[j] * x[j];
+    }
+  }
+  __device__ __forceinline__ void make_pre(int v, F2 (&f)[kPairs]) const {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) f[j] = ow;
+    if (wp) {
+      unpack<T>(__ldg(wp + v), f);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) f[j] = f[j] + ow;
+    }
+  }
+  // The eight values of vector v lie as two halves of 16 bytes, each next to its neighbours': lanes
+  // that read consecutive vectors then meet every bank once.
+  __device__ __forceinline__ int at(int which, int v, int j) const {
+    return ((which * 2 + j / 2) * n_vec + v) * 2 + j % 2;
+  }
+  __device__ __forceinline__ void read(int which, int v, F2 (&f)[kPairs]) const {
+#pragma unroll
+    for (int j = 0; j < kPairs; j += 2) {
+      const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(shared + at(which, v, j));
+      f[j].v = x.x;
+      f[j + 1].v = x.y;
+    }
+  }
+  __device__ __forceinline__ void post(int v, F2 (&f)[kPairs]) const {
+    if constexpr (kWide) make_post(v, f); else read(0, v, f);
+  }
+  __device__ __forceinline__ void pre(int v, F2 (&f)[kPairs]) const {
+    if constexpr (kWide) make_pre(v, f); else read(1, v, f);
+  }
+};
 
 constexpr int kMaxGroups = 28;   // groups of one warp need no barrier; others are at most 14
-constexpr int kGroupCta = 896;   // threads of a forward CTA: 72 registers each
-// Threads of a backward CTA, 168 registers each: the two per-channel sums and D of two rows of 7168
-// take three quarters of the register file, which leaves room to compute only in few threads
-// with many vectors each.
-constexpr int kBwdCta = 384;
-
-// The product of the gate per channel or element and the post weight, c q (token gate apart).
-template <typename T, int GATE>
-__device__ __forceinline__ void gate_weight(const uint4& gv, const uint4& qv, F2 oq,
-                                            F2 (&gw)[kPairs]) {
-  unpack<T>(qv, gw);
-#pragma unroll
-  for (int j = 0; j < kPairs; ++j) gw[j] = gw[j] + oq;
-  if constexpr (GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_ELEMENT) {
-    F2 g[kPairs];
-    unpack<T>(gv, g);
-#pragma unroll
-    for (int j = 0; j < kPairs; ++j) gw[j] = gw[j] * g[j];
-  }
-}
-
+constexpr int kGroupCta = 896;   // threads of a CTA: 72 registers each
 template <typename T, int VPT, int GATE, bool kWide>
 __global__ void __launch_bounds__(kWide ? 512 : kGroupCta, 1)
     norm_group_kernel(const NormArgs p, const GroupShape shape, uint4* r_out, uint4* h_out) {
   constexpr int kTensors = GATE == MOE_GATE_ELEMENT ? 3 : 2;  // y, x, gate
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ float s_red[2][1][32];
-  uint4* s_chan = reinterpret_cast<uint4*>(dyn);
   Place<1> me(shape.threads, s_red);
   // [2 rows][tensor][n_vec] of this group
-  uint4* buf = s_chan + (kWide ? 0 : 3 * p.n_vec) + (size_t)me.g * 2 * kTensors * p.n_vec;
-  load_channel<kWide>(p, s_chan);
+  uint4* buf = reinterpret_cast<uint4*>(dyn) + (kWide ? 0 : kChanRows * p.n_vec) +
+               (size_t)me.g * 2 * kTensors * p.n_vec;
+  const Channels<T, kWide> chan(p, dyn);
   __syncthreads();
   const int step = gridDim.x * shape.groups;
   auto fetch = [&](int t, int half) {
@@ -271,8 +313,7 @@ __global__ void __launch_bounds__(kWide ? 512 : kGroupCta, 1)
     }
     copy_commit();
   };
-  const F2 oq = f2(p.wq ? p.o : 1.0f), ow = f2(p.wp ? p.o : 1.0f), a = f2(p.a);
-  const uint4* cg = GATE == MOE_GATE_CHANNEL ? p.g : nullptr;
+  const F2 a = f2(p.a);
   const int t0 = blockIdx.x + me.g * gridDim.x;
   fetch(t0, 0);
   int half = 0;
@@ -306,8 +347,12 @@ __global__ void __launch_bounds__(kWide ? 512 : kGroupCta, 1)
       const int v = me.tid + i * shape.threads;
       if (v >= p.n_vec) continue;
       F2 gw[kPairs], x[kPairs];
-      gate_weight<T, GATE>(GATE == MOE_GATE_ELEMENT ? b[2 * p.n_vec + v] : chan<kWide>(cg, s_chan, v),
-                           chan<kWide>(p.wq, s_chan + p.n_vec, v), oq, gw);
+      chan.post(v, gw);
+      if constexpr (GATE == MOE_GATE_ELEMENT) {
+        unpack<T>(b[2 * p.n_vec + v], x);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) gw[j] = gw[j] * x[j];
+      }
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) r[i][j] = r[i][j] * sc * gw[j];
       if (p.x) {
@@ -328,9 +373,9 @@ __global__ void __launch_bounds__(kWide ? 512 : kGroupCta, 1)
         const int v = me.tid + i * shape.threads;
         if (v >= p.n_vec) continue;
         F2 f[kPairs];
-        unpack<T>(chan<kWide>(p.wp, s_chan + 2 * p.n_vec, v), f);
+        chan.pre(v, f);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) f[j] = (f[j] + ow) * (r[i][j] * rr);
+        for (int j = 0; j < kPairs; ++j) f[j] = f[j] * (r[i][j] * rr);
         h_out[row + v] = pack<T>(f);
       }
     }
@@ -341,96 +386,103 @@ __global__ void __launch_bounds__(kWide ? 512 : kGroupCta, 1)
 // D = dr + rr (dh w - rhat mean(dh w rhat));  dx = a D;  dg = D u;
 // dy = ry (g D q - yhat mean(g D q yhat)).  r is computed again from y and x.
 template <typename T, int VPT, int GATE, bool kWide>
-__global__ void __launch_bounds__(kBwdCta, 1)
+__global__ void __launch_bounds__(kWide ? 512 : 448, 1)
     norm_group_bwd_kernel(const NormArgs p, const NormGrads q, const GroupShape shape) {
   constexpr int kTensors = GATE == MOE_GATE_ELEMENT ? 5 : 4;  // y, x, dr, dh, gate
+  constexpr int kRows = kWide ? 1 : 2;  // rows in shared memory: the next one too, if it fits
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ float s_red[2][2][32];
-  uint4* s_chan = reinterpret_cast<uint4*>(dyn);
+  pdl_trigger();  // the sums over the CTAs wait for this grid before they read
   Place<2> me(shape.threads, s_red);
-  uint4* rows = s_chan + (kWide ? 0 : 3 * p.n_vec);
-  uint4* buf = rows + (size_t)me.g * (kTensors + 1) * p.n_vec;
-  // y has two buffers: the last step of a row reads it while the next row is on its way
-  uint4* y_cur = buf;
-  uint4* y_next = buf + kTensors * p.n_vec;
-  load_channel<kWide>(p, s_chan);
+  const int n_vec = p.n_vec;
+  uint4* rows = reinterpret_cast<uint4*>(dyn) + (kWide ? 0 : kChanRows * n_vec);
+  uint4* buf = rows + (size_t)me.g * kRows * kTensors * n_vec;  // [row][tensor][n_vec]
+  const Channels<T, kWide> chan(p, dyn);
   // what is not there stays zero
-  for (int v = threadIdx.x; v < shape.groups * (kTensors + 1) * p.n_vec; v += blockDim.x)
+  for (int v = threadIdx.x; v < shape.groups * kRows * kTensors * n_vec; v += blockDim.x)
     rows[v] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   const int step = gridDim.x * shape.groups;
-  auto fetch = [&](int t) {
+  auto fetch = [&](int t, int half) {
     if (t < p.T) {
-      const size_t row = (size_t)t * p.n_vec;
+      const size_t row = (size_t)t * n_vec;
+      uint4* b = buf + half * kTensors * n_vec;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = me.tid + i * shape.threads;
-        if (v >= p.n_vec) continue;
-        copy_async(y_next + v, p.y + row + v);
-        if (p.x) copy_async(buf + p.n_vec + v, p.x + row + v);
-        if (q.dr) copy_async(buf + 2 * p.n_vec + v, q.dr + row + v);
-        if (p.pre) copy_async(buf + 3 * p.n_vec + v, q.dh + row + v);
-        if constexpr (GATE == MOE_GATE_ELEMENT)
-          copy_async(buf + 4 * p.n_vec + v, p.g + row + v);
+        if (v >= n_vec) continue;
+        copy_async(b + v, p.y + row + v);
+        if (p.x) copy_async(b + n_vec + v, p.x + row + v);
+        if (q.dr) copy_async(b + 2 * n_vec + v, q.dr + row + v);
+        if (p.pre) copy_async(b + 3 * n_vec + v, q.dh + row + v);
+        if constexpr (GATE == MOE_GATE_ELEMENT) copy_async(b + 4 * n_vec + v, p.g + row + v);
       }
     }
     copy_commit();
   };
-  const F2 oq = f2(p.wq ? p.o : 1.0f), ow = f2(p.wp ? p.o : 1.0f), a = f2(p.a);
-  const uint4* cg = GATE == MOE_GATE_CHANNEL ? p.g : nullptr;
+  const F2 a = f2(p.a);
   F2 sum_a[VPT][kPairs], sum_p[VPT][kPairs];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) sum_a[i][j] = sum_p[i][j] = f2(0.0f);
-  const int t0 = blockIdx.x + me.g * gridDim.x;
-  fetch(t0);
-  for (int t = t0; t < p.T; t += step) {
-    copy_wait<0>();
-    uint4* const y_row = y_next;
-    y_next = y_cur;
-    y_cur = y_row;
-    const size_t row = (size_t)t * p.n_vec;
-    const float gt = GATE == MOE_GATE_TOKEN ? token_gate<T>(p, t) : 1.0f;
-    F2 d[VPT][kPairs];  // r, then D
-    float ss[2] = {0.0f, 0.0f};
-    float ry = 1.0f;
-    if (p.post) {
-      F2 s = f2(0.0f);
+  // This thread's part of a row's sum of y^2.
+  auto square = [&](const uint4* b) {
+    F2 s = f2(0.0f);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = me.tid + i * shape.threads;
-        if (v >= p.n_vec) continue;
-        F2 y[kPairs];
-        unpack<T>(y_row[v], y);
+    for (int i = 0; i < VPT; ++i) {
+      const int v = me.tid + i * shape.threads;
+      if (v >= n_vec) continue;
+      F2 y[kPairs];
+      unpack<T>(b[v], y);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) s = f2_fma(y[j], y[j], s);
-      }
-      ss[0] = f2_sum(s);
-      me.sum(ss, 1);
-      ry = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+      for (int j = 0; j < kPairs; ++j) s = f2_fma(y[j], y[j], s);
     }
-    const F2 sc = f2(ry * gt);
+    return f2_sum(s);
+  };
+  const int t0 = blockIdx.x + me.g * gridDim.x;
+  float ss[2] = {0.0f, 0.0f};
+  float ry = 1.0f;  // of the current row; the next one's is reduced with this row's last sum
+  fetch(t0, 0);
+  int half = 0;
+  if (p.post && t0 < p.T) {
+    copy_wait<0>();
+    ss[0] = square(buf);
+    me.sum(ss, 1);
+    ry = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
+  }
+  for (int t = t0; t < p.T; t += step) {
+    if constexpr (!kWide) fetch(t + step, half ^ 1);
+    copy_wait<kRows - 1>();
+    const size_t row = (size_t)t * n_vec;
+    const uint4* b = buf + half * kTensors * n_vec;
+    const float gt = GATE == MOE_GATE_TOKEN ? token_gate<T>(p, t) : 1.0f;
+    F2 d[VPT][kPairs];  // r, then D, then D c q
     float rr = 0.0f, c = 0.0f;  // D = dr + rr dh w - c r
     if (p.pre) {
       F2 s0 = f2(0.0f), s1 = f2(0.0f);
+      const F2 sc = f2(ry * gt);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = me.tid + i * shape.threads;
-        if (v >= p.n_vec) continue;
-        F2 y[kPairs], x[kPairs], dn[kPairs], w[kPairs];
-        unpack<T>(y_row[v], y);
-        gate_weight<T, GATE>(GATE == MOE_GATE_ELEMENT ? buf[4 * p.n_vec + v] : chan<kWide>(cg, s_chan, v),
-                             chan<kWide>(p.wq, s_chan + p.n_vec, v), oq, w);
-        unpack<T>(buf[p.n_vec + v], x);
+        if (v >= n_vec) continue;
+        F2 y[kPairs], x[kPairs], w[kPairs];
+        unpack<T>(b[v], y);
+        chan.post(v, w);
+        if constexpr (GATE == MOE_GATE_ELEMENT) {
+          unpack<T>(b[4 * n_vec + v], x);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) w[j] = w[j] * x[j];
+        }
+        unpack<T>(b[n_vec + v], x);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) d[i][j] = f2_fma(a, x[j], y[j] * sc * w[j]);
-        unpack<T>(buf[3 * p.n_vec + v], dn);
-        unpack<T>(chan<kWide>(p.wp, s_chan + 2 * p.n_vec, v), w);
+        unpack<T>(b[3 * n_vec + v], x);
+        chan.pre(v, w);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           s0 = f2_fma(d[i][j], d[i][j], s0);
-          s1 = f2_fma(d[i][j], dn[j] * (w[j] + ow), s1);
+          s1 = f2_fma(d[i][j], x[j] * w[j], s1);
         }
       }
       ss[0] = f2_sum(s0);
@@ -444,17 +496,16 @@ __global__ void __launch_bounds__(kBwdCta, 1)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = me.tid + i * shape.threads;
-      if (v >= p.n_vec) continue;
-      F2 f[kPairs], y[kPairs];
-      unpack<T>(buf[2 * p.n_vec + v], f);
+      if (v >= n_vec) continue;
+      F2 f[kPairs], y[kPairs], w[kPairs];
+      unpack<T>(b[2 * n_vec + v], f);
       if (p.pre) {
-        F2 dn[kPairs], w[kPairs];
-        unpack<T>(buf[3 * p.n_vec + v], dn);
-        unpack<T>(chan<kWide>(p.wp, s_chan + 2 * p.n_vec, v), w);
+        unpack<T>(b[3 * n_vec + v], y);
+        chan.pre(v, w);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          sum_p[i][j] = f2_fma(dn[j], d[i][j] * rr2, sum_p[i][j]);
-          d[i][j] = f2_fma(rr2, dn[j] * (w[j] + ow), f2_fma(c2, d[i][j], f[j]));
+          sum_p[i][j] = f2_fma(y[j], d[i][j] * rr2, sum_p[i][j]);
+          d[i][j] = f2_fma(rr2, y[j] * w[j], f2_fma(c2, d[i][j], f[j]));
         }
       } else {
 #pragma unroll
@@ -465,24 +516,21 @@ __global__ void __launch_bounds__(kBwdCta, 1)
         for (int j = 0; j < kPairs; ++j) f[j] = a * d[i][j];
         q.dx[row + v] = pack<T>(f);
       }
-      unpack<T>(y_row[v], y);
+      unpack<T>(b[v], y);
+      chan.post(v, w);
       if constexpr (GATE == MOE_GATE_ELEMENT) {
-        F2 g[kPairs], w[kPairs];
-        unpack<T>(buf[4 * p.n_vec + v], g);
-        unpack<T>(chan<kWide>(p.wq, s_chan + p.n_vec, v), w);
+        F2 g[kPairs];
+        unpack<T>(b[4 * n_vec + v], g);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           const F2 e = d[i][j] * (y[j] * ry2);
-          f[j] = e * (w[j] + oq);  // D u
-          const F2 ge = g[j] * e;
-          sum_a[i][j] = sum_a[i][j] + ge;
-          s = f2_fma(ge, w[j] + oq, s);
-          d[i][j] = d[i][j] * (g[j] * (w[j] + oq));
+          f[j] = e * w[j];  // D u
+          sum_a[i][j] = f2_fma(g[j], e, sum_a[i][j]);
+          s = f2_fma(g[j], f[j], s);
+          d[i][j] = d[i][j] * (g[j] * w[j]);
         }
         if (q.dg) q.dg[row + v] = pack<T>(f);
       } else {
-        gate_weight<T, GATE>(chan<kWide>(cg, s_chan, v),
-                             chan<kWide>(p.wq, s_chan + p.n_vec, v), oq, f);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           const F2 e = d[i][j] * (y[j] * ry2);
@@ -490,30 +538,47 @@ __global__ void __launch_bounds__(kBwdCta, 1)
             sum_a[i][j] = f2_fma(gt2, e, sum_a[i][j]);
           else
             sum_a[i][j] = sum_a[i][j] + e;
-          s = f2_fma(e, f[j], s);
-          d[i][j] = d[i][j] * f[j];
+          s = f2_fma(e, w[j], s);
+          d[i][j] = d[i][j] * w[j];
         }
       }
     }
-    fetch(t + step);  // this row's buffers have been read
+    ss[0] = ss[1] = 0.0f;
+    const bool more = !kWide && p.post && t + step < p.T;
     if (p.post || GATE == MOE_GATE_TOKEN) {
       ss[0] = f2_sum(s);
-      me.sum(ss, 1);
+      if (more) {
+        copy_wait<0>();
+        ss[1] = square(buf + (half ^ 1) * kTensors * n_vec);
+      }
+      me.sum(ss);
       if (GATE == MOE_GATE_TOKEN && q.dg_token && me.tid == 0)
         reinterpret_cast<T*>(q.dg_token)[t] = DT<T>::from_f(ss[0]);
     }
-    if (q.dy) {  // d = D c q here
+    if (q.dy) {
       const F2 k1 = f2(ry * gt);
       const F2 k2 = f2(p.post ? -ss[0] * gt * p.inv_h * ry * ry : 0.0f);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = me.tid + i * shape.threads;
-        if (v >= p.n_vec) continue;
+        if (v >= n_vec) continue;
         F2 y[kPairs];
-        unpack<T>(y_row[v], y);
+        unpack<T>(b[v], y);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) y[j] = f2_fma(k2, y[j], k1 * d[i][j]);
         q.dy[row + v] = pack<T>(y);
+      }
+    }
+    if constexpr (!kWide) {
+      half ^= 1;
+      if (more) ry = rsqrtf(fmaf(ss[1], p.inv_h, p.eps));
+    } else {
+      fetch(t + step, 0);
+      if (p.post && t + step < p.T) {
+        copy_wait<0>();
+        ss[0] = square(buf);
+        me.sum(ss, 1);
+        ry = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
       }
     }
   }
@@ -623,10 +688,10 @@ int threads_for(int n_vec, int vpt) {
   return (n + 31) / 32 * 32;
 }
 
-constexpr int kSmemMax = 220 * 1024;  // leaves room for the static arrays
+constexpr int kSmemMax = 226 * 1024;  // leaves room for the static arrays
 
-// As many groups as the threads, the barriers and the shared memory allow; `chans` per-channel
-// vectors lie beside the groups' `bufs` row buffers.
+// As many groups as the threads, the barriers and the shared memory allow; `chans` rows'
+// worth of per-channel vectors lies beside the groups' `bufs` row buffers.
 GroupShape group_shape(const NormArgs& p, int vpt, int most, int chans, int bufs) {
   GroupShape s;
   s.threads = threads_for(p.n_vec, vpt);
@@ -662,7 +727,7 @@ cudaError_t launch_group(const GroupShape& s, int ctas, cudaStream_t stream, Arg
 bool fwd_wide(const NormArgs& p) { return threads_for(p.n_vec, 2) > kGroupCta / 2; }
 GroupShape fwd_shape(const NormArgs& p) {
   const int bufs = p.gate == MOE_GATE_ELEMENT ? 6 : 4;
-  return fwd_wide(p) ? group_shape(p, 4, 512, 0, bufs) : group_shape(p, 2, kGroupCta, 3, bufs);
+  return fwd_wide(p) ? group_shape(p, 4, 512, 0, bufs) : group_shape(p, 2, kGroupCta, kChanRows, bufs);
 }
 template <typename T, int GATE>
 cudaError_t fwd_groups(const NormArgs& p, uint4* r, uint4* h, cudaStream_t s) {
@@ -694,16 +759,15 @@ cudaError_t fwd_typed(const NormArgs& p, void* r, void* h, cudaStream_t s) {
   }
 }
 
-// Backward: five vectors per thread (two groups up to rows of 7680) while the per-channel vectors
-// fit beside the rows; six beyond.
+// Backward: one vector per thread up to rows of 7168, four beyond.
 template <typename T, int GATE>
 cudaError_t bwd_groups(const NormArgs& p, const NormGrads& q, int ctas, cudaStream_t s) {
-  const int bufs = GATE == MOE_GATE_ELEMENT ? 6 : 5;
-  const GroupShape g = group_shape(p, 5, kBwdCta, 3, bufs);
+  const int bufs = GATE == MOE_GATE_ELEMENT ? 5 : 4;
+  const GroupShape g = group_shape(p, 2, 448, kChanRows, 2 * bufs);
   if (g.groups >= 1)
-    return launch_group<norm_group_bwd_kernel<T, 5, GATE, false>>(g, ctas, s, p, q, g);
-  const GroupShape w = group_shape(p, 6, kBwdCta, 0, bufs);
-  return launch_group<norm_group_bwd_kernel<T, 6, GATE, true>>(w, ctas, s, p, q, w);
+    return launch_group<norm_group_bwd_kernel<T, 2, GATE, false>>(g, ctas, s, p, q, g);
+  const GroupShape w = group_shape(p, 4, 512, 0, bufs);
+  return launch_group<norm_group_bwd_kernel<T, 4, GATE, true>>(w, ctas, s, p, q, w);
 }
 
 template <typename T>
@@ -721,7 +785,7 @@ cudaError_t bwd_typed(const NormArgs& p, const NormGrads& q, int ctas, const Red
   }
   if (q.n_cols == 0) return cudaSuccess;
   return launch_k(norm_reduce_kernel<T>, dim3((p.H + kRedX - 1) / kRedX, q.n_cols),
-                  dim3(kRedX, kRedY), 0, s, false, (const float*)q.part, ctas, q.n_cols, p.H,
+                  dim3(kRedX, kRedY), 0, s, p.T > 0, (const float*)q.part, ctas, q.n_cols, p.H,
                   red);
 }
 

@@ -71,9 +71,11 @@ struct Row {
 #define EACH(i, j)                  \
   _Pragma("unroll") for (int i = 0; i < N; ++i) _Pragma("unroll") for (int j = 0; j < VEC; ++j)
 
-// Sigmoid s and 1 - s, both to f32 precision at either end.
+// Sigmoid s and 1 - s, each good relative to itself at either end.  The exponentials here are
+// __expf: its relative error grows with the argument, 2^-24 of it, but so does e^-|argument|
+// fall, and what a row sums to is off by a few 2^-24.
 __device__ __forceinline__ void sigmoid2(float x, float& s, float& om) {
-  const float t = expf(-fabsf(x));
+  const float t = __expf(-fabsf(x));
   const float d = __fdividef(1.0f, 1.0f + t);
   s = x >= 0.0f ? d : t * d;
   om = x >= 0.0f ? t * d : d;
@@ -107,7 +109,7 @@ __device__ __forceinline__ float row_scores(Row<VEC, N>& x, Row<VEC, N>& om, int
   m = warp_max(m);
   if (m == -INFINITY) m = 0.0f;
   EACH(i, j) {
-    x.v[i][j] = expf(x.v[i][j] - m);
+    x.v[i][j] = __expf(x.v[i][j] - m);
     om.v[i][j] = 1.0f;
     sum += x.v[i][j];
   }
@@ -211,9 +213,9 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 // ---- balance loss, second pass ---------------------------------------------------------------
-// One CTA per (32 experts, sequence): 32 lanes of chunks per expert, joined in a fixed order.
+// One CTA per (32 experts, sequence): 16 rows of lanes share the chunks of an expert, joined in a fixed order.
 // The CTA that finishes last adds the CTAs' parts of the loss, again in a fixed order.
-constexpr int kFinE = 32, kFinC = 32;
+constexpr int kFinE = 32, kFinC = 16;
 
 __global__ void __launch_bounds__(kFinE * kFinC)
     balance_final_kernel(int T, int E, int K, int n_seq, int chunk, float coeff,
@@ -272,8 +274,9 @@ __global__ void __launch_bounds__(kFinE * kFinC)
     }
     __syncthreads();
     if (threadIdx.y == 0) {
-      const int T_all = __reduce_add_sync(kAll, s_live[threadIdx.x]);
-      const int n_all = __reduce_add_sync(kAll, s_seqs[threadIdx.x]);
+      const bool mine = threadIdx.x < kFinC;
+      const int T_all = __reduce_add_sync(kAll, mine ? s_live[threadIdx.x] : 0);
+      const int n_all = __reduce_add_sync(kAll, mine ? s_seqs[threadIdx.x] : 0);
 #pragma unroll
       for (int y = 1; y < kFinC; ++y) {
         p += s_p[y][threadIdx.x];
