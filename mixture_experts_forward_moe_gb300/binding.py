@@ -2,12 +2,13 @@
 
 Argument marshalling only: every step of the path runs in the library's CUDA kernels.  torch is
 used for device memory (outputs, workspaces) and for the current CUDA stream.  There is no
-fallback: if the library cannot be loaded the call raises.
+fallback: if the library cannot be loaded the call raises.  The calls around the routed experts
+are marshalled by a compiled module over the same library.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -25,9 +26,8 @@ _DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 _SCORING = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}
 # moe_activation_t: the two gated forms keep 2F rows per expert in w_gate_up, ReLU2 keeps F.
 _ACTIVATIONS = {"silu": 0, "gelu_tanh": 1, "relu2": 2}
-# moe_linear_act_t and moe_gate_t.
+# moe_linear_act_t.
 _LINEAR_ACTS = {"none": 0, "silu": 1, "gelu_tanh": 2, "relu2": 3}
-GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = 0, 1, 2, 3
 
 
 def gate_up_rows(activation: str, F: int) -> int:
@@ -825,50 +825,41 @@ def moe_grouped_gemm_fp8(a, a_scale, b, b_scale, layout_metadata, out=None, work
 
 
 # ------------------------------------------------------------------ around the routed experts
-# These calls are short beside their host time, so the checks below compare first and build a
-# message (through _need) only when something does not fit.
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+# These calls take a few microseconds on the device, so their marshalling is compiled
+# (csrc/calls.cpp): the checks of tensors, the outputs and the scratch.  Everything is on the
+# device of the first tensor and on its current stream, or on `stream`, which is then current
+# while the outputs are allocated.
+_calls = None
 
 
-def _fits(t, name, dtype, shape):
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous()):
-        _need(t, name, dtype, shape)
+def _load_calls():
+    global _calls
+    L = lib()  # builds both; the module links against the library
+    with _lock:
+        if _calls is None and L is not None:
+            name = "gb300moe_calls"
+            spec = importlib.util.spec_from_file_location(name, _build.CALLS)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.set_error(MoeError)
+            _calls = mod
+    return _calls
 
 
-def _handle(stream, device):
-    """The cudaStream_t of a call on `device`."""
-    return (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-            else stream.cuda_stream)
-
-
-def _on(stream):
-    """Makes `stream` current while a call allocates, so that torch's allocator reuses the memory
-    in that stream's order."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _scratch(nbytes, device, handle):
-    """Workspace of a call on the stream `handle` (current): one per stream and host thread, since
-    calls on other streams may run at the same time.  A captured call gets its own, which lives in
-    the graph's memory."""
-    if torch.cuda.is_current_stream_capturing():
-        return new_workspace(nbytes, device)
-    key = (device, threading.get_ident(), handle)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _ws_cache[key] = new_workspace(nbytes, device)
-    return ws
+def _call(name, stream, args):
+    c = _calls or _load_calls()
+    if stream is None:
+        return getattr(c, name)(*args)
+    with torch.cuda.stream(stream):
+        return getattr(c, name)(*args)
 
 
 def call_workspace(device=None, stream=None) -> torch.Tensor:
-    """The workspace that the calls below use on `stream` when none is given (its status word:
-    get_device_status)."""
-    if device is None or device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    with _on(stream):
-        return _scratch(256, device, _handle(stream, device))
+    """The scratch that the calls below use on `stream` when no workspace is given (its status
+    word: get_device_status)."""
+    index = None if device is None else torch.device(device).index
+    return _call("scratch", stream,
+                 (256, torch.cuda.current_device() if index is None else index))
 
 
 def moe_linear(x, w, bias=None, activation="none", residual=None, out_dtype=None, out=None,
@@ -876,75 +867,13 @@ def moe_linear(x, w, bias=None, activation="none", residual=None, out_dtype=None
     """act(x w^T + bias) + residual (include/moe.h: moe_linear).  x [T, K] and w [N, K] in bf16 or
     f16, bias [N] in their type; residual and the result [T, N] in `out_dtype`: x's (default) or
     float32.  ``activation``: "none", "silu", "gelu_tanh" or "relu2".  `out` may be the residual."""
-    if x.dim() != 2 or w.dim() != 2:
-        raise ValueError("x and w must have two dimensions")
-    T, K = x.shape
-    N = w.shape[0]
-    dt = x.dtype
-    code = _DTYPES.get(dt)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dt}")
     act = _LINEAR_ACTS.get(activation)
     if act is None:
         raise ValueError(f"unsupported activation {activation}")
-    odt = dt if out_dtype is None else out_dtype
-    if odt is not dt and odt is not torch.float32:
-        raise ValueError(f"out_dtype must be {dt} or torch.float32, got {odt}")
-    _fits(x, "x", dt, (T, K))
-    _fits(w, "w", dt, (N, K))
-    if bias is not None:
-        _fits(bias, "bias", dt, (N,))
-    if residual is not None:
-        _fits(residual, "residual", odt, (T, N))
-    if out is not None:
-        _fits(out, "out", odt, (T, N))
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return moe_linear(x, w, bias, activation, residual, out_dtype, out, workspace)
-    dev = x.device
-    s = _handle(None, dev)
-    if out is None:
-        out = torch.empty((T, N), dtype=odt, device=dev)
-    if workspace is None:
-        workspace = _scratch(256, dev, s)
-    g = Linear(T, N, K, code, act, odt is torch.float32)
-    rc = lib().moe_linear(ctypes.byref(g), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
-                          out.data_ptr(), workspace.data_ptr(), workspace.numel(), s)
-    if rc:
-        _check(rc, "moe_linear")
-    return out
-
-
-def _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
-                residual_scale, weight_offset, eps) -> BlockNorm:
-    if branch.dim() != 2:
-        raise ValueError("branch must have two dimensions")
-    T, H = branch.shape
-    dt = branch.dtype
-    code = _DTYPES.get(dt)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dt}")
-    _fits(branch, "branch", dt, (T, H))
-    if residual is not None:
-        _fits(residual, "residual", dt, (T, H))
-    kind = GATE_NONE
-    if gate is not None:
-        shape = gate.shape
-        # a gate of T = H values is per channel; [T, 1] is always per token
-        if shape == (H,):
-            kind = GATE_CHANNEL
-        elif shape == (T,) or shape == (T, 1):
-            kind = GATE_TOKEN
-        else:
-            kind = GATE_ELEMENT
-            shape = (T, H)
-        _fits(gate, "gate", dt, shape)
-    if post_weight is not None:
-        _fits(post_weight, "post_weight", dt, (H,))
-    if pre_weight is not None:
-        _fits(pre_weight, "pre_weight", dt, (H,))
-    return BlockNorm(T, H, code, kind, bool(post_norm), bool(pre_norm), residual_scale,
-                     weight_offset, eps)
+    f32 = out_dtype is torch.float32
+    if not f32 and out_dtype is not None and out_dtype is not x.dtype:
+        raise ValueError(f"out_dtype must be {x.dtype} or torch.float32, got {out_dtype}")
+    return _call("linear", stream, (x, w, bias, act, residual, f32, out, workspace))
 
 
 def moe_block_norm(branch, residual=None, gate=None, post_weight=None, pre_weight=None,
@@ -955,23 +884,9 @@ def moe_block_norm(branch, residual=None, gate=None, post_weight=None, pre_weigh
     residual_scale * residual, and the norm of that for the next block (pre_norm).  Returns
     (stream, normed), None for what is not computed (want_stream, pre_norm).  `stream_out` may be
     the residual or the branch."""
-    p = _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
-                    residual_scale, weight_offset, eps)
-    if stream_out is not None:
-        _fits(stream_out, "stream_out", branch.dtype, branch.shape)
-    normed = None
-    with _on(stream):
-        if stream_out is None and want_stream:
-            stream_out = torch.empty_like(branch)
-        if pre_norm:
-            normed = torch.empty_like(branch)
-        rc = lib().moe_block_norm_fwd(ctypes.byref(p), branch.data_ptr(), _ptr(residual),
-                                      _ptr(gate), _ptr(post_weight), _ptr(pre_weight),
-                                      _ptr(stream_out), _ptr(normed),
-                                      _handle(stream, branch.device))
-    if rc:
-        _check(rc, "moe_block_norm_fwd")
-    return stream_out, normed
+    return _call("block_norm", stream,
+                 (branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
+                  residual_scale, weight_offset, eps, stream_out, want_stream))
 
 
 def moe_block_norm_bwd(d_stream, d_normed, branch, residual=None, gate=None, post_weight=None,
@@ -980,90 +895,21 @@ def moe_block_norm_bwd(d_stream, d_normed, branch, residual=None, gate=None, pos
     """The gradients of moe_block_norm (include/moe.h: moe_block_norm_bwd) for the same inputs and
     options; d_stream may be None, d_normed is None without pre_norm.  Returns a dict of d_branch
     and, where there is such an input, d_residual, d_gate, d_post_weight and d_pre_weight."""
-    p = _block_norm(branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
-                    residual_scale, weight_offset, eps)
-    if d_stream is not None:
-        _fits(d_stream, "d_stream", branch.dtype, branch.shape)
-    if (d_normed is not None) != bool(pre_norm):
-        raise ValueError("d_normed goes with pre_norm")
-    if d_normed is not None:
-        _fits(d_normed, "d_normed", branch.dtype, branch.shape)
-    L = lib()
-    empty = torch.empty_like
-    with _on(stream):
-        s = _handle(stream, branch.device)
-        if workspace is None:
-            workspace = _scratch(L.moe_block_norm_bwd_workspace_size(ctypes.byref(p)),
-                                 branch.device, s)
-        out = {"d_branch": empty(branch)}
-        if residual is not None:
-            out["d_residual"] = empty(residual)
-        if gate is not None:
-            out["d_gate"] = empty(gate)
-        if post_weight is not None:
-            out["d_post_weight"] = empty(post_weight)
-        if pre_weight is not None:
-            out["d_pre_weight"] = empty(pre_weight)
-        get = out.get
-        rc = L.moe_block_norm_bwd(
-            ctypes.byref(p), _ptr(d_stream), _ptr(d_normed), branch.data_ptr(), _ptr(residual),
-            _ptr(gate), _ptr(post_weight), _ptr(pre_weight), out["d_branch"].data_ptr(),
-            _ptr(get("d_residual")), _ptr(get("d_gate")), _ptr(get("d_post_weight")),
-            _ptr(get("d_pre_weight")), workspace.data_ptr(), workspace.numel(), s)
-    if rc:
-        _check(rc, "moe_block_norm_bwd")
-    return out
-
-
-def _router_args(gating_output, topk_ids, seq_offsets, scoring_func, renormalize, factor):
-    if gating_output.dim() != 2 or topk_ids.dim() != 2:
-        raise ValueError("gating_output and topk_ids must have two dimensions")
-    scoring = _SCORING.get(scoring_func)
-    if scoring is None:
-        raise ValueError(f"unsupported scoring_func {scoring_func}")
-    T, E = gating_output.shape
-    k = topk_ids.shape[1]
-    _fits(gating_output, "gating_output", torch.float32, (T, E))
-    _fits(topk_ids, "topk_ids", torch.int32, (T, k))
-    n_seq = 1
-    if seq_offsets is not None:
-        n_seq = seq_offsets.numel() - 1
-        if seq_offsets.dim() != 1 or n_seq < 1:
-            raise ValueError("seq_offsets must hold n_seq + 1 offsets")
-        _fits(seq_offsets, "seq_offsets", torch.int32, (n_seq + 1,))
-    p = MoeProblem(T, 8, E, 8, k, MOE_BF16, scoring, bool(renormalize), 0, 0, factor)
-    return p, T, E, k, n_seq
+    return _call("block_norm_bwd", stream,
+                 (branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
+                  residual_scale, weight_offset, eps, d_stream, d_normed, workspace))
 
 
 def moe_balance_loss(gating_output, topk_ids, coeff, scoring_func="softmax", seq_offsets=None,
                      workspace=None, stream=None):
     """Per-expert counts and the balance loss of ragged sequences (include/moe.h:
     moe_balance_loss_fwd).  Returns a dict of loss [1] and, per sequence, counts [n_seq, E] int32,
-    live_tokens [n_seq] int32, prob_sum and coef [n_seq, E]; coef is what moe_router_bwd takes.
-    The results are views of one allocation."""
-    p, _, E, _, n = _router_args(gating_output, topk_ids, seq_offsets, scoring_func, True, 1.0)
-    dev = gating_output.device
-    L = lib()
-    with _on(stream):
-        s = _handle(stream, dev)
-        if workspace is None:
-            workspace = _scratch(L.moe_balance_loss_workspace_size(ctypes.byref(p), n), dev, s)
-        # [prob_sum | coef | loss, then counts | live_tokens], each on a 16-byte boundary
-        table = (n * E + 3) // 4 * 4
-        f32 = torch.empty(3 * table + 4 + n, dtype=torch.float32, device=dev)
-        at = f32.data_ptr()
-        rc = L.moe_balance_loss_fwd(
-            ctypes.byref(p), n, coeff, gating_output.data_ptr(), topk_ids.data_ptr(),
-            _ptr(seq_offsets), at + 8 * table, at + 8 * table + 16, at + 12 * table + 16, at,
-            at + 4 * table, workspace.data_ptr(), workspace.numel(), s)
-    if rc:
-        _check(rc, "moe_balance_loss_fwd")
-    i32 = f32.view(torch.int32)
-    return {"loss": f32[2 * table:2 * table + 1],
-            "counts": i32.as_strided((n, E), (E, 1), 2 * table + 4),
-            "live_tokens": i32.as_strided((n,), (1,), 3 * table + 4),
-            "prob_sum": f32.as_strided((n, E), (E, 1), 0),
-            "coef": f32.as_strided((n, E), (E, 1), table)}
+    live_tokens [n_seq] int32, prob_sum and coef [n_seq, E]; coef is what moe_router_bwd takes."""
+    scoring = _SCORING.get(scoring_func)
+    if scoring is None:
+        raise ValueError(f"unsupported scoring_func {scoring_func}")
+    return _call("balance_loss", stream,
+                 (gating_output, topk_ids, seq_offsets, scoring, True, 1.0, coeff, workspace))
 
 
 def moe_router_bwd(gating_output, topk_ids, d_topk_weights=None, coef=None, d_loss=None,
@@ -1072,25 +918,9 @@ def moe_router_bwd(gating_output, topk_ids, d_topk_weights=None, coef=None, d_lo
     """The gradient of the router logits (include/moe.h: moe_router_bwd) from d_topk_weights
     [T, top_k] (of moe_route's weights) and from the balance loss: `coef` of moe_balance_loss
     times d_loss (a device scalar, 1 when None).  Returns d_gating_output [T, E] f32."""
-    p, T, E, k, n = _router_args(gating_output, topk_ids, seq_offsets, scoring_func, renormalize,
-                                 routed_scaling_factor)
-    if d_topk_weights is not None:
-        _fits(d_topk_weights, "d_topk_weights", torch.float32, (T, k))
-    if coef is not None:
-        _fits(coef, "coef", torch.float32, (n, E))
-    if d_loss is not None:
-        if d_loss.numel() != 1:
-            raise ValueError("d_loss must hold one value")
-        _need(d_loss, "d_loss", torch.float32)
-    if out is not None:
-        _fits(out, "out", torch.float32, (T, E))
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(gating_output)
-        rc = lib().moe_router_bwd(ctypes.byref(p), n, gating_output.data_ptr(),
-                                  topk_ids.data_ptr(), _ptr(d_topk_weights), _ptr(coef),
-                                  _ptr(seq_offsets), _ptr(d_loss), out.data_ptr(),
-                                  _handle(stream, gating_output.device))
-    if rc:
-        _check(rc, "moe_router_bwd")
-    return out
+    scoring = _SCORING.get(scoring_func)
+    if scoring is None:
+        raise ValueError(f"unsupported scoring_func {scoring_func}")
+    return _call("router_bwd", stream,
+                 (gating_output, topk_ids, seq_offsets, scoring, renormalize,
+                  routed_scaling_factor, d_topk_weights, coef, d_loss, out))
