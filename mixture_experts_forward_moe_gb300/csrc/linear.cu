@@ -1,9 +1,10 @@
 // linear.cu -- dense product with bias, activation and residual in its epilogue (include/moe.h:
 // moe_linear): out = act(x w^T + b) + residual, 16-bit operands, f32 accumulation.
 //
-// Up to kGemvRows rows of x the product is a stream of the weights and runs on the CUDA cores
-// (gemv_kernel).  Beyond that it runs on tcgen05 (mma_kernel): the weights are the MMA's M side
-// (128 rows), the rows of x its N side (BN), so that few rows of x cost few columns.
+// One row of x (a few, when the product is small) is a stream of the weights and runs on the CUDA
+// cores (gemv_kernel).  Everything else runs on tcgen05: the weights are the MMA's M side, the rows
+// of x its N side (BN), so that few rows of x cost few columns.  Up to 64 rows a CTA has a tile of
+// 128 weight rows (mma_kernel), beyond that a pair of SMs has one of 256 (pair_kernel).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -870,7 +871,11 @@ cudaError_t launch_gemv(const LinArgs& p, const void* x, const void* w, cudaStre
 template <typename T>
 cudaError_t launch_typed(const LinArgs& p, int dtype, const void* x, const void* w,
                          cudaStream_t s) {
-  if (p.T <= kGemvRows) return launch_gemv<T>(p, x, w, s);
+  // Two to four rows cost the CUDA cores two to four times the arithmetic of one, which hides behind
+  // the weights' bytes no more: 7168 x 7168 took 18.5, 22.6, 27.8 and 38.7 us against 19.6 on the
+  // tensor cores, 256 x 7168 took 2.6 to 3.5 against 5.9, and 2048 x 2048 crosses at four rows.
+  if (p.T == 1 || (p.T <= kGemvRows && (int64_t)p.T * p.N * p.K <= 1 << 24))
+    return launch_gemv<T>(p, x, w, s);
   if (p.T <= 16) return launch_mma<T, 16>(p, dtype, x, w, s);
   if (p.T <= 32) return launch_mma<T, 32>(p, dtype, x, w, s);
   if (p.T <= 64) return launch_mma<T, 64>(p, dtype, x, w, s);

@@ -6,7 +6,7 @@
 #include <limits.h>
 #include <math.h>
 
-#include "common.cuh"
+#include "vec16.cuh"
 #include "ptx.cuh"
 
 namespace gb300moe {
@@ -24,16 +24,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
-  return v;
-}
-
-// Sum / maximum over the `width` lanes (a power of two) that start at a multiple of it.
-__device__ __forceinline__ float group_sum(float v, int width) {
-  for (int off = width >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
-  return v;
-}
-__device__ __forceinline__ float group_max(float v, int width) {
-  for (int off = width >> 1; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
   return v;
 }
 
@@ -71,14 +61,80 @@ struct Row {
 #define EACH(i, j)                  \
   _Pragma("unroll") for (int i = 0; i < N; ++i) _Pragma("unroll") for (int j = 0; j < VEC; ++j)
 
-// Sigmoid s and 1 - s, each good relative to itself at either end.  The exponentials here are
-// __expf: its relative error grows with the argument, 2^-24 of it, but so does e^-|argument|
-// fall, and what a row sums to is off by a few 2^-24.
+// e^x and 1/x by the special-function unit alone, tiny results flushed to 0.  The error of e^x
+// relative to itself grows with |x|, 2^-24 of it, while e^x (x <= 0 here) falls faster, so a row's
+// sum is off by a few 2^-24.
+__device__ __forceinline__ float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Sigmoid s and 1 - s, each good relative to itself at either end.
 __device__ __forceinline__ void sigmoid2(float x, float& s, float& om) {
-  const float t = __expf(-fabsf(x));
-  const float d = __fdividef(1.0f, 1.0f + t);
-  s = x >= 0.0f ? d : t * d;
-  om = x >= 0.0f ? t * d : d;
+  const float t = exp_fast(-fabsf(x));
+  const float d = rcp_fast(1.0f + t), td = t * d;
+  s = x >= 0.0f ? d : td;
+  om = x >= 0.0f ? td : d;
+}
+// Sums and the gradient over a row, two values per instruction where there are pairs.
+template <int VEC, int N>
+__device__ __forceinline__ float row_sum(const Row<VEC, N>& x) {
+  if constexpr (VEC == 4) {
+    F2 s = f2(0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      s = s + (f2(x.v[i][0], x.v[i][1]) + f2(x.v[i][2], x.v[i][3]));
+    return f2_sum(s);
+  } else {
+    float s = 0.0f;
+    EACH(i, j) s += x.v[i][j];
+    return s;
+  }
+}
+template <int VEC, int N>
+__device__ __forceinline__ float row_dot(const Row<VEC, N>& x, const Row<VEC, N>& y) {
+  if constexpr (VEC == 4) {
+    F2 s = f2(0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2)
+        s = f2_fma(f2(x.v[i][j], x.v[i][j + 1]), f2(y.v[i][j], y.v[i][j + 1]), s);
+    return f2_sum(s);
+  } else {
+    float s = 0.0f;
+    EACH(i, j) s = fmaf(x.v[i][j], y.v[i][j], s);
+    return s;
+  }
+}
+// v = (v inv (c scale - b) + q) om
+template <int VEC, int N>
+__device__ __forceinline__ void row_gradient(Row<VEC, N>& v, float inv, const Row<VEC, N>& c,
+                                             float scale, float b, const Row<VEC, N>& q,
+                                             const Row<VEC, N>& om) {
+  if constexpr (VEC == 4) {
+    const F2 i2 = f2(inv), s2 = f2(scale), b2 = f2(-b);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const F2 g = f2_fma(f2(v.v[i][j], v.v[i][j + 1]) * i2,
+                            f2_fma(f2(c.v[i][j], c.v[i][j + 1]), s2, b2),
+                            f2(q.v[i][j], q.v[i][j + 1])) *
+                     f2(om.v[i][j], om.v[i][j + 1]);
+        const float2 r = f2_get(g);
+        v.v[i][j] = r.x;
+        v.v[i][j + 1] = r.y;
+      }
+  } else {
+    EACH(i, j) v.v[i][j] =
+        fmaf(v.v[i][j] * inv, fmaf(c.v[i][j], scale, -b), q.v[i][j]) * om.v[i][j];
+  }
 }
 // Below this sum of sigmoids every logit is under -57, where sigmoid(x) is e^x to all of f32's
 // digits: the row (or selection) is then shifted by its largest logit, as a softmax is, instead
@@ -93,27 +149,22 @@ __device__ __forceinline__ float row_scores(Row<VEC, N>& x, Row<VEC, N>& om, int
   float sum = 0.0f;
   if (scoring == MOE_SIGMOID) {
     Row<VEC, N> s;
-    EACH(i, j) {
-      sigmoid2(x.v[i][j], s.v[i][j], om.v[i][j]);
-      sum += s.v[i][j];
-    }
-    sum = warp_sum(sum);
+    EACH(i, j) sigmoid2(x.v[i][j], s.v[i][j], om.v[i][j]);
+    sum = warp_sum(row_sum(s));
     if (!__any_sync(kAll, sum < kTinySum)) {
       x = s;
       return __fdividef(1.0f, sum);
     }
-    sum = 0.0f;
   }
   float m = -INFINITY;
   EACH(i, j) m = fmaxf(m, x.v[i][j]);
   m = warp_max(m);
   if (m == -INFINITY) m = 0.0f;
   EACH(i, j) {
-    x.v[i][j] = __expf(x.v[i][j] - m);
+    x.v[i][j] = exp_fast(x.v[i][j] - m);
     om.v[i][j] = 1.0f;
-    sum += x.v[i][j];
   }
-  sum = warp_sum(sum);
+  sum = warp_sum(row_sum(x));
   return sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
 }
 
@@ -338,29 +389,19 @@ __global__ void __launch_bounds__(kWarps * 32)
   __syncwarp();
   const float scale = d_loss ? *d_loss : 1.0f;
   const int mine = my_offset(off, n_seq, lane);
-  int width = 1;  // lanes that hold a token's routes
-  while (width < K) width <<= 1;
   const int stride = gridDim.x * kWarps;
-  // the next token's row, ids and weights are on their way while this one's are worked on
-  Row<VEC, N> next;
-  int next_id = -1;
-  float next_g = 0.0f;
-  auto fetch = [&](int t) {
-    if (t >= T) return;
-    next.load(x + (size_t)t * E, E, lane, -INFINITY);
-    next_id = lane < K ? ids[(size_t)t * K + lane] : -1;
-    next_g = dw && lane < K ? dw[(size_t)t * K + lane] : 0.0f;
-  };
-  fetch(blockIdx.x * kWarps + warp);
   for (int t = blockIdx.x * kWarps + warp; t < T; t += stride) {
-    Row<VEC, N> v = next, om;
-    const int id = next_id;
-    const float g0 = next_g;
-    const bool on = id >= 0 && id < E;
-    const float xs = on && dw ? x[(size_t)t * E + id] : -INFINITY;
-    // x may be out: the rows that are fetched ahead are this warp's own, written later
-    fetch(t + stride);
+    const float* row = x + (size_t)t * E;
     float* dst = out + (size_t)t * E;
+    Row<VEC, N> v, om;
+    v.load(row, E, lane, -INFINITY);
+    const int id = lane < K ? ids[(size_t)t * K + lane] : -1;
+    const bool on = id >= 0 && id < E;
+    float g = 0.0f, xs = -INFINITY;
+    if (dw && on) {
+      g = dw[(size_t)t * K + lane] * rsf;
+      xs = row[id];
+    }
     if (!__any_sync(kAll, on)) {
       const Row<VEC, N> zero = {};
       zero.store(dst, E, lane);
@@ -379,37 +420,12 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (c) cc.load(c, E, lane, 0.0f);
     const float inv = row_scores(v, om, scoring);
     float mean_c = 0.0f;
-    if (c) {
-      EACH(i, j) mean_c = fmaf(cc.v[i][j], v.v[i][j], mean_c);
-      mean_c = warp_sum(mean_c) * inv;
-    }
+    if (c) mean_c = warp_sum(row_dot(cc, v)) * inv;
     float all = 0.0f;
+    Row<VEC, N> q_row = {};
     if (dw) {
-      const float g = on ? g0 * rsf : 0.0f;
       float q;
-      if (scoring == MOE_SIGMOID) {
-        float s, unused;
-        sigmoid2(xs, s, unused);
-        if (renorm) {
-          float sum = group_sum(s, width);
-          // (decided by the lanes that hold the routes, for all lanes: the others' sums are 0)
-          if (__shfl_sync(kAll, sum, 0) < kTinySum) {
-            const float m = group_max(xs, width);
-            s = m == -INFINITY ? 0.0f : expf(xs - m);
-            sum = group_sum(s, width);
-          }
-          const float w = sum == 0.0f ? 0.0f : __fdividef(s, sum);
-          q = w * (g - group_sum(w * g, width));
-        } else {
-          q = s * g;
-        }
-      } else if (renorm) {
-        const float m = group_max(xs, width);
-        const float s = m == -INFINITY ? 0.0f : expf(xs - m);
-        const float sum = group_sum(s, width);
-        const float w = sum == 0.0f ? 0.0f : __fdividef(s, sum);
-        q = w * (g - group_sum(w * g, width));
-      } else {
+      if (!renorm && scoring == MOE_SOFTMAX) {
         // the row's scores are in their owners' registers
         v.store(s_row, E, lane);
         __syncwarp();
@@ -418,6 +434,26 @@ __global__ void __launch_bounds__(kWarps * 32)
         __syncwarp();
         for (int e = lane; e < pitch; e += 32) s_row[e] = 0.0f;
         __syncwarp();
+      } else {
+        float s, unused;
+        bool shift = scoring == MOE_SOFTMAX;
+        if (!shift) sigmoid2(xs, s, unused);
+        if (!renorm) {
+          q = s * g;
+        } else {
+          float sum = 0.0f;
+          if (!shift) {
+            sum = warp_sum(s);
+            shift = __any_sync(kAll, sum < kTinySum);
+          }
+          if (shift) {  // by the selection's own largest logit: it may lie far below the row's
+            const float m = warp_max(xs);
+            s = m == -INFINITY ? 0.0f : exp_fast(xs - m);
+            sum = warp_sum(s);
+          }
+          const float w = sum == 0.0f ? 0.0f : __fdividef(s, sum);
+          q = w * (g - warp_sum(w * g));
+        }
       }
       // An expert named twice gets the sum of its routes, in route order, from the first.
       const unsigned same = __match_any_sync(kAll, on ? id : -1 - lane);
@@ -431,16 +467,12 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
       if (on && (int)__ffs(same) - 1 == lane) s_row[id] = tot;
       __syncwarp();
-      Row<VEC, N> qr;
-      qr.load(s_row, E, lane, 0.0f);
-      EACH(i, j) v.v[i][j] = (v.v[i][j] * inv * (cc.v[i][j] * scale - mean_c * scale - all) +
-                              qr.v[i][j]) * om.v[i][j];
+      q_row.load(s_row, E, lane, 0.0f);
       __syncwarp();
       if (on) s_row[id] = 0.0f;
       __syncwarp();
-    } else {
-      EACH(i, j) v.v[i][j] = v.v[i][j] * inv * scale * (cc.v[i][j] - mean_c) * om.v[i][j];
     }
+    row_gradient(v, inv, cc, scale, mean_c * scale + all, q_row, om);
     v.store(dst, E, lane);
   }
 }
