@@ -374,8 +374,10 @@ __global__ void __launch_bounds__(kFinE * kFinC)
 // with c the loss' coefficients, q the route weights' terms of the selected experts and A what
 // softmax weights without renormalisation take from every expert (1 - s_j is 1 for softmax).
 // The q of a token meet the row in shared memory.
+// Four CTAs per SM up to 384 experts (64 registers): a token is a chain of loads and reductions, and
+// only other warps hide it (384 experts, 32768 tokens: 31.5 us with three, 27 with four).
 template <int VEC, int N>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, N * VEC <= 12 ? 4 : 1)
     router_bwd_kernel(int T, int E, int K, int n_seq, int scoring, int renorm, float rsf,
                       const float* x, const int32_t* __restrict__ ids,
                       const float* __restrict__ dw, const float* __restrict__ coef,
@@ -455,17 +457,24 @@ __global__ void __launch_bounds__(kWarps * 32)
           q = w * (g - warp_sum(w * g));
         }
       }
-      // An expert named twice gets the sum of its routes, in route order, from the first.
-      const unsigned same = __match_any_sync(kAll, on ? id : -1 - lane);
+      // An expert named twice gets the sum of its routes, in route order, from the first.  Whether
+      // there is one shows when every route leaves its number at its expert: one gets lost.
+      if (on) s_row[id] = __int_as_float(lane);
+      __syncwarp();
+      const bool lost = on && __float_as_int(s_row[id]) != lane;
+      __syncwarp();
+      bool first = on;
       float tot = q;
-      if (__any_sync(kAll, on && __popc(same) > 1)) {
+      if (__any_sync(kAll, lost)) {
+        const unsigned same = __match_any_sync(kAll, on ? id : -1 - lane);
+        first = on && (int)__ffs(same) - 1 == lane;
         tot = 0.0f;
         for (int j = 0; j < K; ++j) {
           const float qj = __shfl_sync(kAll, q, j);
           if ((same >> j) & 1u) tot += qj;
         }
       }
-      if (on && (int)__ffs(same) - 1 == lane) s_row[id] = tot;
+      if (first) s_row[id] = tot;
       __syncwarp();
       q_row.load(s_row, E, lane, 0.0f);
       __syncwarp();
@@ -560,7 +569,7 @@ cudaError_t launch_router_bwd(const moe_problem_t& p, int n_seq, const float* x,
                               cudaStream_t s) {
   if (p.T == 0) return cudaSuccess;
   const int need = (p.T + kWarps - 1) / kWarps;
-  const int most = num_sms() * 8;
+  const int most = num_sms() * 4;  // what is resident: a second wave would start over
   const size_t smem = (size_t)kWarps * (p.E + 3) * 4;
 #define BWD_(V, N)                                                                                \
   launch_k(router_bwd_kernel<V, N>, dim3(need < most ? need : most), dim3(kWarps * 32), smem, s, \
