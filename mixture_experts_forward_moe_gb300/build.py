@@ -82,7 +82,7 @@ def _link_calls(obj: str) -> None:
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [cxx, "-shared", "-o", tmp, obj, "-L", BUILD, "-l:" + os.path.basename(LIB),
            "-Wl,-rpath,$ORIGIN", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
-           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the Python module failed:\n{r.stdout}\n{r.stderr}")

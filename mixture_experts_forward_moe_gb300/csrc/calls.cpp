@@ -3,8 +3,7 @@
 // Those calls take a few microseconds on the device, less than marshalling them through ctypes.
 #define PY_SSIZE_T_CLEAN
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
 #include <Python.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -109,6 +108,12 @@ bool failed(moe_status_t rc, const char* what) {
   return true;
 }
 
+// An output on `like`'s device (current).
+at::Tensor fresh(const at::Tensor& like, c10::IntArrayRef shape, at::ScalarType dtype) {
+  return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
+}
+at::Tensor fresh(const at::Tensor& like) { return fresh(like, like.sizes(), like.scalar_type()); }
+
 at::Tensor zeros(int64_t bytes, c10::Device dev) {
   return at::zeros({bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
 }
@@ -177,7 +182,7 @@ PyObject* call_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   need_if(out, "out", odt, {g.T, g.N}, x);
   c10::cuda::CUDAGuard guard(x.device());
   const auto s = stream_of(x);
-  if (!out.defined()) out = at::empty({g.T, g.N}, x.options().dtype(odt));
+  if (!out.defined()) out = fresh(x, {g.T, g.N}, odt);
   const at::Tensor ws = workspace(a[7], (int64_t)moe_linear_workspace_size(&g), s);
   if (failed(moe_linear(&g, ptr(x), ptr(w), ptr(bias), ptr(res), ptr(out), ptr(ws),
                         (size_t)ws.numel(), s.stream()),
@@ -240,8 +245,8 @@ PyObject* call_block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor r = optional(a[10], "stream_out"), h;
   need_if(r, "stream_out", m.y.scalar_type(), m.y.sizes(), m.y);
   c10::cuda::CUDAGuard guard(m.y.device());
-  if (!r.defined() && as_bool(a[11])) r = at::empty_like(m.y);
-  if (m.p.pre_norm) h = at::empty_like(m.y);
+  if (!r.defined() && as_bool(a[11])) r = fresh(m.y);
+  if (m.p.pre_norm) h = fresh(m.y);
   if (failed(moe_block_norm_fwd(&m.p, ptr(m.y), ptr(m.x), ptr(m.g), ptr(m.wq), ptr(m.wp), ptr(r),
                                 ptr(h), stream_of(m.y).stream()),
              "moe_block_norm_fwd"))
@@ -274,7 +279,7 @@ PyObject* call_block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c10::cuda::CUDAGuard guard(m.y.device());
   const auto s = stream_of(m.y);
   const at::Tensor ws = workspace(a[12], (int64_t)moe_block_norm_bwd_workspace_size(&m.p), s);
-  auto like = [](const at::Tensor& t) { return t.defined() ? at::empty_like(t) : at::Tensor(); };
+  auto like = [](const at::Tensor& t) { return t.defined() ? fresh(t) : at::Tensor(); };
   const at::Tensor dy = like(m.y), dx = like(m.x), dg = like(m.g), dq = like(m.wq),
                    dp = like(m.wp);
   if (failed(moe_block_norm_bwd(&m.p, ptr(dr), ptr(dh), ptr(m.y), ptr(m.x), ptr(m.g), ptr(m.wq),
@@ -335,10 +340,11 @@ PyObject* call_balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto s = stream_of(r.x);
   const at::Tensor ws =
       workspace(a[7], (int64_t)moe_balance_loss_workspace_size(&r.p, r.n_seq), s);
-  const auto f32 = r.x.options(), i32 = f32.dtype(at::kInt);
-  const at::Tensor loss = at::empty({1}, f32), counts = at::empty({r.n_seq, r.p.E}, i32),
-                   live = at::empty({r.n_seq}, i32), sums = at::empty({r.n_seq, r.p.E}, f32),
-                   coef = at::empty({r.n_seq, r.p.E}, f32);
+  const at::Tensor loss = fresh(r.x, {1}, at::kFloat),
+                   counts = fresh(r.x, {r.n_seq, r.p.E}, at::kInt),
+                   live = fresh(r.x, {r.n_seq}, at::kInt),
+                   sums = fresh(r.x, {r.n_seq, r.p.E}, at::kFloat),
+                   coef = fresh(r.x, {r.n_seq, r.p.E}, at::kFloat);
   if (failed(moe_balance_loss_fwd(&r.p, r.n_seq, as_float(a[6]), r.logits(), r.routes(),
                                   r.offsets(), static_cast<float*>(ptr(loss)),
                                   static_cast<int32_t*>(ptr(counts)),
@@ -374,7 +380,7 @@ PyObject* call_router_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need_if(dl, "d_loss", at::kFloat, dl.sizes(), r.x);
   }
   c10::cuda::CUDAGuard guard(r.x.device());
-  if (!out.defined()) out = at::empty_like(r.x);
+  if (!out.defined()) out = fresh(r.x);
   if (failed(moe_router_bwd(&r.p, r.n_seq, r.logits(), r.routes(),
                             static_cast<const float*>(ptr(dw)),
                             static_cast<const float*>(ptr(coef)), r.offsets(),

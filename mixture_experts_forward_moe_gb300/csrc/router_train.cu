@@ -264,21 +264,25 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 // ---- balance loss, second pass ---------------------------------------------------------------
-// One CTA per (32 experts, sequence): 16 rows of lanes share the chunks of an expert, joined in a fixed order.
-// The CTA that finishes last adds the CTAs' parts of the loss, again in a fixed order.
-constexpr int kFinE = 32, kFinC = 16;
+// A CTA takes `cols` experts (a multiple of 32) of a sequence; its threads are rows of `cols`, and
+// row y adds the chunks y, y + rows, ..., then the rows are added in order.  The CTA that finishes
+// last adds the CTAs' parts of the loss, again in a fixed order.
+constexpr int kFinThreads = 512;
 
-__global__ void __launch_bounds__(kFinE * kFinC)
-    balance_final_kernel(int T, int E, int K, int n_seq, int chunk, float coeff,
+__global__ void __launch_bounds__(kFinThreads)
+    balance_final_kernel(int T, int E, int K, int n_seq, int chunk, int cols, float coeff,
                          const int32_t* __restrict__ off, const Records rec,
                          float* __restrict__ loss, int32_t* __restrict__ counts,
                          int32_t* __restrict__ live_out, float* __restrict__ prob_sum,
                          float* __restrict__ coef, float* part, int* ticket, int* status) {
-  __shared__ float s_p[kFinC][kFinE];
-  __shared__ int s_c[kFinC][kFinE];
-  __shared__ int s_live[kFinC], s_seqs[kFinC];
+  __shared__ float s_p[kFinThreads];
+  __shared__ int s_c[kFinThreads];
+  __shared__ int s_live[kFinThreads / 32], s_seqs[kFinThreads / 32];
+  __shared__ float s_loss[kFinThreads / 32];
   __shared__ int s_last;
-  const int tid = threadIdx.y * kFinE + threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int y = tid / cols, col = tid - y * cols;
+  const int rows = kFinThreads / cols;
   // The chunks of sequence s are [first, last]; empty when it has no tokens.
   auto range = [&](int s, int& first, int& last) {
     const int a = off ? clamp_i(off[s], 0, T) : 0;
@@ -286,11 +290,11 @@ __global__ void __launch_bounds__(kFinE * kFinC)
     first = a / chunk;
     last = b > a ? (b - 1) / chunk : first - 1;
   };
-  const int e = blockIdx.x * kFinE + threadIdx.x;
+  const int e = blockIdx.x * cols + col;
   pdl_wait();
   // Sequences with live tokens.
   int seqs = 0;
-  for (int s = tid; s < n_seq; s += kFinE * kFinC) {
+  for (int s = tid; s < n_seq; s += kFinThreads) {
     int c, last;
     range(s, c, last);
     bool any = false;
@@ -305,33 +309,32 @@ __global__ void __launch_bounds__(kFinE * kFinC)
     int first, last;
     range(s, first, last);
     int live = 0;
-    for (int c = first + tid; c <= last; c += kFinE * kFinC) live += rec.live[(size_t)c + s];
+    for (int c = first + tid; c <= last; c += kFinThreads) live += rec.live[(size_t)c + s];
     float p = 0.0f;
     int cnt = 0;
-    if (e < E)
+    if (e < E && y < rows)
 #pragma unroll 8
-      for (int c = first + (int)threadIdx.y; c <= last; c += kFinC) {
+      for (int c = first + y; c <= last; c += rows) {
         const size_t r = ((size_t)c + s) * E + e;
         p += rec.prob[r];
         cnt += rec.count[r];
       }
     live = __reduce_add_sync(kAll, live);
     const int n = __reduce_add_sync(kAll, seqs);
-    s_p[threadIdx.y][threadIdx.x] = p;
-    s_c[threadIdx.y][threadIdx.x] = cnt;
-    if (threadIdx.x == 0) {
-      s_live[threadIdx.y] = live;
-      s_seqs[threadIdx.y] = n;
+    s_p[tid] = p;
+    s_c[tid] = cnt;
+    if (lane == 0) {
+      s_live[warp] = live;
+      s_seqs[warp] = n;
     }
     __syncthreads();
-    if (threadIdx.y == 0) {
-      const bool mine = threadIdx.x < kFinC;
-      const int T_all = __reduce_add_sync(kAll, mine ? s_live[threadIdx.x] : 0);
-      const int n_all = __reduce_add_sync(kAll, mine ? s_seqs[threadIdx.x] : 0);
-#pragma unroll
-      for (int y = 1; y < kFinC; ++y) {
-        p += s_p[y][threadIdx.x];
-        cnt += s_c[y][threadIdx.x];
+    if (y == 0) {  // whole warps: cols is a multiple of 32
+      const bool mine = lane < kFinThreads / 32;
+      const int T_all = __reduce_add_sync(kAll, mine ? s_live[lane] : 0);
+      const int n_all = __reduce_add_sync(kAll, mine ? s_seqs[lane] : 0);
+      for (int r = 1; r < rows; ++r) {
+        p += s_p[r * cols + col];
+        cnt += s_c[r * cols + col];
       }
       if (e < E) {
         const float T_s = (float)max(T_all, 1);
@@ -343,28 +346,34 @@ __global__ void __launch_bounds__(kFinE * kFinC)
         coef[o] = w;
         loss_part = fmaf(w, p, loss_part);
       }
-      if (blockIdx.x == 0 && threadIdx.x == 0) live_out[s] = T_all;
+      if (blockIdx.x == 0 && tid == 0) live_out[s] = T_all;
     }
     __syncthreads();
   }
+  loss_part = warp_sum(loss_part);
+  if (lane == 0) s_loss[warp] = loss_part;
+  __syncthreads();
+  if (warp != 0) return;
+  loss_part = warp_sum(lane < kFinThreads / 32 ? s_loss[lane] : 0.0f);
   const int n_parts = gridDim.x * gridDim.y;
-  if (threadIdx.y == 0) {
-    loss_part = warp_sum(loss_part);
-    if (threadIdx.x == 0) {
-      part[blockIdx.y * gridDim.x + blockIdx.x] = loss_part;
-      __threadfence();
-      s_last = atomicAdd(ticket, 1) == n_parts - 1;
-    }
-    __syncwarp();
-    if (s_last) {
-      __threadfence();
-      float l = 0.0f;
-      for (int i = threadIdx.x; i < n_parts; i += kFinE) l += __ldcg(part + i);
-      l = warp_sum(l);
-      if (threadIdx.x == 0) {
-        *loss = l;
-        *ticket = 0;
-      }
+  if (n_parts == 1) {
+    if (lane == 0) *loss = loss_part;
+    return;
+  }
+  if (lane == 0) {
+    part[blockIdx.y * gridDim.x + blockIdx.x] = loss_part;
+    __threadfence();
+    s_last = atomicAdd(ticket, 1) == n_parts - 1;
+  }
+  __syncwarp();
+  if (s_last) {
+    __threadfence();
+    float l = 0.0f;
+    for (int i = lane; i < n_parts; i += 32) l += __ldcg(part + i);
+    l = warp_sum(l);
+    if (lane == 0) {
+      *loss = l;
+      *ticket = 0;
     }
   }
 }
@@ -491,7 +500,7 @@ constexpr int kChunkCtas = 608;
 
 // Workspace of the balance loss past its header: the records and the parts of the loss.
 struct BalanceLayout {
-  int chunk, n_chunks, e_tiles, seq_ctas;
+  int chunk, n_chunks, cols, e_tiles, seq_ctas;
   size_t prob, count, live, part, total;
 };
 BalanceLayout balance_layout(int T, int E, int n_seq) {
@@ -500,7 +509,13 @@ BalanceLayout balance_layout(int T, int E, int n_seq) {
   L.chunk = ((T + kChunkCtas - 1) / kChunkCtas + kWarps - 1) / kWarps * kWarps;
   if (L.chunk < kWarps) L.chunk = kWarps;
   L.n_chunks = (T + L.chunk - 1) / L.chunk;
-  L.e_tiles = (E + kFinE - 1) / kFinE;
+  // One CTA for everything spares the join of the CTAs' parts of the loss, as long as each of its
+  // threads has few records to read.
+  const int all = (E + 31) / 32 * 32;
+  L.cols = n_seq == 1 && all <= kFinThreads && (int64_t)L.n_chunks * all <= 16 * kFinThreads
+               ? all
+               : 32;
+  L.e_tiles = (E + L.cols - 1) / L.cols;
   L.seq_ctas = n_seq < 512 ? n_seq : 512;
   size_t o = kHeaderBytes;
   auto take = [&](size_t bytes) {
@@ -558,8 +573,8 @@ cudaError_t launch_balance_loss(const moe_problem_t& p, int n_seq, float coeff, 
 #undef CHUNK_
     if (e != cudaSuccess) return e;
   }
-  return launch_k(balance_final_kernel, dim3(L.e_tiles, L.seq_ctas), dim3(kFinE, kFinC), 0, s,
-                  p.T > 0, p.T, p.E, p.top_k, n_seq, L.chunk, coeff, off, rec, loss, counts,
+  return launch_k(balance_final_kernel, dim3(L.e_tiles, L.seq_ctas), dim3(kFinThreads), 0, s,
+                  p.T > 0, p.T, p.E, p.top_k, n_seq, L.chunk, L.cols, coeff, off, rec, loss, counts,
                   live, prob_sum, coef, reinterpret_cast<float*>(ws + L.part), ticket, status);
 }
 
