@@ -158,6 +158,16 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_shared_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -167,39 +177,50 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   return v;
 }
 
-// Eight consecutive outputs of row t from their f32 sums; n is a multiple of 8, `bias` holds the
-// biases of the columns.  With N a multiple of 8 they are whole vectors; otherwise one by one.
+// Eight consecutive outputs of row t from their f32 sums, as whole vectors: N is a multiple of 8.
 template <typename T>
 struct Finish {
   const LinArgs& p;
   int n;
-  bool vec;
   float bias[8];
   __device__ __forceinline__ Finish(const LinArgs& a, int col) : p(a), n(col) {
-    vec = (a.N & 7) == 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      bias[j] = a.bias && n + j < a.N ? DT<T>::to_f(static_cast<const T*>(a.bias)[n + j]) : 0.0f;
+    for (int j = 0; j < 8; ++j) bias[j] = 0.0f;
+    if (a.bias && n < a.N)
+      unpack<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.bias) + n), bias);
   }
-  // The residual, asked for before the sums are there.
-  __device__ __forceinline__ void residual(int t, float (&r)[8]) const {
-    const int64_t o = (int64_t)t * p.N + n;
+  // The residuals of kCols rows t, t + step, ... below t1, asked for together: a branch or a
+  // conversion between two loads would wait for the first.
+  template <int kCols>
+  __device__ __forceinline__ void residual(int t, int step, int t1, float (&r)[kCols][8]) const {
+    if (!p.res || n >= p.N) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = 0.0f;
-    if (!p.res || n >= p.N) return;
-    if (vec && p.out_f32) {
-      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.res) + o);
-      const float4 a = src[0], b = src[1];
-      r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
-      r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
-    } else if (vec) {
-      unpack<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.res) + o), r);
+      for (int i = 0; i < kCols; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] = 0.0f;
+    } else if (p.out_f32) {
+      float4 v[kCols][2];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const float4* src = reinterpret_cast<const float4*>(
+            static_cast<const float*>(p.res) + (int64_t)(t + i * step < t1 ? t + i * step : t) * p.N +
+            n);
+        v[i][0] = src[0];
+        v[i][1] = src[1];
+      }
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        r[i][0] = v[i][0].x, r[i][1] = v[i][0].y, r[i][2] = v[i][0].z, r[i][3] = v[i][0].w;
+        r[i][4] = v[i][1].x, r[i][5] = v[i][1].y, r[i][6] = v[i][1].z, r[i][7] = v[i][1].w;
+      }
     } else {
+      uint4 v[kCols];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (n + j < p.N)
-          r[j] = p.out_f32 ? static_cast<const float*>(p.res)[o + j]
-                           : DT<T>::to_f(static_cast<const T*>(p.res)[o + j]);
+      for (int i = 0; i < kCols; ++i)
+        v[i] = *reinterpret_cast<const uint4*>(
+            static_cast<const T*>(p.res) + (int64_t)(t + i * step < t1 ? t + i * step : t) * p.N + n);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) unpack<T>(v[i], r[i]);
     }
   }
   __device__ __forceinline__ void store(int t, float (&z)[8], const float (&r)[8]) const {
@@ -213,24 +234,87 @@ struct Finish {
     if (p.res)
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[j] += r[j];
-    if (vec && p.out_f32) {
+    if (p.out_f32) {
       float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
       dst[0] = make_float4(z[0], z[1], z[2], z[3]);
       dst[1] = make_float4(z[4], z[5], z[6], z[7]);
-    } else if (vec) {
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + o) = pack<T>(z);
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (n + j >= p.N) break;
-        if (p.out_f32)
-          static_cast<float*>(p.out)[o + j] = z[j];
-        else
-          static_cast<T*>(p.out)[o + j] = DT<T>::from_f(z[j]);
-      }
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + o) = pack<T>(z);
     }
   }
 };
+
+// f[k] = from[at(k)], f32 or T, all asked for before the first is converted; 0 without `have`.
+template <typename T, int kCount, typename At>
+__device__ __forceinline__ void load_raw(float (&f)[kCount], bool have, const void* from, bool f32,
+                                         At at) {
+#pragma unroll
+  for (int k = 0; k < kCount; ++k) f[k] = 0.0f;
+  if (!have) return;
+  if (f32) {
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) f[k] = static_cast<const float*>(from)[at(k)];
+  } else {
+    T raw[kCount];
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) raw[k] = static_cast<const T*>(from)[at(k)];
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) f[k] = DT<T>::to_f(raw[k]);
+  }
+}
+
+// The join below for any N: consecutive threads take consecutive outputs one by one.
+template <typename T, int kSplit>
+__device__ __forceinline__ void join_scalar(const LinArgs& p, uint32_t base, int c0, int c1,
+                                            int n0, int t0, uint32_t stride, uint32_t first) {
+  constexpr int kAtOnce = kSplit == 1 ? 16 : (kSplit == 2 ? 8 : (kSplit <= 4 ? 4 : 2));
+  const int end = c1 * kSlab;
+  for (int i = c0 * kSlab + (int)threadIdx.x; i < end; i += kAtOnce * (int)blockDim.x) {
+    // everything is asked for before the first output is written: a store may hide any load
+    float v[kAtOnce][kSplit], r[kAtOnce], b[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int at = i + k * (int)blockDim.x < end ? i + k * (int)blockDim.x : i;
+#pragma unroll
+      for (int s = 0; s < kSplit; ++s)
+        v[k][s] = kSplit > 1 ? ld_cluster_f1(cluster_map(base + (uint32_t)at * 4u,
+                                                         (uint32_t)s * stride + first))
+                             : ld_shared_f1(base + (uint32_t)at * 4u);
+    }
+    // Bias and residual; an output that is not there stands for the first of the tile.
+    auto place = [&](int k, int& n) -> int64_t {
+      const int at = i + k * (int)blockDim.x;
+      n = n0 + at % kSlab;
+      const bool in = at < end && n < p.N;
+      if (!in) n = n0;
+      return (int64_t)(t0 + (in ? at / kSlab : c0)) * p.N + n;
+    };
+    load_raw<T, kAtOnce>(b, p.bias && n0 < p.N, p.bias, false, [&](int k) -> int64_t {
+      int n;
+      place(k, n);
+      return n;
+    });
+    load_raw<T, kAtOnce>(r, p.res && n0 < p.N, p.res, p.out_f32 != 0, [&](int k) {
+      int n;
+      return place(k, n);
+    });
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int at = i + k * (int)blockDim.x;
+      const int n = n0 + at % kSlab;
+      if (at >= end || n >= p.N) continue;
+      float z = v[k][0];
+#pragma unroll
+      for (int s = 1; s < kSplit; ++s) z += v[k][s];
+      z = activate(z + b[k], p.act) + r[k];
+      const int64_t o = (int64_t)(t0 + at / kSlab) * p.N + n;
+      if (p.out_f32)
+        static_cast<float*>(p.out)[o] = z;
+      else
+        static_cast<T*>(p.out)[o] = DT<T>::from_f(z);
+    }
+  }
+}
 
 // The f32 sums of a tile lie in shared memory as [column][128 weight rows] at `base`, in kSplit
 // parts of K that belong to the cluster's CTAs s * stride + first.  This CTA (part `part`) adds
@@ -241,6 +325,8 @@ template <typename T, int kSplit>
 __device__ __forceinline__ void join_parts(const LinArgs& p, uint32_t base, int cols, int n0,
                                            int t0, int part, uint32_t stride, uint32_t first) {
   const int c1 = cols * (part + 1) / kSplit;
+  if ((p.N & 7) != 0)
+    return join_scalar<T, kSplit>(p, base, cols * part / kSplit, c1, n0, t0, stride, first);
   const int g = threadIdx.x & 15;
   const Finish<T> f(p, n0 + g * 8);
   constexpr int kCols = kSplit <= 2 ? 4 : (kSplit <= 4 ? 2 : 1);  // rows of x at a time
@@ -264,9 +350,7 @@ __device__ __forceinline__ void join_parts(const LinArgs& p, uint32_t base, int 
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < kCols; ++i)
-      if (c + i * step < c1) f.residual(t0 + c + i * step, r[i]);
+    f.template residual<kCols>(t0 + c, step, t0 + c1, r);
 #pragma unroll
     for (int i = 0; i < kCols; ++i) {
       if (c + i * step >= c1) break;
@@ -545,6 +629,7 @@ struct PairShape {
   static constexpr int kStageBytes = kKps * kBlockBytes;
   static constexpr int kStages = BN == 128 ? 4 : 3;
   static constexpr int kSmem = kStages * kStageBytes + 1024;
+  static constexpr int kMaxStages = BN == 128 ? 4 : 6;  // of a CTA alone on its SM
   static constexpr int kBufs = kF32 ? 2 : 1;
   static constexpr int kTmemCols = kBufs * BN;
   static_assert(kPerSm * (kSmem + 2048) <= 228 * 1024 && kPerSm * kTmemCols <= 512, "per SM");
@@ -565,12 +650,11 @@ __device__ __forceinline__ void umma_commit_both(uint32_t bar, uint32_t even) {
 template <typename T, int BN, bool kF32>
 __global__ void __launch_bounds__(kMmaThreads, PairShape<BN, kF32>::kPerSm)
     pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                const LinArgs p, int split) {
+                const LinArgs p, int split, int stages) {
   using S = PairShape<BN, kF32>;
-  constexpr int stages = S::kStages;
   extern __shared__ uint8_t dsmem[];
-  __shared__ __align__(8) uint64_t full_bar[stages];
-  __shared__ __align__(8) uint64_t empty_bar[stages];
+  __shared__ __align__(8) uint64_t full_bar[S::kMaxStages];
+  __shared__ __align__(8) uint64_t empty_bar[S::kMaxStages];
   __shared__ __align__(8) uint64_t tfull_bar[S::kBufs];
   __shared__ __align__(8) uint64_t tempty_bar[S::kBufs];
   __shared__ __align__(8) uint64_t drain_bar;
@@ -591,6 +675,7 @@ __global__ void __launch_bounds__(kMmaThreads, PairShape<BN, kF32>::kPerSm)
   const int kb0 = (int)((int64_t)num_kb * part / split);
   const int kb1 = (int)((int64_t)num_kb * (part + 1) / split);
   const int cols = p.T - t0 < BN ? p.T - t0 : BN;
+  const int mma_n = (cols + 31) & ~31;  // each CTA holds half of these rows of x
   const int chunk = kF32 ? kDrainKb : kb1 - kb0;  // blocks of one accumulator pass
 
   if (warp == 0) {
@@ -630,7 +715,7 @@ __global__ void __launch_bounds__(kMmaThreads, PairShape<BN, kF32>::kPerSm)
     if (elect_one()) {
       Ring r(empty_bar, stages, 1u);
       int issued = 0;
-      const int tx = t0 + (int)side * (BN / 2);
+      const int tx = t0 + (int)side * (mma_n / 2);
       for (int kb = kb0; kb < kb1; kb += S::kKps) {
         if (!r.ready && !wait(r.bar(), r.parity)) break;
         uint8_t* st = smem + r.stage * S::kStageBytes;
@@ -666,7 +751,7 @@ __global__ void __launch_bounds__(kMmaThreads, PairShape<BN, kF32>::kPerSm)
       uint32_t buf_phase = 0;
       bool ok = true;
       const uint32_t base = smem_u32(smem);
-      const uint32_t idesc = idesc_f16(256, BN, DT<T>::kIsBF16);
+      const uint32_t idesc = idesc_f16(256, mma_n, DT<T>::kIsBF16);
       const uint32_t empty_own = smem_u32(empty_bar), tfull_own = smem_u32(tfull_bar);
       for (int kc = kb0; kc < kb1 && ok; kc += chunk) {
         if (kF32 && !wait(&tempty_bar[buf], buf_phase ^ 1u)) break;
@@ -775,6 +860,8 @@ __global__ void __launch_bounds__(kMmaThreads, PairShape<BN, kF32>::kPerSm)
 }
 
 // ---- host side ---------------------------------------------------------------------------------
+constexpr int kSmemLimit = 226 * 1024;  // dynamic; leaves room for the static variables
+
 // Sets a kernel's shared-memory limit, once per device; `Kernel` names the instance.
 template <auto Kernel>
 cudaError_t set_smem_limit(int bytes) {
@@ -791,10 +878,41 @@ cudaError_t set_smem_limit(int bytes) {
   return result[dev];
 }
 
+// Clusters of `cluster` CTAs with `smem` bytes each (one size per kernel) that the device holds at
+// once: a cluster stays within one group of SMs, so this can be less than SMs / cluster.
+template <auto Kernel>
+int max_clusters(int cluster, int smem) {
+  static int cached[64][9];
+  static std::once_flag once[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || cluster > 8) return 0;
+  std::call_once(once[dev][cluster], [=] {
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cluster);
+    cfg.blockDim = dim3(kMmaThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (set_smem_limit<Kernel>(kSmemLimit) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      n = 0;
+    }
+    cached[dev][cluster] = n;
+  });
+  return cached[dev][cluster];
+}
+
 template <auto Kernel, typename... Rest>
 cudaError_t launch_tiles(const LinArgs& p, int dtype, const void* x, const void* w, int box_x,
                          int smem, int64_t ctas, int cluster, cudaStream_t s, Rest... rest) {
-  const cudaError_t e = set_smem_limit<Kernel>(227 * 1024 - 1024);
+  const cudaError_t e = set_smem_limit<Kernel>(kSmemLimit);
   if (e != cudaSuccess) return e;
   CUtensorMap tmW, tmX;
   if (!make_map16(&tmW, dtype, w, (uint64_t)p.K, (uint64_t)p.N, kSlab) ||
@@ -829,7 +947,7 @@ cudaError_t launch_mma(const LinArgs& p, int dtype, const void* x, const void* w
     ++split;
   // Alone on its SM a CTA takes all the shared memory for stages.
   int stages = Shape<BN>::kStages;
-  if (tiles * split <= num_sms()) stages = 225 * 1024 / Shape<BN>::kStageBytes;
+  if (tiles * split <= num_sms()) stages = (kSmemLimit - 1024) / Shape<BN>::kStageBytes;
   if (stages > kMaxStages) stages = kMaxStages;
   return launch_tiles<mma_kernel<T, BN>>(p, dtype, x, w, BN,
                                          stages * Shape<BN>::kStageBytes + 1024, tiles * split,
@@ -843,10 +961,16 @@ cudaError_t launch_pair(const LinArgs& p, int dtype, const void* x, const void* 
   const int num_kb = (p.K + kBlockK - 1) / kBlockK;
   int split = 1;
   if (BN == 128)  // a part of a 256-column tile does not fit beside a second CTA
-    while (split < 4 && tiles * (split + 1) * 2 <= num_sms() && num_kb >= (split + 1) * 7) ++split;
-  return launch_tiles<pair_kernel<T, BN, kF32>>(p, dtype, x, w, BN / 2,
-                                                PairShape<BN, kF32>::kSmem, tiles * split * 2,
-                                                2 * split, s, split);
+    while (split < 4 && num_kb >= (split + 1) * 7 &&
+           tiles <= max_clusters<pair_kernel<T, BN, kF32>>(2 * (split + 1),
+                                                              PairShape<BN, kF32>::kSmem))
+      ++split;
+  // A CTA alone on its SM needs the stages of two to keep as many bytes on the way.
+  const bool alone = tiles * split * 2 <= num_sms();
+  const int stages = alone ? PairShape<BN, kF32>::kMaxStages : PairShape<BN, kF32>::kStages;
+  return launch_tiles<pair_kernel<T, BN, kF32>>(
+      p, dtype, x, w, BN / 2, stages * PairShape<BN, kF32>::kStageBytes + 1024,
+      tiles * split * 2, 2 * split, s, split, stages);
 }
 
 template <typename T>
@@ -868,6 +992,12 @@ cudaError_t launch_gemv(const LinArgs& p, const void* x, const void* w, cudaStre
   }
 }
 
+// Products of at most this many 128 x 64 x 64 blocks stay with one-CTA tiles: a pair's start and
+// cluster barriers cost more than its better use of shared memory gains (905 x 224 x 296, 150
+// blocks: 7.0 us against 8.9; 826 x 494 x 1808, 1508: 11.8 against 13.9; 512 x 256 x 7168, 1792:
+// 15.9 against 13.3; 128 x 2048 x 4096, 2048: 13.3 against 11.0).
+constexpr int64_t kSmallTiles = 1600;
+
 template <typename T>
 cudaError_t launch_typed(const LinArgs& p, int dtype, const void* x, const void* w,
                          cudaStream_t s) {
@@ -878,12 +1008,19 @@ cudaError_t launch_typed(const LinArgs& p, int dtype, const void* x, const void*
     return launch_gemv<T>(p, x, w, s);
   if (p.T <= 16) return launch_mma<T, 16>(p, dtype, x, w, s);
   if (p.T <= 32) return launch_mma<T, 32>(p, dtype, x, w, s);
-  if (p.T <= 64) return launch_mma<T, 64>(p, dtype, x, w, s);
+  const int64_t kbs = ceil_div(p.K, kBlockK);
+  if (p.T <= 64 || ceil_div(p.N, kSlab) * ceil_div(p.T, 64) * kbs <= kSmallTiles)
+    return launch_mma<T, 64>(p, dtype, x, w, s);
   if (p.out_f32) return launch_pair<T, 128, true>(p, dtype, x, w, s);
-  // 256 columns once those tiles alone give every SM one
-  if (ceil_div(p.N, 2 * kSlab) * ceil_div(p.T, 256) * 2 >= num_sms())
-    return launch_pair<T, 256, false>(p, dtype, x, w, s);
-  return launch_pair<T, 128, false>(p, dtype, x, w, s);
+  // The time of the busiest SM, in thirds of a pass over K with a 128-column tile: those run one
+  // per SM at a time.  A 256-column tile alone on its SM takes 1.4 of them (512 x 4096 x 7168: 28
+  // and 39 us), two that share an SM 2.7 (8192^3: 895 us in 128 columns, 594 in 256).
+  const int64_t slabs = ceil_div(p.N, 2 * kSlab), sms = num_sms();
+  const int64_t narrow = 3 * ceil_div(slabs * ceil_div(p.T, 128) * 2, sms);
+  const int64_t wide_ctas = slabs * ceil_div(p.T, 256) * 2;
+  const int64_t wide = wide_ctas <= sms ? 4 : 8 * ceil_div(wide_ctas, 2 * sms);
+  return wide <= narrow ? launch_pair<T, 256, false>(p, dtype, x, w, s)
+                        : launch_pair<T, 128, false>(p, dtype, x, w, s);
 }
 
 }  // namespace
