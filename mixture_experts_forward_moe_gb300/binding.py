@@ -894,7 +894,8 @@ def moe_block_norm_bwd(d_stream, d_normed, branch, residual=None, gate=None, pos
                        weight_offset=0.0, eps=1e-6, workspace=None, stream=None):
     """The gradients of moe_block_norm (include/moe.h: moe_block_norm_bwd) for the same inputs and
     options; d_stream may be None, d_normed is None without pre_norm.  Returns a dict of d_branch
-    and, where there is such an input, d_residual, d_gate, d_post_weight and d_pre_weight."""
+    and, where there is such an input, d_residual, d_gate, d_post_weight and d_pre_weight; those
+    per channel share one allocation."""
     return _call("block_norm_bwd", stream,
                  (branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
                   residual_scale, weight_offset, eps, d_stream, d_normed, workspace))
@@ -904,7 +905,8 @@ def moe_balance_loss(gating_output, topk_ids, coeff, scoring_func="softmax", seq
                      workspace=None, stream=None):
     """Per-expert counts and the balance loss of ragged sequences (include/moe.h:
     moe_balance_loss_fwd).  Returns a dict of loss [1] and, per sequence, counts [n_seq, E] int32,
-    live_tokens [n_seq] int32, prob_sum and coef [n_seq, E]; coef is what moe_router_bwd takes."""
+    live_tokens [n_seq] int32, prob_sum and coef [n_seq, E]; coef is what moe_router_bwd takes.
+    They share one allocation."""
     scoring = _SCORING.get(scoring_func)
     if scoring is None:
         raise ValueError(f"unsupported scoring_func {scoring_func}")

@@ -398,9 +398,9 @@ __global__ void __launch_bounds__(kWide ? 512 : 448, 1)
   uint4* rows = reinterpret_cast<uint4*>(dyn) + (kWide ? 0 : kChanRows * n_vec);
   uint4* buf = rows + (size_t)me.g * kRows * kTensors * n_vec;  // [row][tensor][n_vec]
   const Channels<T, kWide> chan(p, dyn);
-  // what is not there stays zero
-  for (int v = threadIdx.x; v < shape.groups * kRows * kTensors * n_vec; v += blockDim.x)
-    rows[v] = make_uint4(0, 0, 0, 0);
+  if (!p.x || !q.dr || !p.pre)  // what is not there stays zero
+    for (int v = threadIdx.x; v < shape.groups * kRows * kTensors * n_vec; v += blockDim.x)
+      rows[v] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   const int step = gridDim.x * shape.groups;
   auto fetch = [&](int t, int half) {

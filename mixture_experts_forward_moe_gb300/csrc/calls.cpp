@@ -114,6 +114,16 @@ at::Tensor fresh(const at::Tensor& like, c10::IntArrayRef shape, at::ScalarType 
 }
 at::Tensor fresh(const at::Tensor& like) { return fresh(like, like.sizes(), like.scalar_type()); }
 
+// Small outputs share one allocation: contiguous tensors of `base`'s storage, `offset` in elements.
+at::Tensor part_of(const at::Tensor& base, int64_t offset, c10::IntArrayRef shape,
+                   at::ScalarType dtype) {
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(),
+                                                   c10::scalarTypeToTypeMeta(dtype));
+  impl->set_storage_offset(offset);
+  impl->set_sizes_contiguous(shape);
+  return at::Tensor(std::move(impl));
+}
+
 at::Tensor zeros(int64_t bytes, c10::Device dev) {
   return at::zeros({bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
 }
@@ -280,8 +290,22 @@ PyObject* call_block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto s = stream_of(m.y);
   const at::Tensor ws = workspace(a[12], (int64_t)moe_block_norm_bwd_workspace_size(&m.p), s);
   auto like = [](const at::Tensor& t) { return t.defined() ? fresh(t) : at::Tensor(); };
-  const at::Tensor dy = like(m.y), dx = like(m.x), dg = like(m.g), dq = like(m.wq),
-                   dp = like(m.wp);
+  const at::Tensor dy = like(m.y), dx = like(m.x);
+  at::Tensor dg, dq, dp;  // the per-channel ones lie in one allocation
+  const bool gc = m.p.gate == MOE_GATE_CHANNEL;
+  const int chans = gc + m.wq.defined() + m.wp.defined();
+  if (chans > 0) {
+    const at::ScalarType dt = m.y.scalar_type();
+    const at::Tensor all = fresh(m.y, {(int64_t)chans * m.p.H}, dt);
+    int64_t at = 0;
+    for (auto [have, d] : {std::pair<bool, at::Tensor*>(gc, &dg), {m.wq.defined(), &dq},
+                           {m.wp.defined(), &dp}})
+      if (have) {
+        *d = part_of(all, at, {m.p.H}, dt);
+        at += m.p.H;
+      }
+  }
+  if (!gc) dg = like(m.g);
   if (failed(moe_block_norm_bwd(&m.p, ptr(dr), ptr(dh), ptr(m.y), ptr(m.x), ptr(m.g), ptr(m.wq),
                                 ptr(m.wp), ptr(dy), ptr(dx), ptr(dg), ptr(dq), ptr(dp), ptr(ws),
                                 (size_t)ws.numel(), s.stream()),
@@ -340,11 +364,14 @@ PyObject* call_balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto s = stream_of(r.x);
   const at::Tensor ws =
       workspace(a[7], (int64_t)moe_balance_loss_workspace_size(&r.p, r.n_seq), s);
-  const at::Tensor loss = fresh(r.x, {1}, at::kFloat),
-                   counts = fresh(r.x, {r.n_seq, r.p.E}, at::kInt),
-                   live = fresh(r.x, {r.n_seq}, at::kInt),
-                   sums = fresh(r.x, {r.n_seq, r.p.E}, at::kFloat),
-                   coef = fresh(r.x, {r.n_seq, r.p.E}, at::kFloat);
+  // prob_sum, coef, counts, live_tokens, loss: 32-bit values, each on a 16-byte boundary
+  const int64_t table = ((int64_t)r.n_seq * r.p.E + 3) / 4 * 4, few = (r.n_seq + 3) / 4 * 4;
+  const at::Tensor all = fresh(r.x, {3 * table + few + 1}, at::kFloat);
+  const at::Tensor sums = part_of(all, 0, {r.n_seq, r.p.E}, at::kFloat),
+                   coef = part_of(all, table, {r.n_seq, r.p.E}, at::kFloat),
+                   counts = part_of(all, 2 * table, {r.n_seq, r.p.E}, at::kInt),
+                   live = part_of(all, 3 * table, {r.n_seq}, at::kInt),
+                   loss = part_of(all, 3 * table + few, {1}, at::kFloat);
   if (failed(moe_balance_loss_fwd(&r.p, r.n_seq, as_float(a[6]), r.logits(), r.routes(),
                                   r.offsets(), static_cast<float*>(ptr(loss)),
                                   static_cast<int32_t*>(ptr(counts)),
