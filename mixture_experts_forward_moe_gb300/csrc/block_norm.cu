@@ -282,10 +282,10 @@ struct Channels {
   }
 };
 
-constexpr int kMaxGroups = 28;   // groups of one warp need no barrier; others are at most 14
-constexpr int kGroupCta = 896;   // threads of a CTA: 72 registers each
+constexpr int kFwdCta = 1024;  // threads of a forward CTA: 64 registers each
+constexpr int kBwdCta = 512;   // of a backward CTA: 128 registers, for the per-channel sums
 template <typename T, int VPT, int GATE, bool kWide>
-__global__ void __launch_bounds__(kWide ? 512 : kGroupCta, 1)
+__global__ void __launch_bounds__(kWide ? 512 : kFwdCta, 1)
     norm_group_kernel(const NormArgs p, const GroupShape shape, uint4* r_out, uint4* h_out) {
   constexpr int kTensors = GATE == MOE_GATE_ELEMENT ? 3 : 2;  // y, x, gate
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kWide ? 512 : kGroupCta, 1)
 // D = dr + rr (dh w - rhat mean(dh w rhat));  dx = a D;  dg = D u;
 // dy = ry (g D q - yhat mean(g D q yhat)).  r is computed again from y and x.
 template <typename T, int VPT, int GATE, bool kWide>
-__global__ void __launch_bounds__(kWide ? 512 : 448, 1)
+__global__ void __launch_bounds__(kBwdCta, 1)
     norm_group_bwd_kernel(const NormArgs p, const NormGrads q, const GroupShape shape) {
   constexpr int kTensors = GATE == MOE_GATE_ELEMENT ? 5 : 4;  // y, x, dr, dh, gate
   constexpr int kRows = kWide ? 1 : 2;  // rows in shared memory: the next one too, if it fits
@@ -696,8 +696,8 @@ GroupShape group_shape(const NormArgs& p, int vpt, int most, int chans, int bufs
   GroupShape s;
   s.threads = threads_for(p.n_vec, vpt);
   s.groups = most / s.threads;
-  if (s.threads > 32 && s.groups > 14) s.groups = 14;
-  if (s.groups > kMaxGroups) s.groups = kMaxGroups;
+  // a group of one warp needs no barrier; there are fifteen for the others
+  if (s.threads > 32 && s.groups > 15) s.groups = 15;
   const int row = p.n_vec * 16;
   const int fit = (kSmemMax - chans * row) / (bufs * row);
   if (s.groups > fit) s.groups = fit;
@@ -722,12 +722,12 @@ cudaError_t launch_group(const GroupShape& s, int ctas, cudaStream_t stream, Arg
   return launch_k(Kernel, dim3(ctas), dim3(s.threads * s.groups), s.smem, stream, false, args...);
 }
 
-// Forward: two vectors per thread up to rows of 7168, so that a CTA holds two groups or more;
+// Forward: two vectors per thread up to rows of 8192, so that the threads make two groups or more;
 // four beyond.
-bool fwd_wide(const NormArgs& p) { return threads_for(p.n_vec, 2) > kGroupCta / 2; }
+bool fwd_wide(const NormArgs& p) { return threads_for(p.n_vec, 2) > kFwdCta / 2; }
 GroupShape fwd_shape(const NormArgs& p) {
   const int bufs = p.gate == MOE_GATE_ELEMENT ? 6 : 4;
-  return fwd_wide(p) ? group_shape(p, 4, 512, 0, bufs) : group_shape(p, 2, kGroupCta, kChanRows, bufs);
+  return fwd_wide(p) ? group_shape(p, 4, 512, 0, bufs) : group_shape(p, 2, kFwdCta, kChanRows, bufs);
 }
 template <typename T, int GATE>
 cudaError_t fwd_groups(const NormArgs& p, uint4* r, uint4* h, cudaStream_t s) {
@@ -759,14 +759,14 @@ cudaError_t fwd_typed(const NormArgs& p, void* r, void* h, cudaStream_t s) {
   }
 }
 
-// Backward: one vector per thread up to rows of 7168, four beyond.
+// Backward: two vectors per thread up to rows of 8192, four beyond.
 template <typename T, int GATE>
 cudaError_t bwd_groups(const NormArgs& p, const NormGrads& q, int ctas, cudaStream_t s) {
   const int bufs = GATE == MOE_GATE_ELEMENT ? 5 : 4;
-  const GroupShape g = group_shape(p, 2, 448, kChanRows, 2 * bufs);
+  const GroupShape g = group_shape(p, 2, kBwdCta, kChanRows, 2 * bufs);
   if (g.groups >= 1)
     return launch_group<norm_group_bwd_kernel<T, 2, GATE, false>>(g, ctas, s, p, q, g);
-  const GroupShape w = group_shape(p, 4, 512, 0, bufs);
+  const GroupShape w = group_shape(p, 4, kBwdCta, 0, bufs);
   return launch_group<norm_group_bwd_kernel<T, 4, GATE, true>>(w, ctas, s, p, q, w);
 }
 
