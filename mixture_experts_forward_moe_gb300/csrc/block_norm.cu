@@ -11,6 +11,11 @@
 //                 vectors of its next row to shared memory (cp.async) while it works on the
 //                 current one: nobody else reads them, so no barrier orders them.  The
 //                 per-channel vectors lie in shared memory once per CTA.
+//
+// The bytes of the rows bound both directions; measured on a GB300 (copy 6.8 TB/s), bf16, gate per
+// channel: forward 4096 x 7168 in 39 us (0.88 of the copy rate; 4096 x 4096 0.97), one row 3.0 us.
+// Backward 4096 x 7168 in 79 us (0.66): shared memory bandwidth and the reductions of one row after
+// another, one row at a time per thread group.
 #include <mutex>
 
 #include "vec16.cuh"

@@ -2,7 +2,12 @@
 // moe_router_bwd): per-expert counts, the balance loss over ragged sequences, and the gradient of
 // the logits from that loss and from the route weights.
 //
-// One warp per token, its row of logits spread over the lanes, as in the router itself.
+// One warp per token, its row of logits spread over the lanes, as in the router itself.  A token is
+// a chain of a load, an exponential per expert and two to five warp reductions, so the kernels are
+// bound by that chain and the warps that hide it before they are by memory.  Measured on a GB300:
+// loss of 32768 tokens, 256 experts, 11 sequences 17.6 us (5.1 us at the copy rate),
+// of 512 tokens 6.6; gradient of 32768 tokens, 384 experts 25.5 us (0.59 of the copy rate), of 512
+// tokens 2.8.
 #include <limits.h>
 #include <math.h>
 
@@ -603,7 +608,9 @@ __global__ void __launch_bounds__(kWarps * 32, N * VEC <= 12 ? 4 : 1)
   }
 }
 
-// CTAs of the first pass: four on each of a GB300's 152 SMs.
+// CTAs of the first pass: four on each of a GB300's 152 SMs (32768 tokens of 256 experts, both
+// passes: 17.3 us, with two on each 19.5).  Part of the order of the sums, so the same on every
+// device.
 constexpr int kChunkCtas = 608;
 constexpr int kFinCtas = 304;
 
@@ -680,8 +687,8 @@ cudaError_t launch_balance_loss(const moe_problem_t& p, int n_seq, float coeff, 
   // other, while that costs less than a second launch (26 tokens of 370 experts 6.1 us against 6.2,
   // 64 of 128 8.4 against 5.8; 13 tokens in 18 sequences 6.5 against 12.9).
   const int groups = kSmallThreads / ((p.E + 31) / 32 * 32);
-  if (p.T <= kSmallTokens && p.T <= 32 + 8 * (n_seq - 1) && n_seq <= kSmallSeqs && (int64_t)p.T * p.E <= 16384 &&
-      (int64_t)n_seq * p.E <= 32768 && (n_seq + groups - 1) / groups <= 16) {
+  if (p.T <= kSmallTokens && p.T <= 32 + 8 * (n_seq - 1) && n_seq <= kSmallSeqs &&
+      (int64_t)p.T * p.E <= 16384 && (int64_t)n_seq * p.E <= 32768 && (n_seq + groups - 1) / groups <= 16) {
 #define SMALL_(V, N)                                                                          \
   launch_k(balance_small_kernel<V, N>, dim3(1), dim3(kSmallThreads), 0, s, false, p.T, p.E,   \
            p.top_k, n_seq, p.scoring, coeff, x, ids, off, loss, counts, live, prob_sum, coef, \
