@@ -9,7 +9,7 @@
 // What bounds it, and what it measured on a GB300 (bf16; a copy runs at 6.8 TB/s, a
 // large library product at 1951 TFLOP/s in a burst and 1718 sustained):
 //   one row: the weights' bytes; 7168 x 7168 in 18.6 us, 0.81 of the copy rate
-//   16 and 64 rows: the same, and the start and join of a launch; 20.4 and 24.2 us
+//   16 and 64 rows: the same, and the start and join of a launch; 20.0 and 22.2 us
 //   4096 x 7168 x 18432 with the residual: the MMAs; 560-590 us, 0.94-0.99 of the burst rate
 //   4096 x 7168 x 2048: the MMAs and the epilogue of the last wave; 87 us, 0.71
 //   4096 x 256 x 7168 to f32: the tiles' loads from L2 and the join; 22 us, 0.45
@@ -949,10 +949,14 @@ cudaError_t launch_mma(const LinArgs& p, int dtype, const void* x, const void* w
                        cudaStream_t s) {
   const int64_t tiles = ceil_div(p.N, kSlab) * ceil_div(p.T, BN);
   const int num_kb = (p.K + kBlockK - 1) / kBlockK;
-  // Split K while two CTAs per SM take the parts and each keeps at least seven 64-k blocks.
+  // Split K while the SMs take the parts, two each (one of 64-row tiles), and each part keeps at
+  // least seven 64-k blocks.  16 x 7168 x 7168: 20.0 us in the five parts of this rule, 20.4 in two,
+  // 21.1 in four, 23.5 in eight.  64 rows: 22.2 in the two parts of this rule, 24.3 in one or five.
+  // 33 x 4096 x 2048: 7.2 in its four, 8.3 in one, 7.0 in three, 8.5 in eight.  Against two per SM
+  // 64-row tiles lose most at 826 x 494 x 1808, 10.9 to 10.6.
+  const int64_t room = (int64_t)num_sms() * (BN == 64 ? 1 : 2);
   int split = 1;
-  while (split < 8 && tiles * (split + 1) <= (int64_t)num_sms() * 2 && num_kb >= (split + 1) * 7)
-    ++split;
+  while (split < 8 && tiles * (split + 1) <= room && num_kb >= (split + 1) * 7) ++split;
   // Alone on its SM a CTA takes all the shared memory for stages.
   int stages = Shape<BN>::kStages;
   if (tiles * split <= num_sms()) stages = (kSmemLimit - 1024) / Shape<BN>::kStageBytes;
