@@ -13,9 +13,9 @@
 //                 per-channel vectors lie in shared memory once per CTA.
 //
 // The bytes of the rows bound both directions; measured on a GB300 (copy 6.8 TB/s), bf16, gate per
-// channel: forward 4096 x 7168 in 39 us (0.88 of the copy rate; 4096 x 4096 0.97), one row 3.0 us.
-// Backward 4096 x 7168 in 79 us (0.66): shared memory bandwidth and the reductions of one row after
-// another, one row at a time per thread group.
+// channel: forward 4096 x 7168 in 39.5-42 us (0.83-0.88 of the copy rate; 4096 x 4096 0.97), one row
+// 3.0-3.9 us.  Backward 4096 x 7168 in 80 us (0.65): its warps, 22% of what an SM holds, wait most
+// for shared memory (short scoreboard), with no pipe above 53%.
 #include <mutex>
 
 #include "vec16.cuh"

@@ -10,7 +10,8 @@
 // large library product at 1951 TFLOP/s in a burst and 1718 sustained):
 //   one row: the weights' bytes; 7168 x 7168 in 18.6 us, 0.81 of the copy rate
 //   16 and 64 rows: the same, and the start and join of a launch; 20.0 and 22.2 us
-//   4096 x 7168 x 18432 with the residual: the MMAs; 560-590 us, 0.94-0.99 of the burst rate
+//   4096 x 7168 x 18432 with the residual: the MMAs (tensor pipe 90% active); 556-590 us, 0.94-1.00 of the burst
+//     rate
 //   4096 x 7168 x 2048: the MMAs and the epilogue of the last wave; 87 us, 0.71
 //   4096 x 256 x 7168 to f32: the tiles' loads from L2 and the join; 22 us, 0.45
 #include <cuda.h>
@@ -1014,8 +1015,9 @@ template <typename T>
 cudaError_t launch_typed(const LinArgs& p, int dtype, const void* x, const void* w,
                          cudaStream_t s) {
   // Two to four rows cost the CUDA cores two to four times the arithmetic of one, which hides behind
-  // the weights' bytes no more: 7168 x 7168 took 18.5, 22.6, 27.8 and 38.7 us against 19.6 on the
-  // tensor cores, 256 x 7168 took 2.6 to 3.5 against 5.9, and 2048 x 2048 crosses at four rows.
+  // the weights' bytes no more: 7168 x 7168 took 18.4, 22.6, 27.9 and 38.8 us against 19.5 on the
+  // tensor cores, 256 x 7168 with two to four rows 3.1 to 3.8 against 5.8, and 2048 x 2048 crosses at
+  // four rows.
   if (p.T == 1 || (p.T <= kGemvRows && (int64_t)p.T * p.N * p.K <= 1 << 24))
     return launch_gemv<T>(p, x, w, s);
   if (p.T <= 16) return launch_mma<T, 16>(p, dtype, x, w, s);
