@@ -10,8 +10,8 @@
 // large library product at 1951 TFLOP/s in a burst and 1718 sustained):
 //   one row: the weights' bytes; 7168 x 7168 in 18.6 us, 0.81 of the copy rate
 //   16 and 64 rows: the same, and the start and join of a launch; 20.0 and 22.2 us
-//   4096 x 7168 x 18432 with the residual: the MMAs (tensor pipe 90% active); 556-590 us, 0.94-1.00 of the burst
-//     rate
+//   4096 x 7168 x 18432 with the residual: the MMAs (tensor pipe 90% active); 556-590 us, 0.94-1.00
+//     of the burst rate
 //   4096 x 7168 x 2048: the MMAs and the epilogue of the last wave; 87 us, 0.71
 //   4096 x 256 x 7168 to f32: the tiles' loads from L2 and the join; 22 us, 0.45
 #include <cuda.h>
@@ -945,19 +945,30 @@ cudaError_t launch_tiles(const LinArgs& p, int dtype, const void* x, const void*
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Split K while the SMs take the parts, two each (one of 64-row tiles), and each part keeps at
+// least seven 64-k blocks.  16 x 7168 x 7168: 20.0 us in the five parts of this rule, 20.4 in two,
+// 21.1 in four, 23.5 in eight.  64 rows: 22.2 in the two parts of this rule, 24.3 in one or five.
+// 33 x 4096 x 2048: 7.2 in its four, 8.3 in one, 7.0 in three, 8.5 in eight.  Against two per SM
+// 64-row tiles lose most at 826 x 494 x 1808, 10.9 to 10.6.  f32 results take the second part per SM
+// there too while an accumulator would meet more than kDrainKb blocks.
+template <int BN>
+int mma_split(const LinArgs& p) {
+  const int64_t tiles = ceil_div(p.N, kSlab) * ceil_div(p.T, BN), num_kb = ceil_div(p.K, kBlockK);
+  const int64_t sms = num_sms();
+  int split = 1;
+  while (split < 8 && num_kb >= (split + 1) * 7) {
+    const bool long_sums = p.out_f32 && num_kb > (int64_t)kAccs * split * kDrainKb;
+    if (tiles * (split + 1) > (BN != 64 || long_sums ? 2 * sms : sms)) break;
+    ++split;
+  }
+  return split;
+}
+
 template <typename T, int BN>
 cudaError_t launch_mma(const LinArgs& p, int dtype, const void* x, const void* w,
                        cudaStream_t s) {
   const int64_t tiles = ceil_div(p.N, kSlab) * ceil_div(p.T, BN);
-  const int num_kb = (p.K + kBlockK - 1) / kBlockK;
-  // Split K while the SMs take the parts, two each (one of 64-row tiles), and each part keeps at
-  // least seven 64-k blocks.  16 x 7168 x 7168: 20.0 us in the five parts of this rule, 20.4 in two,
-  // 21.1 in four, 23.5 in eight.  64 rows: 22.2 in the two parts of this rule, 24.3 in one or five.
-  // 33 x 4096 x 2048: 7.2 in its four, 8.3 in one, 7.0 in three, 8.5 in eight.  Against two per SM
-  // 64-row tiles lose most at 826 x 494 x 1808, 10.9 to 10.6.
-  const int64_t room = (int64_t)num_sms() * (BN == 64 ? 1 : 2);
-  int split = 1;
-  while (split < 8 && tiles * (split + 1) <= room && num_kb >= (split + 1) * 7) ++split;
+  const int split = mma_split<BN>(p);
   // Alone on its SM a CTA takes all the shared memory for stages.
   int stages = Shape<BN>::kStages;
   if (tiles * split <= num_sms()) stages = (kSmemLimit - 1024) / Shape<BN>::kStageBytes;
@@ -1023,7 +1034,15 @@ cudaError_t launch_typed(const LinArgs& p, int dtype, const void* x, const void*
   if (p.T <= 16) return launch_mma<T, 16>(p, dtype, x, w, s);
   if (p.T <= 32) return launch_mma<T, 32>(p, dtype, x, w, s);
   const int64_t kbs = ceil_div(p.K, kBlockK);
-  if (p.T <= 64 || ceil_div(p.N, kSlab) * ceil_div(p.T, 64) * kbs <= kSmallTiles)
+  // Up to kSlab columns a pair's second CTA has no column of its own: 4096 x 128 x 2048 took 11.1 us
+  // on pairs and 8.3 here, 32768 x 128 x 1024 36.4 and 21.8, 8192 x 32 x 4096 20.1 and 17.0.  (Three
+  // slabs lose a quarter of a pair, and less than pairs gain: 8192 x 384 x 7168 41.5 and 72.6.)
+  // f32 results take this way only while an accumulator meets no more blocks than one of a pair
+  // does: past that 2048 x 128 x 18432 was off by 1.1e-6 (norms) here and 4.8e-7 on pairs.
+  const bool narrow_out =
+      p.N <= kSlab && (!p.out_f32 || kbs <= (int64_t)kAccs * mma_split<64>(p) * kDrainKb);
+  if (p.T <= 64 || narrow_out ||
+      ceil_div(p.N, kSlab) * ceil_div(p.T, 64) * kbs <= kSmallTiles)
     return launch_mma<T, 64>(p, dtype, x, w, s);
   if (p.out_f32) return launch_pair<T, 128, true>(p, dtype, x, w, s);
   // The time of the busiest SM, in thirds of a pass over K with a 128-column tile: those run one

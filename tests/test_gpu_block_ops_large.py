@@ -26,7 +26,22 @@ LINEAR = [
 ]
 
 
-@pytest.mark.parametrize("T,N,K,dtype,act,bias,res,f32", LINEAR)
+# few output columns (at most one 128-row slab of weights) and many rows, on both sides of the edge
+NARROW = [
+    (4096, 128, 2048, BF, "none", True, False, True),
+    (4097, 100, 7168, HF, "gelu_tanh", True, True, False),
+    (2048, 127, 18432, BF, "none", False, False, True),
+    (9001, 64, 1032, BF, "silu", True, True, False),
+    (20000, 1, 2048, HF, "none", True, False, True),
+    (16384, 128, 7168, BF, "none", True, True, True),
+    (2500, 129, 7168, BF, "relu2", True, True, False),
+    (4096, 128, 7168, BF, "none", True, False, True),     # f32: two tiles on an SM, K in four parts
+    (64, 7168, 7168, BF, "none", False, True, True),
+    (40, 9728, 7168, HF, "none", False, False, True),
+]
+
+
+@pytest.mark.parametrize("T,N,K,dtype,act,bias,res,f32", LINEAR + NARROW)
 def test_linear(T, N, K, dtype, act, bias, res, f32, cuda_device):
     odt = torch.float32 if f32 else dtype
     x = rand(T, K, seed=1, dtype=dtype)
@@ -49,6 +64,23 @@ def test_linear(T, N, K, dtype, act, bias, res, f32, cuda_device):
         err = err + 2 * R.F32 * (a.abs() + r.double().abs())
     over = (out.double() - a).abs() - err - R.half_step(a, odt) * (1 + 2.0 ** -7)
     assert float(over.max()) <= 0, float(over.max())
+
+
+# The f32 sums' error in norms: an accumulator meets at most eight 64-k blocks, 32 additions, and
+# each may truncate by a step (2^-23) of a partial sum that in norms is at most the result.  The
+# truncations of one accumulator go one way, so they add: 32 * 2^-23, and half of it on average
+# (a truncation loses half a step).  The sums of accumulators and parts add a few roundings.
+@pytest.mark.parametrize("T,N,K", [(4096, 128, 2048), (4096, 128, 7168), (2048, 128, 18432),
+                                   (64, 7168, 7168), (300, 128, 32768), (96, 300, 18432)])
+def test_linear_f32_sums_stay_short(T, N, K, cuda_device):
+    x, w = rand(T, K, seed=5, dtype=BF), rand(N, K, seed=6, std=K ** -0.5, dtype=BF)
+    guard = 1 << 12
+    buf = torch.full((T * N + 2 * guard,), -77.0, device=cuda_device)
+    out = buf[guard:guard + T * N].view(T, N)
+    B.moe_linear(x, w, out_dtype=torch.float32, out=out)
+    z = x.double() @ w.double().T
+    assert float((out.double() - z).norm() / z.norm()) <= 16 * 2.0 ** -23
+    assert bool((buf[:guard] == -77).all()) and bool((buf[guard + T * N:] == -77).all())
 
 
 # T, H, dtype, gate, post, pre, a, o, residual
