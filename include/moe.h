@@ -580,9 +580,11 @@ moe_status_t moe_block_norm_bwd(const moe_block_norm_t* p, const void* d_stream,
  *   non-decreasing in [0, T] (NULL: one sequence of all T tokens, n_seq = 1); n_seq <= 2^20;
  *   loss [1] f32, counts [n_seq, E] int32, live_tokens [n_seq] int32 (T_s), prob_sum and coef
  *   [n_seq, E] f32: all out, written in full.  Sums are f32 in a fixed order.
- *   workspace  moe_balance_loss_workspace_size(p, n_seq) bytes.  An id outside [-1, E) counts as
- *              -1 and sets MOE_ERR_BAD_EXPERT_ID in its status word; offsets that decrease or
- *              leave [0, T] set MOE_ERR_INVALID_ARG there (the outputs are then not valid).
+ *   workspace  moe_balance_loss_workspace_size(p, n_seq) bytes, of which only the status word has
+ *              to be 0 before the first use (moe_workspace_init); other entry points may have used
+ *              it.  An id outside [-1, E) counts as -1 and sets MOE_ERR_BAD_EXPERT_ID in the status
+ *              word; offsets that decrease or leave [0, T] set MOE_ERR_INVALID_ARG there (the
+ *              outputs are then not valid).
  */
 size_t moe_balance_loss_workspace_size(const moe_problem_t* p, int32_t n_seq);
 moe_status_t moe_balance_loss_fwd(const moe_problem_t* p, int32_t n_seq, float coeff,

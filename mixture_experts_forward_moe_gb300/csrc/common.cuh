@@ -25,9 +25,11 @@ constexpr int kTileRowsNvfp4Min = 32;  // NVFP4 gate/up tiles at the smallest de
 constexpr int kSlab = 128;
 constexpr int kBlockK = 64;
 
-// Workspace header: status word at offset 0, tile counter at offset 64.
+// Workspace header: status word at offset 0; the lengths of a call's two tile lists at offsets 64
+// and 128, which the call writes and leaves there.
 constexpr size_t kHeaderBytes = 256;
-constexpr size_t kTicketOffset = 128;  // balance loss: CTAs done (zero between calls)
+constexpr size_t kTilesOffset = 64;
+constexpr size_t kTiles2Offset = 128;
 
 // Experts whose weights this GPU holds (an expert-parallel shard, or all E), and the problem
 // as the post-routing stages see it: ids are local indices in [0, local_experts) or -1.

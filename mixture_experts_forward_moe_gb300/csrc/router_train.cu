@@ -210,12 +210,14 @@ template <int VEC, int N>
 __global__ void __launch_bounds__(kWarps * 32)
     balance_chunk_kernel(int T, int E, int K, int n_seq, int scoring, int chunk,
                          const float* __restrict__ x, const int32_t* __restrict__ ids,
-                         const int32_t* __restrict__ off, const Records rec, int* status) {
+                         const int32_t* __restrict__ off, const Records rec, int* ticket,
+                         int* status) {
   extern __shared__ uint8_t dyn[];
   const int pitch = (E + 3) & ~3;
   float* s_prob = reinterpret_cast<float*>(dyn);                   // [kWarps][pitch]
   int* s_count = reinterpret_cast<int*>(s_prob + kWarps * pitch);  // [E]
   __shared__ int s_live;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;  // the second pass' count of its CTAs
   pdl_trigger();  // the second pass waits for this grid before it reads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = blockIdx.x * chunk;
@@ -274,8 +276,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 // ---- balance loss, second pass ---------------------------------------------------------------
 // A unit is 32 experts of a sequence.  A CTA takes `per_cta` units, each by 32 / per_cta warps (a
 // power of two; by one warp, in turns, past 32): warp r of R adds the chunks r, r + R, ..., and the
-// warps' sums are added in order.  The CTA that finishes last adds the CTAs' parts of the loss,
-// again in a fixed order.
+// warps' sums are added in order.  The CTA that finishes last, by `ticket` (0 at the start of the
+// launch), adds the CTAs' parts of the loss, again in a fixed order.
 constexpr int kFinWarps = 32;
 
 __global__ void __launch_bounds__(kFinWarps * 32)
@@ -383,10 +385,7 @@ __global__ void __launch_bounds__(kFinWarps * 32)
     float l = 0.0f;
     for (int i = lane; i < (int)gridDim.x; i += 32) l += __ldcg(part + i);
     l = warp_sum(l);
-    if (lane == 0) {
-      *loss = l;
-      *ticket = 0;
-    }
+    if (lane == 0) *loss = l;
   }
 }
 
@@ -614,10 +613,11 @@ __global__ void __launch_bounds__(kWarps * 32, N * VEC <= 12 ? 4 : 1)
 constexpr int kChunkCtas = 608;
 constexpr int kFinCtas = 304;
 
-// Workspace of the balance loss past its header: the records and the parts of the loss.
+// Workspace of the balance loss past its header (whose words other calls own): the records, the
+// parts of the loss and the ticket, all of them written by the call that reads them.
 struct BalanceLayout {
   int chunk, n_chunks, per_cta, fin_ctas;
-  size_t prob, count, live, part, total;
+  size_t prob, count, live, part, ticket, total;
 };
 BalanceLayout balance_layout(int T, int E, int n_seq) {
   BalanceLayout L;
@@ -642,6 +642,7 @@ BalanceLayout balance_layout(int T, int E, int n_seq) {
   L.count = take(n_rec * E * sizeof(int32_t));
   L.live = take(n_rec * sizeof(int32_t));
   L.part = take((size_t)L.fin_ctas * sizeof(float));
+  L.ticket = take(sizeof(int));
   L.total = o;
   return L;
 }
@@ -682,7 +683,7 @@ cudaError_t launch_balance_loss(const moe_problem_t& p, int n_seq, float coeff, 
   rec.count = reinterpret_cast<int32_t*>(ws + L.count);
   rec.live = reinterpret_cast<int32_t*>(ws + L.live);
   int* status = reinterpret_cast<int*>(ws);
-  int* ticket = reinterpret_cast<int*>(ws + kTicketOffset);
+  int* ticket = reinterpret_cast<int*>(ws + L.ticket);
   // Few tokens: one launch of one CTA, whose second step takes a sequence's tokens one after the
   // other, while that costs less than a second launch (26 tokens of 370 experts 6.1 us against 6.2,
   // 64 of 128 8.4 against 5.8; 13 tokens in 18 sequences 6.5 against 12.9).
@@ -700,9 +701,12 @@ cudaError_t launch_balance_loss(const moe_problem_t& p, int n_seq, float coeff, 
     const size_t smem = (size_t)(kWarps + 1) * (p.E + 3) * 4;
 #define CHUNK_(V, N)                                                                             \
   launch_k(balance_chunk_kernel<V, N>, dim3(L.n_chunks), dim3(kWarps * 32), smem, s, false, p.T, \
-           p.E, p.top_k, n_seq, p.scoring, L.chunk, x, ids, off, rec, status)
+           p.E, p.top_k, n_seq, p.scoring, L.chunk, x, ids, off, rec, ticket, status)
     const cudaError_t e = ROUTER_ROW(p.E, CHUNK_);
 #undef CHUNK_
+    if (e != cudaSuccess) return e;
+  } else {  // no first pass
+    const cudaError_t e = cudaMemsetAsync(ticket, 0, sizeof(int), s);
     if (e != cudaSuccess) return e;
   }
   return launch_k(balance_final_kernel, dim3(L.fin_ctas), dim3(kFinWarps * 32), 0, s,

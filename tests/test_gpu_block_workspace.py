@@ -1,0 +1,80 @@
+"""Workspaces of the operators around the routed experts: one that other calls have used, one of
+uninitialised memory, and the scratch that calls without a workspace share."""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+import block_reference as R
+from helpers import run_fused
+from mixture_experts_forward_moe_gb300 import binding as B
+from mixture_experts_forward_moe_gb300 import inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def router_case(T, E, k, lens, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, E, generator=g)
+    ids = x.topk(k, dim=1).indices.to(torch.int32)
+    ids[torch.rand(T, generator=g) < 0.05] = -1
+    off = None if lens is None else torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    return x.cuda(), ids.cuda(), None if off is None else off.cuda()
+
+
+def balance_bytes(T, E, k, n_seq):
+    p = B.make_problem(T, 8, E, 8, k)
+    return int(B.lib().moe_balance_loss_workspace_size(ctypes.byref(p), n_seq))
+
+
+def assert_balance(got, x, ids, off, scoring):
+    T = x.shape[0]
+    loss, counts, live, sums, coef = R.balance64(x.cpu().double(), ids.cpu(), 0.25, scoring, off)
+    assert torch.equal(got["counts"].cpu(), counts)
+    assert torch.equal(got["live_tokens"].cpu(), live)
+    rel = (64 + T) * R.F32  # 64 roundings of a probability, and the sum over tokens
+    R.assert_within(got["prob_sum"], sums, rel * sums + 1e-37, "prob_sum")
+    R.assert_within(got["coef"], coef, 16 * R.F32 * coef, "coef")
+    R.assert_within(got["loss"], loss.view(1), (rel + 32 * R.F32) * loss.view(1), "loss")
+
+
+# T, E, k, lengths, scoring: the loss is joined by several CTAs
+SHARED = [
+    (1024, 256, 8, None, "softmax"),
+    (1500, 256, 8, [37] * 40 + [20], "sigmoid"),
+    (0, 256, 8, [0] * 700, "softmax"),
+]
+
+
+@pytest.mark.parametrize("T,E,k,lens,scoring", SHARED)
+def test_balance_loss_on_the_workspace_of_the_fused_forward(T, E, k, lens, scoring, cuda_device):
+    w = inputs.Workload("shared-workspace", T=512, H=256, E=64, F=128, top_k=4)
+    d = inputs.generate(w, seed=1, device=cuda_device)
+    prob = B.make_problem(w.T, w.H, w.E, w.F, w.top_k)
+    n_seq = 1 if lens is None else len(lens)
+    ws = B.new_workspace(max(B.workspace_size(prob), balance_bytes(T, E, k, n_seq)))
+    x, ids, off = router_case(T, E, k, lens, seed=2)
+    want = None
+    for _ in range(2):
+        out = run_fused(w, d, workspace=ws)
+        want = out.clone() if want is None else want
+        assert torch.equal(out, want)
+        # what an output that is not written would show
+        poison = torch.full((3 * n_seq * E + n_seq + 64,), float("nan"), device=cuda_device)
+        del poison
+        got = B.moe_balance_loss(x, ids, 0.25, scoring, seq_offsets=off, workspace=ws)
+        assert B.get_device_status(ws) == B.MOE_OK
+        assert_balance(got, x, ids, off, scoring)
+
+
+@pytest.mark.parametrize("T,E,k,lens,scoring", SHARED)
+def test_balance_loss_needs_no_more_than_a_clear_status_word(T, E, k, lens, scoring, cuda_device):
+    n_seq = 1 if lens is None else len(lens)
+    ws = torch.full((balance_bytes(T, E, k, n_seq),), 0x5b, dtype=torch.uint8, device=cuda_device)
+    ws[:4] = 0
+    x, ids, off = router_case(T, E, k, lens, seed=3)
+    for _ in range(2):
+        got = B.moe_balance_loss(x, ids, 0.25, scoring, seq_offsets=off, workspace=ws)
+        assert B.get_device_status(ws) == B.MOE_OK
+        assert_balance(got, x, ids, off, scoring)
