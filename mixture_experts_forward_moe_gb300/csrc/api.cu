@@ -237,8 +237,8 @@ P* at(void* ws, size_t off) {
 }
 
 int* status_word(void* ws) { return static_cast<int*>(ws); }
-int* tile_counter(void* ws) { return at<int>(ws, kTilesOffset); }
-int* tile_counter2(void* ws) { return at<int>(ws, kTiles2Offset); }
+int* tile_counter(void* ws) { return at<int>(ws, 64); }
+int* tile_counter2(void* ws) { return at<int>(ws, 128); }
 
 moe_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 

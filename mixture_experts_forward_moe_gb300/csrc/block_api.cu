@@ -3,7 +3,7 @@
 // moe_balance_loss_fwd and moe_router_bwd.
 #include <math.h>
 
-#include "common.cuh"
+#include "block_ops.cuh"
 
 using namespace gb300moe;
 

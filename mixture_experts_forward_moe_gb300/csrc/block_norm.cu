@@ -18,6 +18,7 @@
 // for shared memory (short scoreboard), with no pipe above 53%.
 #include <mutex>
 
+#include "block_ops.cuh"
 #include "vec16.cuh"
 #include "ptx.cuh"
 

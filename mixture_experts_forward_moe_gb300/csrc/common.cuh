@@ -26,10 +26,8 @@ constexpr int kSlab = 128;
 constexpr int kBlockK = 64;
 
 // Workspace header: status word at offset 0; the lengths of a call's two tile lists at offsets 64
-// and 128, which the call writes and leaves there.
+// and 128 (api.cu), which the call writes and leaves there.
 constexpr size_t kHeaderBytes = 256;
-constexpr size_t kTilesOffset = 64;
-constexpr size_t kTiles2Offset = 128;
 
 // Experts whose weights this GPU holds (an expert-parallel shard, or all E), and the problem
 // as the post-routing stages see it: ids are local indices in [0, local_experts) or -1.
@@ -254,27 +252,6 @@ cudaError_t launch_gemm(const GemmCall& c, cudaStream_t s, bool pdl);
 // this device.
 cudaError_t launch_gemm_pair(const GemmCall& c, cudaStream_t s, bool pdl);
 bool pair_gemm_available(int dtype);
-
-// Around the routed experts (linear.cu, block_norm.cu, router_train.cu; checked arguments).
-cudaError_t launch_linear(const moe_linear_t& g, const void* x, const void* w, const void* bias,
-                          const void* residual, void* out, int* status, cudaStream_t s);
-int block_norm_bwd_ctas(int T);
-cudaError_t launch_block_norm_fwd(const moe_block_norm_t& b, const void* branch,
-                                  const void* residual, const void* gate, const void* wq,
-                                  const void* wp, void* r, void* h, cudaStream_t s);
-cudaError_t launch_block_norm_bwd(const moe_block_norm_t& b, const void* dr, const void* dh,
-                                  const void* branch, const void* residual, const void* gate,
-                                  const void* wq, const void* wp, void* dy, void* dx, void* dg,
-                                  void* dwq, void* dwp, float* part, cudaStream_t s);
-size_t balance_workspace_bytes(int T, int E, int n_seq);
-cudaError_t launch_balance_loss(const moe_problem_t& p, int n_seq, float coeff, const float* x,
-                                const int32_t* ids, const int32_t* off, float* loss,
-                                int32_t* counts, int32_t* live, float* prob_sum, float* coef,
-                                void* workspace, cudaStream_t s);
-cudaError_t launch_router_bwd(const moe_problem_t& p, int n_seq, const float* x,
-                              const int32_t* ids, const float* dw, const float* coef,
-                              const int32_t* off, const float* d_loss, float* out,
-                              cudaStream_t s);
 
 uint64_t wait_limit_ns();
 int num_sms();

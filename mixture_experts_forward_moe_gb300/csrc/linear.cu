@@ -19,6 +19,7 @@
 
 #include <mutex>
 
+#include "block_ops.cuh"
 #include "vec16.cuh"
 #include "ptx.cuh"
 

@@ -11,6 +11,7 @@
 #include <limits.h>
 #include <math.h>
 
+#include "block_ops.cuh"
 #include "vec16.cuh"
 #include "ptx.cuh"
 
