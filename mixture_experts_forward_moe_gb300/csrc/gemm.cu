@@ -332,6 +332,12 @@ __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity) 
   }
 }
 
+// The copies of the last `stages` of `issued` stages land.
+static __device__ __noinline__ void land_copies(uint64_t* bars, int stages, int issued) {
+  for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+    mbar_wait_drain(&bars[i % stages], (uint32_t)((i / stages) & 1));
+}
+
 // kBal: the units are spread evenly over balanced_ctas(units, gridDim.x) CTAs (decode-sized
 // launches); otherwise every CTA takes units c, c + gridDim.x, ...  kRouted: the NVFP4 gate/up
 // kernel for token rows, whose roles may take their units from the router's ids (the 16-bit
@@ -363,6 +369,7 @@ __global__ void __launch_bounds__(Cfg<kGemm1, kN, kW4, k2Cta>::kThreads,
   __shared__ int s_n_units;
   __shared__ int s_ks;          // work items per unit (2: split-K)
   __shared__ int s_split_last;  // epilogue: this half finished the unit second
+  __shared__ int s_issued[2];   // stages that the producers asked for (weights apart: NVFP4)
   __shared__ uint32_t s_emask[(kGemm1 && (!kW4 || kRouted)) ? 32 : 1];  // routed experts
   __shared__ int ent_col[kGemm1 ? kN : 1];
   __shared__ int ent_dst[kN];
@@ -524,7 +531,8 @@ __global__ void __launch_bounds__(Cfg<kGemm1, kN, kW4, k2Cta>::kThreads,
           }
         }
       }
-      if (*abort_flag) {
+      s_issued[1] = issued;
+      if (*abort_flag) {  // asked again at the end; without this look the NVFP4 kernels took 1% longer
         const int n = issued < C::kNW ? issued : C::kNW;
         for (int i = issued - n; i < issued; ++i)
           mbar_wait_drain(&wfull_bar[i % C::kNW], (uint32_t)((i / C::kNW) & 1));
@@ -568,6 +576,7 @@ __global__ void __launch_bounds__(Cfg<kGemm1, kN, kW4, k2Cta>::kThreads,
           }
         }
       }
+      s_issued[0] = issued;
       if (*abort_flag) {
         const int n = issued < C::kNT ? issued : C::kNT;
         for (int i = issued - n; i < issued; ++i)
@@ -731,12 +740,7 @@ __global__ void __launch_bounds__(Cfg<kGemm1, kN, kW4, k2Cta>::kThreads,
           }
         }
       }
-      if (*abort_flag) {
-        // Let every copy still in flight land before the CTA goes away.
-        const int n = issued < C::kStages ? issued : C::kStages;
-        for (int i = issued - n; i < issued; ++i)
-          mbar_wait_drain(&full_bar[i % C::kStages], (uint32_t)((i / C::kStages) & 1));
-      }
+      s_issued[0] = issued;
     }
   } else if (warp == 1 || (C::kDual && warp == C::kMma2Warp)) {
     // ------------------------------------------------------------------ MMA issuer(s)
@@ -1083,6 +1087,12 @@ __global__ void __launch_bounds__(Cfg<kGemm1, kN, kW4, k2Cta>::kThreads,
 
   tc_fence_before();
   __syncthreads();
+  // Behind the last wait of every role (one may give up after a producer's last copy): let the
+  // copies still in flight land before the CTA goes away.
+  if (threadIdx.x == 0 && *abort_flag) {
+    land_copies(full_bar, C::kFullBars, s_issued[0]);
+    if constexpr (kW4) land_copies(wfull_bar, C::kNW, s_issued[1]);
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(F8Cfg<k2Cta>::kThreads, F8Cfg<k2Cta>::kMinBloc
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
   __shared__ int s_n_units;
+  __shared__ int s_issued;  // stages that the producer asked for
   __shared__ int s_tfirst[kF8FusedGroups + 1], s_row0[kF8FusedGroups], s_cnt[kF8FusedGroups];
   __shared__ __align__(16) float s_sa[2][2][kTileRows];  // column scales of a stage's k blocks
 
@@ -289,11 +290,7 @@ __global__ void __launch_bounds__(F8Cfg<k2Cta>::kThreads, F8Cfg<k2Cta>::kMinBloc
             }
           }
         }
-        if (*abort_flag) {
-          const int n = issued < p.stages ? issued : p.stages;
-          for (int i = issued - n; i < issued; ++i)
-            f8_wait_drain(&full_bar[i % p.stages], (uint32_t)((i / p.stages) & 1));
-        }
+        s_issued = issued;
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------------ MMA issuer
@@ -463,6 +460,11 @@ __global__ void __launch_bounds__(F8Cfg<k2Cta>::kThreads, F8Cfg<k2Cta>::kMinBloc
 
   tc_fence_before();
   __syncthreads();
+  // Behind the last wait of every role (one may give up after the producer's last copy): let the
+  // copies still in flight land before the CTA goes away.
+  if (threadIdx.x == 0 && *abort_flag)
+    for (int i = s_issued > p.stages ? s_issued - p.stages : 0; i < s_issued; ++i)
+      f8_wait_drain(&full_bar[i % p.stages], (uint32_t)((i / p.stages) & 1));
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

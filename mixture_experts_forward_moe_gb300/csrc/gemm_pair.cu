@@ -115,6 +115,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
   __shared__ int s_n_units;
+  __shared__ int s_issued;  // stages that the producer asked for
   __shared__ int ent_dst[kPN];
   __shared__ float col_scale[kPN];
 
@@ -232,15 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
           }
         }
       }
-      if (*abort_flag) {
-        // Let this CTA's copies in flight land before it goes away (the even CTA's full phase
-        // also waits for the odd CTA's forward, hence one total budget).
-        const uint64_t t0 = global_timer_ns();
-        const int n = issued < kPStages ? issued : kPStages;
-        for (int i = issued - n; i < issued; ++i)
-          while (!mbar_try_wait(&full_bar[i % kPStages], (uint32_t)((i / kPStages) & 1)))
-            if (global_timer_ns() - t0 > kPDrainNs) break;
-      }
+      s_issued = issued;
     }
   } else if (warp == 1 && !leader) {
     // ---------------------------------------------------------------- forwarder (odd CTA)
@@ -383,6 +376,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   __syncwarp();
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still touch its shared memory
+  // Behind the last wait of every role (one may give up after the producer's last copy): let this
+  // CTA's copies in flight land before it goes away (the even CTA's full phase also waits for the
+  // odd CTA's forward, hence one total budget).
+  if (threadIdx.x == 0 && *abort_flag) {
+    const uint64_t t0 = global_timer_ns();
+    for (int i = s_issued > kPStages ? s_issued - kPStages : 0; i < s_issued; ++i)
+      while (!mbar_try_wait(&full_bar[i % kPStages], (uint32_t)((i / kPStages) & 1)))
+        if (global_timer_ns() - t0 > kPDrainNs) break;
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kPTmemCols);
