@@ -455,9 +455,14 @@ __global__ void __launch_bounds__(kGemvWarps * 32)
 // gave up still meets the barriers and waits, bounded, for its copies and MMAs in flight.
 // The tensor cores add to an accumulator with truncation, so its error grows with the number of
 // additions: the 64-k blocks go round kAccs accumulators, which the epilogue adds.
+// kLong: f32 results of so many blocks that an accumulator would meet more than kDrainKb of them.
+// It meets kDrainKb in a row, and the epilogue warps add it to sums in registers while the next ones
+// fill.  128 x 128 x 32768: 16.5 us and an error of 4.8e-7 in norms; without it 15.1 us and 1.0e-6; on
+// SM pairs, which do the same, 29.7 us.  16 x 19584 x 7168: 49.1 us and 4.8e-7, without 49.2 and 1.8e-6.
 constexpr int kMmaThreads = 192;
 constexpr int kAccs = 4;
 constexpr int kMaxStages = 12;
+constexpr int kDrainKb = 8;
 
 template <int BN>
 struct Shape {
@@ -472,7 +477,7 @@ struct Shape {
   static_assert(BN * kSlab * 4 <= kStages * kStageBytes, "the accumulators of a join");
 };
 
-template <typename T, int BN>
+template <typename T, int BN, bool kLong>
 __global__ void __launch_bounds__(kMmaThreads)
     mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                const LinArgs p, int split, int stages) {
@@ -481,6 +486,8 @@ __global__ void __launch_bounds__(kMmaThreads)
   __shared__ __align__(8) uint64_t full_bar[kMaxStages];
   __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
   __shared__ __align__(8) uint64_t done_bar;
+  __shared__ __align__(8) uint64_t tfull_bar[kAccs];   // kLong: an accumulator is to be added,
+  __shared__ __align__(8) uint64_t tempty_bar[kAccs];  // and was
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   // the same offset in every CTA of the cluster: the join reads the peers' tiles there
@@ -511,6 +518,11 @@ __global__ void __launch_bounds__(kMmaThreads)
         mbar_init(&empty_bar[s], 1);
       }
       mbar_init(&done_bar, 1);
+      if constexpr (kLong)
+        for (int a = 0; a < kAccs; ++a) {
+          mbar_init(&tfull_bar[a], 1);
+          mbar_init(&tempty_bar[a], 4);  // an arrival per epilogue warp
+        }
       s_abort = 0;
       fence_mbar_init();
     }
@@ -544,21 +556,58 @@ __global__ void __launch_bounds__(kMmaThreads)
       const uint32_t base = smem_u32(smem);
       const uint32_t idesc = idesc_f16_m128(BN, DT<T>::kIsBF16);
       for (int kb = kb0; kb < kb1; ++kb) {
+        const int i = kb - kb0;
+        const int pass = i / kDrainKb, acc = kLong ? pass % kAccs : i % kAccs;
+        const bool fresh = kLong ? i % kDrainKb == 0 : i < kAccs;  // the accumulator starts over
+        if (kLong && fresh && pass >= kAccs &&
+            !wait_bar(&tempty_bar[acc], (uint32_t)((pass / kAccs - 1) & 1), abort_flag, p.limit_ns,
+                      p.status))
+          break;
         if (!r.ready && !wait_bar(r.bar(), r.parity, abort_flag, p.limit_ns, p.status)) break;
         tc_fence_after();
         const uint32_t sa = base + (uint32_t)(r.stage * S::kStageBytes);
         const uint32_t sb = sa + (uint32_t)S::kABytes;
-        const uint32_t d = tmem + (uint32_t)((kb - kb0) % kAccs * BN);
+        const uint32_t d = tmem + (uint32_t)(acc * BN);
         uint64_t* empty = &empty_bar[r.stage];
         r.next();
 #pragma unroll
         for (int k = 0; k < kBlockK / 16; ++k)
           umma_f16(d, sw128_kmajor_desc(sa + k * 32), sw128_kmajor_desc(sb + k * 32), idesc,
-                   (kb - kb0 >= kAccs || k > 0) ? 1u : 0u);
+                   (!fresh || k > 0) ? 1u : 0u);
         umma_commit(empty);
+        if (kLong && (i % kDrainKb == kDrainKb - 1 || kb + 1 == kb1)) umma_commit(&tfull_bar[acc]);
       }
       // done_bar flips when every MMA issued has completed
       umma_commit(&done_bar);
+    }
+  } else if constexpr (kLong) {
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    float sum[BN] = {};
+    bool ok = true;
+    for (int pass = 0; kb0 + pass * kDrainKb < kb1 && ok; ++pass) {
+      const int acc = pass % kAccs;
+      ok = __all_sync(kAll, wait_bar(&tfull_bar[acc], (uint32_t)((pass / kAccs) & 1), abort_flag,
+                                     p.limit_ns, p.status));
+      tc_fence_after();
+      if (!ok) break;
+#pragma unroll
+      for (int c0 = 0; c0 < BN; c0 += 16) {
+        float v[16];
+        tmem_ld_x16(tb + (uint32_t)(acc * BN + c0), v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[c0 + j] += v[j];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty_bar[acc]);
+    }
+    // the last pass' MMAs have completed, so nothing reads the stages any more
+    float* stash = reinterpret_cast<float*>(smem);
+    if (ok) {
+#pragma unroll
+      for (int c = 0; c < BN; ++c)
+        if (c < cols) stash[c * kSlab + row] = sum[c];
     }
   } else {
     const bool ok =
@@ -616,7 +665,6 @@ __global__ void __launch_bounds__(kMmaThreads)
 // kF32: f32 results.  Every kDrainKb blocks the MMAs move on to the other of two accumulators
 // and the epilogue warps add the finished one to sums in registers, rounded to nearest (the
 // tensor cores truncate; a chain over all of K would cost several bits).
-constexpr int kDrainKb = 8;
 constexpr int kJoinCols = 128;  // columns whose sums are in shared memory at a time (64 KB)
 
 // TMEM address of the lanes that an epilogue warp may read.
@@ -958,19 +1006,23 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // least seven 64-k blocks.  16 x 7168 x 7168: 20.0 us in the five parts of this rule, 20.4 in two,
 // 21.1 in four, 23.5 in eight.  64 rows: 22.2 in the two parts of this rule, 24.3 in one or five.
 // 33 x 4096 x 2048: 7.2 in its four, 8.3 in one, 7.0 in three, 8.5 in eight.  Against two per SM
-// 64-row tiles lose most at 826 x 494 x 1808, 10.9 to 10.6.  f32 results take the second part per SM
-// there too while an accumulator would meet more than kDrainKb blocks.
+// 64-row tiles lose most at 826 x 494 x 1808, 10.9 to 10.6.
 template <int BN>
 int mma_split(const LinArgs& p) {
   const int64_t tiles = ceil_div(p.N, kSlab) * ceil_div(p.T, BN), num_kb = ceil_div(p.K, kBlockK);
   const int64_t sms = num_sms();
   int split = 1;
-  while (split < 8 && num_kb >= (split + 1) * 7) {
-    const bool long_sums = p.out_f32 && num_kb > (int64_t)kAccs * split * kDrainKb;
-    if (tiles * (split + 1) > (BN != 64 || long_sums ? 2 * sms : sms)) break;
+  while (split < 8 && num_kb >= (split + 1) * 7 &&
+         tiles * (split + 1) <= (BN == 64 ? sms : 2 * sms))
     ++split;
-  }
   return split;
+}
+
+// f32 results of which an accumulator of a one-CTA tile would meet more than kDrainKb blocks: past
+// that 2048 x 128 x 18432 was off by 1.1e-6 (norms), and by 4.8e-7 within.
+template <int BN>
+bool long_sums(const LinArgs& p) {
+  return p.out_f32 && ceil_div(p.K, kBlockK) > (int64_t)kAccs * mma_split<BN>(p) * kDrainKb;
 }
 
 template <typename T, int BN>
@@ -982,9 +1034,11 @@ cudaError_t launch_mma(const LinArgs& p, int dtype, const void* x, const void* w
   int stages = Shape<BN>::kStages;
   if (tiles * split <= num_sms()) stages = (kSmemLimit - 1024) / Shape<BN>::kStageBytes;
   if (stages > kMaxStages) stages = kMaxStages;
-  return launch_tiles<mma_kernel<T, BN>>(p, dtype, x, w, BN,
-                                         stages * Shape<BN>::kStageBytes + 1024, tiles * split,
-                                         split, s, split, stages);
+  const int smem = stages * Shape<BN>::kStageBytes + 1024;
+  return long_sums<BN>(p) ? launch_tiles<mma_kernel<T, BN, true>>(
+                                p, dtype, x, w, BN, smem, tiles * split, split, s, split, stages)
+                          : launch_tiles<mma_kernel<T, BN, false>>(
+                                p, dtype, x, w, BN, smem, tiles * split, split, s, split, stages);
 }
 
 template <typename T, int BN, bool kF32>
@@ -1046,10 +1100,8 @@ cudaError_t launch_typed(const LinArgs& p, int dtype, const void* x, const void*
   // Up to kSlab columns a pair's second CTA has no column of its own: 4096 x 128 x 2048 took 11.1 us
   // on pairs and 8.3 here, 32768 x 128 x 1024 36.4 and 21.8, 8192 x 32 x 4096 20.1 and 17.0.  (Three
   // slabs lose a quarter of a pair, and less than pairs gain: 8192 x 384 x 7168 41.5 and 72.6.)
-  // f32 results take this way only while an accumulator meets no more blocks than one of a pair
-  // does: past that 2048 x 128 x 18432 was off by 1.1e-6 (norms) here and 4.8e-7 on pairs.
-  const bool narrow_out =
-      p.N <= kSlab && (!p.out_f32 || kbs <= (int64_t)kAccs * mma_split<64>(p) * kDrainKb);
+  // f32 results of long sums stay on pairs there.
+  const bool narrow_out = p.N <= kSlab && !long_sums<64>(p);
   if (p.T <= 64 || narrow_out ||
       ceil_div(p.N, kSlab) * ceil_div(p.T, 64) * kbs <= kSmallTiles)
     return launch_mma<T, 64>(p, dtype, x, w, s);
