@@ -530,7 +530,8 @@ typedef struct {
  *   stream = a * residual + gate * u
  *   normed = stream * rr * (o + pre_weight),  rr = 1/sqrt(mean(stream^2) + eps)   (pre_norm)
  * in f32 (normed comes from the stream before its rounding), each output rounded once.
- *   branch [T, H]; residual [T, H] or NULL (0); gate as p->gate says (NULL iff MOE_GATE_NONE);
+ *   branch [T, H]; residual [T, H] or NULL (0); gate as p->gate says (NULL with MOE_GATE_NONE, and
+ *   where it has no elements);
  *   post_weight, pre_weight [H] or NULL (the factor o + weight is then 1);
  *   stream_out [T, H] or NULL; normed_out [T, H] iff pre_norm.
  *   stream_out may be the residual or the branch itself; outputs overlap nothing else.

@@ -46,7 +46,9 @@ moe_status_t check_norm(const moe_block_norm_t* p) {
 moe_status_t check_norm_inputs(const moe_block_norm_t& p, const void* branch,
                                const void* residual, const void* gate, const void* wq,
                                const void* wp) {
-  if ((p.gate != MOE_GATE_NONE) != (gate != nullptr)) return MOE_ERR_INVALID_ARG;
+  // a gate per token or element of no rows has no elements, and may have no address
+  const bool empty = p.T == 0 && (p.gate == MOE_GATE_TOKEN || p.gate == MOE_GATE_ELEMENT);
+  if (p.gate == MOE_GATE_NONE ? gate != nullptr : !gate && !empty) return MOE_ERR_INVALID_ARG;
   if (p.T > 0 && !branch) return MOE_ERR_INVALID_ARG;
   if ((wq && !p.post_norm) || (wp && !p.pre_norm)) return MOE_ERR_INVALID_ARG;
   if (!aligned(branch, residual, gate, wq, wp)) return MOE_ERR_INVALID_ARG;
