@@ -57,8 +57,8 @@ def forward(p, w_gate):
     act = B.moe_gemm1_swiglu(h, s["sorted_ids"], s["offsets"], p["w_gate_up"], p["k"])
     rows = B.moe_gemm2(act, s["sorted_ids"], s["offsets"], w, p["w_down"], T, p["k"])
     y = B.moe_combine(rows, s["inv_route"], T, p["k"])
-    norm = dict(branch=y, residual=p["x"], gate=p["scale"], post_weight=p["post"],
-                pre_weight=p["nxt"])
+    norm = dict(branch=y, residual=p["x"], gate=p["scale"], gate_kind="channel",
+                post_weight=p["post"], pre_weight=p["nxt"])
     _, normed = B.moe_block_norm(**norm, want_stream=False)
     balance = B.moe_balance_loss(logits, ids, COEFF, seq_offsets=p["offsets"])
     return dict(h=h, logits=logits, ids=ids, w=w, rows=rows, inv=s["inv_route"], y=y, norm=norm,

@@ -28,6 +28,8 @@ _SCORING = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}
 _ACTIVATIONS = {"silu": 0, "gelu_tanh": 1, "relu2": 2}
 # moe_linear_act_t.
 _LINEAR_ACTS = {"none": 0, "silu": 1, "gelu_tanh": 2, "relu2": 3}
+# moe_gate_t; None: by the gate's shape.
+_GATE_KINDS = {None: -1, "channel": 1, "token": 2, "element": 3}
 
 
 def gate_up_rows(activation: str, F: int) -> int:
@@ -876,29 +878,39 @@ def moe_linear(x, w, bias=None, activation="none", residual=None, out_dtype=None
     return _call("linear", stream, (x, w, bias, act, residual, f32, out, workspace))
 
 
+def _gate_kind(kind):
+    if kind not in _GATE_KINDS:
+        raise ValueError(f"unsupported gate_kind {kind}")
+    return _GATE_KINDS[kind]
+
+
 def moe_block_norm(branch, residual=None, gate=None, post_weight=None, pre_weight=None,
                    post_norm=True, pre_norm=True, residual_scale=1.0, weight_offset=0.0, eps=1e-6,
-                   stream_out=None, want_stream=True, stream=None):
+                   stream_out=None, want_stream=True, stream=None, gate_kind=None):
     """What stands between two blocks (include/moe.h: moe_block_norm_fwd): the norm of `branch`
     (post_norm), times `gate` ([H] per channel, [T] or [T, 1] per token, [T, H]), plus
     residual_scale * residual, and the norm of that for the next block (pre_norm).  Returns
     (stream, normed), None for what is not computed (want_stream, pre_norm).  `stream_out` may be
-    the residual or the branch."""
+    the residual or the branch.  ``gate_kind``: "channel", "token" or "element"; without it the
+    gate's shape tells, and a gate of one dimension is refused where T equals H."""
     return _call("block_norm", stream,
                  (branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
-                  residual_scale, weight_offset, eps, stream_out, want_stream))
+                  residual_scale, weight_offset, eps, _gate_kind(gate_kind), stream_out,
+                  want_stream))
 
 
 def moe_block_norm_bwd(d_stream, d_normed, branch, residual=None, gate=None, post_weight=None,
                        pre_weight=None, post_norm=True, pre_norm=True, residual_scale=1.0,
-                       weight_offset=0.0, eps=1e-6, workspace=None, stream=None):
+                       weight_offset=0.0, eps=1e-6, workspace=None, stream=None,
+                       gate_kind=None):
     """The gradients of moe_block_norm (include/moe.h: moe_block_norm_bwd) for the same inputs and
     options; d_stream may be None, d_normed is None without pre_norm.  Returns a dict of d_branch
     and, where there is such an input, d_residual, d_gate, d_post_weight and d_pre_weight; those
     per channel share one allocation."""
     return _call("block_norm_bwd", stream,
                  (branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
-                  residual_scale, weight_offset, eps, d_stream, d_normed, workspace))
+                  residual_scale, weight_offset, eps, _gate_kind(gate_kind), d_stream, d_normed,
+                  workspace))
 
 
 def moe_balance_loss(gating_output, topk_ids, coeff, scoring_func="softmax", seq_offsets=None,

@@ -203,7 +203,7 @@ PyObject* call_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // The options and inputs of the norm: branch, residual, gate, post_weight, pre_weight, post, pre,
-// residual_scale, weight_offset, eps.
+// residual_scale, weight_offset, eps, gate kind (moe_gate_t, or -1: by the gate's shape).
 struct Norm {
   at::Tensor y, x, g, wq, wp;
   moe_block_norm_t p;
@@ -227,35 +227,42 @@ struct Norm {
     need_if(x, "residual", dt, {p.T, p.H}, y);
     need_if(wq, "post_weight", dt, {p.H}, y);
     need_if(wp, "pre_weight", dt, {p.H}, y);
-    p.gate = MOE_GATE_NONE;
-    if (g.defined()) {
-      // a gate of T = H values is per channel; [T, 1] is always per token
-      if (g.dim() == 1 && g.size(0) == p.H) {
-        p.gate = MOE_GATE_CHANNEL;
+    p.gate = as_int(a[10]);
+    if (!g.defined()) {
+      if (p.gate >= 0) refuse("gate_kind is given without a gate");
+      p.gate = MOE_GATE_NONE;
+    } else {
+      if (p.gate < 0) p.gate = by_shape();
+      if (p.gate == MOE_GATE_CHANNEL)
         need_if(g, "gate", dt, {p.H}, y);
-      } else if (g.dim() == 1 || (g.dim() == 2 && g.size(1) == 1 && p.H != 1)) {
-        p.gate = MOE_GATE_TOKEN;
-        if (g.dim() == 1)
-          need_if(g, "gate", dt, {p.T}, y);
-        else
-          need_if(g, "gate", dt, {p.T, 1}, y);
-      } else {
-        p.gate = MOE_GATE_ELEMENT;
+      else if (p.gate == MOE_GATE_ELEMENT)
         need_if(g, "gate", dt, {p.T, p.H}, y);
-      }
+      else if (g.dim() == 1)
+        need_if(g, "gate", dt, {p.T}, y);
+      else
+        need_if(g, "gate", dt, {p.T, 1}, y);
     }
+  }
+
+ private:
+  // One dimension: its length tells, unless there are as many rows as channels.
+  int by_shape() const {
+    if (g.dim() == 1 && g.size(0) == p.H && p.T == p.H)
+      refuse("a gate of T = H values may be one per channel or per token: give gate_kind");
+    if (g.dim() == 1) return g.size(0) == p.H ? MOE_GATE_CHANNEL : MOE_GATE_TOKEN;
+    return g.dim() == 2 && g.size(1) == 1 ? MOE_GATE_TOKEN : MOE_GATE_ELEMENT;
   }
 };
 
 // block_norm(<Norm>, stream_out, want_stream) -> (stream, normed)
 PyObject* call_block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CALL_BEGIN
-  arguments(n, 12);
+  arguments(n, 13);
   const Norm m(a);
-  at::Tensor r = optional(a[10], "stream_out"), h;
+  at::Tensor r = optional(a[11], "stream_out"), h;
   need_if(r, "stream_out", m.y.scalar_type(), m.y.sizes(), m.y);
   c10::cuda::CUDAGuard guard(m.y.device());
-  if (!r.defined() && as_bool(a[11])) r = fresh(m.y);
+  if (!r.defined() && as_bool(a[12])) r = fresh(m.y);
   if (m.p.pre_norm) h = fresh(m.y);
   if (failed(moe_block_norm_fwd(&m.p, ptr(m.y), ptr(m.x), ptr(m.g), ptr(m.wq), ptr(m.wp), ptr(r),
                                 ptr(h), stream_of(m.y).stream()),
@@ -280,15 +287,15 @@ bool put(PyObject* dict, const char* key, const at::Tensor& t) {
 // block_norm_bwd(<Norm>, d_stream, d_normed, workspace) -> dict
 PyObject* call_block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CALL_BEGIN
-  arguments(n, 13);
+  arguments(n, 14);
   const Norm m(a);
-  const at::Tensor dr = optional(a[10], "d_stream"), dh = optional(a[11], "d_normed");
+  const at::Tensor dr = optional(a[11], "d_stream"), dh = optional(a[12], "d_normed");
   if (dh.defined() != (m.p.pre_norm != 0)) refuse("d_normed goes with pre_norm");
   need_if(dr, "d_stream", m.y.scalar_type(), m.y.sizes(), m.y);
   need_if(dh, "d_normed", m.y.scalar_type(), m.y.sizes(), m.y);
   c10::cuda::CUDAGuard guard(m.y.device());
   const auto s = stream_of(m.y);
-  const at::Tensor ws = workspace(a[12], (int64_t)moe_block_norm_bwd_workspace_size(&m.p), s);
+  const at::Tensor ws = workspace(a[13], (int64_t)moe_block_norm_bwd_workspace_size(&m.p), s);
   auto like = [](const at::Tensor& t) { return t.defined() ? fresh(t) : at::Tensor(); };
   const at::Tensor dy = like(m.y), dx = like(m.x);
   at::Tensor dg, dq, dp;  // the per-channel ones lie in one allocation
