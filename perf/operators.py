@@ -307,6 +307,10 @@ def _library(s):
     from mixture_experts_forward_moe_gb300 import binding as B
 
     op = s["op"]
+    # a gate's length does not tell its kind in a batch of as many rows as channels
+    kind = {}
+    if op in ("norm", "norm_bwd") and s["g"] is not None and s["T"] == s["H"]:
+        kind["gate_kind"] = s["gate"]
     if op == "linear":
         return B.moe_linear(s["x"], s["w"], bias=s["b"], activation=s["act"], residual=s["res"],
                             out_dtype=torch.float32 if s["out_f32"] else None)
@@ -314,13 +318,13 @@ def _library(s):
         stream, normed = B.moe_block_norm(
             s["y"], s["x"], gate=s["g"], post_weight=s["wq"], pre_weight=s["wp"],
             post_norm=s["post"], pre_norm=s["pre"], residual_scale=s["scale"],
-            weight_offset=s["offset"], eps=_EPS)
+            weight_offset=s["offset"], eps=_EPS, **kind)
         return dict(stream=stream, normed=normed)
     if op == "norm_bwd":
         return B.moe_block_norm_bwd(
             s["dr"], s["dh"], s["y"], s["x"], gate=s["g"], post_weight=s["wq"],
             pre_weight=s["wp"], post_norm=s["post"], pre_norm=s["pre"],
-            residual_scale=s["scale"], weight_offset=s["offset"], eps=_EPS)
+            residual_scale=s["scale"], weight_offset=s["offset"], eps=_EPS, **kind)
     if op == "balance":
         return B.moe_balance_loss(s["logits"], s["ids"], s["coeff"], scoring_func=s["scoring"],
                                   seq_offsets=s["offsets"])
