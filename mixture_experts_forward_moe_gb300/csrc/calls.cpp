@@ -128,16 +128,17 @@ at::Tensor zeros(int64_t bytes, c10::Device dev) {
   return at::zeros({bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
 }
 
-// Scratch of the current stream: one per stream and host thread, since calls on other streams may
-// run at the same time, and never freed while a call may still use it (a larger one replaces it;
-// torch's allocator reuses the memory in the stream's order).  A captured call gets its own,
-// which lives in the graph's memory.
+// Scratch of the current stream: one per stream, since calls on other streams may run at the same
+// time, and never freed while a call may still use it (a larger one replaces it; torch's allocator
+// reuses the memory in the stream's order).  Host threads share it: a call holds the interpreter's
+// lock from here to its last launch, so the launches of two calls do not mix.  A captured call gets
+// its own, which lives in the graph's memory.
 at::Tensor scratch(int64_t bytes, const c10::cuda::CUDAStream& s) {
   if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
     return zeros(bytes, s.device());
   using Key = std::pair<int, int64_t>;
-  // leaked on purpose: a destructor at the thread's or the process' end may find no CUDA context
-  static thread_local auto* cache = new std::map<Key, at::Tensor>();
+  // leaked on purpose: a destructor at the process' end may find no CUDA context
+  static auto* cache = new std::map<Key, at::Tensor>();
   at::Tensor& t = (*cache)[Key(s.device_index(), (int64_t)(intptr_t)s.stream())];
   if (!t.defined() || t.numel() < bytes) t = zeros(bytes, s.device());
   return t;

@@ -78,3 +78,33 @@ def test_balance_loss_needs_no_more_than_a_clear_status_word(T, E, k, lens, scor
         got = B.moe_balance_loss(x, ids, 0.25, scoring, seq_offsets=off, workspace=ws)
         assert B.get_device_status(ws) == B.MOE_OK
         assert_balance(got, x, ids, off, scoring)
+
+
+def test_threads_share_the_scratch_of_a_stream(cuda_device):
+    x = torch.randn(64, 512, device=cuda_device).to(torch.bfloat16)
+    y = torch.randn(200, 2048, device=cuda_device).to(torch.bfloat16)
+    g = torch.randn_like(y)
+    want = B.moe_linear(x, x)
+    B.moe_block_norm_bwd(g, g, y)
+    where = B.call_workspace().data_ptr()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    seen, failures = [], []
+
+    def work():
+        try:
+            out = B.moe_linear(x, x)
+            B.moe_block_norm_bwd(g, g, y)
+            seen.append(B.call_workspace().data_ptr())
+            assert torch.equal(out, want)
+        except BaseException as e:  # reported by the test's own thread
+            failures.append(e)
+
+    for _ in range(4):
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not failures
+    assert seen == [where] * 4
+    assert torch.cuda.memory_allocated() == before
