@@ -12,6 +12,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <map>
 #include <string>
 #include <utility>
@@ -128,9 +129,11 @@ at::Tensor zeros(int64_t bytes, c10::Device dev) {
   return at::zeros({bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
 }
 
+constexpr int64_t kHeader = 256;  // of every workspace: the status word first
+
 // Scratch of the current stream: one per stream, since calls on other streams may run at the same
-// time, and never freed while a call may still use it (a larger one replaces it; torch's allocator
-// reuses the memory in the stream's order).  Host threads share it: a call holds the interpreter's
+// time, and never freed while a call may still use it (a larger one replaces it, with what was
+// reported so far; torch's allocator reuses the memory in the stream's order).  Host threads share it: a call holds the interpreter's
 // lock from here to its last launch, so the launches of two calls do not mix.  A captured call gets
 // its own, which lives in the graph's memory.
 at::Tensor scratch(int64_t bytes, const c10::cuda::CUDAStream& s) {
@@ -140,7 +143,11 @@ at::Tensor scratch(int64_t bytes, const c10::cuda::CUDAStream& s) {
   // leaked on purpose: a destructor at the process' end may find no CUDA context
   static auto* cache = new std::map<Key, at::Tensor>();
   at::Tensor& t = (*cache)[Key(s.device_index(), (int64_t)(intptr_t)s.stream())];
-  if (!t.defined() || t.numel() < bytes) t = zeros(bytes, s.device());
+  if (!t.defined() || t.numel() < bytes) {
+    at::Tensor larger = zeros(std::max(bytes, kHeader), s.device());
+    if (t.defined()) larger.narrow(0, 0, kHeader).copy_(t.narrow(0, 0, kHeader));
+    t = std::move(larger);
+  }
   return t;
 }
 // The caller's workspace, or scratch of at least `bytes` bytes.

@@ -108,3 +108,15 @@ def test_threads_share_the_scratch_of_a_stream(cuda_device):
     assert not failures
     assert seen == [where] * 4
     assert torch.cuda.memory_allocated() == before
+
+
+def test_a_larger_scratch_keeps_what_was_reported(cuda_device):
+    x, ids, _ = router_case(70, 32, 4, None, seed=4)
+    ids[5, 1] = 32
+    B.moe_balance_loss(x, ids, 1.0)
+    held = B.call_workspace()
+    # a call that needs twice the scratch
+    grown = B._call("scratch", None, (2 * held.numel(), torch.cuda.current_device()))
+    assert grown.numel() >= 2 * held.numel()
+    assert B.get_device_status(B.call_workspace()) == B.MOE_ERR_BAD_EXPERT_ID
+    assert B.get_device_status(B.call_workspace()) == B.MOE_OK
