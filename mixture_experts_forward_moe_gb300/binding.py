@@ -858,7 +858,8 @@ def _call(name, stream, args):
 
 def call_workspace(device=None, stream=None) -> torch.Tensor:
     """The scratch that the calls below use on `stream` when no workspace is given (its status
-    word: get_device_status)."""
+    word: get_device_status).  A call captured into a graph has one of its own: give it a
+    workspace to read its status."""
     index = None if device is None else torch.device(device).index
     return _call("scratch", stream,
                  (256, torch.cuda.current_device() if index is None else index))

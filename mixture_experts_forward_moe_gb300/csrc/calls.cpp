@@ -156,6 +156,7 @@ at::Tensor workspace(PyObject* o, int64_t bytes, const c10::cuda::CUDAStream& s)
   const at::Tensor& t = tensor(o, "workspace");
   if (!t.is_cuda() || t.scalar_type() != at::kByte || !t.is_contiguous())
     refuse("workspace must be a contiguous uint8 CUDA tensor");
+  if (t.device() != s.device()) refuse("workspace is on another device");
   return t;
 }
 

@@ -120,3 +120,13 @@ def test_a_larger_scratch_keeps_what_was_reported(cuda_device):
     assert grown.numel() >= 2 * held.numel()
     assert B.get_device_status(B.call_workspace()) == B.MOE_ERR_BAD_EXPERT_ID
     assert B.get_device_status(B.call_workspace()) == B.MOE_OK
+
+
+def test_a_workspace_on_another_device_is_refused(cuda_device):
+    x = torch.randn(8, 64, device=cuda_device).to(torch.bfloat16)
+    # none but the first GPU is used here: a host buffer stands for one elsewhere
+    with pytest.raises(ValueError, match="workspace"):
+        B.moe_linear(x, x, workspace=torch.zeros(256, dtype=torch.uint8))
+    if torch.cuda.device_count() > 1:
+        with pytest.raises(ValueError, match="workspace is on another device"):
+            B.moe_linear(x, x, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda:1"))
