@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                          const float* __restrict__ x, const int32_t* __restrict__ ids,
                          const int32_t* __restrict__ off, const Records rec, int* ticket,
                          int* status) {
-  extern __shared__ uint8_t dyn[];
+  extern __shared__ __align__(16) uint8_t dyn[];
   const int pitch = (E + 3) & ~3;
   float* s_prob = reinterpret_cast<float*>(dyn);                   // [kWarps][pitch]
   int* s_count = reinterpret_cast<int*>(s_prob + kWarps * pitch);  // [E]
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kWarps * 32, N * VEC <= 12 ? 4 : 1)
                       const float* __restrict__ dw, const float* __restrict__ coef,
                       const int32_t* __restrict__ off, const float* __restrict__ d_loss,
                       float* out) {
-  extern __shared__ uint8_t dyn[];
+  extern __shared__ __align__(16) uint8_t dyn[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int pitch = (E + 3) & ~3;
   float* s_row = reinterpret_cast<float*>(dyn) + warp * pitch;  // this warp's q, by expert
