@@ -302,9 +302,9 @@ __global__ void __launch_bounds__(kWide ? 512 : kFwdCta, 1)
                (size_t)me.g * 2 * kTensors * p.n_vec;
   const Channels<T, kWide> chan(p, dyn);
   __syncthreads();
-  const int step = gridDim.x * shape.groups;
-  auto fetch = [&](int t, int half) {
-    if (t < p.T) {
+  const unsigned step = gridDim.x * shape.groups, T_all = p.T;  // t + step may pass 2^31
+  auto fetch = [&](unsigned t, int half) {
+    if (t < T_all) {
       const size_t row = (size_t)t * p.n_vec;
       uint4* b = buf + half * kTensors * p.n_vec;
 #pragma unroll
@@ -320,10 +320,10 @@ __global__ void __launch_bounds__(kWide ? 512 : kFwdCta, 1)
     copy_commit();
   };
   const F2 a = f2(p.a);
-  const int t0 = blockIdx.x + me.g * gridDim.x;
+  const unsigned t0 = blockIdx.x + me.g * gridDim.x;
   fetch(t0, 0);
   int half = 0;
-  for (int t = t0; t < p.T; t += step, half ^= 1) {
+  for (unsigned t = t0; t < T_all; t += step, half ^= 1) {
     fetch(t + step, half ^ 1);
     copy_wait<1>();
     const size_t row = (size_t)t * p.n_vec;
@@ -408,9 +408,9 @@ __global__ void __launch_bounds__(kBwdCta, 1)
     for (int v = threadIdx.x; v < shape.groups * kRows * kTensors * n_vec; v += blockDim.x)
       rows[v] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  const int step = gridDim.x * shape.groups;
-  auto fetch = [&](int t, int half) {
-    if (t < p.T) {
+  const unsigned step = gridDim.x * shape.groups, T_all = p.T;  // t + step may pass 2^31
+  auto fetch = [&](unsigned t, int half) {
+    if (t < T_all) {
       const size_t row = (size_t)t * n_vec;
       uint4* b = buf + half * kTensors * n_vec;
 #pragma unroll
@@ -446,18 +446,18 @@ __global__ void __launch_bounds__(kBwdCta, 1)
     }
     return f2_sum(s);
   };
-  const int t0 = blockIdx.x + me.g * gridDim.x;
+  const unsigned t0 = blockIdx.x + me.g * gridDim.x;
   float ss[2] = {0.0f, 0.0f};
   float ry = 1.0f;  // of the current row; the next one's is reduced with this row's last sum
   fetch(t0, 0);
   int half = 0;
-  if (p.post && t0 < p.T) {
+  if (p.post && t0 < T_all) {
     copy_wait<0>();
     ss[0] = square(buf);
     me.sum(ss, 1);
     ry = rsqrtf(fmaf(ss[0], p.inv_h, p.eps));
   }
-  for (int t = t0; t < p.T; t += step) {
+  for (unsigned t = t0; t < T_all; t += step) {
     if constexpr (!kWide) fetch(t + step, half ^ 1);
     copy_wait<kRows - 1>();
     const size_t row = (size_t)t * n_vec;
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kBwdCta, 1)
       }
     }
     ss[0] = ss[1] = 0.0f;
-    const bool more = !kWide && p.post && t + step < p.T;
+    const bool more = !kWide && p.post && t + step < T_all;
     if (p.post || GATE == MOE_GATE_TOKEN) {
       ss[0] = f2_sum(s);
       if (more) {
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kBwdCta, 1)
       if (more) ry = rsqrtf(fmaf(ss[1], p.inv_h, p.eps));
     } else {
       fetch(t + step, 0);
-      if (p.post && t + step < p.T) {
+      if (p.post && t + step < T_all) {
         copy_wait<0>();
         ss[0] = square(buf);
         me.sum(ss, 1);

@@ -79,6 +79,8 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   return false;
 }
 
+// T, N and K may be anything up to 2^31 - 1: no sum of one of them with a tile's size is taken in 32
+// bits.
 struct LinArgs {
   int T, N, K;
   int act, out_f32;
@@ -214,7 +216,7 @@ struct Finish {
 #pragma unroll
       for (int i = 0; i < kCols; ++i) {
         const float4* src = reinterpret_cast<const float4*>(
-            static_cast<const float*>(p.res) + (int64_t)(t + i * step < t1 ? t + i * step : t) * p.N +
+            static_cast<const float*>(p.res) + (int64_t)(i * step < t1 - t ? t + i * step : t) * p.N +
             n);
         v[i][0] = src[0];
         v[i][1] = src[1];
@@ -229,7 +231,7 @@ struct Finish {
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
         v[i] = *reinterpret_cast<const uint4*>(
-            static_cast<const T*>(p.res) + (int64_t)(t + i * step < t1 ? t + i * step : t) * p.N + n);
+            static_cast<const T*>(p.res) + (int64_t)(i * step < t1 - t ? t + i * step : t) * p.N + n);
 #pragma unroll
       for (int i = 0; i < kCols; ++i) unpack<T>(v[i], r[i]);
     }
@@ -497,10 +499,10 @@ __global__ void __launch_bounds__(kMmaThreads)
   volatile int* abort_flag = &s_abort;
   const int rank = split > 1 ? (int)cluster_ctarank() : 0;
   const int tile = blockIdx.x / split;
-  const int slabs = (p.N + kSlab - 1) / kSlab;
+  const int slabs = (p.N - 1) / kSlab + 1;
   const int n0 = (tile % slabs) * kSlab;
   const int t0 = (tile / slabs) * BN;
-  const int num_kb = (p.K + kBlockK - 1) / kBlockK;
+  const int num_kb = (p.K - 1) / kBlockK + 1;
   const int kb0 = (int)((int64_t)num_kb * rank / split);
   const int kb1 = (int)((int64_t)num_kb * (rank + 1) / split);
   const int cols = p.T - t0 < BN ? p.T - t0 : BN;  // live columns
@@ -733,10 +735,10 @@ __global__ void __launch_bounds__(kMmaThreads, PairShape<BN, kF32>::kPerSm)
   const uint32_t side = rank & 1u, even = rank & ~1u;
   const int part = (int)(rank >> 1);
   const int tile = blockIdx.x / (2 * split);
-  const int slabs = (p.N + 2 * kSlab - 1) / (2 * kSlab);
+  const int slabs = (p.N - 1) / (2 * kSlab) + 1;
   const int n0 = (tile % slabs) * 2 * kSlab + (int)side * kSlab;  // this CTA's weight rows
   const int t0 = (tile / slabs) * BN;
-  const int num_kb = (p.K + kBlockK - 1) / kBlockK;
+  const int num_kb = (p.K - 1) / kBlockK + 1;
   const int kb0 = (int)((int64_t)num_kb * part / split);
   const int kb1 = (int)((int64_t)num_kb * (part + 1) / split);
   const int cols = p.T - t0 < BN ? p.T - t0 : BN;
@@ -1045,7 +1047,7 @@ template <typename T, int BN, bool kF32>
 cudaError_t launch_pair(const LinArgs& p, int dtype, const void* x, const void* w,
                         cudaStream_t s) {
   const int64_t tiles = ceil_div(p.N, 2 * kSlab) * ceil_div(p.T, BN);
-  const int num_kb = (p.K + kBlockK - 1) / kBlockK;
+  const int num_kb = (p.K - 1) / kBlockK + 1;
   int split = 1;
   if (BN == 128)  // a part of a 256-column tile does not fit beside a second CTA
     while (split < 4 && num_kb >= (split + 1) * 7 &&
@@ -1068,7 +1070,7 @@ cudaError_t launch_gemv(const LinArgs& p, const void* x, const void* w, cudaStre
          p.K / 8 >= wpr * 2 * 32)
     wpr *= 2;
   const int rows = kGemvWarps / wpr;
-  const dim3 grid((p.N + rows - 1) / rows), block(kGemvWarps * 32);
+  const dim3 grid((p.N - 1) / rows + 1), block(kGemvWarps * 32);
   const uint4* xv = static_cast<const uint4*>(x);
   const uint4* wv = static_cast<const uint4*>(w);
   switch (p.T) {
