@@ -879,12 +879,6 @@ def moe_linear(x, w, bias=None, activation="none", residual=None, out_dtype=None
     return _call("linear", stream, (x, w, bias, act, residual, f32, out, workspace))
 
 
-def _gate_kind(kind):
-    if kind not in _GATE_KINDS:
-        raise ValueError(f"unsupported gate_kind {kind}")
-    return _GATE_KINDS[kind]
-
-
 def moe_block_norm(branch, residual=None, gate=None, post_weight=None, pre_weight=None,
                    post_norm=True, pre_norm=True, residual_scale=1.0, weight_offset=0.0, eps=1e-6,
                    stream_out=None, want_stream=True, stream=None, gate_kind=None):
@@ -894,9 +888,12 @@ def moe_block_norm(branch, residual=None, gate=None, post_weight=None, pre_weigh
     (stream, normed), None for what is not computed (want_stream, pre_norm).  `stream_out` may be
     the residual or the branch.  ``gate_kind``: "channel", "token" or "element"; without it the
     gate's shape tells, and a gate of one dimension is refused where T equals H."""
+    kind = _GATE_KINDS.get(gate_kind)
+    if kind is None:
+        raise ValueError(f"unsupported gate_kind {gate_kind}")
     return _call("block_norm", stream,
                  (branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
-                  residual_scale, weight_offset, eps, _gate_kind(gate_kind), stream_out,
+                  residual_scale, weight_offset, eps, kind, stream_out,
                   want_stream))
 
 
@@ -908,9 +905,12 @@ def moe_block_norm_bwd(d_stream, d_normed, branch, residual=None, gate=None, pos
     options; d_stream may be None, d_normed is None without pre_norm.  Returns a dict of d_branch
     and, where there is such an input, d_residual, d_gate, d_post_weight and d_pre_weight; those
     per channel share one allocation."""
+    kind = _GATE_KINDS.get(gate_kind)
+    if kind is None:
+        raise ValueError(f"unsupported gate_kind {gate_kind}")
     return _call("block_norm_bwd", stream,
                  (branch, residual, gate, post_weight, pre_weight, post_norm, pre_norm,
-                  residual_scale, weight_offset, eps, _gate_kind(gate_kind), d_stream, d_normed,
+                  residual_scale, weight_offset, eps, kind, d_stream, d_normed,
                   workspace))
 
 
