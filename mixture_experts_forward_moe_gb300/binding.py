@@ -110,7 +110,7 @@ def lib():
     global _lib
     with _lock:
         if _lib is None:
-            path = _build.build()
+            path = _build.build_library()
             L = ctypes.CDLL(path)
             P, sz, i32, i64, u64 = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32,
                                     ctypes.c_int64, ctypes.c_uint64)
@@ -836,11 +836,11 @@ _calls = None
 
 def _load_calls():
     global _calls
-    L = lib()  # builds both; the module links against the library
+    L = lib()
     with _lock:
         if _calls is None and L is not None:
             name = "gb300moe_calls"
-            spec = importlib.util.spec_from_file_location(name, _build.CALLS)
+            spec = importlib.util.spec_from_file_location(name, _build.build_calls())
             mod = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(mod)
             mod.set_error(MoeError)

@@ -1,9 +1,10 @@
 """Build libgb300moe.so in-tree with nvcc for sm_103a (no cmake, no setup.py).
 
 Each ``csrc/*.cu`` file is compiled in parallel to an object file under ``_build/`` and the
-objects are linked into ``_build/libgb300moe.so``; ``csrc/calls.cpp``, the Python module over some
-of its calls, goes to ``_build/gb300moe_calls.so``.  A rebuild happens only when a source or
-header is newer than the two.
+objects are linked into ``_build/libgb300moe.so``, which needs nvcc alone; ``csrc/calls.cpp``, the
+Python module over some of its calls, goes to ``_build/gb300moe_calls.so`` and needs a host compiler,
+Python's headers and torch's.  Each is rebuilt only when a source or header of its own is newer, the
+module also for another torch or Python.
 """
 from __future__ import annotations
 
@@ -38,16 +39,40 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+def _newer(target: str, deps) -> bool:
+    if not os.path.exists(target):
+        return False
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _headers())
+
+
+def _calls_built_for() -> str:
+    """What a build of the Python module fits: torch's C++ interface and Python's change between
+    versions."""
+    import torch
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}\n"
+
+
+def calls_up_to_date() -> bool:
+    if not _newer(CALLS, glob.glob(os.path.join(CSRC, "*.cpp")) + _headers()):
+        return False
+    try:
+        with open(CALLS + ".built_for") as f:
+            return f.read() == _calls_built_for()
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and calls_up_to_date()
 
 
 def _compile(nvcc: str, src: str) -> tuple[str, str]:
@@ -87,17 +112,14 @@ def _link_calls(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of the Python module failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
+    with open(tmp, "w") as f:
+        f.write(_calls_built_for())
+    os.replace(tmp, CALLS + ".built_for")
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source and link the shared library; return its path."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    nvcc = _nvcc()
+def _build_library(nvcc: str, verbose: bool) -> None:
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        calls = ex.submit(_compile_calls, nvcc)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         results = list(ex.map(lambda s: _compile(nvcc, s), srcs))
     if verbose:
         for _, log in results:
@@ -109,7 +131,36 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_calls(calls.result())
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile every CUDA source and link the shared library; return its path."""
+    if force or not library_up_to_date():
+        os.makedirs(BUILD, exist_ok=True)
+        _build_library(_nvcc(), verbose)
+    return LIB
+
+
+def build_calls(force: bool = False) -> str:
+    """Compile the Python module against the library (built first); return its path."""
+    build_library()
+    if force or not calls_up_to_date():
+        _link_calls(_compile_calls(_nvcc()))
+    return CALLS
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Build the library and the Python module, side by side; return the library's path.  The
+    library is in place before a module that cannot be built raises."""
+    if not force and up_to_date():
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        stale = force or not calls_up_to_date()
+        calls = ex.submit(_compile_calls, _nvcc()) if stale else None
+        build_library(force, verbose)
+    if calls:
+        _link_calls(calls.result())
     return LIB
 
 
