@@ -77,7 +77,10 @@ def gate_gradient(p, f):
     d_normed = (f["normed"].float() - p["target"].float()).to(torch.bfloat16)
     d_y = B.moe_block_norm_bwd(None, d_normed, **f["norm"])["d_branch"].float()
     T, k = f["w"].shape
-    per_route = f["rows"][f["inv"].long()].view(T, k, -1) / f["w"][:, :, None]
+    # the rows carry their route's weight; one of 0 (a far logit) leaves its logit's gradient, the
+    # weight times a difference, at 0 whatever its row is
+    w = f["w"][:, :, None]
+    per_route = f["rows"][f["inv"].long()].view(T, k, -1) / torch.where(w == 0, 1, w)
     d_w = torch.einsum("tkh,th->tk", per_route, d_y) / n
     d_logits = B.moe_router_bwd(f["logits"], f["ids"], d_w.contiguous(), f["balance"]["coef"],
                                 seq_offsets=p["offsets"])
