@@ -3,16 +3,17 @@
 //
 // One row of x (a few, when the product is small) is a stream of the weights and runs on the CUDA
 // cores (gemv_kernel).  Everything else runs on tcgen05: the weights are the MMA's M side, the rows
-// of x its N side (BN), so that few rows of x cost few columns.  Up to 64 rows a CTA has a tile of
-// 128 weight rows (mma_kernel), beyond that a pair of SMs has one of 256 (pair_kernel).
+// of x its N side (BN), so that few rows of x cost few columns.  Up to 64 rows, in small products and
+// up to 128 columns a CTA has a tile of 128 weight rows (mma_kernel), beyond that a pair of SMs has
+// one of 256 (pair_kernel).
 //
 // What bounds it, and what it measured on a GB300 (bf16; a copy runs at 6.8 TB/s, a
 // large library product at 1951 TFLOP/s in a burst and 1718 sustained):
 //   one row: the weights' bytes; 7168 x 7168 in 18.6 us, 0.81 of the copy rate
-//   16 and 64 rows: the same, and the start and join of a launch; 20.0 and 22.2 us
-//   4096 x 7168 x 18432 with the residual: the MMAs (tensor pipe 90% active); 556-590 us, 0.94-1.00
+//   16 and 64 rows: the same, and the start and join of a launch; 20.0-20.5 and 22.0-22.4 us
+//   4096 x 7168 x 18432 with the residual: the MMAs (tensor pipe 90% active); 549-590 us, 0.94-1.01
 //     of the burst rate
-//   4096 x 7168 x 2048: the MMAs and the epilogue of the last wave; 87 us, 0.71
+//   4096 x 7168 x 2048: the MMAs and the epilogue of the last wave; 82-87 us, 0.71-0.75
 //   4096 x 256 x 7168 to f32: the tiles' loads from L2 and the join; 22 us, 0.45
 #include <cuda.h>
 #include <cudaTypedefs.h>
