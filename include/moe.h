@@ -615,6 +615,117 @@ moe_status_t moe_router_bwd(const moe_problem_t* p, int32_t n_seq, const float* 
                             float* d_gating_output, void* stream);
 
 /* ---------------------------------------------------------------------------------------- */
+/* The dense feed-forward block beside the routed experts (dense layers, shared experts): its   */
+/* gated half, the gradients of both halves, 8-bit checkpoints of what the gradients need, and  */
+/* decoding with 4-bit weights.  No source page has these operators; the formulas here define   */
+/* them.  Tensors start on 16-byte boundaries (MOE_ERR_INVALID_ARG otherwise).  The same call    */
+/* gives the same bits.                                                                         */
+/* ---------------------------------------------------------------------------------------- */
+
+/*
+ * Checkpoints.  A [T, C] tensor (C a multiple of 8) is kept as
+ *   codes   [T, Cp] uint8: E4M3 values, Cp = C rounded up to 128 (zeros behind column C)
+ *   scales  [T, Cp/128] f32: one power of two per 128 channels of a row
+ * and stands for e4m3(codes[t, c]) * scales[t, c/128].  The scale is the smallest 2^e with
+ * max |finite value| <= 448 * 2^e, -118 <= e <= 120 (1 for a group of zeros); values are rounded to
+ * nearest even; infinities and NaN become NaN.  These are also the rows and scales that
+ * moe_grouped_gemm_fp8 takes as a and a_scale (C a multiple of 128).
+ *
+ * moe_checkpoint          x [T, C] dtype -> codes, scales (written in full)
+ * moe_checkpoint_restore  codes, scales -> out [T, C] dtype: exact in bf16 and, within its range,
+ *                         f16; a value rounded past dtype's largest is that one
+ */
+moe_status_t moe_checkpoint(int32_t T, int32_t C, int32_t dtype, const void* x, uint8_t* codes,
+                            float* scales, void* stream);
+moe_status_t moe_checkpoint_restore(int32_t T, int32_t C, int32_t dtype, const uint8_t* codes,
+                                    const float* scales, void* out, void* stream);
+
+typedef struct {
+  int32_t T;          /* rows of x and out; >= 0 */
+  int32_t H;          /* reduction length; a multiple of 8 (4-bit weights: of 32) */
+  int32_t F;          /* output columns; a multiple of 8 (4-bit weights: any), 2F < 2^31 */
+  int32_t dtype;      /* moe_dtype_t of the 16-bit tensors */
+  int32_t activation; /* moe_activation_t: MOE_ACT_SILU or MOE_ACT_GELU_TANH
+                         (MOE_ERR_UNSUPPORTED: MOE_ACT_RELU2 has no up projection) */
+} moe_gated_linear_t;
+
+/*
+ * moe_gated_linear -- both projections, the activation and the product of a feed-forward block:
+ *   gate = x w_gate^T,  up = x w_up^T  (f32)
+ *   out[t, f] = round( act(gate[t, f]) * up[t, f] )
+ *   x [T, H], w_gate_up [2F, H] (gate rows, then up rows), out [T, F]: dtype.
+ *   gate_codes, gate_scales, up_codes, up_scales: checkpoints of gate and up ([T, F], from their
+ *   f32 sums), all four or none.
+ *   workspace  moe_gated_linear_workspace_size(p) bytes (its status word records a wait that gave
+ *   up).  Outputs overlap no input.
+ */
+size_t moe_gated_linear_workspace_size(const moe_gated_linear_t* p);
+moe_status_t moe_gated_linear(const moe_gated_linear_t* p, const void* x, const void* w_gate_up,
+                              void* out, uint8_t* gate_codes, float* gate_scales,
+                              uint8_t* up_codes, float* up_scales, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * moe_gated_linear_bwd -- its gradients.  gate and up are computed again from x, or taken from
+ * their checkpoints (all four of gate_codes ... up_scales):
+ *   d_gate = d_out * up * act'(gate),  d_up = d_out * act(gate)   (each rounded once to dtype, as
+ *                                                                  the operands of the products)
+ *   d_x [T, H]  = d_gate w_gate + d_up w_up
+ *   d_w [2F, H] = [d_gate^T x; d_up^T x]
+ *   out [T, F]  = round( act(gate) * up ), which the next product's d_w needs
+ * with f32 accumulation and one rounding of each output.
+ *   d_out [T, F]; x [T, H], or its checkpoint (x_codes, x_scales; x NULL): needed for d_w, and
+ *   without the checkpoints of gate and up; d_x, d_w and out may each be NULL (not wanted).  With
+ *   T = 0 d_w is 0.  out may be d_out itself; outputs overlap nothing else.
+ *   workspace  moe_gated_linear_bwd_workspace_size(p) bytes.
+ */
+size_t moe_gated_linear_bwd_workspace_size(const moe_gated_linear_t* p);
+moe_status_t moe_gated_linear_bwd(const moe_gated_linear_t* p, const void* d_out, const void* x,
+                                  const uint8_t* x_codes, const float* x_scales,
+                                  const void* w_gate_up, const uint8_t* gate_codes,
+                                  const float* gate_scales, const uint8_t* up_codes,
+                                  const float* up_scales, void* d_x, void* d_w, void* out,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_linear_bwd -- the gradients of moe_linear without an activation (the residual's is d_out):
+ *   d_x [T, K] = d_out w,  d_w [N, K] = d_out^T x,  d_bias [N] = sum_t d_out[t, :]
+ * with f32 accumulation and one rounding of each.
+ *   g: activation MOE_LINEAR_NONE and out_f32 0 (MOE_ERR_UNSUPPORTED otherwise); any N, K a
+ *   multiple of 8.  d_out [T, N]; x [T, K] or its checkpoint (x_codes, x_scales; x NULL), for d_w;
+ *   w [N, K], for d_x; d_x, d_w and d_bias may each be NULL (not wanted).  With T = 0 d_w and
+ *   d_bias are 0.  Outputs overlap nothing.
+ *   workspace  moe_linear_bwd_workspace_size(g) bytes.
+ */
+size_t moe_linear_bwd_workspace_size(const moe_linear_t* g);
+moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void* x,
+                            const uint8_t* x_codes, const float* x_scales, const void* w, void* d_x,
+                            void* d_w, void* d_bias, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * moe_linear_w4a16, moe_gated_linear_w4a16 -- moe_linear and moe_gated_linear with NVFP4 weights,
+ * for the few rows of decoding (the weights are read once for up to 32 rows):
+ *   w[n, k] = e2m1(codes[n, k/2], low nibble: even k) * e4m3(scales[n, k/16]) * alpha
+ *   codes [rows, K/2] and scales [rows, K/16] uint8 as a checkpoint of the model has them (not the
+ *   tiles of moe_nvfp4_pack), rows = N, or 2F (gate rows, then up rows); alpha [1] f32, device.
+ *   K (H) a multiple of 32, T at most 2^20; 16-bit results (out_f32 0).  bias, residual and out as
+ *   for moe_linear; out may be the residual itself.
+ *   e2m1 * e4m3 is exact in f16, in which the products are taken, with f32 accumulation.  bf16 x
+ *   is converted: exact between 2^-14 and 65504 in magnitude, at most 2^-25 off below, and a larger
+ *   value sets MOE_ERR_F16_RANGE in the status word.
+ *   workspace  256 bytes: the status word.
+ */
+moe_status_t moe_linear_w4a16(const moe_linear_t* g, const void* x, const uint8_t* codes,
+                              const uint8_t* scales, const float* alpha, const void* bias,
+                              const void* residual, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream);
+moe_status_t moe_gated_linear_w4a16(const moe_gated_linear_t* p, const void* x,
+                                    const uint8_t* codes, const uint8_t* scales, const float* alpha,
+                                    void* out, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* ---------------------------------------------------------------------------------------- */
 /* Status.                                                                                    */
 /* ---------------------------------------------------------------------------------------- */
 

@@ -51,7 +51,10 @@ EXPORTED = (
     "moe_grouped_gemm_fp8", "moe_host_staging_bytes", "fused_moe_fwd_host",
     "fused_moe_fwd_w4a16_host", "moe_linear_workspace_size", "moe_linear", "moe_block_norm_fwd",
     "moe_block_norm_bwd_workspace_size", "moe_block_norm_bwd", "moe_balance_loss_workspace_size",
-    "moe_balance_loss_fwd", "moe_router_bwd",
+    "moe_balance_loss_fwd", "moe_router_bwd", "moe_checkpoint", "moe_checkpoint_restore",
+    "moe_gated_linear_workspace_size", "moe_gated_linear", "moe_gated_linear_bwd_workspace_size",
+    "moe_gated_linear_bwd", "moe_linear_bwd_workspace_size", "moe_linear_bwd", "moe_linear_w4a16",
+    "moe_gated_linear_w4a16",
 )
 
 
@@ -79,6 +82,13 @@ class Linear(ctypes.Structure):
     _fields_ = [
         ("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
         ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("out_f32", ctypes.c_int32),
+    ]
+
+
+class GatedLinear(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("F", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
     ]
 
 
@@ -177,8 +187,22 @@ def lib():
             L.moe_balance_loss_workspace_size.argtypes = [PP, i32]
             L.moe_balance_loss_fwd.argtypes = [PP, i32, ctypes.c_float] + [P] * 9 + [sz, P]
             L.moe_router_bwd.argtypes = [PP, i32] + [P] * 8
+            PG = ctypes.POINTER(GatedLinear)
+            for fn, desc in (("moe_gated_linear", PG), ("moe_gated_linear_bwd", PG),
+                             ("moe_linear_bwd", PL)):
+                size = getattr(L, fn + "_workspace_size")
+                size.restype, size.argtypes = sz, [desc]
+            L.moe_gated_linear.argtypes = [PG] + [P] * 8 + [sz, P]
+            L.moe_gated_linear_bwd.argtypes = [PG] + [P] * 13 + [sz, P]
+            L.moe_linear_bwd.argtypes = [PL] + [P] * 9 + [sz, P]
+            L.moe_checkpoint.argtypes = [i32, i32, i32, P, P, P, P]
+            L.moe_checkpoint_restore.argtypes = [i32, i32, i32, P, P, P, P]
+            L.moe_linear_w4a16.argtypes = [PL] + [P] * 8 + [sz, P]
+            L.moe_gated_linear_w4a16.argtypes = [PG] + [P] * 6 + [sz, P]
             for fn in ("moe_linear", "moe_block_norm_fwd", "moe_block_norm_bwd",
-                       "moe_balance_loss_fwd", "moe_router_bwd"):
+                       "moe_balance_loss_fwd", "moe_router_bwd", "moe_gated_linear",
+                       "moe_gated_linear_bwd", "moe_linear_bwd", "moe_checkpoint",
+                       "moe_checkpoint_restore", "moe_linear_w4a16", "moe_gated_linear_w4a16"):
                 getattr(L, fn).restype = ctypes.c_int
             for fn in ("fused_moe_fwd", "moe_route", "moe_align_sort", "moe_gemm1_swiglu",
                        "moe_gemm2", "moe_combine", "moe_shared_expert_fwd",
@@ -939,3 +963,111 @@ def moe_router_bwd(gating_output, topk_ids, d_topk_weights=None, coef=None, d_lo
     return _call("router_bwd", stream,
                  (gating_output, topk_ids, seq_offsets, scoring, renormalize,
                   routed_scaling_factor, d_topk_weights, coef, d_loss, out))
+
+
+# ------------------------------------------------------------ the dense feed-forward block
+class Fp8Checkpoint:
+    """An 8-bit checkpoint of a [T, C] tensor (include/moe.h: moe_checkpoint): `codes` uint8
+    [T, C rounded up to 128], E4M3 values; `scale` f32 [T, ceil(C / 128)], powers of two; and C.
+    codes and scale are also what moe_grouped_gemm_fp8 takes as a and a_scale."""
+
+    __slots__ = ("codes", "scale", "C")
+
+    def __init__(self, codes, scale, C):
+        self.codes, self.scale, self.C = codes, scale, C
+
+    @property
+    def shape(self):
+        return (self.codes.shape[0], self.C)
+
+
+def _gated_act(activation):
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"unsupported activation {activation}")
+    return act
+
+
+def _parts(t):
+    """(tensor, codes, scale, channels): a tensor or its checkpoint, as the calls take it."""
+    if isinstance(t, Fp8Checkpoint):
+        return None, t.codes, t.scale, t.C
+    return t, None, None, 0
+
+
+def _ckpt(t, name):
+    if not isinstance(t, Fp8Checkpoint):
+        raise TypeError(f"{name} must be an Fp8Checkpoint")
+    return t.codes, t.scale, t.C
+
+
+def moe_checkpoint(x, stream=None):
+    """The 8-bit checkpoint of x [T, C], bf16 or f16 (include/moe.h: moe_checkpoint)."""
+    codes, scale = _call("checkpoint", stream, (x,))
+    return Fp8Checkpoint(codes, scale, x.shape[1])
+
+
+def moe_checkpoint_restore(saved, dtype=torch.bfloat16, out=None, stream=None):
+    """What an Fp8Checkpoint stands for, [T, C] in `dtype` (include/moe.h: moe_checkpoint_restore)."""
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return _call("restore", stream, (*_ckpt(saved, "saved"), code, out))
+
+
+def moe_gated_linear(x, w_gate_up, activation="silu", save=False, out=None, workspace=None,
+                     stream=None):
+    """act(x w_gate^T) * (x w_up^T) (include/moe.h: moe_gated_linear).  x [T, H] and w_gate_up
+    [2F, H] (gate rows, then up rows) in bf16 or f16; ``activation``: "silu" or "gelu_tanh".  With
+    `save`, returns (out, gate, up): the pre-activations as Fp8Checkpoints, for
+    moe_gated_linear_bwd."""
+    r = _call("gated_linear", stream, (x, w_gate_up, _gated_act(activation), save, out, workspace))
+    if not save:
+        return r
+    out, gc, gs, uc, us = r
+    return out, Fp8Checkpoint(gc, gs, out.shape[1]), Fp8Checkpoint(uc, us, out.shape[1])
+
+
+def moe_gated_linear_bwd(d_out, x, w_gate_up, activation="silu", gate=None, up=None,
+                         want_x=True, want_w=True, want_out=False, workspace=None, stream=None):
+    """The gradients of moe_gated_linear (include/moe.h: moe_gated_linear_bwd).  x [T, H] or its
+    Fp8Checkpoint; with `gate` and `up`, the checkpoints that the forward saved, nothing is computed
+    again (and x may be None without want_w).  Returns a dict of d_x, d_w and, with want_out, out,
+    the forward's result, which moe_linear_bwd of the next product takes."""
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up go together")
+    saved = (None, None, 0) * 2 if gate is None else _ckpt(gate, "gate") + _ckpt(up, "up")
+    return _call("gated_linear_bwd", stream,
+                 (d_out, *_parts(x), w_gate_up, _gated_act(activation), *saved, want_x, want_w,
+                  want_out, workspace))
+
+
+def moe_linear_bwd(d_out, x, w, want_x=True, want_w=True, want_bias=False, workspace=None,
+                   stream=None):
+    """The gradients of moe_linear without an activation (include/moe.h: moe_linear_bwd): d_out
+    [T, N], x [T, K] or its Fp8Checkpoint (None without want_w), w [N, K].  Returns a dict of d_x,
+    d_w and d_bias, those that are wanted."""
+    return _call("linear_bwd", stream,
+                 (d_out, *_parts(x), w, want_x, want_w, want_bias, workspace))
+
+
+def moe_linear_w4a16(x, codes, scales, alpha, bias=None, activation="none", residual=None,
+                     out=None, workspace=None, stream=None):
+    """moe_linear with NVFP4 weights, for the few rows of decoding (include/moe.h:
+    moe_linear_w4a16).  x [T, K] in bf16 or f16; codes [N, K/2] and scales [N, K/16] uint8, alpha
+    [1] f32: as pack_nvfp4_weights takes them, one matrix, not packed.  The status word of the
+    workspace (call_workspace) tells of x past the f16 range."""
+    act = _LINEAR_ACTS.get(activation)
+    if act is None:
+        raise ValueError(f"unsupported activation {activation}")
+    return _call("linear_w4", stream, (x, codes, scales, alpha, bias, act, residual, out,
+                                       workspace))
+
+
+def moe_gated_linear_w4a16(x, codes, scales, alpha, activation="silu", out=None, workspace=None,
+                           stream=None):
+    """moe_gated_linear with NVFP4 weights, for the few rows of decoding (include/moe.h:
+    moe_gated_linear_w4a16): codes [2F, H/2] and scales [2F, H/16] uint8, gate rows then up rows,
+    alpha [1] f32."""
+    return _call("gated_linear_w4", stream, (x, codes, scales, alpha, _gated_act(activation), out,
+                                             workspace))

@@ -1,5 +1,6 @@
-// calls.cpp -- the calls around the routed experts for Python: checks of torch tensors, their
-// outputs and scratch, and the C ABI (include/moe.h) on the current stream, in one step each.
+// calls.cpp -- the calls around the routed experts and of the dense block for Python: checks of
+// torch tensors, their outputs and scratch, and the C ABI (include/moe.h) on the current stream, in
+// one step each.
 // Those calls take a few microseconds on the device, less than marshalling them through ctypes.
 #define PY_SSIZE_T_CLEAN
 #include <ATen/core/Tensor.h>
@@ -435,6 +436,294 @@ PyObject* call_router_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CALL_END
 }
 
+// An 8-bit checkpoint: codes [T, C up to 128], scales [T, groups], or none of them.
+struct Saved {
+  at::Tensor codes, scales;
+  int C = 0;
+  Saved(PyObject* c, PyObject* s, PyObject* channels, const char* name) {
+    codes = optional(c, name);
+    scales = optional(s, name);
+    C = as_int(channels);
+  }
+  Saved(const at::Tensor& like, int64_t T, int64_t channels) : C((int)channels) {
+    const int64_t groups = (channels + 127) / 128;
+    codes = fresh(like, {T, groups * 128}, at::kByte);
+    scales = fresh(like, {T, groups}, at::kFloat);
+  }
+  bool defined() const { return codes.defined(); }
+  void check(const char* name, int64_t T, int64_t channels, const at::Tensor& like) const {
+    if (!defined()) return;
+    if (C != channels)
+      refuse(std::string(name) + " must have " + std::to_string(channels) + " channels, got " +
+             std::to_string(C));
+    const int64_t groups = (channels + 127) / 128;
+    need_if(codes, (std::string(name) + " codes").c_str(), at::kByte, {T, groups * 128}, like);
+    need_if(scales, (std::string(name) + " scale").c_str(), at::kFloat, {T, groups}, like);
+  }
+  uint8_t* c() const { return static_cast<uint8_t*>(ptr(codes)); }
+  float* s() const { return static_cast<float*>(ptr(scales)); }
+};
+
+PyObject* tuple_of(std::initializer_list<at::Tensor> tensors) {
+  PyObject* out = PyTuple_New((Py_ssize_t)tensors.size());
+  if (!out) return nullptr;
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : tensors) PyTuple_SET_ITEM(out, i++, THPVariable_Wrap(t));
+  return out;
+}
+
+// checkpoint(x) -> (codes, scales)
+PyObject* call_checkpoint(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  CALL_BEGIN
+  arguments(n, 1);
+  const at::Tensor& x = tensor(a[0], "x");
+  if (x.dim() != 2) refuse("x must have two dimensions");
+  const int code = dtype_code(x), T = length(x.size(0)), C = length(x.size(1));
+  need(x, "x", x.scalar_type(), {T, C});
+  c10::cuda::CUDAGuard guard(x.device());
+  const Saved to(x, T, C);
+  if (failed(moe_checkpoint(T, C, code, ptr(x), to.c(), to.s(), stream_of(x).stream()),
+             "moe_checkpoint"))
+    return nullptr;
+  return tuple_of({to.codes, to.scales});
+  CALL_END
+}
+
+// restore(codes, scales, C, dtype, out) -> out
+PyObject* call_restore(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  CALL_BEGIN
+  arguments(n, 5);
+  const Saved from(a[0], a[1], a[2], "saved");
+  const int code = as_int(a[3]);
+  at::Tensor out = optional(a[4], "out");
+  if (!from.defined() || from.codes.dim() != 2) refuse("saved codes must have two dimensions");
+  if (!from.codes.is_cuda()) refuse("saved codes must be a CUDA tensor");
+  const int T = length(from.codes.size(0));
+  if (from.C < 1) refuse("saved must have channels");
+  from.check("saved", T, from.C, from.codes);
+  const at::ScalarType dt = code == MOE_BF16 ? at::kBFloat16 : at::kHalf;
+  need_if(out, "out", dt, {T, from.C}, from.codes);
+  c10::cuda::CUDAGuard guard(from.codes.device());
+  if (!out.defined()) out = fresh(from.codes, {T, from.C}, dt);
+  if (failed(moe_checkpoint_restore(T, from.C, code, from.c(), from.s(), ptr(out),
+                                    stream_of(from.codes).stream()),
+             "moe_checkpoint_restore"))
+    return nullptr;
+  return THPVariable_Wrap(std::move(out));
+  CALL_END
+}
+
+// The sizes of a gated product from its rows [T, columns] and [2F, H] weights.
+moe_gated_linear_t gated_sizes(const at::Tensor& rows, const char* name, const at::Tensor& w,
+                               int act) {
+  if (rows.dim() != 2 || w.dim() != 2)
+    refuse(std::string(name) + " and the weights must have two dimensions");
+  if (w.size(0) % 2 != 0) refuse("the weights must hold as many gate rows as up rows");
+  moe_gated_linear_t p;
+  p.dtype = dtype_code(rows);
+  p.T = length(rows.size(0));
+  p.F = length(w.size(0) / 2);
+  p.activation = act;
+  return p;
+}
+
+// gated_linear(x, w_gate_up, act, save, out, workspace)
+PyObject* call_gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  CALL_BEGIN
+  arguments(n, 6);
+  const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w_gate_up");
+  moe_gated_linear_t p = gated_sizes(x, "x", w, as_int(a[2]));
+  const bool save = as_bool(a[3]);
+  at::Tensor out = optional(a[4], "out");
+  const at::ScalarType dt = x.scalar_type();
+  p.H = length(x.size(1));
+  need(x, "x", dt, {p.T, p.H});
+  need_if(w, "w_gate_up", dt, {2 * (int64_t)p.F, p.H}, x);
+  need_if(out, "out", dt, {p.T, p.F}, x);
+  c10::cuda::CUDAGuard guard(x.device());
+  const auto s = stream_of(x);
+  if (!out.defined()) out = fresh(x, {p.T, p.F}, dt);
+  const at::Tensor ws = workspace(a[5], (int64_t)moe_gated_linear_workspace_size(&p), s);
+  if (!save) {
+    if (failed(moe_gated_linear(&p, ptr(x), ptr(w), ptr(out), nullptr, nullptr, nullptr, nullptr,
+                                ptr(ws), (size_t)ws.numel(), s.stream()),
+               "moe_gated_linear"))
+      return nullptr;
+    return THPVariable_Wrap(std::move(out));
+  }
+  const Saved gate(x, p.T, p.F), up(x, p.T, p.F);
+  if (p.T > 0 && failed(moe_gated_linear(&p, ptr(x), ptr(w), ptr(out), gate.c(), gate.s(), up.c(),
+                                         up.s(), ptr(ws), (size_t)ws.numel(), s.stream()),
+                        "moe_gated_linear"))
+    return nullptr;
+  return tuple_of({out, gate.codes, gate.scales, up.codes, up.scales});
+  CALL_END
+}
+
+// gated_linear_bwd(d_out, x, x codes, x scales, x channels, w_gate_up, act, gate codes, scales,
+// channels, up codes, scales, channels, want_x, want_w, want_out, workspace) -> dict
+PyObject* call_gated_linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  CALL_BEGIN
+  arguments(n, 17);
+  const at::Tensor &dy = tensor(a[0], "d_out"), &w = tensor(a[5], "w_gate_up");
+  const at::Tensor x = optional(a[1], "x");
+  const Saved x8(a[2], a[3], a[4], "x"), gate(a[7], a[8], a[9], "gate"),
+      up(a[10], a[11], a[12], "up");
+  moe_gated_linear_t p = gated_sizes(dy, "d_out", w, as_int(a[6]));
+  const bool want_x = as_bool(a[13]), want_w = as_bool(a[14]), want_out = as_bool(a[15]);
+  const at::ScalarType dt = dy.scalar_type();
+  p.H = length(w.size(1));
+  need(dy, "d_out", dt, {p.T, p.F});
+  need_if(w, "w_gate_up", dt, {2 * (int64_t)p.F, p.H}, dy);
+  need_if(x, "x", dt, {p.T, p.H}, dy);
+  x8.check("x", p.T, p.H, dy);
+  gate.check("gate", p.T, p.F, dy);
+  up.check("up", p.T, p.F, dy);
+  if ((want_w || !gate.defined()) && !x.defined() && !x8.defined())
+    refuse("x is needed for d_w, and without gate and up");
+  c10::cuda::CUDAGuard guard(dy.device());
+  const auto s = stream_of(dy);
+  at::Tensor dx, dw, out;
+  if (want_x) dx = fresh(dy, {p.T, p.H}, dt);
+  if (want_w) dw = fresh(w);
+  if (want_out) out = fresh(dy);
+  const at::Tensor ws = workspace(a[16], (int64_t)moe_gated_linear_bwd_workspace_size(&p), s);
+  if (failed(moe_gated_linear_bwd(&p, ptr(dy), ptr(x), x8.c(), x8.s(), ptr(w), gate.c(), gate.s(),
+                                  up.c(), up.s(), ptr(dx), ptr(dw), ptr(out), ptr(ws),
+                                  (size_t)ws.numel(), s.stream()),
+             "moe_gated_linear_bwd"))
+    return nullptr;
+  PyObject* d = PyDict_New();
+  if (!d) return nullptr;
+  if ((!want_x || put(d, "d_x", dx)) && (!want_w || put(d, "d_w", dw)) &&
+      (!want_out || put(d, "out", out)))
+    return d;
+  Py_DECREF(d);
+  return nullptr;
+  CALL_END
+}
+
+// linear_bwd(d_out, x, x codes, x scales, x channels, w, want_x, want_w, want_bias, workspace)
+PyObject* call_linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  CALL_BEGIN
+  arguments(n, 10);
+  const at::Tensor &dy = tensor(a[0], "d_out"), &w = tensor(a[5], "w");
+  const at::Tensor x = optional(a[1], "x");
+  const Saved x8(a[2], a[3], a[4], "x");
+  const bool want_x = as_bool(a[6]), want_w = as_bool(a[7]), want_bias = as_bool(a[8]);
+  if (dy.dim() != 2 || w.dim() != 2) refuse("d_out and w must have two dimensions");
+  moe_linear_t g;
+  g.dtype = dtype_code(dy);
+  g.T = length(dy.size(0));
+  g.N = length(dy.size(1));
+  g.K = length(w.size(1));
+  g.activation = MOE_LINEAR_NONE;
+  g.out_f32 = 0;
+  const at::ScalarType dt = dy.scalar_type();
+  need(dy, "d_out", dt, {g.T, g.N});
+  need_if(w, "w", dt, {g.N, g.K}, dy);
+  need_if(x, "x", dt, {g.T, g.K}, dy);
+  x8.check("x", g.T, g.K, dy);
+  if (want_w && !x.defined() && !x8.defined()) refuse("x is needed for d_w");
+  c10::cuda::CUDAGuard guard(dy.device());
+  const auto s = stream_of(dy);
+  at::Tensor dx, dw, db;
+  if (want_x) dx = fresh(dy, {g.T, g.K}, dt);
+  if (want_w) dw = fresh(w);
+  if (want_bias) db = fresh(dy, {g.N}, dt);
+  const at::Tensor ws = workspace(a[9], (int64_t)moe_linear_bwd_workspace_size(&g), s);
+  if (failed(moe_linear_bwd(&g, ptr(dy), ptr(x), x8.c(), x8.s(), ptr(w), ptr(dx), ptr(dw), ptr(db),
+                            ptr(ws), (size_t)ws.numel(), s.stream()),
+             "moe_linear_bwd"))
+    return nullptr;
+  PyObject* d = PyDict_New();
+  if (!d) return nullptr;
+  if ((!want_x || put(d, "d_x", dx)) && (!want_w || put(d, "d_w", dw)) &&
+      (!want_bias || put(d, "d_bias", db)))
+    return d;
+  Py_DECREF(d);
+  return nullptr;
+  CALL_END
+}
+
+// 4-bit weights of `rows` x K: codes, scales and alpha.
+struct Weights4 {
+  at::Tensor codes, scales, alpha;
+  int64_t rows;
+  Weights4(PyObject* c, PyObject* s, PyObject* al, const at::Tensor& x) {
+    codes = tensor(c, "codes");
+    scales = tensor(s, "scales");
+    alpha = tensor(al, "alpha");
+    if (x.dim() != 2 || codes.dim() != 2) refuse("x and codes must have two dimensions");
+    const int64_t K = x.size(1);
+    rows = codes.size(0);
+    if (K % 32 != 0) refuse("K must be a multiple of 32, got " + std::to_string(K));
+    need_if(codes, "codes", at::kByte, {rows, K / 2}, x);
+    need_if(scales, "scales", at::kByte, {rows, K / 16}, x);
+    need_if(alpha, "alpha", at::kFloat, {1}, x);
+  }
+  const uint8_t* c() const { return static_cast<const uint8_t*>(ptr(codes)); }
+  const uint8_t* s() const { return static_cast<const uint8_t*>(ptr(scales)); }
+  const float* a() const { return static_cast<const float*>(ptr(alpha)); }
+};
+
+// linear_w4(x, codes, scales, alpha, bias, act, residual, out, workspace)
+PyObject* call_linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  CALL_BEGIN
+  arguments(n, 9);
+  const at::Tensor& x = tensor(a[0], "x");
+  if (x.dim() != 2) refuse("x must have two dimensions");
+  moe_linear_t g;
+  g.dtype = dtype_code(x);
+  g.T = length(x.size(0));
+  g.K = length(x.size(1));
+  need(x, "x", x.scalar_type(), {g.T, g.K});
+  const Weights4 w(a[1], a[2], a[3], x);
+  const at::Tensor bias = optional(a[4], "bias"), res = optional(a[6], "residual");
+  at::Tensor out = optional(a[7], "out");
+  const at::ScalarType dt = x.scalar_type();
+  g.N = length(w.rows);
+  g.activation = as_int(a[5]);
+  g.out_f32 = 0;
+  need_if(bias, "bias", dt, {g.N}, x);
+  need_if(res, "residual", dt, {g.T, g.N}, x);
+  need_if(out, "out", dt, {g.T, g.N}, x);
+  c10::cuda::CUDAGuard guard(x.device());
+  const auto s = stream_of(x);
+  if (!out.defined()) out = fresh(x, {g.T, g.N}, dt);
+  const at::Tensor ws = workspace(a[8], kHeader, s);
+  if (failed(moe_linear_w4a16(&g, ptr(x), w.c(), w.s(), w.a(), ptr(bias), ptr(res), ptr(out),
+                              ptr(ws), (size_t)ws.numel(), s.stream()),
+             "moe_linear_w4a16"))
+    return nullptr;
+  return THPVariable_Wrap(std::move(out));
+  CALL_END
+}
+
+// gated_linear_w4(x, codes, scales, alpha, act, out, workspace)
+PyObject* call_gated_linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  CALL_BEGIN
+  arguments(n, 7);
+  const at::Tensor& x = tensor(a[0], "x");
+  const at::Tensor& codes = tensor(a[1], "codes");
+  moe_gated_linear_t p = gated_sizes(x, "x", codes, as_int(a[4]));
+  p.H = length(x.size(1));
+  need(x, "x", x.scalar_type(), {p.T, p.H});
+  const Weights4 w(a[1], a[2], a[3], x);
+  at::Tensor out = optional(a[5], "out");
+  need_if(out, "out", x.scalar_type(), {p.T, p.F}, x);
+  c10::cuda::CUDAGuard guard(x.device());
+  const auto s = stream_of(x);
+  if (!out.defined()) out = fresh(x, {p.T, p.F}, x.scalar_type());
+  const at::Tensor ws = workspace(a[6], kHeader, s);
+  if (failed(moe_gated_linear_w4a16(&p, ptr(x), w.c(), w.s(), w.a(), ptr(out), ptr(ws),
+                                    (size_t)ws.numel(), s.stream()),
+             "moe_gated_linear_w4a16"))
+    return nullptr;
+  return THPVariable_Wrap(std::move(out));
+  CALL_END
+}
+
 // set_error(class): what a status other than MOE_OK raises.
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
@@ -455,6 +744,13 @@ PyMethodDef g_methods[] = {
     method<call_block_norm_bwd>("block_norm_bwd"),
     method<call_balance_loss>("balance_loss"),
     method<call_router_bwd>("router_bwd"),
+    method<call_checkpoint>("checkpoint"),
+    method<call_restore>("restore"),
+    method<call_gated_linear>("gated_linear"),
+    method<call_gated_linear_bwd>("gated_linear_bwd"),
+    method<call_linear_bwd>("linear_bwd"),
+    method<call_linear_w4>("linear_w4"),
+    method<call_gated_linear_w4>("gated_linear_w4"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

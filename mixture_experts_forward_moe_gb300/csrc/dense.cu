@@ -1,0 +1,817 @@
+// dense.cu -- the dense products of a feed-forward block and of its training, on pairs of SMs
+// (tcgen05, cta_group::2), with the gated product, its gradient and 8-bit checkpoints in the
+// epilogue (include/moe.h: moe_gated_linear, moe_gated_linear_bwd, moe_linear_bwd).
+//
+// D[m, n] = sum_k A(m, k) B(n, k), f32 accumulation.  The operands lie in memory as they are:
+//   x w^T       A = x [M, K], B = w [N, K]           both with k contiguous ("K-major")
+//   dy w        A = dy [M, K], B = w [K, N]          B with n contiguous ("MN-major")
+//   dy^T x      A = dy [K, M], B = x [K, N]          both MN-major
+// so nothing is transposed: the tensor cores read a 128-byte-swizzled tile in either order.
+//
+// A pair of CTAs has a tile of 256 x 256: each CTA 128 rows of A and of B, and its 128 rows of
+// the accumulator (two of 256 TMEM columns, so that one tile's epilogue runs under the next one's
+// MMAs).  The grid is persistent, one CTA per SM.  Rows of D are TMEM lanes, so a thread of the
+// epilogue holds 128 or 256 consecutive columns of one row: the gated product, whose tile holds 128
+// gate columns (the even CTA's rows of B) and the 128 up columns that go with them (the odd
+// CTA's), needs no exchange, nor does the largest value of a checkpoint's 128 channels.  Outputs
+// go through shared memory to TMA stores, which cut what lies outside the tensor.
+#include "activation.cuh"
+#include "dense_ops.cuh"
+#include "fp8.cuh"
+#include "pipe.cuh"
+#include "vec16.cuh"
+
+namespace gb300moe {
+
+namespace {
+
+enum Epi { kPlain, kGated, kGatedSave, kGradient, kParts };
+
+constexpr int kTile = 256;
+constexpr int kThreads = 192;
+constexpr int kOperandBytes = kSlab * kBlockK * 2;  // 128 rows of an operand, 64 k
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kBoxBytes = 128 * 128;                // an epilogue box: 128 rows of 128 bytes
+
+template <int kEpi>
+struct Plan {
+  static constexpr bool kGate = kEpi == kGated || kEpi == kGatedSave || kEpi == kGradient;
+  static constexpr int kBoxes = kEpi == kGradient ? 4 : 2;
+  static constexpr int kStages = kEpi == kGradient ? 5 : 6;
+  static constexpr int kSmem = kStages * kStageBytes + kBoxes * kBoxBytes + 1024;
+};
+
+struct Maps {
+  CUtensorMap a, b;
+  CUtensorMap o0, o1, o2;  // outputs: h | gate and up codes, or the two halves of d_pre
+  CUtensorMap in;          // kGradient: d_out
+};
+
+struct Args {
+  int M, N, K;   // outputs (gated: N of 2 N rows of b)
+  int mt, nt;    // tiles
+  int split;     // parts of K
+  int want_out;  // kGradient: h too
+  Ckpt gate, up; // kGatedSave (codes by TMA)
+  int* status;
+  uint64_t limit_ns;
+};
+
+// Descriptor of an MN-major operand with the 128-byte swizzle: boxes of 64 (mn) x 64 (k), a k row
+// 128 bytes; eight k rows further 1024 bytes (stride offset), 64 mn further a box (leading offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBlockK * 128 >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <bool kMn>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int k16) {
+  return kMn ? sw128_mnmajor_desc(saddr + (uint32_t)k16 * 2048u)
+             : sw128_kmajor_desc(saddr + (uint32_t)k16 * 32u);
+}
+
+template <bool kMn>
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
+                                             int mn, int k) {
+  if constexpr (kMn) {
+    tma_load_2d(dst, map, bar, mn, k);
+    tma_load_2d(dst + kBlockK * 128, map, bar, mn + 64, k);
+  } else {
+    tma_load_2d(dst, map, bar, k, mn);
+  }
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the last N groups of this thread have read their shared memory.
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 16 bytes at byte 16 j of row `row` of a box, where the 128-byte swizzle has them.
+__device__ __forceinline__ uint4* box_at(uint8_t* box, int row, int j) {
+  return reinterpret_cast<uint4*>(box + row * 128 + ((j ^ (row & 7)) << 4));
+}
+
+// 32 columns of two places of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld_x32(uint32_t t, float (&a)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a[i] = __uint_as_float(r[i]);
+}
+
+// Tiles in an order that keeps those of one time close: bands of kBand rows of tiles, column by
+// column.  (All of one row of tiles first would read all of b for every 256 rows of a.)
+constexpr int kBand = 8;
+struct Place {
+  int m, n;  // first row of the tile; its column of tiles
+};
+__device__ __forceinline__ Place place_of(const Args& p, int64_t tile) {
+  const int64_t band = (int64_t)kBand * p.nt;
+  const int b = (int)(tile / band);
+  const int in = (int)(tile % band);
+  const int left = p.mt - b * kBand;
+  const int rows = left < kBand ? left : kBand;
+  return Place{(b * kBand + in % rows) * kTile, in / rows};
+}
+
+// Roles (192 threads): warp 0 TMA producer; warp 1 issues the MMAs (even CTA) or tells the even CTA
+// that a stage of this CTA has landed (odd CTA); warps 2-5 epilogue.  Every wait is bounded
+// (MOE_ERR_TIMEOUT in the status word); a pair in which one gave up waits for its copies, MMAs and
+// stores in flight before it leaves.
+template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_kernel(const __grid_constant__ Maps maps, const Args p) {
+  using P = Plan<kEpi>;
+  extern __shared__ uint8_t dsmem[];
+  __shared__ __align__(8) uint64_t full_bar[P::kStages];
+  __shared__ __align__(8) uint64_t empty_bar[P::kStages];
+  __shared__ __align__(8) uint64_t tfull_bar[2];
+  __shared__ __align__(8) uint64_t tempty_bar[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(8) uint64_t in_bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const uint32_t raw = smem_u32(dsmem);
+  uint8_t* smem = dsmem + ((1024u - (raw & 1023u)) & 1023u);
+  uint8_t* boxes = smem + P::kStages * kStageBytes;
+  const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  volatile int* abort_flag = &s_abort;
+  const uint32_t rank = cluster_ctarank();  // in the pair
+  const int side = (int)rank;
+  const int num_kb = (p.K - 1) / kBlockK + 1;
+  const int64_t tiles = (int64_t)p.mt * p.nt, units = tiles * p.split;
+  const int64_t step = num_clusters_x();
+
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < P::kStages; ++s) {
+        // the even CTA's stage is full when its copies and, by the forwarder, the odd CTA's landed
+        mbar_init(&full_bar[s], side == 0 ? 2 : 1);
+        mbar_init(&empty_bar[s], 1);
+      }
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&tfull_bar[b], 1);
+        mbar_init(&tempty_bar[b], 8);  // an arrival per epilogue warp of both CTAs
+      }
+      mbar_init(&drain_bar, 1);
+      mbar_init(&in_bar, 1);
+      s_abort = 0;
+      fence_mbar_init();
+    }
+  } else if (warp == 1) {
+    tmem_alloc_pair(&s_tmem, 512);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  int issued = 0;  // by the producer: stages asked for
+  const uint32_t peer_abort = cluster_map(smem_u32(&s_abort), rank ^ 1u);
+  // by one thread, or by all of a warp; on giving up the peer CTA is told too
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (wait_bar(bar, parity, abort_flag, p.limit_ns, p.status)) return true;
+    st_cluster_u32(peer_abort, 1u);
+    return false;
+  };
+  // k blocks of a part
+  auto part_of = [&](int64_t u, int& kb0, int& kb1) {
+    const int64_t part = u / tiles;
+    kb0 = (int)(num_kb * part / p.split);
+    kb1 = (int)(num_kb * (part + 1) / p.split);
+    return u % tiles;
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      Ring r(empty_bar, P::kStages, 1u);
+      bool ok = true;
+      for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
+        int kb0, kb1;
+        const Place at = place_of(p, part_of(u, kb0, kb1));
+        const int ma = at.m + side * kSlab;
+        // gated: the even CTA has the gate rows of b, the odd one the up rows; gate rows past N
+        // are rows of up, whose columns the epilogue leaves out
+        const int nb = P::kGate || (kEpi == kParts && p.want_out)
+                           ? side * p.N + at.n * kSlab
+                           : at.n * kTile + side * kSlab;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!r.ready && !wait(r.bar(), r.parity)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + r.stage * kStageBytes;
+          uint64_t* full = &full_bar[r.stage];
+          r.next();
+          mbar_arrive_expect_tx(full, (uint32_t)kStageBytes);
+          load_operand<kAMn>(st, &maps.a, full, ma, kb * kBlockK);
+          load_operand<kBMn>(st + kOperandBytes, &maps.b, full, nb, kb * kBlockK);
+          ++issued;
+        }
+      }
+    }
+  } else if (warp == 1 && side != 0) {
+    if (elect_one()) {
+      Ring r(full_bar, P::kStages, 0u);
+      const uint32_t to = cluster_map(smem_u32(full_bar), 0u);
+      bool ok = true;
+      for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
+        int kb0, kb1;
+        part_of(u, kb0, kb1);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!r.ready && !wait(r.bar(), r.parity)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_cluster(to + (uint32_t)r.stage * 8u);
+          r.next();
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      Ring r(full_bar, P::kStages, 0u);
+      int buf = 0;
+      uint32_t buf_phase = 0;
+      bool ok = true;
+      const uint32_t base = smem_u32(smem);
+      const uint32_t idesc = idesc_f16(256, kTile, DT<T>::kIsBF16) | (kAMn ? 1u << 15 : 0u) |
+                             (kBMn ? 1u << 16 : 0u);
+      const uint32_t empty_own = smem_u32(empty_bar), tfull_own = smem_u32(tfull_bar);
+      for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
+        int kb0, kb1;
+        part_of(u, kb0, kb1);
+        if (!wait(&tempty_bar[buf], buf_phase ^ 1u)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * kTile);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!r.ready && !wait(r.bar(), r.parity)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + (uint32_t)(r.stage * kStageBytes);
+          const uint32_t sb = sa + (uint32_t)kOperandBytes;
+          const uint32_t at = (uint32_t)r.stage * 8u;
+          r.next();
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k)
+            umma_f16_pair(d, operand_desc<kAMn>(sa, k), operand_desc<kBMn>(sb, k), idesc,
+                          (kb > kb0 || k > 0) ? 1u : 0u);
+          umma_commit_both(empty_own + at, 0u);
+        }
+        if (!ok) break;
+        umma_commit_both(tfull_own + (uint32_t)buf * 8u, 0u);
+        buf ^= 1;
+        if (buf == 0) buf_phase ^= 1u;
+      }
+      // every MMA issued has completed once drain_bar flips
+      umma_commit_pair(smem_u32(&drain_bar));
+      land_mmas(&drain_bar);
+    }
+  } else {
+    // ---- epilogue ----
+    const int row = (warp & 3) * 32 + lane;
+    const bool leader = threadIdx.x == 64;  // issues the stores
+    const uint32_t tb = tmem_lane(tmem, warp);
+    int buf = 0, box = 0;
+    uint32_t buf_phase = 0, in_phase = 0;
+    auto sync = [] { named_bar_sync(1, 128); };
+    // A box that no store reads any more; two are in use.
+    auto next_box = [&]() -> uint8_t* {
+      if (leader) store_wait_read<1>();
+      sync();
+      uint8_t* b = boxes + box * kBoxBytes;
+      box ^= 1;
+      return b;
+    };
+    // Written boxes to the stores' view; then `issue` by the leader.
+    auto publish = [&](auto issue) {
+      fence_async_shared();
+      sync();
+      if (leader) {
+        issue();
+        store_commit();
+      }
+    };
+    for (int64_t u = cluster_id_x(); u < units; u += step) {
+      int kb0, kb1;
+      const int64_t tile = part_of(u, kb0, kb1);
+      const Place at = place_of(p, tile);
+      const int m = at.m + side * kSlab;
+      const bool live = m < p.M;  // a row of this CTA is one of D's (uniform)
+      if constexpr (kEpi == kGradient) {
+        if (leader && live) {
+          store_wait_read<0>();
+          mbar_arrive_expect_tx(&in_bar, 2 * kBoxBytes);
+          tma_load_2d(boxes, &maps.in, &in_bar, at.n * kSlab, m);
+          tma_load_2d(boxes + kBoxBytes, &maps.in, &in_bar, at.n * kSlab + 64, m);
+        }
+      }
+      const bool got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
+      tc_fence_after();
+      // the four warps leave together: named barriers are between them
+      if (!named_bar_and(2, 128, got)) break;
+      const uint32_t d = tb + (uint32_t)(buf * kTile);
+      if constexpr (kEpi == kPlain) {
+        for (int c = 0; c < 4 && live; ++c) {
+          const int n = at.n * kTile + c * 64;
+          if (n >= p.N) break;
+          float v[64];
+          tmem_ld_x64(d + (uint32_t)(c * 64), v);
+          uint8_t* b = next_box();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = v[j * 8 + i];
+            *box_at(b, row, j) = pack<T>(w);
+          }
+          publish([&] { tma_store_2d(&maps.o0, b, n, m); });
+        }
+      } else if constexpr (kEpi == kParts) {
+        const int part_row = (int)(u / tiles) * p.mt * kTile + m;
+        for (int c = 0; c < 8; ++c) {
+          float v[32];
+          tmem_ld_x32(d + (uint32_t)(c * 32), v);
+          uint8_t* b = next_box();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(box_at(b, row, j)) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          publish([&] { tma_store_2d(&maps.o0, b, at.n * kTile + c * 32, part_row); });
+        }
+      } else if constexpr (kEpi == kGated || kEpi == kGatedSave) {
+        float top_g = 0.0f, top_u = 0.0f;
+        for (int c = 0; c < 2 && live; ++c) {
+          const int n = at.n * kSlab + c * 64;
+          if (n >= p.N) break;
+          uint8_t* b = next_box();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float g[32], v[32];
+            tmem_ld_x32(d + (uint32_t)(c * 64 + h * 32), g);
+            tmem_ld_x32(d + (uint32_t)(kSlab + c * 64 + h * 32), v);
+            if constexpr (kEpi == kGatedSave) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                if (n + h * 32 + (i & ~7) < p.N) {  // N is a multiple of 8
+                  top_g = fmaxf(top_g, finite_abs(g[i]));
+                  top_u = fmaxf(top_u, finite_abs(v[i]));
+                }
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = gate_value<kAct>(g[j * 8 + i]) * v[j * 8 + i];
+              *box_at(b, row, h * 4 + j) = pack<T>(w);
+            }
+          }
+          publish([&] { tma_store_2d(&maps.o0, b, n, m); });
+        }
+        if constexpr (kEpi == kGatedSave) {
+          for (int half = 0; half < 2 && live; ++half) {
+            const Ckpt& to = half == 0 ? p.gate : p.up;
+            const int e = fp8_exponent(half == 0 ? top_g : top_u);
+            if (m + row < p.M)
+              to.scales[(int64_t)(m + row) * p.nt + at.n] = fp8_scale(e);
+            const float inv = fp8_scale(-e);
+            uint8_t* b = next_box();
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              float v[32];
+              tmem_ld_x32(d + (uint32_t)(half * kSlab + h * 32), v);
+              uint32_t q[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                q[i] = at.n * kSlab + h * 32 + ((4 * i) & ~7) < p.N
+                           ? fp8_pack4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv)
+                           : 0u;
+              *box_at(b, row, 2 * h) = make_uint4(q[0], q[1], q[2], q[3]);
+              *box_at(b, row, 2 * h + 1) = make_uint4(q[4], q[5], q[6], q[7]);
+            }
+            publish([&] {
+              tma_store_2d(half == 0 ? &maps.o1 : &maps.o2, b, at.n * kSlab, m);
+            });
+          }
+        }
+      } else {
+        if (live) {
+          const bool there = __all_sync(kAll, wait(&in_bar, in_phase));
+          in_phase ^= 1u;
+          if (!named_bar_and(2, 128, there)) break;
+          uint8_t *bg = boxes + 2 * kBoxBytes, *bu = boxes + 3 * kBoxBytes;
+          for (int c = 0; c < 2; ++c) {
+            const int n = at.n * kSlab + c * 64;
+            if (n >= p.N) break;
+            uint8_t* bh = boxes + c * kBoxBytes;
+            if (c > 0) {
+              if (leader) store_wait_read<0>();
+              sync();
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float g[32], v[32];
+              tmem_ld_x32(d + (uint32_t)(c * 64 + h * 32), g);
+              tmem_ld_x32(d + (uint32_t)(kSlab + c * 64 + h * 32), v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float dh[8], dg[8], du[8], hv[8];
+                unpack<T>(*box_at(bh, row, h * 4 + j), dh);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  float a, s;
+                  gate_slope<kAct>(g[j * 8 + i], a, s);
+                  hv[i] = a * v[j * 8 + i];
+                  dg[i] = dh[i] * v[j * 8 + i] * s;
+                  du[i] = dh[i] * a;
+                }
+                *box_at(bh, row, h * 4 + j) = pack<T>(hv);
+                *box_at(bg, row, h * 4 + j) = pack<T>(dg);
+                *box_at(bu, row, h * 4 + j) = pack<T>(du);
+              }
+            }
+            publish([&] {
+              if (p.want_out) tma_store_2d(&maps.o0, bh, n, m);
+              tma_store_2d(&maps.o1, bg, n, m);
+              tma_store_2d(&maps.o2, bu, n, m);
+            });
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(&tempty_bar[buf]), 0u));
+      buf ^= 1;
+      if (buf == 0) buf_phase ^= 1u;
+    }
+    if (leader) {
+      store_wait_all();
+      // a tile whose d_out was asked for and never used
+      if (kEpi == kGradient && *abort_flag) {
+        const uint64_t t = global_timer_ns();
+        while (!mbar_try_wait(&in_bar, in_phase))
+          if (global_timer_ns() - t > kDrainNs / 100) break;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  // (the even CTA's stages are full only with the odd CTA's copies told of: else a second passes)
+  if (*abort_flag) land_copies(full_bar, issued, P::kStages);
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---- split K: the parts' sums, and the epilogue on them ---------------------------------------
+// A warp takes a row and 128 columns (gated: 128 gate and 128 up columns), a lane four of them; the
+// parts are added in their order.  They were written just before and lie in L2.
+struct JoinArgs {
+  int M, N, nt, split, want_out;
+  int64_t pitch, part;  // elements from row to row and part to part
+  const float* sums;
+  void *o0, *o1, *o2;  // as Maps
+  const void* in;
+  Ckpt gate, up;
+};
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+template <typename T>
+__device__ __forceinline__ void put4(void* base, int64_t at, const float (&v)[4]) {
+  T h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = DT<T>::from_f(v[i]);
+  *reinterpret_cast<uint2*>(static_cast<T*>(base) + at) = *reinterpret_cast<uint2*>(h);
+}
+
+template <typename T, int kEpi, int kAct>
+__global__ void __launch_bounds__(256) join_kernel(const JoinArgs p) {
+  pdl_wait();
+  constexpr bool kGate = Plan<kEpi>::kGate;
+  const int lane = threadIdx.x & 31;
+  const int groups = kGate ? p.nt : 2 * p.nt;  // of 128 outputs
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t m = at / groups;
+  const int g = (int)(at % groups);
+  const int n = g * kSlab + lane * 4;  // this lane's first output
+  if (m >= p.M) return;
+  auto sum = [&](int64_t col) {
+    const float* from = p.sums + m * p.pitch + col;
+    float4 s = *reinterpret_cast<const float4*>(from);
+    for (int i = 1; i < p.split; ++i)
+      s = add4(s, *reinterpret_cast<const float4*>(from + i * p.part));
+    return s;
+  };
+  const bool live = n < p.N;  // N is a multiple of 8
+  if constexpr (!kGate) {
+    if (!live) return;
+    const float4 s = sum(n);
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    put4<T>(p.o0, m * p.N + n, v);
+  } else {
+    float4 sg = make_float4(0.0f, 0.0f, 0.0f, 0.0f), su = sg;
+    if (live) {
+      sg = sum((int64_t)g * kTile + lane * 4);
+      su = sum((int64_t)g * kTile + kSlab + lane * 4);
+    }
+    const float gv[4] = {sg.x, sg.y, sg.z, sg.w}, uv[4] = {su.x, su.y, su.z, su.w};
+    if constexpr (kEpi == kGradient) {
+      if (!live) return;
+      float dh[4], h[4], dg[4], du[4];
+      const uint2 raw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.in) + m * p.N + n);
+      const T* t = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, s;
+        dh[i] = DT<T>::to_f(t[i]);
+        gate_slope<kAct>(gv[i], a, s);
+        h[i] = a * uv[i];
+        dg[i] = dh[i] * uv[i] * s;
+        du[i] = dh[i] * a;
+      }
+      if (p.want_out) put4<T>(p.o0, m * p.N + n, h);
+      put4<T>(p.o1, m * 2 * p.N + n, dg);
+      put4<T>(p.o1, (m * 2 + 1) * p.N + n, du);
+    } else {
+      float h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = gate_value<kAct>(gv[i]) * uv[i];
+      if (live) put4<T>(p.o0, m * p.N + n, h);
+      if constexpr (kEpi == kGatedSave) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float(&v)[4] = half == 0 ? gv : uv;
+          const Ckpt& to = half == 0 ? p.gate : p.up;
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, finite_abs(v[i]));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+          const int e = fp8_exponent(top);
+          if (lane == 0) to.scales[m * p.nt + g] = fp8_scale(e);
+          *reinterpret_cast<uint32_t*>(to.codes + (m * p.nt + g) * kCkptGroup + lane * 4) =
+              live ? fp8_pack4(v[0], v[1], v[2], v[3], fp8_scale(-e)) : 0u;
+        }
+      }
+    }
+  }
+}
+
+// ---- host side ---------------------------------------------------------------------------------
+// Pairs of CTAs that the device holds at once with the shared memory of `Kernel`: a pair stays
+// within one group of SMs, so this can be less than half the SMs.
+template <auto Kernel>
+int max_pairs(int smem) {
+  static int cached[64];
+  static std::once_flag once[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::call_once(once[dev], [=] {
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (set_smem_limit<Kernel>(smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      n = 0;
+    }
+    cached[dev] = n;
+  });
+  return cached[dev];
+}
+
+// A 2-D map of rows `pitch` bytes apart with the 128-byte swizzle, boxes of 128 bytes x box_rows.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, uint64_t inner,
+              uint64_t rows, uint64_t pitch, uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {pitch};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / size), box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+CUtensorMapDataType type16(int dtype) {
+  return dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+bool map16(CUtensorMap* m, int dtype, const void* base, int64_t inner, int64_t rows, int64_t pitch,
+           int box_rows) {
+  return make_map(m, type16(dtype), 2, base, (uint64_t)inner, (uint64_t)rows, (uint64_t)pitch * 2,
+                  (uint32_t)box_rows);
+}
+
+// Parts of K: as many as the SM pairs take tiles at once, of at least kPartBlocks 64-k blocks.
+constexpr int kPartBlocks = 8;
+constexpr int kMaxSplit = 16;
+int split_of(int64_t tiles, int64_t K) {
+  const int64_t pairs = num_sms() / 2, num_kb = ceil_div(K, kBlockK);
+  int split = 1;
+  while (split < kMaxSplit && tiles * (split + 1) <= pairs && num_kb >= (split + 1) * kPartBlocks)
+    ++split;
+  return split;
+}
+int64_t tiles_n(int64_t N, bool gated) { return ceil_div(N, gated ? kSlab : kTile); }
+
+struct Problem {
+  int dtype, M, N, K;
+  const void *a, *b;
+  int64_t a_pitch;
+  void *o0, *o1;  // h or the product; d_pre
+  const void* in;
+  Ckpt gate, up;
+  float* parts;
+  int* status;
+};
+
+template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct>
+cudaError_t run_tiles(const Maps& maps, const Args& p, cudaStream_t s) {
+  constexpr auto kern = dense_kernel<T, kAMn, kBMn, kEpi, kAct>;
+  const int pairs = max_pairs<kern>(Plan<kEpi>::kSmem);
+  if (pairs <= 0) return cudaErrorInvalidConfiguration;
+  const int64_t units = (int64_t)p.mt * p.nt * p.split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)Plan<kEpi>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct>
+cudaError_t run(const Problem& q, cudaStream_t s) {
+  constexpr bool kGate = Plan<kEpi>::kGate;
+  Args p = {};
+  p.M = q.M;
+  p.N = q.N;
+  p.K = q.K;
+  p.mt = (int)ceil_div(q.M, kTile);
+  p.nt = (int)tiles_n(q.N, kGate);
+  p.split = split_of((int64_t)p.mt * p.nt, q.K);
+  p.gate = q.gate;
+  p.up = q.up;
+  p.status = q.status;
+  p.limit_ns = wait_limit_ns();
+  Maps maps;
+  const int64_t rows_b = kGate ? (int64_t)2 * q.N : q.N;
+  bool ok = kAMn ? map16(&maps.a, q.dtype, q.a, q.M, q.K, q.a_pitch, kBlockK)
+                 : map16(&maps.a, q.dtype, q.a, q.K, q.M, q.a_pitch, kSlab);
+  ok = ok && (kBMn ? map16(&maps.b, q.dtype, q.b, rows_b, q.K, rows_b, kBlockK)
+                   : map16(&maps.b, q.dtype, q.b, q.K, rows_b, q.K, kSlab));
+  maps.o0 = maps.o1 = maps.o2 = maps.in = maps.a;  // those a kernel does not use
+  if (p.split > 1) {
+    const int64_t pitch = (int64_t)p.nt * kTile, rows = (int64_t)p.mt * kTile;
+    p.want_out = kGate;  // how the parts' columns lie
+    ok = ok && make_map(&maps.o0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, q.parts, (uint64_t)pitch,
+                        (uint64_t)(rows * p.split), (uint64_t)pitch * 4, kSlab);
+    if (!ok) return cudaErrorInvalidValue;
+    const cudaError_t e = run_tiles<T, kAMn, kBMn, kParts, 0>(maps, p, s);
+    if (e != cudaSuccess) return e;
+    JoinArgs j = {};
+    j.M = q.M;
+    j.N = q.N;
+    j.nt = p.nt;
+    j.split = p.split;
+    j.want_out = kEpi != kGradient || q.o0 != nullptr;
+    j.pitch = pitch;
+    j.part = rows * pitch;
+    j.sums = q.parts;
+    j.o0 = q.o0;
+    j.o1 = q.o1;
+    j.in = q.in;
+    j.gate = q.gate;
+    j.up = q.up;
+    const int64_t warps = (int64_t)q.M * (kGate ? p.nt : 2 * p.nt);
+    return launch_k(join_kernel<T, kEpi, kAct>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s,
+                    true, j);
+  }
+  p.want_out = q.o0 != nullptr;
+  const int64_t N = q.N;
+  if (q.o0) ok = ok && map16(&maps.o0, q.dtype, q.o0, N, q.M, N, kSlab);
+  if constexpr (kEpi == kGradient) {
+    ok = ok && map16(&maps.o1, q.dtype, q.o1, N, q.M, 2 * N, kSlab) &&
+         map16(&maps.o2, q.dtype, static_cast<T*>(q.o1) + N, N, q.M, 2 * N, kSlab) &&
+         map16(&maps.in, q.dtype, q.in, N, q.M, N, kSlab);
+  } else if constexpr (kEpi == kGatedSave) {
+    const uint64_t width = (uint64_t)ckpt_width(N);
+    ok = ok &&
+         make_map(&maps.o1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.gate.codes, width, (uint64_t)q.M,
+                  width, kSlab) &&
+         make_map(&maps.o2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.up.codes, width, (uint64_t)q.M,
+                  width, kSlab);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  return run_tiles<T, kAMn, kBMn, kEpi, kAct>(maps, p, s);
+}
+
+template <int kEpi>
+cudaError_t run_gated(int act, const Problem& q, cudaStream_t s) {
+  if (q.dtype == MOE_BF16)
+    return act == MOE_ACT_SILU
+               ? run<__nv_bfloat16, false, false, kEpi, MOE_ACT_SILU>(q, s)
+               : run<__nv_bfloat16, false, false, kEpi, MOE_ACT_GELU_TANH>(q, s);
+  return act == MOE_ACT_SILU ? run<__half, false, false, kEpi, MOE_ACT_SILU>(q, s)
+                             : run<__half, false, false, kEpi, MOE_ACT_GELU_TANH>(q, s);
+}
+
+}  // namespace
+
+size_t dense_split_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  const int64_t mt = ceil_div(M, kTile), nt = tiles_n(N, gated);
+  const int split = split_of(mt * nt, K);
+  return split > 1 ? (size_t)(mt * nt * split) * kTile * kTile * sizeof(float) : 0;
+}
+
+cudaError_t launch_dense_nn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,
+                            const void* b, void* out, float* parts, int* status, cudaStream_t s) {
+  Problem q = {};
+  q.dtype = dtype, q.M = M, q.N = N, q.K = K, q.a = a, q.a_pitch = a_pitch, q.b = b, q.o0 = out;
+  q.parts = parts, q.status = status;
+  return dtype == MOE_BF16 ? run<__nv_bfloat16, false, true, kPlain, 0>(q, s)
+                           : run<__half, false, true, kPlain, 0>(q, s);
+}
+
+cudaError_t launch_dense_tn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,
+                            const void* b, void* out, float* parts, int* status, cudaStream_t s) {
+  Problem q = {};
+  q.dtype = dtype, q.M = M, q.N = N, q.K = K, q.a = a, q.a_pitch = a_pitch, q.b = b, q.o0 = out;
+  q.parts = parts, q.status = status;
+  return dtype == MOE_BF16 ? run<__nv_bfloat16, true, true, kPlain, 0>(q, s)
+                           : run<__half, true, true, kPlain, 0>(q, s);
+}
+
+cudaError_t launch_gated(int dtype, int act, int T, int F, int H, const void* x, const void* w,
+                         void* out, Ckpt gate, Ckpt up, float* parts, int* status,
+                         cudaStream_t s) {
+  Problem q = {};
+  q.dtype = dtype, q.M = T, q.N = F, q.K = H, q.a = x, q.a_pitch = H, q.b = w, q.o0 = out;
+  q.gate = gate, q.up = up, q.parts = parts, q.status = status;
+  return gate.codes ? run_gated<kGatedSave>(act, q, s) : run_gated<kGated>(act, q, s);
+}
+
+cudaError_t launch_gated_grad(int dtype, int act, int T, int F, int H, const void* x, const void* w,
+                              const void* d_out, void* d_pre, void* out, float* parts, int* status,
+                              cudaStream_t s) {
+  Problem q = {};
+  q.dtype = dtype, q.M = T, q.N = F, q.K = H, q.a = x, q.a_pitch = H, q.b = w, q.o0 = out, q.o1 = d_pre;
+  q.in = d_out, q.parts = parts, q.status = status;
+  return run_gated<kGradient>(act, q, s);
+}
+
+}  // namespace gb300moe

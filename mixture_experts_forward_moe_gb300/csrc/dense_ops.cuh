@@ -1,0 +1,69 @@
+// dense_ops.cuh -- launchers of the dense feed-forward block and its training (dense.cu,
+// dense_rows.cu, checkpoint.cu), called by dense_api.cu with checked arguments.
+#pragma once
+
+#include "common.cuh"
+
+namespace gb300moe {
+
+// Channels that share a scale of a checkpoint; a row of codes is a whole number of such groups.
+constexpr int kCkptGroup = 128;
+inline int64_t ckpt_groups(int64_t C) { return (C + kCkptGroup - 1) / kCkptGroup; }
+inline int64_t ckpt_width(int64_t C) { return ckpt_groups(C) * kCkptGroup; }
+
+// E4M3 codes [T, ckpt_width(C)] and f32 scales [T, ckpt_groups(C)].
+struct Ckpt {
+  uint8_t* codes;
+  float* scales;
+};
+struct CkptIn {
+  const uint8_t* codes;
+  const float* scales;
+};
+
+// f32 partial sums that a product of M x N outputs over K (gated: N gated columns, of two products)
+// leaves in the workspace, in bytes; 0 where K is not split.
+size_t dense_split_bytes(int64_t M, int64_t N, int64_t K, bool gated);
+
+// out[M, N] = sum_k a(m, k) b(k, n): a [M, K] (nn) or [K, M] (tn) with rows a_pitch elements apart
+// (a multiple of 8), b [K, N].
+cudaError_t launch_dense_nn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,
+                            const void* b, void* out, float* parts, int* status, cudaStream_t s);
+cudaError_t launch_dense_tn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,
+                            const void* b, void* out, float* parts, int* status, cudaStream_t s);
+cudaError_t launch_gated(int dtype, int act, int T, int F, int H, const void* x, const void* w,
+                         void* out, Ckpt gate, Ckpt up, float* parts, int* status, cudaStream_t s);
+cudaError_t launch_gated_grad(int dtype, int act, int T, int F, int H, const void* x, const void* w,
+                              const void* d_out, void* d_pre, void* out, float* parts, int* status,
+                              cudaStream_t s);
+
+// Few rows of x against 16-bit or 4-bit weights (dense_rows.cu).
+struct RowsCall {
+  int T, N, K;  // gated: N outputs of 2 N weight rows
+  int dtype;
+  int gated;
+  int act;              // moe_linear_act_t, or moe_activation_t when gated
+  const void* x;
+  const void* w;        // 16-bit weights [rows, K], or
+  const uint8_t* codes; // E2M1 codes [rows, K/2] and
+  const uint8_t* scales;  // E4M3 scales [rows, K/16]
+  const float* alpha;
+  const void* bias;
+  const void* res;
+  void* out;
+  int* status;
+};
+cudaError_t launch_rows(const RowsCall& c, cudaStream_t s);
+
+cudaError_t launch_checkpoint(int dtype, int T, int C, const void* x, Ckpt out, cudaStream_t s);
+cudaError_t launch_restore(int dtype, int T, int C, CkptIn in, void* out, cudaStream_t s);
+cudaError_t launch_gated_grad_saved(int dtype, int act, int T, int F, const void* d_out, CkptIn gate,
+                                    CkptIn up, void* d_pre, void* out, cudaStream_t s);
+// sum[n] = sum_t v[t, n] of [T, N] rows that lie `pitch` (a multiple of 8) elements apart.
+cudaError_t launch_column_sum(int dtype, int T, int N, int64_t pitch, const void* v, void* sum,
+                              cudaStream_t s);
+// [T, N] -> [T, pitch], zeros behind N.
+cudaError_t launch_pad_rows(int dtype, int T, int N, int64_t pitch, const void* v, void* out,
+                            cudaStream_t s);
+
+}  // namespace gb300moe
