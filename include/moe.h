@@ -714,8 +714,10 @@ moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void
  *   e2m1 * e4m3 is exact in f16, in which the products are taken, with f32 accumulation.  bf16 x
  *   is converted: exact between 2^-14 and 65504 in magnitude, at most 2^-25 off below, and a larger
  *   value sets MOE_ERR_F16_RANGE in the status word.
- *   workspace  256 bytes: the status word.
+ *   workspace  moe_linear_w4a16_workspace_size(g), moe_gated_linear_w4a16_workspace_size(p) bytes.
  */
+size_t moe_linear_w4a16_workspace_size(const moe_linear_t* g);
+size_t moe_gated_linear_w4a16_workspace_size(const moe_gated_linear_t* p);
 moe_status_t moe_linear_w4a16(const moe_linear_t* g, const void* x, const uint8_t* codes,
                               const uint8_t* scales, const float* alpha, const void* bias,
                               const void* residual, void* out, void* workspace,

@@ -54,7 +54,8 @@ EXPORTED = (
     "moe_balance_loss_fwd", "moe_router_bwd", "moe_checkpoint", "moe_checkpoint_restore",
     "moe_gated_linear_workspace_size", "moe_gated_linear", "moe_gated_linear_bwd_workspace_size",
     "moe_gated_linear_bwd", "moe_linear_bwd_workspace_size", "moe_linear_bwd", "moe_linear_w4a16",
-    "moe_gated_linear_w4a16",
+    "moe_linear_w4a16_workspace_size", "moe_gated_linear_w4a16",
+    "moe_gated_linear_w4a16_workspace_size",
 )
 
 
@@ -189,7 +190,8 @@ def lib():
             L.moe_router_bwd.argtypes = [PP, i32] + [P] * 8
             PG = ctypes.POINTER(GatedLinear)
             for fn, desc in (("moe_gated_linear", PG), ("moe_gated_linear_bwd", PG),
-                             ("moe_linear_bwd", PL)):
+                             ("moe_linear_bwd", PL), ("moe_linear_w4a16", PL),
+                             ("moe_gated_linear_w4a16", PG)):
                 size = getattr(L, fn + "_workspace_size")
                 size.restype, size.argtypes = sz, [desc]
             L.moe_gated_linear.argtypes = [PG] + [P] * 8 + [sz, P]

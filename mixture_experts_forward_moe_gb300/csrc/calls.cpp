@@ -691,7 +691,7 @@ PyObject* call_linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c10::cuda::CUDAGuard guard(x.device());
   const auto s = stream_of(x);
   if (!out.defined()) out = fresh(x, {g.T, g.N}, dt);
-  const at::Tensor ws = workspace(a[8], kHeader, s);
+  const at::Tensor ws = workspace(a[8], (int64_t)moe_linear_w4a16_workspace_size(&g), s);
   if (failed(moe_linear_w4a16(&g, ptr(x), w.c(), w.s(), w.a(), ptr(bias), ptr(res), ptr(out),
                               ptr(ws), (size_t)ws.numel(), s.stream()),
              "moe_linear_w4a16"))
@@ -715,7 +715,8 @@ PyObject* call_gated_linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   c10::cuda::CUDAGuard guard(x.device());
   const auto s = stream_of(x);
   if (!out.defined()) out = fresh(x, {p.T, p.F}, x.scalar_type());
-  const at::Tensor ws = workspace(a[6], kHeader, s);
+  const at::Tensor ws =
+      workspace(a[6], (int64_t)moe_gated_linear_w4a16_workspace_size(&p), s);
   if (failed(moe_gated_linear_w4a16(&p, ptr(x), w.c(), w.s(), w.a(), ptr(out), ptr(ws),
                                     (size_t)ws.numel(), s.stream()),
              "moe_gated_linear_w4a16"))

@@ -11,10 +11,12 @@
 // A pair of CTAs has a tile of 256 x 256: each CTA 128 rows of A and of B, and its 128 rows of
 // the accumulator (two of 256 TMEM columns, so that one tile's epilogue runs under the next one's
 // MMAs).  The grid is persistent, one CTA per SM.  Rows of D are TMEM lanes, so a thread of the
-// epilogue holds 128 or 256 consecutive columns of one row: the gated product, whose tile holds 128
-// gate columns (the even CTA's rows of B) and the 128 up columns that go with them (the odd
-// CTA's), needs no exchange, nor does the largest value of a checkpoint's 128 channels.  Outputs
-// go through shared memory to TMA stores, which cut what lies outside the tensor.
+// epilogue holds consecutive columns of one row: the gated product, whose tile holds 128 gate columns
+// (the even CTA's rows of B) and the 128 up columns that go with them (the odd CTA's), needs no
+// exchange, and the largest value of a checkpoint's 128 channels one between two threads.  Outputs go
+// through shared memory to TMA stores, which cut what lies outside the tensor.
+// Where the last tiles would leave most pairs idle they are split along K: their f32 sums go to the
+// workspace, and join_kernel adds them in order and finishes the outputs.
 #include "activation.cuh"
 #include "dense_ops.cuh"
 #include "fp8.cuh"
@@ -25,34 +27,45 @@ namespace gb300moe {
 
 namespace {
 
-enum Epi { kPlain, kGated, kGatedSave, kGradient, kParts };
+enum Epi { kPlain, kGated, kGatedSave, kGradient };
 
 constexpr int kTile = 256;
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kOperandBytes = kSlab * kBlockK * 2;  // 128 rows of an operand, 64 k
-constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kBoxBytes = 128 * 128;                // an epilogue box: 128 rows of 128 bytes
+constexpr int kBoxBytes = 128 * 128;  // an epilogue box: 128 rows of 128 bytes
+constexpr int kAllEpilogue = 3;       // named barriers: 1 and 2 of a half, 3 of both
 
-template <int kEpi>
+constexpr bool gated(int epi) { return epi != kPlain; }
+
+// A tile is 256 rows by kBN columns.  Boxes of each half of the epilogue warps, and stages in what is
+// left of shared memory.  (Two boxes and five stages everywhere: 4096 x 4096 x 7168 in 124 us, 117
+// with six stages.)
+template <int kEpi, int kBN>
 struct Plan {
-  static constexpr bool kGate = kEpi == kGated || kEpi == kGatedSave || kEpi == kGradient;
-  static constexpr int kBoxes = kEpi == kGradient ? 4 : 2;
-  static constexpr int kStages = kEpi == kGradient ? 5 : 6;
-  static constexpr int kSmem = kStages * kStageBytes + kBoxes * kBoxBytes + 1024;
+  static constexpr int kStageBytes = kOperandBytes + kBN / 2 * kBlockK * 2;
+  static constexpr int kBoxes = kEpi == kGradient ? 2 : 1;
+  // a gated tile's 64 columns share boxes between the halves
+  static constexpr bool kShared = gated(kEpi) && kBN != kTile;
+  static constexpr int kStages = kBN != kTile ? 8 : kEpi == kGradient ? 5 : 6;
+  static constexpr int kSmem = kStages * kStageBytes + (kShared ? 1 : 2) * kBoxes * kBoxBytes + 1024;
 };
 
 struct Maps {
   CUtensorMap a, b;
   CUtensorMap o0, o1, o2;  // outputs: h | gate and up codes, or the two halves of d_pre
   CUtensorMap in;          // kGradient: d_out
+  CUtensorMap parts;       // sums of the tiles that are split
 };
 
 struct Args {
-  int M, N, K;   // outputs (gated: N of 2 N rows of b)
-  int mt, nt;    // tiles
-  int split;     // parts of K
-  int want_out;  // kGradient: h too
-  Ckpt gate, up; // kGatedSave (codes by TMA)
+  int M, N, K;    // outputs (gated: N of 2 N rows of b)
+  int mt, nt;     // tiles
+  int64_t whole;  // tiles that are not split; then
+  int rest;       // the others, each
+  int split;      // in as many parts of K
+  int a_rows;     // of a K-major a that a copy brings
+  int want_out;   // kGradient: h too
+  Ckpt gate, up;  // kGatedSave (codes by TMA)
   int* status;
   uint64_t limit_ns;
 };
@@ -70,12 +83,12 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int k16) {
              : sw128_kmajor_desc(saddr + (uint32_t)k16 * 32u);
 }
 
-template <bool kMn>
+template <bool kMn, int kRows>
 __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
                                              int mn, int k) {
   if constexpr (kMn) {
     tma_load_2d(dst, map, bar, mn, k);
-    tma_load_2d(dst + kBlockK * 128, map, bar, mn + 64, k);
+    if (kRows > 64) tma_load_2d(dst + kBlockK * 128, map, bar, mn + 64, k);
   } else {
     tma_load_2d(dst, map, bar, k, mn);
   }
@@ -132,61 +145,89 @@ constexpr int kBand = 8;
 struct Place {
   int m, n;  // first row of the tile; its column of tiles
 };
-__device__ __forceinline__ Place place_of(const Args& p, int64_t tile) {
-  const int64_t band = (int64_t)kBand * p.nt;
+__device__ __forceinline__ Place place_of(int mt, int nt, int64_t tile) {
+  const int64_t band = (int64_t)kBand * nt;
   const int b = (int)(tile / band);
   const int in = (int)(tile % band);
-  const int left = p.mt - b * kBand;
+  const int left = mt - b * kBand;
   const int rows = left < kBand ? left : kBand;
   return Place{(b * kBand + in % rows) * kTile, in / rows};
 }
 
-// Roles (192 threads): warp 0 TMA producer; warp 1 issues the MMAs (even CTA) or tells the even CTA
-// that a stage of this CTA has landed (odd CTA); warps 2-5 epilogue.  Every wait is bounded
+// A unit of work: a tile, or a part of one; its 64-k blocks, and where its sums go (-1: finished).
+struct Unit {
+  Place at;
+  int kb0, kb1, row;
+};
+__device__ __forceinline__ Unit unit_of(const Args& p, int num_kb, int64_t u) {
+  Unit r;
+  if (u < p.whole) {
+    r.at = place_of(p.mt, p.nt, u);
+    r.kb0 = 0;
+    r.kb1 = num_kb;
+    r.row = -1;
+  } else {
+    const int i = (int)(u - p.whole), part = i / p.rest;
+    r.at = place_of(p.mt, p.nt, p.whole + i % p.rest);
+    r.kb0 = (int)((int64_t)num_kb * part / p.split);
+    r.kb1 = (int)((int64_t)num_kb * (part + 1) / p.split);
+    r.row = i * kTile;
+  }
+  return r;
+}
+
+// Roles (320 threads): warp 0 TMA producer; warp 1 issues the MMAs (even CTA) or tells the even CTA
+// that a stage of this CTA has landed (odd CTA); warps 2-5 and 6-9 epilogue, each four half of the
+// columns.  (One half for all: 4096 x 2048 x 7168 saved in 145 us.)  Every wait is bounded
 // (MOE_ERR_TIMEOUT in the status word); a pair in which one gave up waits for its copies, MMAs and
 // stores in flight before it leaves.
-template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct>
+template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct, int kBN>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_kernel(const __grid_constant__ Maps maps, const Args p) {
-  using P = Plan<kEpi>;
+  using P = Plan<kEpi, kBN>;
+  constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes;
+  constexpr int kHalf = kBN / 2;  // columns of a half of the warps; gated: gate columns of a tile
   extern __shared__ uint8_t dsmem[];
-  __shared__ __align__(8) uint64_t full_bar[P::kStages];
-  __shared__ __align__(8) uint64_t empty_bar[P::kStages];
+  __shared__ __align__(8) uint64_t full_bar[kStages];
+  __shared__ __align__(8) uint64_t empty_bar[kStages];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
-  __shared__ __align__(8) uint64_t in_bar;
+  __shared__ __align__(8) uint64_t in_bar[2];
+  // kGatedSave: a half's largest value of each row for the other half: of up, and of gate
+  __shared__ float s_top[kEpi == kGatedSave ? 2 : 1][kEpi == kGatedSave ? 128 : 1];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t raw = smem_u32(dsmem);
   uint8_t* smem = dsmem + ((1024u - (raw & 1023u)) & 1023u);
-  uint8_t* boxes = smem + P::kStages * kStageBytes;
   const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort_flag = &s_abort;
   const uint32_t rank = cluster_ctarank();  // in the pair
   const int side = (int)rank;
   const int num_kb = (p.K - 1) / kBlockK + 1;
-  const int64_t tiles = (int64_t)p.mt * p.nt, units = tiles * p.split;
+  const int64_t units = p.whole + (int64_t)p.rest * p.split;
   const int64_t step = num_clusters_x();
 
   if (warp == 0) {
     if (elect_one()) {
-      for (int s = 0; s < P::kStages; ++s) {
+      prefetch_tensormap(&maps.a);
+      prefetch_tensormap(&maps.b);
+      for (int s = 0; s < kStages; ++s) {
         // the even CTA's stage is full when its copies and, by the forwarder, the odd CTA's landed
         mbar_init(&full_bar[s], side == 0 ? 2 : 1);
         mbar_init(&empty_bar[s], 1);
       }
       for (int b = 0; b < 2; ++b) {
         mbar_init(&tfull_bar[b], 1);
-        mbar_init(&tempty_bar[b], 8);  // an arrival per epilogue warp of both CTAs
+        mbar_init(&tempty_bar[b], 16);  // an arrival per epilogue warp of both CTAs
+        mbar_init(&in_bar[b], 1);
       }
       mbar_init(&drain_bar, 1);
-      mbar_init(&in_bar, 1);
       s_abort = 0;
       fence_mbar_init();
     }
   } else if (warp == 1) {
-    tmem_alloc_pair(&s_tmem, 512);
+    tmem_alloc_pair(&s_tmem, 2 * kBN);
     tmem_relinquish_pair();
   }
   __syncwarp();
@@ -194,6 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  pdl_wait();
+  pdl_trigger();
   int issued = 0;  // by the producer: stages asked for
   const uint32_t peer_abort = cluster_map(smem_u32(&s_abort), rank ^ 1u);
   // by one thread, or by all of a warp; on giving up the peer CTA is told too
@@ -202,28 +245,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     st_cluster_u32(peer_abort, 1u);
     return false;
   };
-  // k blocks of a part
-  auto part_of = [&](int64_t u, int& kb0, int& kb1) {
-    const int64_t part = u / tiles;
-    kb0 = (int)(num_kb * part / p.split);
-    kb1 = (int)(num_kb * (part + 1) / p.split);
-    return u % tiles;
-  };
 
   if (warp == 0) {
     if (elect_one()) {
-      Ring r(empty_bar, P::kStages, 1u);
+      Ring r(empty_bar, kStages, 1u);
       bool ok = true;
+      // Fewer than 128 rows of a: the others of its operand hold anything, and make rows of D that
+      // nothing reads.
+      const bool some = kAMn || side == 0 || p.M > kSlab;
+      const int bytes = kStageBytes - (kAMn ? 0 : (kSlab - (some ? p.a_rows : 0)) * kBlockK * 2);
       for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
-        int kb0, kb1;
-        const Place at = place_of(p, part_of(u, kb0, kb1));
-        const int ma = at.m + side * kSlab;
+        const Unit q = unit_of(p, num_kb, u);
+        const int ma = q.at.m + side * kSlab;
         // gated: the even CTA has the gate rows of b, the odd one the up rows; gate rows past N
         // are rows of up, whose columns the epilogue leaves out
-        const int nb = P::kGate || (kEpi == kParts && p.want_out)
-                           ? side * p.N + at.n * kSlab
-                           : at.n * kTile + side * kSlab;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        const int nb = gated(kEpi) ? side * p.N + q.at.n * kHalf : q.at.n * kBN + side * kHalf;
+        for (int kb = q.kb0; kb < q.kb1; ++kb) {
           if (!r.ready && !wait(r.bar(), r.parity)) {
             ok = false;
             break;
@@ -231,22 +268,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* st = smem + r.stage * kStageBytes;
           uint64_t* full = &full_bar[r.stage];
           r.next();
-          mbar_arrive_expect_tx(full, (uint32_t)kStageBytes);
-          load_operand<kAMn>(st, &maps.a, full, ma, kb * kBlockK);
-          load_operand<kBMn>(st + kOperandBytes, &maps.b, full, nb, kb * kBlockK);
+          mbar_arrive_expect_tx(full, (uint32_t)bytes);
+          if (some) load_operand<kAMn, kSlab>(st, &maps.a, full, ma, kb * kBlockK);
+          load_operand<kBMn, kHalf>(st + kOperandBytes, &maps.b, full, nb, kb * kBlockK);
           ++issued;
         }
       }
     }
   } else if (warp == 1 && side != 0) {
     if (elect_one()) {
-      Ring r(full_bar, P::kStages, 0u);
+      Ring r(full_bar, kStages, 0u);
       const uint32_t to = cluster_map(smem_u32(full_bar), 0u);
       bool ok = true;
       for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
-        int kb0, kb1;
-        part_of(u, kb0, kb1);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        const Unit q = unit_of(p, num_kb, u);
+        for (int kb = q.kb0; kb < q.kb1; ++kb) {
           if (!r.ready && !wait(r.bar(), r.parity)) {
             ok = false;
             break;
@@ -258,21 +294,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      Ring r(full_bar, P::kStages, 0u);
+      Ring r(full_bar, kStages, 0u);
       int buf = 0;
       uint32_t buf_phase = 0;
       bool ok = true;
       const uint32_t base = smem_u32(smem);
-      const uint32_t idesc = idesc_f16(256, kTile, DT<T>::kIsBF16) | (kAMn ? 1u << 15 : 0u) |
+      const uint32_t idesc = idesc_f16(256, kBN, DT<T>::kIsBF16) | (kAMn ? 1u << 15 : 0u) |
                              (kBMn ? 1u << 16 : 0u);
       const uint32_t empty_own = smem_u32(empty_bar), tfull_own = smem_u32(tfull_bar);
       for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
-        int kb0, kb1;
-        part_of(u, kb0, kb1);
+        const Unit q = unit_of(p, num_kb, u);
         if (!wait(&tempty_bar[buf], buf_phase ^ 1u)) break;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * kTile);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t d = tmem + (uint32_t)(buf * kBN);
+        for (int kb = q.kb0; kb < q.kb1; ++kb) {
           if (!r.ready && !wait(r.bar(), r.parity)) {
             ok = false;
             break;
@@ -285,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k)
             umma_f16_pair(d, operand_desc<kAMn>(sa, k), operand_desc<kBMn>(sb, k), idesc,
-                          (kb > kb0 || k > 0) ? 1u : 0u);
+                          (kb > q.kb0 || k > 0) ? 1u : 0u);
           umma_commit_both(empty_own + at, 0u);
         }
         if (!ok) break;
@@ -299,19 +334,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---- epilogue ----
+    const int half = (warp - 2) >> 2;  // of the columns
     const int row = (warp & 3) * 32 + lane;
-    const bool leader = threadIdx.x == 64;  // issues the stores
+    // issues the half's stores, or those of both
+    const bool leader = ((threadIdx.x - 64) & (P::kShared ? 255 : 127)) == 0;
     const uint32_t tb = tmem_lane(tmem, warp);
-    int buf = 0, box = 0;
+    uint8_t* boxes =
+        smem + kStages * kStageBytes + (P::kShared ? 0 : half * P::kBoxes * kBoxBytes);
+    uint64_t* in = &in_bar[P::kShared ? 0 : half];
+    int buf = 0;
     uint32_t buf_phase = 0, in_phase = 0;
-    auto sync = [] { named_bar_sync(1, 128); };
-    // A box that no store reads any more; two are in use.
+    auto sync = [&] {
+      if (P::kShared)
+        named_bar_sync(kAllEpilogue, 256);
+      else
+        named_bar_sync(1 + half, 128);
+    };
+    // The half's (first) box, once no store reads it any more.
     auto next_box = [&]() -> uint8_t* {
-      if (leader) store_wait_read<1>();
+      if (leader) store_wait_read<0>();
       sync();
-      uint8_t* b = boxes + box * kBoxBytes;
-      box ^= 1;
-      return b;
+      return boxes;
     };
     // Written boxes to the stores' view; then `issue` by the leader.
     auto publish = [&](auto issue) {
@@ -323,30 +366,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     for (int64_t u = cluster_id_x(); u < units; u += step) {
-      int kb0, kb1;
-      const int64_t tile = part_of(u, kb0, kb1);
-      const Place at = place_of(p, tile);
-      const int m = at.m + side * kSlab;
+      const Unit q = unit_of(p, num_kb, u);
+      const int m = q.at.m + side * kSlab;
       const bool live = m < p.M;  // a row of this CTA is one of D's (uniform)
+      const bool part = q.row >= 0;
+      const int n0 = q.at.n * kHalf + (P::kShared ? 0 : half * 64);  // gated: the box's first column
+      const bool input = kEpi == kGradient && live && !part;
       if constexpr (kEpi == kGradient) {
-        if (leader && live) {
+        if (leader && input) {
           store_wait_read<0>();
-          mbar_arrive_expect_tx(&in_bar, 2 * kBoxBytes);
-          tma_load_2d(boxes, &maps.in, &in_bar, at.n * kSlab, m);
-          tma_load_2d(boxes + kBoxBytes, &maps.in, &in_bar, at.n * kSlab + 64, m);
+          mbar_arrive_expect_tx(in, kBoxBytes);
+          tma_load_2d(boxes, &maps.in, in, n0, m);
         }
       }
-      const bool got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
+      bool got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
       tc_fence_after();
-      // the four warps leave together: named barriers are between them
-      if (!named_bar_and(2, 128, got)) break;
-      const uint32_t d = tb + (uint32_t)(buf * kTile);
-      if constexpr (kEpi == kPlain) {
+      if (input) {
+        got = __all_sync(kAll, got && wait(in, in_phase));
+        if (got) in_phase ^= 1u;
+      }
+      // the eight warps leave together: named barriers are between them
+      if (!named_bar_and(kAllEpilogue, 256, got)) break;
+      const uint32_t d = tb + (uint32_t)(buf * kBN);
+      // gated: this warp's 32-column pieces of the gate columns, and where they lie in the box
+      constexpr int kPieces = kHalf / 64;
+      const int col0 = half * (kHalf / 2), piece0 = P::kShared ? half : 0;
+      if (kBN == kTile && part) {
         for (int c = 0; c < 4 && live; ++c) {
-          const int n = at.n * kTile + c * 64;
-          if (n >= p.N) break;
+          const int col = half * 128 + c * 32;
+          float v[32];
+          tmem_ld_x32(d + (uint32_t)col, v);
+          uint8_t* b = next_box();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(box_at(b, row, j)) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          publish([&] { tma_store_2d(&maps.parts, b, col, q.row + side * kSlab); });
+        }
+      } else if constexpr (kEpi == kPlain) {
+        for (int c = 0; c < kHalf / 64 && live; ++c) {
+          const int col = half * kHalf + c * 64, to = q.at.n * kBN + col;
+          if (to >= p.N) break;
           float v[64];
-          tmem_ld_x64(d + (uint32_t)(c * 64), v);
+          tmem_ld_x64(d + (uint32_t)col, v);
           uint8_t* b = next_box();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -355,35 +417,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 8; ++i) w[i] = v[j * 8 + i];
             *box_at(b, row, j) = pack<T>(w);
           }
-          publish([&] { tma_store_2d(&maps.o0, b, n, m); });
-        }
-      } else if constexpr (kEpi == kParts) {
-        const int part_row = (int)(u / tiles) * p.mt * kTile + m;
-        for (int c = 0; c < 8; ++c) {
-          float v[32];
-          tmem_ld_x32(d + (uint32_t)(c * 32), v);
-          uint8_t* b = next_box();
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4*>(box_at(b, row, j)) =
-                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          publish([&] { tma_store_2d(&maps.o0, b, at.n * kTile + c * 32, part_row); });
+          publish([&] { tma_store_2d(&maps.o0, b, to, m); });
         }
       } else if constexpr (kEpi == kGated || kEpi == kGatedSave) {
         float top_g = 0.0f, top_u = 0.0f;
-        for (int c = 0; c < 2 && live; ++c) {
-          const int n = at.n * kSlab + c * 64;
-          if (n >= p.N) break;
+        if (live && n0 < p.N) {
           uint8_t* b = next_box();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kPieces; ++h) {
             float g[32], v[32];
-            tmem_ld_x32(d + (uint32_t)(c * 64 + h * 32), g);
-            tmem_ld_x32(d + (uint32_t)(kSlab + c * 64 + h * 32), v);
+            tmem_ld_x32(d + (uint32_t)(col0 + h * 32), g);
+            tmem_ld_x32(d + (uint32_t)(kHalf + col0 + h * 32), v);
             if constexpr (kEpi == kGatedSave) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                if (n + h * 32 + (i & ~7) < p.N) {  // N is a multiple of 8
+                if (n0 + h * 32 + (i & ~7) < p.N) {  // N is a multiple of 8
                   top_g = fmaxf(top_g, finite_abs(g[i]));
                   top_u = fmaxf(top_u, finite_abs(v[i]));
                 }
@@ -394,78 +442,77 @@ __global__ void __launch_bounds__(kThreads, 1)
               float w[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) w[i] = gate_value<kAct>(g[j * 8 + i]) * v[j * 8 + i];
-              *box_at(b, row, h * 4 + j) = pack<T>(w);
+              *box_at(b, row, (piece0 + h) * 4 + j) = pack<T>(w);
             }
           }
-          publish([&] { tma_store_2d(&maps.o0, b, n, m); });
+          publish([&] { tma_store_2d(&maps.o0, b, n0, m); });
         }
         if constexpr (kEpi == kGatedSave) {
-          for (int half = 0; half < 2 && live; ++half) {
+          // the first half of the warps has the gate's codes, the second up's
+          s_top[half][row] = half == 0 ? top_u : top_g;
+          named_bar_sync(kAllEpilogue, 256);
+          if (live) {
             const Ckpt& to = half == 0 ? p.gate : p.up;
-            const int e = fp8_exponent(half == 0 ? top_g : top_u);
-            if (m + row < p.M)
-              to.scales[(int64_t)(m + row) * p.nt + at.n] = fp8_scale(e);
+            const int e = fp8_exponent(fmaxf(half == 0 ? top_g : top_u, s_top[half ^ 1][row]));
+            if (m + row < p.M) to.scales[(int64_t)(m + row) * p.nt + q.at.n] = fp8_scale(e);
             const float inv = fp8_scale(-e);
             uint8_t* b = next_box();
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               float v[32];
               tmem_ld_x32(d + (uint32_t)(half * kSlab + h * 32), v);
-              uint32_t q[8];
+              uint32_t c[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                q[i] = at.n * kSlab + h * 32 + ((4 * i) & ~7) < p.N
+                c[i] = q.at.n * kSlab + h * 32 + ((4 * i) & ~7) < p.N
                            ? fp8_pack4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv)
                            : 0u;
-              *box_at(b, row, 2 * h) = make_uint4(q[0], q[1], q[2], q[3]);
-              *box_at(b, row, 2 * h + 1) = make_uint4(q[4], q[5], q[6], q[7]);
+              *box_at(b, row, 2 * h) = make_uint4(c[0], c[1], c[2], c[3]);
+              *box_at(b, row, 2 * h + 1) = make_uint4(c[4], c[5], c[6], c[7]);
             }
             publish([&] {
-              tma_store_2d(half == 0 ? &maps.o1 : &maps.o2, b, at.n * kSlab, m);
+              tma_store_2d(half == 0 ? &maps.o1 : &maps.o2, b, q.at.n * kSlab, m);
             });
           }
         }
       } else {
-        if (live) {
-          const bool there = __all_sync(kAll, wait(&in_bar, in_phase));
-          in_phase ^= 1u;
-          if (!named_bar_and(2, 128, there)) break;
-          uint8_t *bg = boxes + 2 * kBoxBytes, *bu = boxes + 3 * kBoxBytes;
-          for (int c = 0; c < 2; ++c) {
-            const int n = at.n * kSlab + c * 64;
-            if (n >= p.N) break;
-            uint8_t* bh = boxes + c * kBoxBytes;
-            if (c > 0) {
-              if (leader) store_wait_read<0>();
-              sync();
-            }
+        if (live && n0 < p.N) {
+          // d_out lies in the first box, where its place takes d_gate; h waits in registers until
+          // the store of d_up has read the second one
+          uint8_t *bg = boxes, *bu = boxes + kBoxBytes;
+          uint4 hold[kPieces * 4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float g[32], v[32];
-              tmem_ld_x32(d + (uint32_t)(c * 64 + h * 32), g);
-              tmem_ld_x32(d + (uint32_t)(kSlab + c * 64 + h * 32), v);
+          for (int h = 0; h < kPieces; ++h) {
+            float g[32], v[32];
+            tmem_ld_x32(d + (uint32_t)(col0 + h * 32), g);
+            tmem_ld_x32(d + (uint32_t)(kHalf + col0 + h * 32), v);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float dh[8], dg[8], du[8], hv[8];
-                unpack<T>(*box_at(bh, row, h * 4 + j), dh);
+            for (int j = 0; j < 4; ++j) {
+              float dh[8], dg[8], du[8], hv[8];
+              unpack<T>(*box_at(bg, row, (piece0 + h) * 4 + j), dh);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  float a, s;
-                  gate_slope<kAct>(g[j * 8 + i], a, s);
-                  hv[i] = a * v[j * 8 + i];
-                  dg[i] = dh[i] * v[j * 8 + i] * s;
-                  du[i] = dh[i] * a;
-                }
-                *box_at(bh, row, h * 4 + j) = pack<T>(hv);
-                *box_at(bg, row, h * 4 + j) = pack<T>(dg);
-                *box_at(bu, row, h * 4 + j) = pack<T>(du);
+              for (int i = 0; i < 8; ++i) {
+                float a, s;
+                gate_slope<kAct>(g[j * 8 + i], a, s);
+                hv[i] = a * v[j * 8 + i];
+                dg[i] = dh[i] * v[j * 8 + i] * s;
+                du[i] = dh[i] * a;
               }
+              hold[h * 4 + j] = pack<T>(hv);
+              *box_at(bg, row, (piece0 + h) * 4 + j) = pack<T>(dg);
+              *box_at(bu, row, (piece0 + h) * 4 + j) = pack<T>(du);
             }
-            publish([&] {
-              if (p.want_out) tma_store_2d(&maps.o0, bh, n, m);
-              tma_store_2d(&maps.o1, bg, n, m);
-              tma_store_2d(&maps.o2, bu, n, m);
-            });
+          }
+          publish([&] {
+            tma_store_2d(&maps.o1, bg, n0, m);
+            tma_store_2d(&maps.o2, bu, n0, m);
+          });
+          if (p.want_out) {
+            if (leader) store_wait_read<0>();
+            sync();
+#pragma unroll
+            for (int j = 0; j < kPieces * 4; ++j) *box_at(bu, row, piece0 * 4 + j) = hold[j];
+            publish([&] { tma_store_2d(&maps.o0, bu, n0, m); });
           }
         }
       }
@@ -477,10 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (leader) {
       store_wait_all();
-      // a tile whose d_out was asked for and never used
+      // d_out of a tile that gave up may still be on its way
       if (kEpi == kGradient && *abort_flag) {
         const uint64_t t = global_timer_ns();
-        while (!mbar_try_wait(&in_bar, in_phase))
+        while (!mbar_try_wait(in, in_phase))
           if (global_timer_ns() - t > kDrainNs / 100) break;
       }
     }
@@ -490,22 +537,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   // (the even CTA's stages are full only with the odd CTA's copies told of: else a second passes)
-  if (*abort_flag) land_copies(full_bar, issued, P::kStages);
+  if (*abort_flag) land_copies(full_bar, issued, kStages);
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, 2 * kBN);
   }
 }
 
-// ---- split K: the parts' sums, and the epilogue on them ---------------------------------------
-// A warp takes a row and 128 columns (gated: 128 gate and 128 up columns), a lane four of them; the
-// parts are added in their order.  They were written just before and lie in L2.
+// ---- tiles split along K: the parts' sums, and the epilogue on them ----------------------------
+// A warp takes a row of a tile and 128 columns (gated: 128 gate and 128 up columns), a lane four of
+// them; the parts are added in their order.  They were written just before and lie in L2.
 struct JoinArgs {
-  int M, N, nt, split, want_out;
-  int64_t pitch, part;  // elements from row to row and part to part
-  const float* sums;
-  void *o0, *o1, *o2;  // as Maps
+  int M, N, mt, nt, rows;  // rows of a tile that may be any
+  int64_t whole;
+  int rest, split, want_out;
+  const float* sums;  // [split][rest][kTile][kTile]
+  void *o0, *o1;      // as Maps; d_pre
   const void* in;
   Ckpt gate, up;
 };
@@ -525,32 +573,43 @@ __device__ __forceinline__ void put4(void* base, int64_t at, const float (&v)[4]
 template <typename T, int kEpi, int kAct>
 __global__ void __launch_bounds__(256) join_kernel(const JoinArgs p) {
   pdl_wait();
-  constexpr bool kGate = Plan<kEpi>::kGate;
+  pdl_trigger();
+  constexpr int kGroups = gated(kEpi) ? 1 : 2;
   const int lane = threadIdx.x & 31;
-  const int groups = kGate ? p.nt : 2 * p.nt;  // of 128 outputs
   const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t m = at / groups;
-  const int g = (int)(at % groups);
-  const int n = g * kSlab + lane * 4;  // this lane's first output
+  const int g = (int)(at % kGroups);
+  const int row = (int)(at / kGroups % p.rows);
+  const int64_t tile = at / kGroups / p.rows;
+  if (tile >= p.rest) return;
+  const Place q = place_of(p.mt, p.nt, p.whole + tile);
+  const int64_t m = (int64_t)q.m + row;
+  const int n = gated(kEpi) ? q.n * kSlab + lane * 4 : q.n * kTile + g * kSlab + lane * 4;
   if (m >= p.M) return;
-  auto sum = [&](int64_t col) {
-    const float* from = p.sums + m * p.pitch + col;
+  const int64_t part = (int64_t)p.rest * kTile * kTile;
+  auto sum = [&](int col) {
+    const float* from = p.sums + (tile * kTile + row) * kTile + col;
     float4 s = *reinterpret_cast<const float4*>(from);
-    for (int i = 1; i < p.split; ++i)
-      s = add4(s, *reinterpret_cast<const float4*>(from + i * p.part));
+    int i = 1;
+    for (; i + 3 <= p.split; i += 3) {  // three on their way at a time
+      const float4 a = *reinterpret_cast<const float4*>(from + i * part);
+      const float4 b = *reinterpret_cast<const float4*>(from + (i + 1) * part);
+      const float4 c = *reinterpret_cast<const float4*>(from + (i + 2) * part);
+      s = add4(add4(add4(s, a), b), c);
+    }
+    for (; i < p.split; ++i) s = add4(s, *reinterpret_cast<const float4*>(from + i * part));
     return s;
   };
   const bool live = n < p.N;  // N is a multiple of 8
-  if constexpr (!kGate) {
+  if constexpr (!gated(kEpi)) {
     if (!live) return;
-    const float4 s = sum(n);
+    const float4 s = sum(g * kSlab + lane * 4);
     const float v[4] = {s.x, s.y, s.z, s.w};
     put4<T>(p.o0, m * p.N + n, v);
   } else {
     float4 sg = make_float4(0.0f, 0.0f, 0.0f, 0.0f), su = sg;
     if (live) {
-      sg = sum((int64_t)g * kTile + lane * 4);
-      su = sum((int64_t)g * kTile + kSlab + lane * 4);
+      sg = sum(lane * 4);
+      su = sum(kSlab + lane * 4);
     }
     const float gv[4] = {sg.x, sg.y, sg.z, sg.w}, uv[4] = {su.x, su.y, su.z, su.w};
     if constexpr (kEpi == kGradient) {
@@ -586,8 +645,8 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinArgs p) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
           const int e = fp8_exponent(top);
-          if (lane == 0) to.scales[m * p.nt + g] = fp8_scale(e);
-          *reinterpret_cast<uint32_t*>(to.codes + (m * p.nt + g) * kCkptGroup + lane * 4) =
+          if (lane == 0) to.scales[m * p.nt + q.n] = fp8_scale(e);
+          *reinterpret_cast<uint32_t*>(to.codes + (m * p.nt + q.n) * kCkptGroup + lane * 4) =
               live ? fp8_pack4(v[0], v[1], v[2], v[3], fp8_scale(-e)) : 0u;
         }
       }
@@ -649,17 +708,40 @@ bool map16(CUtensorMap* m, int dtype, const void* base, int64_t inner, int64_t r
                   (uint32_t)box_rows);
 }
 
-// Parts of K: as many as the SM pairs take tiles at once, of at least kPartBlocks 64-k blocks.
-constexpr int kPartBlocks = 8;
-constexpr int kMaxSplit = 16;
-int split_of(int64_t tiles, int64_t K) {
+// Which tiles are split, and in how many parts of K.  `pairs` take their tiles in turn; the last
+// `rest` of them, which would leave most pairs idle, are split so that all have a part.  A part has
+// at least eight 64-k blocks, and splitting has to gain more blocks than joining costs.
+struct Split {
+  int64_t whole;
+  int rest, split;
+};
+constexpr int kMaxSplit = 16, kPartBlocks = 8, kJoinBlocks = 16;
+Split split_of(int64_t tiles, int64_t K) {
   const int64_t pairs = num_sms() / 2, num_kb = ceil_div(K, kBlockK);
-  int split = 1;
-  while (split < kMaxSplit && tiles * (split + 1) <= pairs && num_kb >= (split + 1) * kPartBlocks)
-    ++split;
-  return split;
+  const int64_t rest = tiles % pairs;
+  int64_t split = rest > 0 ? pairs / rest : 1;
+  if (split > num_kb / kPartBlocks) split = num_kb / kPartBlocks;
+  if (split > kMaxSplit) split = kMaxSplit;
+  if (split < 2 || num_kb - ceil_div(num_kb, split) <= kJoinBlocks) return Split{tiles, 0, 1};
+  return Split{tiles - rest, (int)rest, (int)split};
 }
-int64_t tiles_n(int64_t N, bool gated) { return ceil_div(N, gated ? kSlab : kTile); }
+int64_t tiles_n(int64_t N, bool gate, int bn) { return ceil_div(N, gate ? bn / 2 : bn); }
+
+// Tiles of 128 columns where those of 256 leave pairs idle.  In units of a 64-k block of a 256-column
+// tile: a narrow one costs 0.65 (the loads of a, which it shares with fewer columns), a tile's start
+// and epilogue about 16 and 12.
+bool narrow(int64_t M, int64_t N, int64_t K, bool gate) {
+  const int64_t pairs = num_sms() / 2, mt = ceil_div(M, kTile), num_kb = ceil_div(K, kBlockK);
+  const int64_t wide_tiles = mt * tiles_n(N, gate, kTile);
+  const Split sp = split_of(wide_tiles, K);
+  double wide = (double)(sp.whole / pairs) * (num_kb + 16);
+  if (sp.rest > 0)
+    wide += ceil_div(num_kb, sp.split) + 16 + kJoinBlocks;
+  else if (sp.whole % pairs)
+    wide += num_kb + 16;
+  const double thin = (double)ceil_div(mt * tiles_n(N, gate, 128), pairs) * (0.65 * num_kb + 12);
+  return thin < wide;
+}
 
 struct Problem {
   int dtype, M, N, K;
@@ -672,76 +754,35 @@ struct Problem {
   int* status;
 };
 
-template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct>
-cudaError_t run_tiles(const Maps& maps, const Args& p, cudaStream_t s) {
-  constexpr auto kern = dense_kernel<T, kAMn, kBMn, kEpi, kAct>;
-  const int pairs = max_pairs<kern>(Plan<kEpi>::kSmem);
-  if (pairs <= 0) return cudaErrorInvalidConfiguration;
-  const int64_t units = (int64_t)p.mt * p.nt * p.split;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)Plan<kEpi>::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps, p);
-}
-
-template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct>
-cudaError_t run(const Problem& q, cudaStream_t s) {
-  constexpr bool kGate = Plan<kEpi>::kGate;
+template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct, int kBN>
+cudaError_t run_tiles(const Problem& q, cudaStream_t s) {
+  constexpr bool kGate = gated(kEpi);
+  using P = Plan<kEpi, kBN>;
+  constexpr auto kern = dense_kernel<T, kAMn, kBMn, kEpi, kAct, kBN>;
   Args p = {};
   p.M = q.M;
   p.N = q.N;
   p.K = q.K;
   p.mt = (int)ceil_div(q.M, kTile);
-  p.nt = (int)tiles_n(q.N, kGate);
-  p.split = split_of((int64_t)p.mt * p.nt, q.K);
+  p.nt = (int)tiles_n(q.N, kGate, kBN);
+  const int64_t tiles = (int64_t)p.mt * p.nt;
+  const Split sp = kBN == kTile ? split_of(tiles, q.K) : Split{tiles, 0, 1};
+  p.whole = sp.whole;
+  p.rest = sp.rest;
+  p.split = sp.split;
+  p.a_rows = q.M < kSlab ? (q.M + 7) / 8 * 8 : kSlab;
+  p.want_out = q.o0 != nullptr;
   p.gate = q.gate;
   p.up = q.up;
   p.status = q.status;
   p.limit_ns = wait_limit_ns();
   Maps maps;
-  const int64_t rows_b = kGate ? (int64_t)2 * q.N : q.N;
+  const int64_t N = q.N, rows_b = kGate ? 2 * N : N;
   bool ok = kAMn ? map16(&maps.a, q.dtype, q.a, q.M, q.K, q.a_pitch, kBlockK)
-                 : map16(&maps.a, q.dtype, q.a, q.K, q.M, q.a_pitch, kSlab);
+                 : map16(&maps.a, q.dtype, q.a, q.K, q.M, q.a_pitch, p.a_rows);
   ok = ok && (kBMn ? map16(&maps.b, q.dtype, q.b, rows_b, q.K, rows_b, kBlockK)
-                   : map16(&maps.b, q.dtype, q.b, q.K, rows_b, q.K, kSlab));
-  maps.o0 = maps.o1 = maps.o2 = maps.in = maps.a;  // those a kernel does not use
-  if (p.split > 1) {
-    const int64_t pitch = (int64_t)p.nt * kTile, rows = (int64_t)p.mt * kTile;
-    p.want_out = kGate;  // how the parts' columns lie
-    ok = ok && make_map(&maps.o0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, q.parts, (uint64_t)pitch,
-                        (uint64_t)(rows * p.split), (uint64_t)pitch * 4, kSlab);
-    if (!ok) return cudaErrorInvalidValue;
-    const cudaError_t e = run_tiles<T, kAMn, kBMn, kParts, 0>(maps, p, s);
-    if (e != cudaSuccess) return e;
-    JoinArgs j = {};
-    j.M = q.M;
-    j.N = q.N;
-    j.nt = p.nt;
-    j.split = p.split;
-    j.want_out = kEpi != kGradient || q.o0 != nullptr;
-    j.pitch = pitch;
-    j.part = rows * pitch;
-    j.sums = q.parts;
-    j.o0 = q.o0;
-    j.o1 = q.o1;
-    j.in = q.in;
-    j.gate = q.gate;
-    j.up = q.up;
-    const int64_t warps = (int64_t)q.M * (kGate ? p.nt : 2 * p.nt);
-    return launch_k(join_kernel<T, kEpi, kAct>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s,
-                    true, j);
-  }
-  p.want_out = q.o0 != nullptr;
-  const int64_t N = q.N;
+                   : map16(&maps.b, q.dtype, q.b, q.K, rows_b, q.K, kBN / 2));
+  maps.o0 = maps.o1 = maps.o2 = maps.in = maps.parts = maps.a;  // those that are not used
   if (q.o0) ok = ok && map16(&maps.o0, q.dtype, q.o0, N, q.M, N, kSlab);
   if constexpr (kEpi == kGradient) {
     ok = ok && map16(&maps.o1, q.dtype, q.o1, N, q.M, 2 * N, kSlab) &&
@@ -755,8 +796,56 @@ cudaError_t run(const Problem& q, cudaStream_t s) {
          make_map(&maps.o2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.up.codes, width, (uint64_t)q.M,
                   width, kSlab);
   }
+  if (p.rest > 0)
+    ok = ok && make_map(&maps.parts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, q.parts, kTile,
+                        (uint64_t)p.rest * p.split * kTile, kTile * 4, kSlab);
   if (!ok) return cudaErrorInvalidValue;
-  return run_tiles<T, kAMn, kBMn, kEpi, kAct>(maps, p, s);
+  const int pairs = max_pairs<kern>(P::kSmem);
+  if (pairs <= 0) return cudaErrorInvalidConfiguration;
+  const int64_t units = p.whole + (int64_t)p.rest * p.split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)P::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps, p);
+  if (e != cudaSuccess || p.rest == 0) return e;
+  JoinArgs j = {};
+  j.M = q.M;
+  j.N = q.N;
+  j.mt = p.mt;
+  j.nt = p.nt;
+  j.rows = q.M < kTile ? q.M : kTile;
+  j.whole = p.whole;
+  j.rest = p.rest;
+  j.split = p.split;
+  j.want_out = p.want_out;
+  j.sums = q.parts;
+  j.o0 = q.o0;
+  j.o1 = q.o1;
+  j.in = q.in;
+  j.gate = q.gate;
+  j.up = q.up;
+  const int64_t warps = (int64_t)p.rest * j.rows * (kGate ? 1 : 2);
+  return launch_k(join_kernel<T, kEpi, kAct>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s,
+                  true, j);
+}
+
+template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct>
+cudaError_t run(const Problem& q, cudaStream_t s) {
+  if constexpr (kEpi != kGatedSave) {  // whose checkpoints have 128 channels to a scale
+    if (narrow(q.M, q.N, q.K, gated(kEpi))) return run_tiles<T, kAMn, kBMn, kEpi, kAct, 128>(q, s);
+  }
+  return run_tiles<T, kAMn, kBMn, kEpi, kAct, kTile>(q, s);
 }
 
 template <int kEpi>
@@ -771,11 +860,10 @@ cudaError_t run_gated(int act, const Problem& q, cudaStream_t s) {
 
 }  // namespace
 
-size_t dense_split_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+size_t dense_split_bytes(int64_t M, int64_t N, int64_t K, bool gate) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  const int64_t mt = ceil_div(M, kTile), nt = tiles_n(N, gated);
-  const int split = split_of(mt * nt, K);
-  return split > 1 ? (size_t)(mt * nt * split) * kTile * kTile * sizeof(float) : 0;
+  const Split sp = split_of(ceil_div(M, kTile) * tiles_n(N, gate, kTile), K);
+  return (size_t)sp.rest * sp.split * kTile * kTile * sizeof(float);
 }
 
 cudaError_t launch_dense_nn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,

@@ -31,8 +31,12 @@ moe_status_t check_gated(const moe_gated_linear_t* p) {
 // Both parts of a checkpoint, or neither.
 bool both(const void* codes, const void* scales) { return (codes != nullptr) == (scales != nullptr); }
 
-// Few tokens that save nothing: the weights are streamed (dense_rows.cu).
-bool few_rows(const moe_gated_linear_t& p, bool save) { return !save && p.T <= 16; }
+// Few tokens that save nothing: the weights are streamed (dense_rows.cu).  From three tokens on only
+// where there are too few weights for the tiles of dense.cu to fill the SMs (8 x 2048 x 7168: 22.0 us
+// against 26; 8 x 18432 x 7168: 113 against 88).
+bool few_rows(const moe_gated_linear_t& p, bool save) {
+  return !save && (p.T <= 2 || (p.T <= 16 && 2 * (int64_t)p.F * p.H <= 1 << 26));
+}
 
 size_t gated_bytes(const moe_gated_linear_t& p) {
   return kHeaderBytes + align256(dense_split_bytes(p.T, p.F, p.H, true));
@@ -81,6 +85,20 @@ constexpr int32_t kMaxW4Rows = 1 << 20;
 moe_status_t check_w4(int32_t T, int32_t N, int32_t K) {
   if (T < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
   return K % 32 != 0 || T > kMaxW4Rows ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+moe_status_t check_linear_w4(const moe_linear_t* g) {
+  if (!g || !dtype_ok(g->dtype)) return MOE_ERR_INVALID_ARG;
+  if (g->activation < MOE_LINEAR_NONE || g->activation > MOE_LINEAR_RELU2)
+    return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = check_w4(g->T, g->N, g->K);
+  return st == MOE_OK && g->out_f32 ? MOE_ERR_UNSUPPORTED : st;
+}
+moe_status_t check_gated_w4(const moe_gated_linear_t* p) {
+  if (!p || !dtype_ok(p->dtype)) return MOE_ERR_INVALID_ARG;
+  if (p->activation < MOE_ACT_SILU || p->activation > MOE_ACT_RELU2) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = check_w4(p->T, p->F, p->H);
+  if (st != MOE_OK) return st;
+  return p->activation == MOE_ACT_RELU2 || p->F > INT32_MAX / 2 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 }  // namespace
@@ -246,16 +264,16 @@ moe_status_t moe_checkpoint_restore(int32_t T, int32_t C, int32_t dtype, const u
       launch_restore(dtype, T, C, CkptIn{codes, scales}, out, (cudaStream_t)stream));
 }
 
+size_t moe_linear_w4a16_workspace_size(const moe_linear_t* g) {
+  return check_linear_w4(g) == MOE_OK ? kHeaderBytes : 0;
+}
+
 moe_status_t moe_linear_w4a16(const moe_linear_t* g, const void* x, const uint8_t* codes,
                               const uint8_t* scales, const float* alpha, const void* bias,
                               const void* residual, void* out, void* workspace,
                               size_t workspace_bytes, void* stream) {
-  if (!g || !dtype_ok(g->dtype)) return MOE_ERR_INVALID_ARG;
-  if (g->activation < MOE_LINEAR_NONE || g->activation > MOE_LINEAR_RELU2)
-    return MOE_ERR_INVALID_ARG;
-  const moe_status_t st = check_w4(g->T, g->N, g->K);
+  const moe_status_t st = check_linear_w4(g);
   if (st != MOE_OK) return st;
-  if (g->out_f32) return MOE_ERR_UNSUPPORTED;
   if (!workspace || !codes || !scales || !alpha || (g->T > 0 && (!x || !out)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(x, codes, scales, bias, residual, out, workspace)) return MOE_ERR_INVALID_ARG;
@@ -268,15 +286,16 @@ moe_status_t moe_linear_w4a16(const moe_linear_t* g, const void* x, const uint8_
   return from_cuda(launch_rows(c, (cudaStream_t)stream));
 }
 
+size_t moe_gated_linear_w4a16_workspace_size(const moe_gated_linear_t* p) {
+  return check_gated_w4(p) == MOE_OK ? kHeaderBytes : 0;
+}
+
 moe_status_t moe_gated_linear_w4a16(const moe_gated_linear_t* p, const void* x,
                                     const uint8_t* codes, const uint8_t* scales, const float* alpha,
                                     void* out, void* workspace, size_t workspace_bytes,
                                     void* stream) {
-  if (!p || !dtype_ok(p->dtype)) return MOE_ERR_INVALID_ARG;
-  if (p->activation < MOE_ACT_SILU || p->activation > MOE_ACT_RELU2) return MOE_ERR_INVALID_ARG;
-  const moe_status_t st = check_w4(p->T, p->F, p->H);
+  const moe_status_t st = check_gated_w4(p);
   if (st != MOE_OK) return st;
-  if (p->activation == MOE_ACT_RELU2 || p->F > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   if (!workspace || !codes || !scales || !alpha || (p->T > 0 && (!x || !out)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(x, codes, scales, out, workspace)) return MOE_ERR_INVALID_ARG;
