@@ -59,28 +59,28 @@ struct Block {
   static constexpr int kK = 8 * kLaneK;        // k of a block: two vectors of four lanes, 128 bytes
   static constexpr int kUnits = kLaneK / 8;    // 16-byte units of x that go with a vector
 };
-// How weights lie: 16 bits; 4 bits with the scales of a block on 16 bytes (K a multiple of 256); 4
-// bits with any K.
+// How weights lie: 16 bits; 4 bits, a block's 16 scales of a row on 16 bytes (K a multiple of 256); 4
+// bits with any K, whose scales start on any even byte.
 enum Kind { kBits16, kBits4, kBits4Any };
-// A warp's stage: two vectors of 16 rows per lane, and the scales: 16 bytes a row, or for any K the
-// four-byte word that holds a lane's two.
+// Bytes of a row that hold a block's scales, and a warp's stage: two vectors of 16 rows per lane, and
+// the scales.
+template <Kind kKind>
+constexpr int scale_bytes() {
+  return kKind == kBits16 ? 0 : kKind == kBits4 ? 16 : 32;
+}
 template <Kind kKind, int kMT>
 constexpr int stage_bytes() {
-  return kMT * (2 * 2 * 32 * 16 + (kKind == kBits16 ? 0 : kKind == kBits4 ? 16 * 16 : 2 * 2 * 32 * 4));
+  return kMT * (2 * 2 * 32 * 16 + 16 * scale_bytes<kKind>());
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
                : "memory");
 }
-// Zeros where not `in`; nothing is read then.
-__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool in) {
+// `bytes` of the 16; zeros behind them.
+__device__ __forceinline__ void copy16_part(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(in ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -94,11 +94,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(a)
                : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds4(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t lds2(uint32_t a) {
@@ -144,6 +139,7 @@ __device__ __forceinline__ void finish(const RowsCall& p, int64_t row, int64_t n
 template <typename T, Kind kKind, int kMT, int kNT, bool kGated, int kStages>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int parts, int chunk) {
   constexpr bool kW4 = kKind != kBits16;
+  constexpr int kScaleBytes = scale_bytes<kKind>();
   using B = Block<kW4>;
   using X = typename std::conditional<kW4, __half, T>::type;  // what the MMAs take
   constexpr int kCols = 8 * kNT;
@@ -180,17 +176,24 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
     for (int h = 0; h < 2; ++h)
       from[i][h] = (kW4 ? p.codes : static_cast<const uint8_t*>(p.w)) + row_of(i, h * 8 + g) * pitch +
                    (int64_t)first * 128 + t * 16;
-  const uint8_t* scale_from = nullptr;  // kBits4: of row lane, as one of 16 kMT
-  if constexpr (kKind == kBits4)
-    scale_from = p.scales + row_of(lane >> 4 & (kMT - 1), lane & 15) * (p.K / 16) + (int64_t)first * 16;
-  const int64_t scale_end =
-      kKind == kBits4Any ? (kGated ? 2 * (int64_t)p.N : p.N) * (p.K / 16) : 0;
-  int64_t scale_at[kMT][2];  // kBits4Any: the rows' first scales
+  // 4 bits: lanes 0-15 copy a row's 16 bytes each, or the first half of its 32 and lanes 16-31 the
+  // other; `scale_in` is where this lane's first scale lies in them, which is the same in every
+  // block.  (Rows 4-7 and 12-15 have their halves swapped: eight rows' reads touch different banks.)
+  const uint8_t* scale_from[kMT];
+  int scale_in[kMT][2];
+  const uint8_t* scale_end = nullptr;
+  if constexpr (kW4) {
+    scale_end = p.scales + (kGated ? 2 * (int64_t)p.N : p.N) * (p.K / 16);
 #pragma unroll
-  for (int i = 0; i < kMT; ++i)
+    for (int i = 0; i < kMT; ++i) {
+      const int64_t at = row_of(i, lane & 15) * (p.K / 16) + (int64_t)first * 16;
+      scale_from[i] = p.scales + (at & ~int64_t(15)) + (lane >> 4) * 16;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      scale_at[i][h] = kKind == kBits4Any ? row_of(i, h * 8 + g) * (p.K / 16) : 0;
+      for (int h = 0; h < 2; ++h)
+        scale_in[i][h] =
+            (kKind == kBits4 ? 0 : (int)(row_of(i, h * 8 + g) * (p.K / 16) & 15)) + t * 2;
+    }
+  }
 
   // Vector (i, h, v) of a lane at ((i * 2 + h) * 2 + v) * 512 of its stage, 16 bytes a lane.
   auto load = [&](int b, int stage) {
@@ -213,33 +216,29 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
           for (int i = 0; i < kMT; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              copy16_if(to + (uint32_t)(((i * 2 + h) * 2 + v) * 512),
-                        in ? from[i][h] + v * 64 : from[i][h] - t * 16, in);
+              copy16_part(to + (uint32_t)(((i * 2 + h) * 2 + v) * 512),
+                          in ? from[i][h] + v * 64 : from[i][h] - t * 16, in ? 16 : 0);
         }
       }
 #pragma unroll
       for (int i = 0; i < kMT; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) from[i][h] += 128;
-      if constexpr (kKind == kBits4) {
-        if (kMT == 2 || lane < 16) copy16(to + kScaleAt, scale_from);
-        scale_from += 16;
-      }
-      if constexpr (kKind == kBits4Any) {
-        // the aligned words that hold the lane's two scales; the tensor may end inside one
+      if constexpr (kW4) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const bool in = (v * 4 + t) * B::kLaneK < left;
-#pragma unroll
-          for (int i = 0; i < kMT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int64_t s =
-                  (scale_at[i][h] + (in ? b * 16 + v * 8 + t * 2 : 0)) & ~int64_t(3);
-              const int bytes = scale_end - s < 4 ? (int)(scale_end - s) : 4;
-              copy4(to + (uint32_t)(kScaleAt + ((i * 2 + h) * 2 + v) * 128) - (uint32_t)lane * 12u,
-                    p.scales + s, in ? bytes : 0);
-            }
+        for (int i = 0; i < kMT; ++i) {
+          const uint32_t dst = ring + (uint32_t)(stage * kStageBytes + kScaleAt +
+                                                 (i * 16 + (lane & 15)) * kScaleBytes);
+          if constexpr (kKind == kBits4) {
+            if (lane < 16) copy16(dst, scale_from[i]);
+          } else {
+            // the tensor may end inside the vector, or before it
+            const int64_t rest = scale_end - scale_from[i];
+            const int bytes = rest >= 16 ? 16 : rest > 0 ? (int)rest : 0;
+            copy16_part(dst + (uint32_t)(((lane >> 4) ^ ((lane >> 2) & 1)) * 16),
+                        bytes > 0 ? scale_from[i] : p.scales, bytes);
+          }
+          scale_from[i] += 16;
         }
       }
     }
@@ -274,9 +273,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
     }
   };
 
-  float acc[kMT][kNT][4] = {};
+  // Consecutive MMAs of one accumulator wait for one another: a single tile has two.
+  constexpr int kAccs = kMT * kNT == 1 ? 2 : 1;
+  float acc[kAccs][kMT][kNT][4] = {};
   // `xb`: this lane's first unit of the block's x, for row g
-  auto multiply = [&](int stage, uint32_t xb) {
+  auto multiply = [&](int stage, uint32_t xb, int left) {
     const uint32_t at = ring + (uint32_t)(stage * kStageBytes) + (uint32_t)lane * 16u;
     const uint32_t at_s = ring + (uint32_t)(stage * kStageBytes + kScaleAt);
 #pragma unroll
@@ -298,15 +299,14 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
           uint32_t s[2][2];  // scales of the lane's first and second 16 k, in both halves
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            const uint32_t row = at_s + (uint32_t)((i * 16 + h * 8 + g) * kScaleBytes);
             uint32_t two;
-            if constexpr (kKind == kBits4) {
-              two = lds2(at_s + (uint32_t)((i * 16 + h * 8 + g) * 16 + v * 8 + t * 2));
-            } else {
-              const uint32_t word =
-                  lds4(at_s + (uint32_t)(((i * 2 + h) * 2 + v) * 128) + (uint32_t)lane * 4u);
-              // the word's low or high half, as its row and k are
-              two = ((scale_at[i][h] + t * 2) & 2) != 0 ? word >> 16 : word;
-            }
+            if constexpr (kKind == kBits4)
+              two = lds2(row + (uint32_t)(t * 2 + v * 8));
+            else  // behind K lie the next row's, which could be NaN
+              two = (v * 4 + t) * B::kLaneK < left
+                        ? lds2(row + (uint32_t)((scale_in[i][h] + v * 8) ^ ((g & 4) << 2)))
+                        : 0u;
             two_scales(two, s[h]);
           }
 #pragma unroll
@@ -316,15 +316,15 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
             nvfp4_decode8(word_of(w[1], c), s[1][c >> 1], q1);
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
-              mma_16816<X>(acc[i][j], q0[0], q1[0], q0[1], q1[1], xv[j][c].x, xv[j][c].y);
-              mma_16816<X>(acc[i][j], q0[2], q1[2], q0[3], q1[3], xv[j][c].z, xv[j][c].w);
+              mma_16816<X>(acc[0][i][j], q0[0], q1[0], q0[1], q1[1], xv[j][c].x, xv[j][c].y);
+              mma_16816<X>(acc[kAccs - 1][i][j], q0[2], q1[2], q0[3], q1[3], xv[j][c].z, xv[j][c].w);
             }
           }
         } else {
 #pragma unroll
           for (int j = 0; j < kNT; ++j) {
-            mma_16816<X>(acc[i][j], w[0].x, w[1].x, w[0].y, w[1].y, xv[j][0].x, xv[j][0].y);
-            mma_16816<X>(acc[i][j], w[0].z, w[1].z, w[0].w, w[1].w, xv[j][0].z, xv[j][0].w);
+            mma_16816<X>(acc[0][i][j], w[0].x, w[1].x, w[0].y, w[1].y, xv[j][0].x, xv[j][0].y);
+            mma_16816<X>(acc[kAccs - 1][i][j], w[0].z, w[1].z, w[0].w, w[1].w, xv[j][0].z, xv[j][0].w);
           }
         }
       }
@@ -341,10 +341,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
     const int end = last - b0 < chunk ? last - b0 : chunk;
     for (int b = 0; b < end; ++b) {
       copy_wait<kStages - 2>();
-      if (kKind == kBits4) __syncwarp();  // the scales are other lanes' copies
+      if (kW4) __syncwarp();  // the scales are other lanes' copies
       // into the stage that the block before this one has left
       load(b0 + b + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
-      multiply(stage, xs + (uint32_t)(g * x_pitch + b * B::kK * 2 + t * 16));
+      multiply(stage, xs + (uint32_t)(g * x_pitch + b * B::kK * 2 + t * 16),
+               b0 + b + 1 < all ? B::kK : p.K - (all - 1) * B::kK);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
   }
@@ -364,7 +365,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       for (int c = 0; c < 4; ++c) {
         const int w = warp * kOuts;
         const int r = kGated ? (c >> 1) * kUp + w + i * 8 + g : w + i * 16 + (c >> 1) * 8 + g;
-        sums[(j * 8 + 2 * t + (c & 1)) * kAll + r] = acc[i][j][c];
+        sums[(j * 8 + 2 * t + (c & 1)) * kAll + r] =
+            kAccs == 1 ? acc[0][i][j][c] : acc[0][i][j][c] + acc[kAccs - 1][i][j][c];
       }
   if (parts > 1)
     cluster_sync();
