@@ -50,6 +50,13 @@ struct Plan {
   static constexpr int kSmem = kStages * kStageBytes + (kShared ? 1 : 2) * kBoxes * kBoxBytes + 1024;
 };
 
+// The tensor cores add to an accumulator with truncation, and 448 additions (K = 7168) move a sum by
+// 1e-5 of its terms: nothing in 16 bits, but one value in a thousand of a checkpoint becomes its
+// neighbour.  Where pre-activations are saved the accumulators are added, rounded, to sums in
+// registers after as many 64-k blocks; 0: never.
+template <int kEpi>
+constexpr int kDrainBlocks = kEpi == kGatedSave ? 8 : 0;
+
 struct Maps {
   CUtensorMap a, b;
   CUtensorMap o0, o1, o2;  // outputs: h | gate and up codes, or the two halves of d_pre
@@ -187,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using P = Plan<kEpi, kBN>;
   constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes;
   constexpr int kHalf = kBN / 2;  // columns of a half of the warps; gated: gate columns of a tile
+  constexpr int kDrain = kDrainBlocks<kEpi>;
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[kStages];
   __shared__ __align__(8) uint64_t empty_bar[kStages];
@@ -194,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t tempty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ __align__(8) uint64_t in_bar[2];
-  // kGatedSave: a half's largest value of each row for the other half: of up, and of gate
-  __shared__ float s_top[kEpi == kGatedSave ? 2 : 1][kEpi == kGatedSave ? 128 : 1];
+  // kGatedSave: the exponents of a half's largest gate and up of each row
+  __shared__ int8_t s_exp[2][2][kEpi == kGatedSave ? 128 : 1];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t raw = smem_u32(dsmem);
@@ -304,29 +312,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t empty_own = smem_u32(empty_bar), tfull_own = smem_u32(tfull_bar);
       for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
         const Unit q = unit_of(p, num_kb, u);
-        if (!wait(&tempty_bar[buf], buf_phase ^ 1u)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * kBN);
-        for (int kb = q.kb0; kb < q.kb1; ++kb) {
-          if (!r.ready && !wait(r.bar(), r.parity)) {
+        const int pass = kDrain > 0 ? kDrain : q.kb1 - q.kb0;  // blocks of one accumulator
+        for (int kc = q.kb0; kc < q.kb1 && ok; kc += pass) {
+          if (!wait(&tempty_bar[buf], buf_phase ^ 1u)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + (uint32_t)(r.stage * kStageBytes);
-          const uint32_t sb = sa + (uint32_t)kOperandBytes;
-          const uint32_t at = (uint32_t)r.stage * 8u;
-          r.next();
+          const uint32_t d = tmem + (uint32_t)(buf * kBN);
+          const int ke = kc + pass < q.kb1 ? kc + pass : q.kb1;
+          for (int kb = kc; kb < ke; ++kb) {
+            if (!r.ready && !wait(r.bar(), r.parity)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = base + (uint32_t)(r.stage * kStageBytes);
+            const uint32_t sb = sa + (uint32_t)kOperandBytes;
+            const uint32_t at = (uint32_t)r.stage * 8u;
+            r.next();
 #pragma unroll
-          for (int k = 0; k < kBlockK / 16; ++k)
-            umma_f16_pair(d, operand_desc<kAMn>(sa, k), operand_desc<kBMn>(sb, k), idesc,
-                          (kb > q.kb0 || k > 0) ? 1u : 0u);
-          umma_commit_both(empty_own + at, 0u);
+            for (int k = 0; k < kBlockK / 16; ++k)
+              umma_f16_pair(d, operand_desc<kAMn>(sa, k), operand_desc<kBMn>(sb, k), idesc,
+                            (kb > kc || k > 0) ? 1u : 0u);
+            umma_commit_both(empty_own + at, 0u);
+          }
+          if (!ok) break;
+          umma_commit_both(tfull_own + (uint32_t)buf * 8u, 0u);
+          buf ^= 1;
+          if (buf == 0) buf_phase ^= 1u;
         }
-        if (!ok) break;
-        umma_commit_both(tfull_own + (uint32_t)buf * 8u, 0u);
-        buf ^= 1;
-        if (buf == 0) buf_phase ^= 1u;
       }
       // every MMA issued has completed once drain_bar flips
       umma_commit_pair(smem_u32(&drain_bar));
@@ -379,8 +394,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(boxes, &maps.in, in, n0, m);
         }
       }
-      bool got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
-      tc_fence_after();
+      bool got = true;
+      float sums[kDrain > 0 ? 2 : 1][kDrain > 0 ? 64 : 1];  // gate and up
+      if constexpr (kDrain > 0) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) sums[0][i] = sums[1][i] = 0.0f;
+        for (int kc = q.kb0; kc < q.kb1 && got; kc += kDrain) {
+          got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
+          tc_fence_after();
+          if (!got) break;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float v[32];
+            tmem_ld_x32(tb + (uint32_t)(buf * kBN + (h >> 1) * kHalf + half * 64 + (h & 1) * 32), v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sums[h >> 1][(h & 1) * 32 + i] += v[i];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(&tempty_bar[buf]), 0u));
+          buf ^= 1;
+          if (buf == 0) buf_phase ^= 1u;
+        }
+      } else {
+        got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
+        tc_fence_after();
+      }
       if (input) {
         got = __all_sync(kAll, got && wait(in, in_phase));
         if (got) in_phase ^= 1u;
@@ -393,9 +432,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col0 = half * (kHalf / 2), piece0 = P::kShared ? half : 0;
       if (kBN == kTile && part) {
         for (int c = 0; c < 4 && live; ++c) {
-          const int col = half * 128 + c * 32;
+          int col = half * 128 + c * 32;
           float v[32];
-          tmem_ld_x32(d + (uint32_t)col, v);
+          if constexpr (kDrain > 0) {
+            col = (c >> 1) * kHalf + half * 64 + (c & 1) * 32;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = c < 2 ? (c == 0 ? sums[0][i] : sums[0][32 + i])
+                           : (c == 2 ? sums[kDrain > 0][i] : sums[kDrain > 0][32 + i]);
+          } else {
+            tmem_ld_x32(d + (uint32_t)col, v);
+          }
           uint8_t* b = next_box();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -419,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           publish([&] { tma_store_2d(&maps.o0, b, to, m); });
         }
-      } else if constexpr (kEpi == kGated || kEpi == kGatedSave) {
-        float top_g = 0.0f, top_u = 0.0f;
+      } else if constexpr (kEpi == kGated) {
         if (live && n0 < p.N) {
           uint8_t* b = next_box();
 #pragma unroll
@@ -428,15 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             float g[32], v[32];
             tmem_ld_x32(d + (uint32_t)(col0 + h * 32), g);
             tmem_ld_x32(d + (uint32_t)(kHalf + col0 + h * 32), v);
-            if constexpr (kEpi == kGatedSave) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (n0 + h * 32 + (i & ~7) < p.N) {  // N is a multiple of 8
-                  top_g = fmaxf(top_g, finite_abs(g[i]));
-                  top_u = fmaxf(top_u, finite_abs(v[i]));
-                }
-              }
-            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float w[8];
@@ -447,33 +484,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           publish([&] { tma_store_2d(&maps.o0, b, n0, m); });
         }
-        if constexpr (kEpi == kGatedSave) {
-          // the first half of the warps has the gate's codes, the second up's
-          s_top[half][row] = half == 0 ? top_u : top_g;
-          named_bar_sync(kAllEpilogue, 256);
-          if (live) {
-            const Ckpt& to = half == 0 ? p.gate : p.up;
-            const int e = fp8_exponent(fmaxf(half == 0 ? top_g : top_u, s_top[half ^ 1][row]));
-            if (m + row < p.M) to.scales[(int64_t)(m + row) * p.nt + q.at.n] = fp8_scale(e);
-            const float inv = fp8_scale(-e);
-            uint8_t* b = next_box();
+      } else if constexpr (kEpi == kGatedSave) {
+        // columns behind N are gate rows that belong to up, or nothing
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              float v[32];
-              tmem_ld_x32(d + (uint32_t)(half * kSlab + h * 32), v);
-              uint32_t c[8];
+        for (int i = 0; i < 64; ++i)
+          if (n0 + (i & ~7) >= p.N) sums[0][i] = sums[1][i] = 0.0f;  // N is a multiple of 8
+        if (live && n0 < p.N) {
+          uint8_t* b = next_box();
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                c[i] = q.at.n * kSlab + h * 32 + ((4 * i) & ~7) < p.N
-                           ? fp8_pack4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv)
-                           : 0u;
-              *box_at(b, row, 2 * h) = make_uint4(c[0], c[1], c[2], c[3]);
-              *box_at(b, row, 2 * h + 1) = make_uint4(c[4], c[5], c[6], c[7]);
-            }
-            publish([&] {
-              tma_store_2d(half == 0 ? &maps.o1 : &maps.o2, b, q.at.n * kSlab, m);
-            });
+          for (int j = 0; j < 8; ++j) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = gate_value<kAct>(sums[0][j * 8 + i]) * sums[1][j * 8 + i];
+            *box_at(b, row, j) = pack<T>(w);
           }
+          publish([&] { tma_store_2d(&maps.o0, b, n0, m); });
+        }
+        // Both halves write the codes of gate (first box) and up (second).
+        if (leader) store_wait_read<0>();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) top = fmaxf(top, finite_abs(sums[k][i]));
+          s_exp[half][k][row] = (int8_t)(top == 0.0f ? -128 : fp8_exponent(top));
+        }
+        named_bar_sync(kAllEpilogue, 256);
+        uint8_t* first = smem + kStages * kStageBytes;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          // the larger value's exponent; a group of zeros has a scale of 1
+          const int most = max((int)s_exp[0][k][row], (int)s_exp[1][k][row]);
+          const int e = most == -128 ? 0 : most;
+          if (k == half && live && m + row < p.M)
+            (k == 0 ? p.gate : p.up).scales[(int64_t)(m + row) * p.nt + q.at.n] = fp8_scale(e);
+          const float inv = fp8_scale(-e);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              c[i] = fp8_pack4(sums[k][j * 16 + 4 * i], sums[k][j * 16 + 4 * i + 1],
+                               sums[k][j * 16 + 4 * i + 2], sums[k][j * 16 + 4 * i + 3], inv);
+            *box_at(first + k * kBoxBytes, row, half * 4 + j) = make_uint4(c[0], c[1], c[2], c[3]);
+          }
+        }
+        fence_async_shared();
+        named_bar_sync(kAllEpilogue, 256);
+        if (leader && live) {
+          tma_store_2d(half == 0 ? &maps.o1 : &maps.o2, boxes, q.at.n * kSlab, m);
+          store_commit();
         }
       } else {
         if (live && n0 < p.N) {
@@ -516,11 +577,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(&tempty_bar[buf]), 0u));
-      buf ^= 1;
-      if (buf == 0) buf_phase ^= 1u;
+      if constexpr (kDrain == 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(&tempty_bar[buf]), 0u));
+        buf ^= 1;
+        if (buf == 0) buf_phase ^= 1u;
+      }
     }
     if (leader) {
       store_wait_all();
