@@ -31,11 +31,11 @@ moe_status_t check_gated(const moe_gated_linear_t* p) {
 // Both parts of a checkpoint, or neither.
 bool both(const void* codes, const void* scales) { return (codes != nullptr) == (scales != nullptr); }
 
-// Few tokens that save nothing: the weights are streamed (dense_rows.cu).  From three tokens on only
-// where there are too few weights for the tiles of dense.cu to fill the SMs (8 x 2048 x 7168: 22.0 us
+// Few tokens that save nothing: the weights are streamed (dense_rows.cu).  From two tokens on only
+// where there are too few weights for the tiles of dense.cu to fill the SMs (8 x 2048 x 7168: 20.4 us
 // against 26; 8 x 18432 x 7168: 113 against 88).
 bool few_rows(const moe_gated_linear_t& p, bool save) {
-  return !save && (p.T <= 2 || (p.T <= 16 && 2 * (int64_t)p.F * p.H <= 1 << 26));
+  return !save && (p.T == 1 || (p.T <= 16 && 2 * (int64_t)p.F * p.H <= 1 << 26));
 }
 
 size_t gated_bytes(const moe_gated_linear_t& p) {
@@ -219,15 +219,17 @@ moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void
   char* ws = static_cast<char*>(workspace);
   int* status = static_cast<int*>(workspace);
   float* parts = reinterpret_cast<float*>(ws + at.parts);
-  if (at.pitch != g->N) {  // a row of d_out does not start on 16 bytes
-    if (const cudaError_t e = launch_pad_rows(g->dtype, g->T, g->N, at.pitch, d_out, ws + at.d_out,
-                                              s))
+  // Rows of d_out that do not start on 16 bytes are copied, in the pass that adds them if there is one.
+  const bool pad = at.pitch != g->N;
+  if (d_bias) {
+    if (const cudaError_t e = launch_column_sum(g->dtype, g->T, g->N, at.pitch, d_out,
+                                                pad ? ws + at.d_out : nullptr, d_bias, s))
       return from_cuda(e);
-    d_out = ws + at.d_out;
+  } else if (pad) {
+    if (const cudaError_t e = launch_pad_rows(g->T, g->N, at.pitch, d_out, ws + at.d_out, s))
+      return from_cuda(e);
   }
-  if (d_bias)
-    if (const cudaError_t e = launch_column_sum(g->dtype, g->T, g->N, at.pitch, d_out, d_bias, s))
-      return from_cuda(e);
+  if (pad) d_out = ws + at.d_out;
   if (d_x)
     if (const cudaError_t e = launch_dense_nn(g->dtype, g->T, g->K, g->N, d_out, at.pitch, w, d_x,
                                               parts, status, s))

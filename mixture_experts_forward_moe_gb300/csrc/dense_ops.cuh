@@ -59,11 +59,11 @@ cudaError_t launch_checkpoint(int dtype, int T, int C, const void* x, Ckpt out, 
 cudaError_t launch_restore(int dtype, int T, int C, CkptIn in, void* out, cudaStream_t s);
 cudaError_t launch_gated_grad_saved(int dtype, int act, int T, int F, const void* d_out, CkptIn gate,
                                     CkptIn up, void* d_pre, void* out, cudaStream_t s);
-// sum[n] = sum_t v[t, n] of [T, N] rows that lie `pitch` (a multiple of 8) elements apart.
-cudaError_t launch_column_sum(int dtype, int T, int N, int64_t pitch, const void* v, void* sum,
-                              cudaStream_t s);
-// [T, N] -> [T, pitch], zeros behind N.
-cudaError_t launch_pad_rows(int dtype, int T, int N, int64_t pitch, const void* v, void* out,
-                            cudaStream_t s);
+// sum[n] = sum_t v[t, n] of [T, N] rows that lie `pitch` (a multiple of 8) elements apart; with
+// `padded` rows that lie N apart, which are copied there, `pitch` apart.
+cudaError_t launch_column_sum(int dtype, int T, int N, int64_t pitch, const void* v, void* padded,
+                              void* sum, cudaStream_t s);
+// [T, N] -> [T, pitch], anything behind N.
+cudaError_t launch_pad_rows(int T, int N, int64_t pitch, const void* v, void* out, cudaStream_t s);
 
 }  // namespace gb300moe

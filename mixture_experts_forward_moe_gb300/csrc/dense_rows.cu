@@ -395,18 +395,18 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   if (parts > 1) cluster_sync();  // a peer may still read this CTA's sums
 }
 
-// ---- 16-bit weights, a few rows of x: on the CUDA cores ----------------------------------------
-// A gate row and its up row by `wpr` warps (a power of two) of the CTA's eight.
-template <typename T, int kNT>
-__global__ void __launch_bounds__(256) gated_gemv_kernel(const RowsCall p, int wpr) {
-  __shared__ float s_part[8][2 * kNT];
+// ---- 16-bit weights, one row of x: on the CUDA cores --------------------------------------------
+// A gate row and its up row by `wpr` warps (a power of two) of the CTA's.  Small CTAs even out the SMs
+// (eight warps: 2048 x 7168 in 17.4 us, four 16.5), and each lane has 128 bytes on their way (64: 18.3).
+constexpr int kGemvWarps = 4;
+template <typename T>
+__global__ void __launch_bounds__(kGemvWarps * 32) gated_gemv_kernel(const RowsCall p, int wpr) {
+  __shared__ float s_part[kGemvWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int outs = 8 / wpr;
+  const int outs = kGemvWarps / wpr;
   const int64_t n = (int64_t)blockIdx.x * outs + warp / wpr;
   const int kv = p.K / 8;
-  F2 acc[2][kNT];
-#pragma unroll
-  for (int c = 0; c < kNT; ++c) acc[0][c] = acc[1][c] = f2(0.0f);
+  F2 gate = f2(0.0f), up = f2(0.0f);
   if (n < p.N) {
     const uint4* wg = static_cast<const uint4*>(p.w) + n * kv;
     const uint4* wu = wg + (int64_t)p.N * kv;
@@ -424,43 +424,35 @@ __global__ void __launch_bounds__(256) gated_gemv_kernel(const RowsCall p, int w
       for (int a = 0; a < kAhead; ++a) {
         const int i = i0 + a * wpr * 32;
         if (i >= kv) break;
-        F2 fg[4], fu[4];
+        F2 fg[4], fu[4], fx[4];
         unpack<T>(g[a], fg);
         unpack<T>(u[a], fu);
+        unpack<T>(__ldg(x + i), fx);
 #pragma unroll
-        for (int c = 0; c < kNT; ++c) {
-          F2 fx[4];
-          unpack<T>(__ldg(x + (int64_t)(c < p.T ? c : 0) * kv + i), fx);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[0][c] = f2_fma(fg[j], fx[j], acc[0][c]);
-            acc[1][c] = f2_fma(fu[j], fx[j], acc[1][c]);
-          }
+        for (int j = 0; j < 4; ++j) {
+          gate = f2_fma(fg[j], fx[j], gate);
+          up = f2_fma(fu[j], fx[j], up);
         }
       }
     }
   }
+  float z[2] = {f2_sum(gate), f2_sum(up)};
 #pragma unroll
-  for (int c = 0; c < kNT; ++c)
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v = f2_sum(acc[h][c]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) s_part[warp][h * kNT + c] = v;
-    }
+    for (int o = 16; o > 0; o >>= 1) z[h] += __shfl_xor_sync(0xffffffffu, z[h], o);
+    if (lane == 0) s_part[warp][h] = z[h];
+  }
   __syncthreads();
-  const int i = threadIdx.x;
-  if (i < outs * p.T) {
-    const int r = i % outs, c = i / outs;
-    const int64_t no = (int64_t)blockIdx.x * outs + r;
-    if (no >= p.N) return;
-    float gate = 0.0f, up = 0.0f;
+  const int r = threadIdx.x;
+  const int64_t no = (int64_t)blockIdx.x * outs + r;
+  if (r < outs && no < p.N) {
+    float a = 0.0f, b = 0.0f;
     for (int q = 0; q < wpr; ++q) {
-      gate += s_part[r * wpr + q][c];
-      up += s_part[r * wpr + q][kNT + c];
+      a += s_part[r * wpr + q][0];
+      b += s_part[r * wpr + q][1];
     }
-    finish<T, true>(p, c, no, gate, up);
+    finish<T, true>(p, 0, no, a, b);
   }
 }
 
@@ -523,20 +515,16 @@ cudaError_t pick(const RowsCall& c, cudaStream_t s) {
   return go<T, kKind, kGated, 2, 4>(c, s);
 }
 
-template <typename T, int kNT>
-cudaError_t go_gemv(const RowsCall& c, cudaStream_t s) {
-  int wpr = 1;
-  while (wpr < 8 && (int64_t)c.N * wpr < (int64_t)num_sms() * 16 && c.K / 8 >= wpr * 2 * 32) wpr *= 2;
-  const int outs = 8 / wpr;
-  return launch_k(gated_gemv_kernel<T, kNT>, dim3((unsigned)((c.N - 1) / outs + 1)), dim3(256), 0, s,
-                  false, c, wpr);
-}
-
 template <typename T>
 cudaError_t typed(const RowsCall& c, cudaStream_t s) {
-  // Two rows double the arithmetic of one, which is then no longer hidden: 18432 x 7168 81 and 90 us.
-  if (!c.codes && c.T == 1) return go_gemv<T, 1>(c, s);
-  if (!c.codes && c.T == 2) return go_gemv<T, 2>(c, s);
+  if (!c.codes && c.T == 1) {
+    int wpr = 1;  // enough for about sixteen warps per SM
+    while (wpr < kGemvWarps && (int64_t)c.N * wpr < (int64_t)num_sms() * 16 && c.K / 8 >= wpr * 2 * 32)
+      wpr *= 2;
+    return launch_k(gated_gemv_kernel<T>, dim3((unsigned)((c.N - 1) / (kGemvWarps / wpr) + 1)),
+                    dim3(kGemvWarps * 32), 0,
+                    s, false, c, wpr);
+  }
   if (!c.codes) return pick<T, kBits16, true>(c, s);
   if (c.K % 256 == 0)
     return c.gated ? pick<T, kBits4, true>(c, s) : pick<T, kBits4, false>(c, s);
