@@ -46,6 +46,31 @@ struct Rows {
 
 constexpr int kAhead = 4;  // units that a thread asks for together
 
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+};
+template <>
+struct Pair<__half> {
+  using type = __half2;
+};
+// The largest magnitude of sixteen values; NaN does not count.
+template <typename T>
+__device__ __forceinline__ float top16(const uint4& a, const uint4& b) {
+  using P = typename Pair<T>::type;
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t t = 0u;
+  P top = *reinterpret_cast<const P*>(&t);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t m = w[j] & 0x7fff7fffu;
+    top = __hmax2(top, *reinterpret_cast<const P*>(&m));
+  }
+  return fmaxf(DT<T>::to_f(top.x), DT<T>::to_f(top.y));
+}
+
 // x [T, vecs] vectors of eight values.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -72,15 +97,28 @@ __global__ void __launch_bounds__(kThreads)
     for (int k = 0; k < kAhead; ++k) {
       if (first + k * kThreads >= b.end) break;
       const int i = first + k * kThreads + (threadIdx.x & 31);
-      float f[2][8], top = 0.0f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        unpack<T>(v[k][h], f[h]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(f[h][j]));
-      }
+      // The largest magnitude of 16 bits two by two, NaN left out; where it is an infinity, again
+      // without those.
+      float top = top16<T>(v[k][0], v[k][1]);
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float f[2][8];
+      unpack<T>(v[k][0], f[0]);
+      unpack<T>(v[k][1], f[1]);
+      const bool far = !(top <= 3.402823466e38f);
+      if (__any_sync(0xffffffffu, far)) {
+        float t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t = fmaxf(t, fmaxf(finite_abs(f[0][j]), finite_abs(f[1][j])));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+        top = t;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // infinities become NaN, as the conversion does not make them
+          f[0][j] += f[0][j] - f[0][j];
+          f[1][j] += f[1][j] - f[1][j];
+        }
+      }
       if (i >= b.end) continue;
       int64_t row;
       int u;
@@ -88,10 +126,10 @@ __global__ void __launch_bounds__(kThreads)
       const int e = fp8_exponent(top);
       const float inv = fp8_scale(-e);
       codes[row * b.per_row + u] =
-          make_uint4(fp8_pack4(f[0][0], f[0][1], f[0][2], f[0][3], inv),
-                     fp8_pack4(f[0][4], f[0][5], f[0][6], f[0][7], inv),
-                     fp8_pack4(f[1][0], f[1][1], f[1][2], f[1][3], inv),
-                     fp8_pack4(f[1][4], f[1][5], f[1][6], f[1][7], inv));
+          make_uint4(fp8_pack4_finite(f[0][0], f[0][1], f[0][2], f[0][3], inv),
+                     fp8_pack4_finite(f[0][4], f[0][5], f[0][6], f[0][7], inv),
+                     fp8_pack4_finite(f[1][0], f[1][1], f[1][2], f[1][3], inv),
+                     fp8_pack4_finite(f[1][4], f[1][5], f[1][6], f[1][7], inv));
       if ((u & 7) == 0) scales[row * groups + (u >> 3)] = fp8_scale(e);
     }
   }
@@ -152,8 +190,10 @@ __global__ void __launch_bounds__(kThreads)
         restore8(h == 0 ? q[k].x : q[k].z, h == 0 ? q[k].y : q[k].w, scale[k], f);
         // a value next to the type's largest may have been rounded past it; NaN stays
         constexpr float top = Largest<T>::value;
+        if (scale[k] > top / 512.0f) {  // else 448 scales are within
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] > top ? top : (f[j] < -top ? -top : f[j]);
+          for (int j = 0; j < 8; ++j) f[j] = f[j] > top ? top : (f[j] < -top ? -top : f[j]);
+        }
         if (2 * u + h < vecs) out[row * vecs + 2 * u + h] = pack<T>(f);
       }
     }

@@ -24,13 +24,9 @@ __device__ __forceinline__ int fp8_exponent(float top) {
 }
 __device__ __forceinline__ float fp8_scale(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Codes of four values times `inv`, the first in the lowest byte.
-__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d, float inv) {
-  // the conversion would take infinities to 448; v - v is NaN for them
-  a = a * inv + (a - a);
-  b = b * inv + (b - b);
-  c = c * inv + (c - c);
-  d = d * inv + (d - d);
+// Codes of four values, finite or NaN, times `inv`, the first in the lowest byte.
+__device__ __forceinline__ uint32_t fp8_pack4_finite(float a, float b, float c, float d, float inv) {
+  a *= inv, b *= inv, c *= inv, d *= inv;
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\t"
       "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
@@ -39,6 +35,11 @@ __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d
       : "=r"(r)
       : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
+}
+
+// The same of any values: the conversion would take infinities to 448, and v - v is NaN for them.
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d, float inv) {
+  return fp8_pack4_finite(a + (a - a), b + (b - b), c + (c - c), d + (d - d), inv);
 }
 
 // Four codes (lowest byte first) -> their values in f32, not scaled.
