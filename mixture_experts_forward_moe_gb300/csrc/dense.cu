@@ -115,9 +115,6 @@ template <int N>
 __device__ __forceinline__ void store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void store_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -215,6 +212,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int num_kb = (p.K - 1) / kBlockK + 1;
   const int64_t units = p.whole + (int64_t)p.rest * p.split;
   const int64_t step = num_clusters_x();
+  // Fewer than 128 rows of a: the others of its operand hold anything, and make rows of D that nothing
+  // reads.
+  const bool some = kAMn || side == 0 || p.M > kSlab;
+  const int bytes = kStageBytes - (kAMn ? 0 : (kSlab - (some ? p.a_rows : 0)) * kBlockK * 2);
+  auto load_block = [&](const Unit& q, int kb, int stage) {
+    uint8_t* st = smem + stage * kStageBytes;
+    uint64_t* full = &full_bar[stage];
+    // gated: the even CTA has the gate rows of b, the odd one the up rows; gate rows past N are rows
+    // of up, whose columns the epilogue leaves out
+    const int nb = gated(kEpi) ? side * p.N + q.at.n * kHalf : q.at.n * kBN + side * kHalf;
+    mbar_arrive_expect_tx(full, (uint32_t)bytes);
+    if (some) load_operand<kAMn, kSlab>(st, &maps.a, full, q.at.m + side * kSlab, kb * kBlockK);
+    load_operand<kBMn, kHalf>(st + kOperandBytes, &maps.b, full, nb, kb * kBlockK);
+  };
+  int issued = 0;  // by the producer (the same thread is elected here and below): stages asked for
 
   if (warp == 0) {
     if (elect_one()) {
@@ -233,6 +245,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&drain_bar, 1);
       s_abort = 0;
       fence_mbar_init();
+      fence_async_shared();  // the barriers, to the copies
+      // the first stages are on their way while the pair starts
+      pdl_wait();
+      const Unit q = unit_of(p, num_kb, cluster_id_x());
+      for (; issued < kStages && q.kb0 + issued < q.kb1; ++issued)
+        load_block(q, q.kb0 + issued, issued);
     }
   } else if (warp == 1) {
     tmem_alloc_pair(&s_tmem, 2 * kBN);
@@ -240,12 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync();
+  __syncthreads();
+  cluster_leave();  // the peer's barriers are there (fence_mbar_init released them)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_wait();
   pdl_trigger();
-  int issued = 0;  // by the producer: stages asked for
   const uint32_t peer_abort = cluster_map(smem_u32(&s_abort), rank ^ 1u);
   // by one thread, or by all of a warp; on giving up the peer CTA is told too
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -258,27 +276,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       Ring r(empty_bar, kStages, 1u);
       bool ok = true;
-      // Fewer than 128 rows of a: the others of its operand hold anything, and make rows of D that
-      // nothing reads.
-      const bool some = kAMn || side == 0 || p.M > kSlab;
-      const int bytes = kStageBytes - (kAMn ? 0 : (kSlab - (some ? p.a_rows : 0)) * kBlockK * 2);
+      const int early = issued;
+      for (int i = 0; i < early; ++i) r.next();
       for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
         const Unit q = unit_of(p, num_kb, u);
-        const int ma = q.at.m + side * kSlab;
-        // gated: the even CTA has the gate rows of b, the odd one the up rows; gate rows past N
-        // are rows of up, whose columns the epilogue leaves out
-        const int nb = gated(kEpi) ? side * p.N + q.at.n * kHalf : q.at.n * kBN + side * kHalf;
-        for (int kb = q.kb0; kb < q.kb1; ++kb) {
+        for (int kb = u < step ? q.kb0 + early : q.kb0; kb < q.kb1; ++kb) {
           if (!r.ready && !wait(r.bar(), r.parity)) {
             ok = false;
             break;
           }
-          uint8_t* st = smem + r.stage * kStageBytes;
-          uint64_t* full = &full_bar[r.stage];
+          const int stage = r.stage;
           r.next();
-          mbar_arrive_expect_tx(full, (uint32_t)bytes);
-          if (some) load_operand<kAMn, kSlab>(st, &maps.a, full, ma, kb * kBlockK);
-          load_operand<kBMn, kHalf>(st + kOperandBytes, &maps.b, full, nb, kb * kBlockK);
+          load_block(q, kb, stage);
           ++issued;
         }
       }
@@ -380,6 +389,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         store_commit();
       }
     };
+    // Passes of an accumulator over `blocks` k blocks.
+    auto passes = [&](int blocks) { return kDrain > 0 ? (blocks - 1) / kDrain + 1 : 1; };
+    // The accumulator has been read; `left` passes of unit u follow.  Where no later pass takes this
+    // buffer nobody waits for the arrival, and the even CTA may leave before it comes.
+    auto free_buffer = [&](int left, int64_t u) {
+      if (left < 2 && u + step < units) {
+        const Unit n = unit_of(p, num_kb, u + step);
+        left += passes(n.kb1 - n.kb0) + (u + 2 * step < units ? 1 : 0);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && left >= 2)
+        mbar_arrive_cluster(cluster_map(smem_u32(&tempty_bar[buf]), 0u));
+      buf ^= 1;
+      if (buf == 0) buf_phase ^= 1u;
+    };
     for (int64_t u = cluster_id_x(); u < units; u += step) {
       const Unit q = unit_of(p, num_kb, u);
       const int m = q.at.m + side * kSlab;
@@ -410,11 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) sums[h >> 1][(h & 1) * 32 + i] += v[i];
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(&tempty_bar[buf]), 0u));
-          buf ^= 1;
-          if (buf == 0) buf_phase ^= 1u;
+          free_buffer(passes(q.kb1 - kc) - 1, u);
         }
       } else {
         got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
@@ -577,16 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if constexpr (kDrain == 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_map(smem_u32(&tempty_bar[buf]), 0u));
-        buf ^= 1;
-        if (buf == 0) buf_phase ^= 1u;
-      }
+      if constexpr (kDrain == 0) free_buffer(0, u);
     }
     if (leader) {
-      store_wait_all();
+      store_wait_read<0>();  // the writes themselves end with the kernel
       // d_out of a tile that gave up may still be on its way
       if (kEpi == kGradient && *abort_flag) {
         const uint64_t t = global_timer_ns();
@@ -597,7 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync();
+  // Every arrival sent to the peer has been waited for there, unless one gave up: then what was sent
+  // is released first.  (A release in every case costs 0.6 us: it waits for the stores to memory.)
+  __syncthreads();
+  if (*abort_flag)
+    cluster_sync();
+  else
+    cluster_leave();
   tc_fence_after();
   // (the even CTA's stages are full only with the odd CTA's copies told of: else a second passes)
   if (*abort_flag) land_copies(full_bar, issued, kStages);

@@ -282,13 +282,6 @@ __device__ __forceinline__ void join(const LinArgs& p, uint32_t base, int cols, 
   }
 }
 
-// Cluster barrier after which a CTA may leave: it orders nothing but the peers' finished reads
-// (cluster_sync's release would first wait for this CTA's global stores).
-__device__ __forceinline__ void cluster_leave() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::
-                   : "memory");
-}
-
 // ---- few rows: weights streamed once through the CUDA cores -----------------------------------
 constexpr int kGemvRows = 4;
 constexpr int kGemvWarps = 8;

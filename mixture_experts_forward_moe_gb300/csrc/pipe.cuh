@@ -116,6 +116,13 @@ __device__ __forceinline__ void umma_commit_both(uint32_t bar, uint32_t even) {
       : "memory");
 }
 
+// Cluster barrier after which a CTA may leave: it orders nothing but the peers' finished reads
+// (cluster_sync's release would first wait for this CTA's global stores).
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::
+                   : "memory");
+}
+
 // ---- host side ---------------------------------------------------------------------------------
 constexpr int kSmemLimit = 226 * 1024;  // dynamic; leaves room for the static variables
 
