@@ -11,7 +11,7 @@
 #include "activation.cuh"
 #include "dense_ops.cuh"
 #include "fp8.cuh"
-#include "ptx.cuh"
+#include "pipe.cuh"
 #include "vec16.cuh"
 
 namespace gb300moe {
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     sum[group * 64 + c] = DT<T>::from_f(a);
   }
-  if (parts > 1) cluster_sync();  // the first CTA may still read the others' sums
+  if (parts > 1) cluster_leave();  // the first CTA may still read the others' sums
 }
 
 __global__ void __launch_bounds__(kThreads)

@@ -25,8 +25,6 @@
 
 #include <type_traits>
 
-
-
 namespace gb300moe {
 
 namespace {
@@ -49,6 +47,11 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Into L2 alone: also before the wait for the kernel before this one, which may write what is there.
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
@@ -257,8 +260,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
         const int i = first + a * kWarps * 32, c = i / units;
         const int64_t k = (int64_t)b0 * B::kK + (i - c * units) * 8;
         v[a] = i < end && k < p.K
-                   ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) +
-                                                          (t0 + c) * p.K + k))
+                   ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + (t0 + c) * p.K + k)
                    : zero4();
       }
 #pragma unroll
@@ -331,6 +333,16 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
     }
   };
 
+  // The first blocks come into L2 while the kernel before this one ends.
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s)
+    if (t == 0 && first + s < last)
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) prefetch_l2(from[i][h] + s * 128);
+  pdl_wait();
+  pdl_trigger();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load(first + s, s);
   int stage = 0;
@@ -354,7 +366,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
 
   // Sums [cols][kAll]: the weight rows of the CTA, a gated product's gate rows before its up rows.
   constexpr int kAll = kWarps * 16 * kMT, kUp = kWarps * kOuts;
-  const float alpha = kW4 ? __ldg(p.alpha) : 1.0f;
+  const float alpha = kW4 ? *p.alpha : 1.0f;
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -377,6 +389,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   const int end = (part + 1) * kUp * cols / parts;
   for (int i = part * kUp * cols / parts + threadIdx.x; i < end; i += kWarps * 32) {
     const int c = i / kUp, r = i % kUp;
+    if (n0 + r >= p.N) continue;  // (every read of a peer is waited for by its output)
     float z = 0.0f, up = 0.0f;
     if (parts > 1) {
       const uint32_t at = xs + (uint32_t)((c * kAll + r) * 4);
@@ -390,9 +403,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       z = sums[c * kAll + r];
       if (kGated) up = sums[c * kAll + kUp + r];
     }
-    if (n0 + r < p.N) finish<T, kGated>(p, t0 + c, n0 + r, z * alpha, up * alpha);
+    finish<T, kGated>(p, t0 + c, n0 + r, z * alpha, up * alpha);
   }
-  if (parts > 1) cluster_sync();  // a peer may still read this CTA's sums
+  if (parts > 1) cluster_leave();  // a peer may still read this CTA's sums
 }
 
 // ---- 16-bit weights, one row of x: on the CUDA cores --------------------------------------------
@@ -412,7 +425,15 @@ __global__ void __launch_bounds__(kGemvWarps * 32) gated_gemv_kernel(const RowsC
     const uint4* wu = wg + (int64_t)p.N * kv;
     const uint4* x = static_cast<const uint4*>(p.x);
     constexpr int kAhead = 4;
-    for (int i0 = warp % wpr * 32 + lane; i0 < kv; i0 += kAhead * wpr * 32) {
+    const int i1 = warp % wpr * 32 + lane;
+    for (int a = 0; a < kAhead; ++a)
+      if (lane % 8 == 0 && i1 + a * wpr * 32 < kv) {
+        prefetch_l2(wg + i1 + a * wpr * 32);
+        prefetch_l2(wu + i1 + a * wpr * 32);
+      }
+    pdl_wait();
+    pdl_trigger();
+    for (int i0 = i1; i0 < kv; i0 += kAhead * wpr * 32) {
       uint4 g[kAhead], u[kAhead];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
@@ -427,7 +448,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32) gated_gemv_kernel(const RowsC
         F2 fg[4], fu[4], fx[4];
         unpack<T>(g[a], fg);
         unpack<T>(u[a], fu);
-        unpack<T>(__ldg(x + i), fx);
+        unpack<T>(x[i], fx);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           gate = f2_fma(fg[j], fx[j], gate);
@@ -495,13 +516,15 @@ cudaError_t go(const RowsCall& c, cudaStream_t s) {
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)parts;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)parts;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = parts > 1 ? 1 : 0;
+  cfg.numAttrs = parts > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, c, parts, chunk);
 }
 
@@ -522,8 +545,7 @@ cudaError_t typed(const RowsCall& c, cudaStream_t s) {
     while (wpr < kGemvWarps && (int64_t)c.N * wpr < (int64_t)num_sms() * 16 && c.K / 8 >= wpr * 2 * 32)
       wpr *= 2;
     return launch_k(gated_gemv_kernel<T>, dim3((unsigned)((c.N - 1) / (kGemvWarps / wpr) + 1)),
-                    dim3(kGemvWarps * 32), 0,
-                    s, false, c, wpr);
+                    dim3(kGemvWarps * 32), 0, s, true, c, wpr);
   }
   if (!c.codes) return pick<T, kBits16, true>(c, s);
   if (c.K % 256 == 0)
