@@ -17,11 +17,14 @@
 // through shared memory to TMA stores, which cut what lies outside the tensor.
 // Where the last tiles would leave most pairs idle they are split along K: their f32 sums go to the
 // workspace, and join_kernel adds them in order and finishes the outputs.
+// A call's two gradients (dy w and dy^T x) are one launch, whose pairs share out the tiles of both.
 #include "activation.cuh"
 #include "dense_ops.cuh"
 #include "fp8.cuh"
 #include "pipe.cuh"
 #include "vec16.cuh"
+
+#include <math.h>
 
 namespace gb300moe {
 
@@ -58,21 +61,31 @@ template <int kEpi>
 constexpr int kDrainBlocks = kEpi == kGatedSave ? 8 : 0;
 
 struct Maps {
-  CUtensorMap a, b;
-  CUtensorMap o0, o1, o2;  // outputs: h | gate and up codes, or the two halves of d_pre
-  CUtensorMap in;          // kGradient: d_out
-  CUtensorMap parts;       // sums of the tiles that are split
+  CUtensorMap a[2], b[2], o0[2];  // of each product; o0: h, gated
+  CUtensorMap o1, o2;             // gate and up codes, or the two halves of d_pre
+  CUtensorMap in;                 // kGradient: d_out
+  CUtensorMap parts;              // sums of the tiles that are split
 };
 
+// A product.
+struct Prod {
+  int M, N, num_kb;  // outputs (gated: N of 2 N rows of b), 64-k blocks
+  int mt, nt;        // tiles
+  int64_t whole;     // tiles that are not split; then
+  int rest;          // the others, each
+  int split;         // in as many parts of K,
+  int part_row;      // whose sums begin there
+  int a_mn;          // a is MN-major (kPlain)
+  int a_rows;        // of a K-major a that a copy brings
+};
 struct Args {
-  int M, N, K;    // outputs (gated: N of 2 N rows of b)
-  int mt, nt;     // tiles
-  int64_t whole;  // tiles that are not split; then
-  int rest;       // the others, each
-  int split;      // in as many parts of K
-  int a_rows;     // of a K-major a that a copy brings
-  int want_out;   // kGradient: h too
-  Ckpt gate, up;  // kGatedSave (codes by TMA)
+  Prod q[2];
+  int64_t units[2];  // tiles and parts of each; a unit of the first costs no less
+  // kPlain (see unit_at): every pair takes `own` of the first's units, the first `more` pairs one
+  // more, and all take `rounds` of the second's
+  int64_t own, more, rounds;
+  int want_out;      // kGradient: h too
+  Ckpt gate, up;     // kGatedSave (codes by TMA)
   int* status;
   uint64_t limit_ns;
 };
@@ -84,16 +97,16 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-template <bool kMn>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int k16) {
-  return kMn ? sw128_mnmajor_desc(saddr + (uint32_t)k16 * 2048u)
-             : sw128_kmajor_desc(saddr + (uint32_t)k16 * 32u);
+// Of an operand in either order, and what 16 k further add to it (in units of 16 bytes).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, bool mn) {
+  return mn ? sw128_mnmajor_desc(saddr) : sw128_kmajor_desc(saddr);
 }
+__device__ __forceinline__ uint64_t k16_step(bool mn) { return mn ? 2048 / 16 : 32 / 16; }
 
-template <bool kMn, int kRows>
+template <int kRows>
 __device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
-                                             int mn, int k) {
-  if constexpr (kMn) {
+                                             int mn, int k, bool is_mn) {
+  if (is_mn) {
     tma_load_2d(dst, map, bar, mn, k);
     if (kRows > 64) tma_load_2d(dst + kBlockK * 128, map, bar, mn + 64, k);
   } else {
@@ -160,24 +173,49 @@ __device__ __forceinline__ Place place_of(int mt, int nt, int64_t tile) {
 
 // A unit of work: a tile, or a part of one; its 64-k blocks, and where its sums go (-1: finished).
 struct Unit {
+  int prod;
   Place at;
   int kb0, kb1, row;
 };
-__device__ __forceinline__ Unit unit_of(const Args& p, int num_kb, int64_t u) {
+template <int kEpi>
+__device__ __forceinline__ Unit unit_of(const Args& p, int64_t u) {
   Unit r;
-  if (u < p.whole) {
-    r.at = place_of(p.mt, p.nt, u);
+  r.prod = kEpi == kPlain && u >= p.units[0] ? 1 : 0;
+  const Prod& q = p.q[r.prod];
+  if (r.prod) u -= p.units[0];
+  if (u < q.whole) {
+    r.at = place_of(q.mt, q.nt, u);
     r.kb0 = 0;
-    r.kb1 = num_kb;
+    r.kb1 = q.num_kb;
     r.row = -1;
   } else {
-    const int i = (int)(u - p.whole), part = i / p.rest;
-    r.at = place_of(p.mt, p.nt, p.whole + i % p.rest);
-    r.kb0 = (int)((int64_t)num_kb * part / p.split);
-    r.kb1 = (int)((int64_t)num_kb * (part + 1) / p.split);
-    r.row = i * kTile;
+    const int i = (int)(u - q.whole), part = i / q.rest;
+    r.at = place_of(q.mt, q.nt, q.whole + i % q.rest);
+    r.kb0 = (int)((int64_t)q.num_kb * part / q.split);
+    r.kb1 = (int)((int64_t)q.num_kb * (part + 1) / q.split);
+    r.row = q.part_row + i * kTile;
   }
   return r;
+}
+
+// The s-th unit of this pair, -1 past its last.  Pairs take the first product's units in turn, which
+// leaves some with one more of them; of the second's all take as many, and the others the rest.
+template <int kEpi>
+__device__ __forceinline__ int64_t unit_at(const Args& p, int64_t s) {
+  const int64_t pairs = num_clusters_x(), i = cluster_id_x();
+  if constexpr (kEpi == kPlain) {
+    const int64_t own = p.own + (i < p.more ? 1 : 0);
+    if (s >= own) {
+      s -= own;
+      if (s >= p.rounds && i < p.more) return -1;
+      const int64_t v = s < p.rounds ? s * pairs + i
+                                     : p.rounds * pairs + (s - p.rounds) * (pairs - p.more) +
+                                           (i - p.more);
+      return v < p.units[1] ? p.units[0] + v : -1;
+    }
+  }
+  const int64_t u = i + s * pairs;
+  return u < p.units[0] ? u : -1;
 }
 
 // Roles (320 threads): warp 0 TMA producer; warp 1 issues the MMAs (even CTA) or tells the even CTA
@@ -185,13 +223,14 @@ __device__ __forceinline__ Unit unit_of(const Args& p, int num_kb, int64_t u) {
 // columns.  (One half for all: 4096 x 2048 x 7168 saved in 145 us.)  Every wait is bounded
 // (MOE_ERR_TIMEOUT in the status word); a pair in which one gave up waits for its copies, MMAs and
 // stores in flight before it leaves.
-template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct, int kBN>
+template <typename T, int kEpi, int kAct, int kBN>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_kernel(const __grid_constant__ Maps maps, const Args p) {
   using P = Plan<kEpi, kBN>;
   constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes;
   constexpr int kHalf = kBN / 2;  // columns of a half of the warps; gated: gate columns of a tile
   constexpr int kDrain = kDrainBlocks<kEpi>;
+  constexpr bool kBMn = kEpi == kPlain;
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[kStages];
   __shared__ __align__(8) uint64_t empty_bar[kStages];
@@ -209,29 +248,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &s_abort;
   const uint32_t rank = cluster_ctarank();  // in the pair
   const int side = (int)rank;
-  const int num_kb = (p.K - 1) / kBlockK + 1;
-  const int64_t units = p.whole + (int64_t)p.rest * p.split;
-  const int64_t step = num_clusters_x();
-  // Fewer than 128 rows of a: the others of its operand hold anything, and make rows of D that nothing
-  // reads.
-  const bool some = kAMn || side == 0 || p.M > kSlab;
-  const int bytes = kStageBytes - (kAMn ? 0 : (kSlab - (some ? p.a_rows : 0)) * kBlockK * 2);
   auto load_block = [&](const Unit& q, int kb, int stage) {
+    const Prod& d = p.q[q.prod];
     uint8_t* st = smem + stage * kStageBytes;
     uint64_t* full = &full_bar[stage];
+    const bool a_mn = kEpi == kPlain && d.a_mn;
+    // Fewer than 128 rows of a: the others of its operand hold anything, and make rows of D that
+    // nothing reads.
+    const bool some = a_mn || side == 0 || d.M > kSlab;
+    const int left_out = a_mn ? 0 : (kSlab - (some ? d.a_rows : 0)) * kBlockK * 2;
     // gated: the even CTA has the gate rows of b, the odd one the up rows; gate rows past N are rows
     // of up, whose columns the epilogue leaves out
-    const int nb = gated(kEpi) ? side * p.N + q.at.n * kHalf : q.at.n * kBN + side * kHalf;
-    mbar_arrive_expect_tx(full, (uint32_t)bytes);
-    if (some) load_operand<kAMn, kSlab>(st, &maps.a, full, q.at.m + side * kSlab, kb * kBlockK);
-    load_operand<kBMn, kHalf>(st + kOperandBytes, &maps.b, full, nb, kb * kBlockK);
+    const int nb = gated(kEpi) ? side * d.N + q.at.n * kHalf : q.at.n * kBN + side * kHalf;
+    mbar_arrive_expect_tx(full, (uint32_t)(kStageBytes - left_out));
+    if (some)
+      load_operand<kSlab>(st, &maps.a[q.prod], full, q.at.m + side * kSlab, kb * kBlockK, a_mn);
+    load_operand<kHalf>(st + kOperandBytes, &maps.b[q.prod], full, nb, kb * kBlockK, kBMn);
   };
   int issued = 0;  // by the producer (the same thread is elected here and below): stages asked for
 
   if (warp == 0) {
     if (elect_one()) {
-      prefetch_tensormap(&maps.a);
-      prefetch_tensormap(&maps.b);
+      prefetch_tensormap(&maps.a[0]);
+      prefetch_tensormap(&maps.b[0]);
       for (int s = 0; s < kStages; ++s) {
         // the even CTA's stage is full when its copies and, by the forwarder, the odd CTA's landed
         mbar_init(&full_bar[s], side == 0 ? 2 : 1);
@@ -248,9 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_shared();  // the barriers, to the copies
       // the first stages are on their way while the pair starts
       pdl_wait();
-      const Unit q = unit_of(p, num_kb, cluster_id_x());
-      for (; issued < kStages && q.kb0 + issued < q.kb1; ++issued)
-        load_block(q, q.kb0 + issued, issued);
+      const int64_t u = unit_at<kEpi>(p, 0);
+      if (u >= 0) {
+        const Unit q = unit_of<kEpi>(p, u);
+        for (; issued < kStages && q.kb0 + issued < q.kb1; ++issued)
+          load_block(q, q.kb0 + issued, issued);
+      }
     }
   } else if (warp == 1) {
     tmem_alloc_pair(&s_tmem, 2 * kBN);
@@ -278,9 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const int early = issued;
       for (int i = 0; i < early; ++i) r.next();
-      for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
-        const Unit q = unit_of(p, num_kb, u);
-        for (int kb = u < step ? q.kb0 + early : q.kb0; kb < q.kb1; ++kb) {
+      int64_t u;
+      for (int64_t s = 0; ok && (u = unit_at<kEpi>(p, s)) >= 0; ++s) {
+        const Unit q = unit_of<kEpi>(p, u);
+        for (int kb = s == 0 ? q.kb0 + early : q.kb0; kb < q.kb1; ++kb) {
           if (!r.ready && !wait(r.bar(), r.parity)) {
             ok = false;
             break;
@@ -297,8 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring r(full_bar, kStages, 0u);
       const uint32_t to = cluster_map(smem_u32(full_bar), 0u);
       bool ok = true;
-      for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
-        const Unit q = unit_of(p, num_kb, u);
+      int64_t u;
+      for (int64_t s = 0; ok && (u = unit_at<kEpi>(p, s)) >= 0; ++s) {
+        const Unit q = unit_of<kEpi>(p, u);
         for (int kb = q.kb0; kb < q.kb1; ++kb) {
           if (!r.ready && !wait(r.bar(), r.parity)) {
             ok = false;
@@ -316,12 +360,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t buf_phase = 0;
       bool ok = true;
       const uint32_t base = smem_u32(smem);
-      const uint32_t idesc = idesc_f16(256, kBN, DT<T>::kIsBF16) | (kAMn ? 1u << 15 : 0u) |
-                             (kBMn ? 1u << 16 : 0u);
+      const uint32_t idesc_b = idesc_f16(256, kBN, DT<T>::kIsBF16) | (kBMn ? 1u << 16 : 0u);
       const uint32_t empty_own = smem_u32(empty_bar), tfull_own = smem_u32(tfull_bar);
-      for (int64_t u = cluster_id_x(); u < units && ok; u += step) {
-        const Unit q = unit_of(p, num_kb, u);
+      int64_t u;
+      for (int64_t s = 0; ok && (u = unit_at<kEpi>(p, s)) >= 0; ++s) {
+        const Unit q = unit_of<kEpi>(p, u);
         const int pass = kDrain > 0 ? kDrain : q.kb1 - q.kb0;  // blocks of one accumulator
+        const bool a_mn = kEpi == kPlain && p.q[q.prod].a_mn;
+        const uint32_t idesc = idesc_b | (a_mn ? 1u << 15 : 0u);
+        const uint64_t a_step = k16_step(a_mn);
         for (int kc = q.kb0; kc < q.kb1 && ok; kc += pass) {
           if (!wait(&tempty_bar[buf], buf_phase ^ 1u)) {
             ok = false;
@@ -338,11 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t sa = base + (uint32_t)(r.stage * kStageBytes);
             const uint32_t sb = sa + (uint32_t)kOperandBytes;
+            const uint64_t da = operand_desc(sa, a_mn), db = operand_desc(sb, kBMn);
             const uint32_t at = (uint32_t)r.stage * 8u;
             r.next();
 #pragma unroll
             for (int k = 0; k < kBlockK / 16; ++k)
-              umma_f16_pair(d, operand_desc<kAMn>(sa, k), operand_desc<kBMn>(sb, k), idesc,
+              umma_f16_pair(d, da + k * a_step, db + k * k16_step(kBMn), idesc,
                             (kb > kc || k > 0) ? 1u : 0u);
             umma_commit_both(empty_own + at, 0u);
           }
@@ -391,12 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Passes of an accumulator over `blocks` k blocks.
     auto passes = [&](int blocks) { return kDrain > 0 ? (blocks - 1) / kDrain + 1 : 1; };
-    // The accumulator has been read; `left` passes of unit u follow.  Where no later pass takes this
-    // buffer nobody waits for the arrival, and the even CTA may leave before it comes.
-    auto free_buffer = [&](int left, int64_t u) {
-      if (left < 2 && u + step < units) {
-        const Unit n = unit_of(p, num_kb, u + step);
-        left += passes(n.kb1 - n.kb0) + (u + 2 * step < units ? 1 : 0);
+    // The accumulator has been read; `left` passes of the s-th unit follow.  Where no later pass takes
+    // this buffer nobody waits for the arrival, and the even CTA may leave before it comes.
+    auto free_buffer = [&](int left, int64_t s) {
+      const int64_t next = left < 2 ? unit_at<kEpi>(p, s + 1) : -1;
+      if (next >= 0) {
+        const Unit n = unit_of<kEpi>(p, next);
+        left += passes(n.kb1 - n.kb0) + (unit_at<kEpi>(p, s + 2) >= 0 ? 1 : 0);
       }
       tc_fence_before();
       __syncwarp();
@@ -405,10 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       buf ^= 1;
       if (buf == 0) buf_phase ^= 1u;
     };
-    for (int64_t u = cluster_id_x(); u < units; u += step) {
-      const Unit q = unit_of(p, num_kb, u);
+    int64_t u;
+    for (int64_t s = 0; (u = unit_at<kEpi>(p, s)) >= 0; ++s) {
+      const Unit q = unit_of<kEpi>(p, u);
+      const int M = p.q[q.prod].M, N = p.q[q.prod].N;
       const int m = q.at.m + side * kSlab;
-      const bool live = m < p.M;  // a row of this CTA is one of D's (uniform)
+      const bool live = m < M;  // a row of this CTA is one of D's (uniform)
       const bool part = q.row >= 0;
       const int n0 = q.at.n * kHalf + (P::kShared ? 0 : half * 64);  // gated: the box's first column
       const bool input = kEpi == kGradient && live && !part;
@@ -435,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) sums[h >> 1][(h & 1) * 32 + i] += v[i];
           }
-          free_buffer(passes(q.kb1 - kc) - 1, u);
+          free_buffer(passes(q.kb1 - kc) - 1, s);
         }
       } else {
         got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
@@ -474,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if constexpr (kEpi == kPlain) {
         for (int c = 0; c < kHalf / 64 && live; ++c) {
           const int col = half * kHalf + c * 64, to = q.at.n * kBN + col;
-          if (to >= p.N) break;
+          if (to >= N) break;
           float v[64];
           tmem_ld_x64(d + (uint32_t)col, v);
           uint8_t* b = next_box();
@@ -485,10 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 8; ++i) w[i] = v[j * 8 + i];
             *box_at(b, row, j) = pack<T>(w);
           }
-          publish([&] { tma_store_2d(&maps.o0, b, to, m); });
+          publish([&] { tma_store_2d(&maps.o0[q.prod], b, to, m); });
         }
       } else if constexpr (kEpi == kGated) {
-        if (live && n0 < p.N) {
+        if (live && n0 < N) {
           uint8_t* b = next_box();
 #pragma unroll
           for (int h = 0; h < kPieces; ++h) {
@@ -503,14 +554,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               *box_at(b, row, (piece0 + h) * 4 + j) = pack<T>(w);
             }
           }
-          publish([&] { tma_store_2d(&maps.o0, b, n0, m); });
+          publish([&] { tma_store_2d(&maps.o0[q.prod], b, n0, m); });
         }
       } else if constexpr (kEpi == kGatedSave) {
         // columns behind N are gate rows that belong to up, or nothing
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          if (n0 + (i & ~7) >= p.N) sums[0][i] = sums[1][i] = 0.0f;  // N is a multiple of 8
-        if (live && n0 < p.N) {
+          if (n0 + (i & ~7) >= N) sums[0][i] = sums[1][i] = 0.0f;  // N is a multiple of 8
+        if (live && n0 < N) {
           uint8_t* b = next_box();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -520,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               w[i] = gate_value<kAct>(sums[0][j * 8 + i]) * sums[1][j * 8 + i];
             *box_at(b, row, j) = pack<T>(w);
           }
-          publish([&] { tma_store_2d(&maps.o0, b, n0, m); });
+          publish([&] { tma_store_2d(&maps.o0[q.prod], b, n0, m); });
         }
         // Both halves write the codes of gate (first box) and up (second).
         if (leader) store_wait_read<0>();
@@ -538,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the larger value's exponent; a group of zeros has a scale of 1
           const int most = max((int)s_exp[0][k][row], (int)s_exp[1][k][row]);
           const int e = most == -128 ? 0 : most;
-          if (k == half && live && m + row < p.M)
-            (k == 0 ? p.gate : p.up).scales[(int64_t)(m + row) * p.nt + q.at.n] = fp8_scale(e);
+          if (k == half && live && m + row < M)
+            (k == 0 ? p.gate : p.up).scales[(int64_t)(m + row) * p.q[0].nt + q.at.n] = fp8_scale(e);
           const float inv = fp8_scale(-e);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -558,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_commit();
         }
       } else {
-        if (live && n0 < p.N) {
+        if (live && n0 < N) {
           // d_out lies in the first box, where its place takes d_gate; h waits in registers until
           // the store of d_up has read the second one
           uint8_t *bg = boxes, *bu = boxes + kBoxBytes;
@@ -594,11 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             sync();
 #pragma unroll
             for (int j = 0; j < kPieces * 4; ++j) *box_at(bu, row, piece0 * 4 + j) = hold[j];
-            publish([&] { tma_store_2d(&maps.o0, bu, n0, m); });
+            publish([&] { tma_store_2d(&maps.o0[q.prod], bu, n0, m); });
           }
         }
       }
-      if constexpr (kDrain == 0) free_buffer(0, u);
+      if constexpr (kDrain == 0) free_buffer(0, s);
     }
     if (leader) {
       store_wait_read<0>();  // the writes themselves end with the kernel
@@ -827,68 +878,209 @@ bool narrow(int64_t M, int64_t N, int64_t K, bool gate) {
   return thin < wide;
 }
 
+// The units and parts of a product in tiles of `bn` columns.
+Prod prod_of(int M, int N, int K, bool gate, int bn, Split sp) {
+  Prod q = {};
+  q.M = M;
+  q.N = N;
+  q.num_kb = (int)ceil_div(K, kBlockK);
+  q.mt = (int)ceil_div(M, kTile);
+  q.nt = (int)tiles_n(N, gate, bn);
+  q.whole = sp.whole;
+  q.rest = sp.rest;
+  q.split = sp.split;
+  q.a_rows = M < kSlab ? (M + 7) / 8 * 8 : kSlab;
+  return q;
+}
+int64_t units_of(const Prod& q) { return q.whole + (int64_t)q.rest * q.split; }
+
 struct Problem {
-  int dtype, M, N, K;
-  const void *a, *b;
-  int64_t a_pitch;
-  void *o0, *o1;  // h or the product; d_pre
-  const void* in;
-  Ckpt gate, up;
+  int dtype;
   float* parts;
   int* status;
+  // gated
+  int M, N, K;
+  const void *x, *w, *in;
+  void *h, *d_pre;
+  Ckpt gate, up;
+  // kPlain: one or two products, the one with the longer units first
+  const Product* list[2];
+  int n;
 };
 
-template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct, int kBN>
-cudaError_t run_tiles(const Problem& q, cudaStream_t s) {
+// The products of a call: tiles of 256 columns, some split, or of 128.
+struct Choice {
+  int bn;
+  int first;  // the product with the longer units
+  Split sp[2];
+  bool apart;  // a launch for each
+};
+
+// What the busiest pair does, in 64-k blocks of a 256-column tile, where n[0] units of c[0] are shared
+// out before n[1] of c[1] as unit_at does it; `rounds` as there.
+double busiest(const int64_t (&n)[2], const double (&c)[2], int64_t pairs, int64_t* rounds) {
+  const int64_t more = n[0] % pairs, own = n[0] / pairs;
+  int64_t most = 0, all = 0;  // units of the second that a pair takes, and that all take
+  if (n[1] > 0) {
+    const int64_t behind = (int64_t)ceil(c[0] / c[1]);
+    most = (pairs - more) * behind >= n[1] ? ceil_div(n[1], pairs - more)
+                                           : ceil_div(n[1] + more * behind, pairs);
+    all = more == 0 ? most : most > behind ? most - behind : 0;
+  }
+  if (rounds) *rounds = all;
+  const double late = more > 0 ? (own + 1) * c[0] + all * c[1] : 0.0;
+  const double rest = own * c[0] + most * c[1];
+  return late > rest ? late : rest;
+}
+
+// A unit costs its blocks, or its epilogue where that takes longer.
+double unit_cost(int64_t blocks, int bn) {
+  const double mma = bn == kTile ? (double)blocks : 0.65 * blocks;
+  const double epilogue = bn == kTile ? 8.0 : 5.0;
+  return mma > epilogue ? mma : epilogue;
+}
+
+// Two gradients share a launch, which fills the pairs that the first one's last tiles leave idle and
+// starts once: 243 rows of 416 x 1784 take 8 us, in two launches 14, and 4096 rows of 4096 x 4096
+// 157, in two 178.  Its units are whole, though, where a launch for each splits its last tiles: 6943
+// rows of 12360 x 680 take 237 us in one and 210 in two.  The busiest pairs' blocks foretell that to
+// about a tenth (3051 rows of 2960 x 6136: two should gain 7% and lose 4%), which is what a gain has
+// to be.
+constexpr int kStartBlocks = 16;  // what a launch costs
+
+Choice choose(const Product* q, int n) {
+  const int64_t pairs = num_sms() / 2;
+  Choice r = {};
+  if (n == 1) {
+    r.bn = narrow(q[0].M, q[0].N, q[0].K, false) ? 128 : kTile;
+    const int64_t tiles = ceil_div(q[0].M, kTile) * tiles_n(q[0].N, false, r.bn);
+    r.sp[0] = r.bn == kTile ? split_of(tiles, q[0].K) : Split{tiles, 0, 1};
+    return r;
+  }
+  double best = 0.0;
+  for (const int bn : {kTile, 128}) {
+    Choice t = {};
+    t.bn = bn;
+    int64_t tiles[2], kb[2];
+    double work = 0.0;
+    for (int i = 0; i < 2; ++i) {
+      tiles[i] = ceil_div(q[i].M, kTile) * tiles_n(q[i].N, false, bn);
+      kb[i] = ceil_div(q[i].K, kBlockK);
+      work += tiles[i] * unit_cost(kb[i], bn);
+    }
+    const double share = work / pairs;
+    double join = 0.0;
+    for (int i = 0; i < 2; ++i) {
+      t.sp[i] = Split{tiles[i], 0, 1};
+      // A tile that takes longer than a pair's share is split, in parts of at least eight blocks.
+      int64_t split = share > 1.0 ? (int64_t)ceil(kb[i] / share) : kMaxSplit;
+      if (split > kb[i] / kPartBlocks) split = kb[i] / kPartBlocks;
+      if (split > kMaxSplit) split = kMaxSplit;
+      if (split * tiles[i] > 2 * pairs) split = 2 * pairs / tiles[i];
+      if (bn == kTile && split > 1 && kb[i] - ceil_div(kb[i], split) > kJoinBlocks) {
+        t.sp[i] = Split{0, (int)tiles[i], (int)split};
+        join = kJoinBlocks;
+      }
+    }
+    int64_t units[2];
+    double cost[2];
+    for (int i = 0; i < 2; ++i) {
+      units[i] = t.sp[i].whole + (int64_t)t.sp[i].rest * t.sp[i].split;
+      cost[i] = unit_cost(ceil_div(kb[i], t.sp[i].split), bn);
+    }
+    t.first = cost[1] > cost[0];
+    const double total =
+        join + busiest({units[t.first], units[1 - t.first]}, {cost[t.first], cost[1 - t.first]},
+                       pairs, nullptr);
+    if (bn == kTile || total < best) best = total, r = t;
+  }
+  double two = kStartBlocks;
+  for (int i = 0; i < 2; ++i) {
+    const Choice c = choose(q + i, 1);
+    const int64_t kb = ceil_div(q[i].K, kBlockK);
+    const Split& sp = c.sp[0];
+    two += sp.whole / pairs * unit_cost(kb, c.bn);
+    if (sp.rest > 0)
+      two += unit_cost(ceil_div(kb, sp.split), c.bn) + kJoinBlocks;
+    else if (sp.whole % pairs)
+      two += unit_cost(kb, c.bn);
+  }
+  r.apart = two < 0.9 * best;
+  return r;
+}
+
+template <typename T, int kEpi, int kAct, int kBN>
+cudaError_t run_tiles(const Problem& q, const Choice& ch, cudaStream_t s) {
   constexpr bool kGate = gated(kEpi);
   using P = Plan<kEpi, kBN>;
-  constexpr auto kern = dense_kernel<T, kAMn, kBMn, kEpi, kAct, kBN>;
+  constexpr auto kern = dense_kernel<T, kEpi, kAct, kBN>;
   Args p = {};
-  p.M = q.M;
-  p.N = q.N;
-  p.K = q.K;
-  p.mt = (int)ceil_div(q.M, kTile);
-  p.nt = (int)tiles_n(q.N, kGate, kBN);
-  const int64_t tiles = (int64_t)p.mt * p.nt;
-  const Split sp = kBN == kTile ? split_of(tiles, q.K) : Split{tiles, 0, 1};
-  p.whole = sp.whole;
-  p.rest = sp.rest;
-  p.split = sp.split;
-  p.a_rows = q.M < kSlab ? (q.M + 7) / 8 * 8 : kSlab;
-  p.want_out = q.o0 != nullptr;
-  p.gate = q.gate;
-  p.up = q.up;
-  p.status = q.status;
-  p.limit_ns = wait_limit_ns();
-  Maps maps;
-  const int64_t N = q.N, rows_b = kGate ? 2 * N : N;
-  bool ok = kAMn ? map16(&maps.a, q.dtype, q.a, q.M, q.K, q.a_pitch, kBlockK)
-                 : map16(&maps.a, q.dtype, q.a, q.K, q.M, q.a_pitch, p.a_rows);
-  ok = ok && (kBMn ? map16(&maps.b, q.dtype, q.b, rows_b, q.K, rows_b, kBlockK)
-                   : map16(&maps.b, q.dtype, q.b, q.K, rows_b, q.K, kBN / 2));
-  maps.o0 = maps.o1 = maps.o2 = maps.in = maps.parts = maps.a;  // those that are not used
-  if (q.o0) ok = ok && map16(&maps.o0, q.dtype, q.o0, N, q.M, N, kSlab);
+  Maps maps = {};
+  bool ok = true;
+  const int n = kGate ? 1 : q.n;
+  int part_rows = 0;
+  for (int i = 0; i < n; ++i) {
+    const int from = i == 0 ? ch.first : 1 - ch.first;
+    const Product* l = kGate ? nullptr : q.list[from];
+    const int M = kGate ? q.M : l->M, N = kGate ? q.N : l->N, K = kGate ? q.K : l->K;
+    Prod& d = p.q[i];
+    d = prod_of(M, N, K, kGate, kBN, ch.sp[kGate ? 0 : from]);
+    d.a_mn = !kGate && l->tn;
+    d.part_row = part_rows;
+    part_rows += d.rest * d.split * kTile;
+    p.units[i] = units_of(d);
+    if constexpr (kGate) {
+      ok = ok && map16(&maps.a[0], q.dtype, q.x, K, M, K, d.a_rows) &&
+           map16(&maps.b[0], q.dtype, q.w, K, 2 * (int64_t)N, K, kBN / 2);
+    } else {
+      ok = ok &&
+           (l->tn ? map16(&maps.a[i], q.dtype, l->a, M, K, l->a_pitch, kBlockK)
+                  : map16(&maps.a[i], q.dtype, l->a, K, M, l->a_pitch, d.a_rows)) &&
+           map16(&maps.b[i], q.dtype, l->b, N, K, N, kBlockK);
+    }
+    void* out = kGate ? q.h : l->out;
+    if (out)
+      ok = ok && map16(&maps.o0[i], q.dtype, out, N, M, N, kSlab);
+    else
+      maps.o0[i] = maps.a[0];
+  }
+  if (n == 1) maps.a[1] = maps.b[1] = maps.o0[1] = maps.a[0];  // those that are not used
+  maps.o1 = maps.o2 = maps.in = maps.parts = maps.a[0];
   if constexpr (kEpi == kGradient) {
-    ok = ok && map16(&maps.o1, q.dtype, q.o1, N, q.M, 2 * N, kSlab) &&
-         map16(&maps.o2, q.dtype, static_cast<T*>(q.o1) + N, N, q.M, 2 * N, kSlab) &&
+    const int64_t N = q.N;
+    ok = ok && map16(&maps.o1, q.dtype, q.d_pre, N, q.M, 2 * N, kSlab) &&
+         map16(&maps.o2, q.dtype, static_cast<T*>(q.d_pre) + N, N, q.M, 2 * N, kSlab) &&
          map16(&maps.in, q.dtype, q.in, N, q.M, N, kSlab);
   } else if constexpr (kEpi == kGatedSave) {
-    const uint64_t width = (uint64_t)ckpt_width(N);
+    const uint64_t width = (uint64_t)ckpt_width(q.N);
     ok = ok &&
          make_map(&maps.o1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.gate.codes, width, (uint64_t)q.M,
                   width, kSlab) &&
          make_map(&maps.o2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.up.codes, width, (uint64_t)q.M,
                   width, kSlab);
   }
-  if (p.rest > 0)
+  if (part_rows > 0)
     ok = ok && make_map(&maps.parts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, q.parts, kTile,
-                        (uint64_t)p.rest * p.split * kTile, kTile * 4, kSlab);
+                        (uint64_t)part_rows, kTile * 4, kSlab);
   if (!ok) return cudaErrorInvalidValue;
   const int pairs = max_pairs<kern>(P::kSmem);
   if (pairs <= 0) return cudaErrorInvalidConfiguration;
-  const int64_t units = p.whole + (int64_t)p.rest * p.split;
+  const int64_t units = p.units[0] + p.units[1];
+  const int64_t grid = units < pairs ? units : pairs;
+  p.own = p.units[0] / grid;
+  p.more = p.units[0] % grid;
+  if (n == 2)
+    busiest({p.units[0], p.units[1]},
+            {unit_cost(ceil_div(p.q[0].num_kb, p.q[0].split), kBN),
+             unit_cost(ceil_div(p.q[1].num_kb, p.q[1].split), kBN)},
+            grid, &p.rounds);
+  p.want_out = q.h != nullptr;
+  p.gate = q.gate;
+  p.up = q.up;
+  p.status = q.status;
+  p.limit_ns = wait_limit_ns();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
+  cfg.gridDim = dim3((unsigned)(2 * grid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)P::kSmem;
   cfg.stream = s;
@@ -901,78 +1093,103 @@ cudaError_t run_tiles(const Problem& q, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps, p);
-  if (e != cudaSuccess || p.rest == 0) return e;
-  JoinArgs j = {};
-  j.M = q.M;
-  j.N = q.N;
-  j.mt = p.mt;
-  j.nt = p.nt;
-  j.rows = q.M < kTile ? q.M : kTile;
-  j.whole = p.whole;
-  j.rest = p.rest;
-  j.split = p.split;
-  j.want_out = p.want_out;
-  j.sums = q.parts;
-  j.o0 = q.o0;
-  j.o1 = q.o1;
-  j.in = q.in;
-  j.gate = q.gate;
-  j.up = q.up;
-  const int64_t warps = (int64_t)p.rest * j.rows * (kGate ? 1 : 2);
-  return launch_k(join_kernel<T, kEpi, kAct>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s,
-                  true, j);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps, p);
+  for (int i = 0; i < n && e == cudaSuccess; ++i) {
+    const Prod& d = p.q[i];
+    if (d.rest == 0) continue;
+    JoinArgs j = {};
+    j.M = d.M;
+    j.N = d.N;
+    j.mt = d.mt;
+    j.nt = d.nt;
+    j.rows = d.M < kTile ? d.M : kTile;
+    j.whole = d.whole;
+    j.rest = d.rest;
+    j.split = d.split;
+    j.want_out = p.want_out;
+    j.sums = q.parts + (int64_t)d.part_row * kTile;
+    j.o0 = kGate ? q.h : q.list[i == 0 ? ch.first : 1 - ch.first]->out;
+    j.o1 = q.d_pre;
+    j.in = q.in;
+    j.gate = q.gate;
+    j.up = q.up;
+    const int64_t warps = (int64_t)d.rest * j.rows * (kGate ? 1 : 2);
+    e = launch_k(join_kernel<T, kEpi, kAct>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s,
+                 true, j);
+  }
+  return e;
 }
 
-template <typename T, bool kAMn, bool kBMn, int kEpi, int kAct>
+template <typename T, int kEpi, int kAct>
 cudaError_t run(const Problem& q, cudaStream_t s) {
+  Choice ch = {};
+  const int64_t mt = ceil_div(q.M, kTile);
   if constexpr (kEpi != kGatedSave) {  // whose checkpoints have 128 channels to a scale
-    if (narrow(q.M, q.N, q.K, gated(kEpi))) return run_tiles<T, kAMn, kBMn, kEpi, kAct, 128>(q, s);
+    if (narrow(q.M, q.N, q.K, true)) {
+      ch.sp[0] = Split{mt * tiles_n(q.N, true, 128), 0, 1};
+      return run_tiles<T, kEpi, kAct, 128>(q, ch, s);
+    }
   }
-  return run_tiles<T, kAMn, kBMn, kEpi, kAct, kTile>(q, s);
+  ch.sp[0] = split_of(mt * tiles_n(q.N, true, kTile), q.K);
+  return run_tiles<T, kEpi, kAct, kTile>(q, ch, s);
+}
+
+template <typename T>
+cudaError_t run_products(const Problem& q, const Choice& ch, cudaStream_t s) {
+  return ch.bn == kTile ? run_tiles<T, kPlain, 0, kTile>(q, ch, s)
+                        : run_tiles<T, kPlain, 0, 128>(q, ch, s);
 }
 
 template <int kEpi>
 cudaError_t run_gated(int act, const Problem& q, cudaStream_t s) {
   if (q.dtype == MOE_BF16)
     return act == MOE_ACT_SILU
-               ? run<__nv_bfloat16, false, false, kEpi, MOE_ACT_SILU>(q, s)
-               : run<__nv_bfloat16, false, false, kEpi, MOE_ACT_GELU_TANH>(q, s);
-  return act == MOE_ACT_SILU ? run<__half, false, false, kEpi, MOE_ACT_SILU>(q, s)
-                             : run<__half, false, false, kEpi, MOE_ACT_GELU_TANH>(q, s);
+               ? run<__nv_bfloat16, kEpi, MOE_ACT_SILU>(q, s)
+               : run<__nv_bfloat16, kEpi, MOE_ACT_GELU_TANH>(q, s);
+  return act == MOE_ACT_SILU ? run<__half, kEpi, MOE_ACT_SILU>(q, s)
+                             : run<__half, kEpi, MOE_ACT_GELU_TANH>(q, s);
 }
 
 }  // namespace
 
-size_t dense_split_bytes(int64_t M, int64_t N, int64_t K, bool gate) {
+size_t gated_split_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  const Split sp = split_of(ceil_div(M, kTile) * tiles_n(N, gate, kTile), K);
+  const Split sp = split_of(ceil_div(M, kTile) * tiles_n(N, true, kTile), K);
   return (size_t)sp.rest * sp.split * kTile * kTile * sizeof(float);
 }
 
-cudaError_t launch_dense_nn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,
-                            const void* b, void* out, float* parts, int* status, cudaStream_t s) {
-  Problem q = {};
-  q.dtype = dtype, q.M = M, q.N = N, q.K = K, q.a = a, q.a_pitch = a_pitch, q.b = b, q.o0 = out;
-  q.parts = parts, q.status = status;
-  return dtype == MOE_BF16 ? run<__nv_bfloat16, false, true, kPlain, 0>(q, s)
-                           : run<__half, false, true, kPlain, 0>(q, s);
+size_t products_split_bytes(const Product* list, int n) {
+  for (int i = 0; i < n; ++i)
+    if (list[i].M <= 0 || list[i].N <= 0 || list[i].K <= 0) return 0;
+  const Choice ch = choose(list, n);
+  if (ch.apart) {
+    const size_t a = products_split_bytes(list, 1), b = products_split_bytes(list + 1, 1);
+    return a > b ? a : b;
+  }
+  size_t tiles = 0;
+  for (int i = 0; i < n; ++i) tiles += (size_t)ch.sp[i].rest * ch.sp[i].split;
+  return tiles * kTile * kTile * sizeof(float);
 }
 
-cudaError_t launch_dense_tn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,
-                            const void* b, void* out, float* parts, int* status, cudaStream_t s) {
+cudaError_t launch_products(int dtype, const Product* list, int n, float* parts, int* status,
+                            cudaStream_t s) {
   Problem q = {};
-  q.dtype = dtype, q.M = M, q.N = N, q.K = K, q.a = a, q.a_pitch = a_pitch, q.b = b, q.o0 = out;
-  q.parts = parts, q.status = status;
-  return dtype == MOE_BF16 ? run<__nv_bfloat16, true, true, kPlain, 0>(q, s)
-                           : run<__half, true, true, kPlain, 0>(q, s);
+  q.dtype = dtype, q.parts = parts, q.status = status, q.n = n;
+  const Choice ch = choose(list, n);
+  if (ch.apart) {
+    const cudaError_t e = launch_products(dtype, list, 1, parts, status, s);
+    return e == cudaSuccess ? launch_products(dtype, list + 1, 1, parts, status, s) : e;
+  }
+  for (int i = 0; i < n; ++i) q.list[i] = list + i;
+  return dtype == MOE_BF16 ? run_products<__nv_bfloat16>(q, ch, s)
+                           : run_products<__half>(q, ch, s);
 }
 
 cudaError_t launch_gated(int dtype, int act, int T, int F, int H, const void* x, const void* w,
                          void* out, Ckpt gate, Ckpt up, float* parts, int* status,
                          cudaStream_t s) {
   Problem q = {};
-  q.dtype = dtype, q.M = T, q.N = F, q.K = H, q.a = x, q.a_pitch = H, q.b = w, q.o0 = out;
+  q.dtype = dtype, q.M = T, q.N = F, q.K = H, q.x = x, q.w = w, q.h = out;
   q.gate = gate, q.up = up, q.parts = parts, q.status = status;
   return gate.codes ? run_gated<kGatedSave>(act, q, s) : run_gated<kGated>(act, q, s);
 }
@@ -981,7 +1198,7 @@ cudaError_t launch_gated_grad(int dtype, int act, int T, int F, int H, const voi
                               const void* d_out, void* d_pre, void* out, float* parts, int* status,
                               cudaStream_t s) {
   Problem q = {};
-  q.dtype = dtype, q.M = T, q.N = F, q.K = H, q.a = x, q.a_pitch = H, q.b = w, q.o0 = out, q.o1 = d_pre;
+  q.dtype = dtype, q.M = T, q.N = F, q.K = H, q.x = x, q.w = w, q.h = out, q.d_pre = d_pre;
   q.in = d_out, q.parts = parts, q.status = status;
   return run_gated<kGradient>(act, q, s);
 }

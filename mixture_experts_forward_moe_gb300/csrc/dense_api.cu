@@ -39,7 +39,27 @@ bool few_rows(const moe_gated_linear_t& p, bool save) {
 }
 
 size_t gated_bytes(const moe_gated_linear_t& p) {
-  return kHeaderBytes + align256(dense_split_bytes(p.T, p.F, p.H, true));
+  return kHeaderBytes + align256(gated_split_bytes(p.T, p.F, p.H));
+}
+
+// The gradients of a product [T, N] of x [T, K] and w [N, K]: d_x and d_w.
+struct Gradients {
+  Product list[2];
+  Gradients(int T, int N, int K, const void* dy, int64_t pitch, const void* x, const void* w,
+            void* d_x, void* d_w)
+      : list{{false, T, K, N, dy, pitch, w, d_x}, {true, N, K, T, dy, pitch, x, d_w}} {}
+};
+// Bytes of their sums, whichever are wanted.
+size_t gradient_bytes(int T, int N, int K) {
+  const Gradients g(T, N, K, nullptr, 0, nullptr, nullptr, nullptr, nullptr);
+  return larger(larger(products_split_bytes(g.list, 1), products_split_bytes(g.list + 1, 1)),
+                products_split_bytes(g.list, 2));
+}
+cudaError_t launch_gradients(int dtype, const Gradients& g, float* parts, int* status,
+                             cudaStream_t s) {
+  const bool x = g.list[0].out != nullptr, w = g.list[1].out != nullptr;
+  if (!x && !w) return cudaSuccess;
+  return launch_products(dtype, g.list + (x ? 0 : 1), x && w ? 2 : 1, parts, status, s);
 }
 
 // moe_gated_linear_bwd: status | d_pre [T, 2F] | x [T, H] | parts of K
@@ -50,10 +70,8 @@ struct GatedBwd {
     d_pre = kHeaderBytes;
     x = d_pre + align256(T * 2 * p.F * 2);
     parts = x + align256(T * p.H * 2);
-    size_t n = dense_split_bytes(p.T, p.F, p.H, true);
-    n = larger(n, dense_split_bytes(p.T, p.H, 2 * (int64_t)p.F, false));
-    n = larger(n, dense_split_bytes(2 * (int64_t)p.F, p.H, p.T, false));
-    bytes = parts + align256(n);
+    bytes = parts + align256(larger(gated_split_bytes(p.T, p.F, p.H),
+                                    gradient_bytes(p.T, 2 * p.F, p.H)));
   }
 };
 
@@ -75,8 +93,7 @@ struct LinearBwd {
     d_out = kHeaderBytes;
     x = d_out + (pitch != g.N ? align256(T * (size_t)pitch * 2) : 0);
     parts = x + align256(T * g.K * 2);
-    bytes = parts + align256(larger(dense_split_bytes(g.T, g.K, g.N, false),
-                                    dense_split_bytes(g.N, g.K, g.T, false)));
+    bytes = parts + align256(gradient_bytes(g.T, g.N, g.K));
   }
 };
 
@@ -182,14 +199,9 @@ moe_status_t moe_gated_linear_bwd(const moe_gated_linear_t* p, const void* d_out
             : launch_gated_grad(p->dtype, p->activation, p->T, p->F, p->H, x, w_gate_up, d_out,
                                 d_pre, out, parts, status, s);
   if (e != cudaSuccess) return from_cuda(e);
-  if (d_x)
-    if (const cudaError_t f = launch_dense_nn(p->dtype, p->T, p->H, 2 * p->F, d_pre,
-                                              2 * (int64_t)p->F, w_gate_up, d_x, parts, status, s))
-      return from_cuda(f);
-  if (d_w)
-    return from_cuda(launch_dense_tn(p->dtype, 2 * p->F, p->H, p->T, d_pre, 2 * (int64_t)p->F, x,
-                                     d_w, parts, status, s));
-  return MOE_OK;
+  return from_cuda(launch_gradients(
+      p->dtype, Gradients(p->T, 2 * p->F, p->H, d_pre, 2 * (int64_t)p->F, x, w_gate_up, d_x, d_w),
+      parts, status, s));
 }
 
 size_t moe_linear_bwd_workspace_size(const moe_linear_t* g) {
@@ -230,21 +242,14 @@ moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void
       return from_cuda(e);
   }
   if (pad) d_out = ws + at.d_out;
-  if (d_x)
-    if (const cudaError_t e = launch_dense_nn(g->dtype, g->T, g->K, g->N, d_out, at.pitch, w, d_x,
-                                              parts, status, s))
+  if (d_w && x_codes) {
+    if (const cudaError_t e = launch_restore(g->dtype, g->T, g->K, CkptIn{x_codes, x_scales},
+                                             ws + at.x, s))
       return from_cuda(e);
-  if (d_w) {
-    if (x_codes) {
-      if (const cudaError_t e = launch_restore(g->dtype, g->T, g->K, CkptIn{x_codes, x_scales},
-                                               ws + at.x, s))
-        return from_cuda(e);
-      x = ws + at.x;
-    }
-    return from_cuda(launch_dense_tn(g->dtype, g->N, g->K, g->T, d_out, at.pitch, x, d_w, parts,
-                                     status, s));
+    x = ws + at.x;
   }
-  return MOE_OK;
+  return from_cuda(launch_gradients(
+      g->dtype, Gradients(g->T, g->N, g->K, d_out, at.pitch, x, w, d_x, d_w), parts, status, s));
 }
 
 moe_status_t moe_checkpoint(int32_t T, int32_t C, int32_t dtype, const void* x, uint8_t* codes,

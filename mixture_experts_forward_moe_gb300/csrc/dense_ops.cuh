@@ -21,16 +21,24 @@ struct CkptIn {
   const float* scales;
 };
 
-// f32 partial sums that a product of M x N outputs over K (gated: N gated columns, of two products)
-// leaves in the workspace, in bytes; 0 where K is not split.
-size_t dense_split_bytes(int64_t M, int64_t N, int64_t K, bool gated);
+// A gradient's product: out[M, N] = sum_k a(m, k) b(k, n); a [M, K], or [K, M] (tn), with rows
+// a_pitch elements apart (a multiple of 8), b [K, N].
+struct Product {
+  bool tn;
+  int M, N, K;
+  const void* a;
+  int64_t a_pitch;
+  const void* b;
+  void* out;
+};
+// One or two of them, of which neither reads the other's result, in one launch.
+cudaError_t launch_products(int dtype, const Product* list, int n, float* parts, int* status,
+                            cudaStream_t s);
+// Bytes of the f32 sums that a launch leaves in the workspace where it splits K: of the same
+// products (the sizes alone), and of a gated product of M x N outputs.
+size_t products_split_bytes(const Product* list, int n);
+size_t gated_split_bytes(int64_t M, int64_t N, int64_t K);
 
-// out[M, N] = sum_k a(m, k) b(k, n): a [M, K] (nn) or [K, M] (tn) with rows a_pitch elements apart
-// (a multiple of 8), b [K, N].
-cudaError_t launch_dense_nn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,
-                            const void* b, void* out, float* parts, int* status, cudaStream_t s);
-cudaError_t launch_dense_tn(int dtype, int M, int N, int K, const void* a, int64_t a_pitch,
-                            const void* b, void* out, float* parts, int* status, cudaStream_t s);
 cudaError_t launch_gated(int dtype, int act, int T, int F, int H, const void* x, const void* w,
                          void* out, Ckpt gate, Ckpt up, float* parts, int* status, cudaStream_t s);
 cudaError_t launch_gated_grad(int dtype, int act, int T, int F, int H, const void* x, const void* w,

@@ -113,6 +113,29 @@ def test_linear_bwd(T, N, K, dtype, saved, cuda_device):
         R.assert_within(got[k], want, bound, k)
 
 
+# The two products of one launch: both split along K with the longer parts first or second, one split,
+# neither; more tiles than pairs, so that pairs take tiles of both; and a launch for each.
+@pytest.mark.parametrize("T,N,K", [
+    (2584, 4310, 48), (4878, 2119, 72), (2586, 4440, 488), (2506, 2255, 672), (1500, 12000, 264),
+    (777, 2333, 2568), (2333, 900, 3080), (4099, 4097, 72),
+    (6943, 12360, 680),
+])
+def test_linear_bwd_shares_pairs(T, N, K, cuda_device):
+    x = rand(T, K, seed=1, dtype=BF)
+    w = rand(N, K, seed=2, std=K ** -0.5, dtype=BF)
+    dy = rand(T, N, seed=3, std=0.5, dtype=BF)
+    got = B.moe_linear_bwd(dy, x, w)
+    again = B.moe_linear_bwd(dy, x, w)
+    assert status(cuda_device) == B.MOE_OK and sorted(got) == ["d_w", "d_x"]
+    ref = D.linear_bwd64(d64(dy), d64(x), d64(w), BF)
+    for k in got:
+        assert torch.equal(got[k], again[k])
+        R.assert_within(got[k], *ref[k], k)
+    # alone, each is the same within its bound
+    R.assert_within(B.moe_linear_bwd(dy, x, w, want_w=False)["d_x"], *ref["d_x"], "d_x")
+    R.assert_within(B.moe_linear_bwd(dy, x, w, want_x=False)["d_w"], *ref["d_w"], "d_w")
+
+
 # T, C
 CHECKPOINT = [(1, 8), (1, 128), (2, 136), (3, 7168), (33, 2056), (300, 1000), (5000, 72), (2, 40000)]
 
