@@ -705,7 +705,7 @@ moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void
 
 /*
  * moe_linear_w4a16, moe_gated_linear_w4a16 -- moe_linear and moe_gated_linear with NVFP4 weights,
- * for the few rows of decoding (the weights are read once for up to 32 rows):
+ * for the rows of decoding (the weights are read once for up to 128 rows):
  *   w[n, k] = e2m1(codes[n, k/2], low nibble: even k) * e4m3(scales[n, k/16]) * alpha
  *   codes [rows, K/2] and scales [rows, K/16] uint8 as a checkpoint of the model has them (not the
  *   tiles of moe_nvfp4_pack), rows = N, or 2F (gate rows, then up rows); alpha [1] f32, device.
@@ -714,7 +714,8 @@ moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void
  *   e2m1 * e4m3 is exact in f16, in which the products are taken, with f32 accumulation.  bf16 x
  *   is converted: exact between 2^-14 and 65504 in magnitude, at most 2^-25 off below, and a larger
  *   value sets MOE_ERR_F16_RANGE in the status word.
- *   workspace  moe_linear_w4a16_workspace_size(g), moe_gated_linear_w4a16_workspace_size(p) bytes.
+ *   workspace  moe_linear_w4a16_workspace_size(g), moe_gated_linear_w4a16_workspace_size(p) bytes
+ *              (more than sixteen rows of bf16 x: also x in f16).
  */
 size_t moe_linear_w4a16_workspace_size(const moe_linear_t* g);
 size_t moe_gated_linear_w4a16_workspace_size(const moe_gated_linear_t* p);

@@ -128,9 +128,6 @@ template <int N>
 __device__ __forceinline__ void store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void fence_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // 16 bytes at byte 16 j of row `row` of a box, where the 128-byte swizzle has them.
 __device__ __forceinline__ uint4* box_at(uint8_t* box, int row, int j) {
@@ -821,25 +818,12 @@ int max_pairs(int smem) {
   return cached[dev];
 }
 
-// A 2-D map of rows `pitch` bytes apart with the 128-byte swizzle, boxes of 128 bytes x box_rows.
-bool make_map(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, uint64_t inner,
-              uint64_t rows, uint64_t pitch, uint32_t box_rows) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {inner, rows};
-  cuuint64_t strides[1] = {pitch};
-  cuuint32_t box[2] = {(cuuint32_t)(128 / size), box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 CUtensorMapDataType type16(int dtype) {
   return dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 bool map16(CUtensorMap* m, int dtype, const void* base, int64_t inner, int64_t rows, int64_t pitch,
            int box_rows) {
-  return make_map(m, type16(dtype), 2, base, (uint64_t)inner, (uint64_t)rows, (uint64_t)pitch * 2,
+  return rows_map(m, type16(dtype), 2, base, (uint64_t)inner, (uint64_t)rows, (uint64_t)pitch * 2,
                   (uint32_t)box_rows);
 }
 
@@ -1054,13 +1038,13 @@ cudaError_t run_tiles(const Problem& q, const Choice& ch, cudaStream_t s) {
   } else if constexpr (kEpi == kGatedSave) {
     const uint64_t width = (uint64_t)ckpt_width(q.N);
     ok = ok &&
-         make_map(&maps.o1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.gate.codes, width, (uint64_t)q.M,
+         rows_map(&maps.o1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.gate.codes, width, (uint64_t)q.M,
                   width, kSlab) &&
-         make_map(&maps.o2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.up.codes, width, (uint64_t)q.M,
+         rows_map(&maps.o2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.up.codes, width, (uint64_t)q.M,
                   width, kSlab);
   }
   if (part_rows > 0)
-    ok = ok && make_map(&maps.parts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, q.parts, kTile,
+    ok = ok && rows_map(&maps.parts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, q.parts, kTile,
                         (uint64_t)part_rows, kTile * 4, kSlab);
   if (!ok) return cudaErrorInvalidValue;
   const int pairs = max_pairs<kern>(P::kSmem);

@@ -99,6 +99,16 @@ struct LinearBwd {
 
 constexpr int32_t kMaxW4Rows = 1 << 20;
 
+// status | x in f16
+size_t w4_workspace(int dtype, int64_t T, int64_t K) {
+  return kHeaderBytes + align256(w4_bytes(dtype, T, K));
+}
+// Past sixteen rows the weights are decoded once for all on the tensor cores.
+cudaError_t launch_rows4(const RowsCall& c, void* workspace, cudaStream_t s) {
+  return c.T > kFewW4Rows ? launch_w4(c, static_cast<char*>(workspace) + kHeaderBytes, s)
+                          : launch_rows(c, s);
+}
+
 moe_status_t check_w4(int32_t T, int32_t N, int32_t K) {
   if (T < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
   return K % 32 != 0 || T > kMaxW4Rows ? MOE_ERR_UNSUPPORTED : MOE_OK;
@@ -272,7 +282,7 @@ moe_status_t moe_checkpoint_restore(int32_t T, int32_t C, int32_t dtype, const u
 }
 
 size_t moe_linear_w4a16_workspace_size(const moe_linear_t* g) {
-  return check_linear_w4(g) == MOE_OK ? kHeaderBytes : 0;
+  return check_linear_w4(g) == MOE_OK ? w4_workspace(g->dtype, g->T, g->K) : 0;
 }
 
 moe_status_t moe_linear_w4a16(const moe_linear_t* g, const void* x, const uint8_t* codes,
@@ -284,17 +294,17 @@ moe_status_t moe_linear_w4a16(const moe_linear_t* g, const void* x, const uint8_
   if (!workspace || !codes || !scales || !alpha || (g->T > 0 && (!x || !out)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(x, codes, scales, bias, residual, out, workspace)) return MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < kHeaderBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < w4_workspace(g->dtype, g->T, g->K)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (g->T == 0) return MOE_OK;
   RowsCall c = {};
   c.T = g->T, c.N = g->N, c.K = g->K, c.dtype = g->dtype, c.act = g->activation;
   c.x = x, c.codes = codes, c.scales = scales, c.alpha = alpha, c.bias = bias, c.res = residual;
   c.out = out, c.status = static_cast<int*>(workspace);
-  return from_cuda(launch_rows(c, (cudaStream_t)stream));
+  return from_cuda(launch_rows4(c, workspace, (cudaStream_t)stream));
 }
 
 size_t moe_gated_linear_w4a16_workspace_size(const moe_gated_linear_t* p) {
-  return check_gated_w4(p) == MOE_OK ? kHeaderBytes : 0;
+  return check_gated_w4(p) == MOE_OK ? w4_workspace(p->dtype, p->T, p->H) : 0;
 }
 
 moe_status_t moe_gated_linear_w4a16(const moe_gated_linear_t* p, const void* x,
@@ -306,13 +316,13 @@ moe_status_t moe_gated_linear_w4a16(const moe_gated_linear_t* p, const void* x,
   if (!workspace || !codes || !scales || !alpha || (p->T > 0 && (!x || !out)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(x, codes, scales, out, workspace)) return MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < kHeaderBytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < w4_workspace(p->dtype, p->T, p->H)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (p->T == 0) return MOE_OK;
   RowsCall c = {};
   c.T = p->T, c.N = p->F, c.K = p->H, c.dtype = p->dtype, c.gated = 1, c.act = p->activation;
   c.x = x, c.codes = codes, c.scales = scales, c.alpha = alpha, c.out = out;
   c.status = static_cast<int*>(workspace);
-  return from_cuda(launch_rows(c, (cudaStream_t)stream));
+  return from_cuda(launch_rows4(c, workspace, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -62,6 +62,10 @@ struct RowsCall {
   int* status;
 };
 cudaError_t launch_rows(const RowsCall& c, cudaStream_t s);
+// The same of 4-bit weights, for more rows of x (dense_w4.cu); x16: w4_bytes of workspace.
+constexpr int kFewW4Rows = 16;
+size_t w4_bytes(int dtype, int64_t T, int64_t K);
+cudaError_t launch_w4(const RowsCall& c, void* x16, cudaStream_t s);
 
 cudaError_t launch_checkpoint(int dtype, int T, int C, const void* x, Ckpt out, cudaStream_t s);
 cudaError_t launch_restore(int dtype, int T, int C, CkptIn in, void* out, cudaStream_t s);

@@ -116,6 +116,11 @@ __device__ __forceinline__ void umma_commit_both(uint32_t bar, uint32_t even) {
       : "memory");
 }
 
+// What threads wrote to shared memory (and barriers they set up), to copies and MMAs.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Cluster barrier after which a CTA may leave: it orders nothing but the peers' finished reads
 // (cluster_sync's release would first wait for this CTA's global stores).
 __device__ __forceinline__ void cluster_leave() {
@@ -125,6 +130,20 @@ __device__ __forceinline__ void cluster_leave() {
 
 // ---- host side ---------------------------------------------------------------------------------
 constexpr int kSmemLimit = 226 * 1024;  // dynamic; leaves room for the static variables
+
+// A 2-D map of rows `pitch` bytes apart with the 128-byte swizzle, boxes of 128 bytes x box_rows.
+inline bool rows_map(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base,
+                     uint64_t inner, uint64_t rows, uint64_t pitch, uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {pitch};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / size), box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Sets a kernel's shared-memory limit, once per device; `Kernel` names the instance.
 template <auto Kernel>

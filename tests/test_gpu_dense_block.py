@@ -220,6 +220,36 @@ def test_linear_w4(T, N, K, dtype, act, bias, res, cuda_device):
     R.assert_within(out, ref, bound, "out")
 
 
+# Past sixteen rows: tiles of 32, 64 and 128 of them, of one and several blocks and parts of K, more
+# tiles than SMs, K that ends inside a block.
+W4_TILES = [
+    (17, 1, 32, BF), (17, 4099, 7168, BF), (31, 130, 2080, HF), (32, 129, 256, BF), (33, 20000, 288, HF),
+    (64, 257, 4128, BF), (65, 1000, 96, BF), (128, 2048, 2048, HF), (129, 40, 5152, BF),
+    (300, 1000, 992, BF),
+]
+
+
+@pytest.mark.parametrize("T,N,K,dtype", W4_TILES)
+def test_w4_tiles(T, N, K, dtype, cuda_device):
+    x = rand(T, K, seed=1, dtype=dtype)
+    x[0, : K // 2] *= 2.0 ** -12  # small values
+    codes, scales, alpha = weights4(2 * N, K, seed=2)
+    alpha = alpha / (K ** 0.5 * 8)
+    w = D.weights64(codes, scales, alpha.cpu())
+    b, r = rand(N, seed=3, dtype=dtype), rand(T, N, seed=4, dtype=dtype)
+    c1, s1 = codes[:N].contiguous(), scales[:N].contiguous()
+    for kw in (dict(bias=b, activation="silu", residual=r), {}):
+        out = B.moe_linear_w4a16(x, c1, s1, alpha, **kw)
+        assert torch.equal(out, B.moe_linear_w4a16(x, c1, s1, alpha, **kw))
+        ref, bound = D.w4_linear64(x, w[:N], kw.get("bias"), kw.get("activation", "none"),
+                                   kw.get("residual"))
+        R.assert_within(out, ref, bound, "out")
+    out = B.moe_gated_linear_w4a16(x, codes, scales, alpha)
+    assert torch.equal(out, B.moe_gated_linear_w4a16(x, codes, scales, alpha))
+    assert out.dtype == dtype and status(cuda_device) == B.MOE_OK
+    R.assert_within(out, *D.w4_gated64(x, w, "silu"), "gated")
+
+
 @pytest.mark.parametrize("T,F,K,dtype,act", [
     (1, 1, 32, HF, "silu"), (1, 2048, 7168, BF, "silu"), (3, 20, 96, BF, "gelu_tanh"),
     (8, 771, 544, HF, "gelu_tanh"), (11, 9, 2048, BF, "silu"), (32, 1536, 4096, BF, "silu"),

@@ -304,6 +304,88 @@ def test_w4_scales_behind_a_row_are_not_used(cuda_device):
     assert bool(torch.isfinite(out[:, 0::2]).all()) and bool(torch.isnan(out[:, 1::2]).all())
 
 
+def w4_bytes(T, N, K, dtype):
+    g = B.Linear(T, N, K, B.MOE_BF16 if dtype is BF else B.MOE_F16, 0, 0)
+    return int(B.lib().moe_linear_w4a16_workspace_size(ctypes.byref(g)))
+
+
+@pytest.mark.parametrize("T", [20, 70])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_w4_tiles_in_a_callers_workspace(T, dtype, cuda_device):
+    """Any contents, canaries behind it, a captured graph, and one that is too small."""
+    N, K = 200, 608
+    codes, scales, alpha = weights4(N, K, 1)
+    x = rand(T, K, seed=1, dtype=dtype)
+    want = B.moe_linear_w4a16(x, codes, scales, alpha)
+    n = w4_bytes(T, N, K, dtype)
+    assert n % 256 == 0 and n >= 256 + (T * K * 2 if dtype is BF else 0)
+    whole = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = whole[:n]
+    ws[:256] = 0
+    assert torch.equal(B.moe_linear_w4a16(x, codes, scales, alpha, workspace=ws), want)
+    assert bool((whole[n:] == 0xFF).all())
+    if dtype is BF:
+        with pytest.raises(B.MoeError, match="workspace"):
+            B.moe_linear_w4a16(x, codes, scales, alpha, workspace=ws[:n - 256])
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        B.moe_linear_w4a16(x, codes, scales, alpha)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = B.moe_linear_w4a16(x, codes, scales, alpha)
+    x2 = rand(T, K, seed=2, dtype=dtype)
+    want2 = B.moe_linear_w4a16(x2, codes, scales, alpha)
+    x.copy_(x2)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want2)
+
+
+def test_w4_tiles_report_values_past_the_f16_range(cuda_device):
+    codes, scales, alpha = weights4(40, 64, 1)
+    ws = B.new_workspace(w4_bytes(20, 40, 64, BF))
+    x = rand(20, 64, seed=1, dtype=BF)
+    for call in (B.moe_linear_w4a16, B.moe_gated_linear_w4a16):
+        x[19, 63] = 1.0
+        call(x, codes, scales, alpha, workspace=ws)
+        assert B.get_device_status(ws) == B.MOE_OK
+        x[19, 63] = 65536.0
+        call(x, codes, scales, alpha, workspace=ws)
+        assert B.get_device_status(ws) == B.MOE_ERR_F16_RANGE
+
+
+def test_w4_tiles_leave_out_scales_behind_a_row(cuda_device):
+    codes, scales, alpha = weights4(41, 96, 1)
+    scales[1::2] = 0x7F  # NaN
+    x = rand(40, 96, seed=1, dtype=HF)
+    x[7] = float("nan")  # and a row of NaN stays in its row
+    out = B.moe_linear_w4a16(x, codes, scales, alpha)
+    assert bool(torch.isnan(out[7]).all()) and bool(torch.isnan(out[:, 1::2]).all())
+    out = torch.cat([out[:7], out[8:]])
+    assert bool(torch.isfinite(out[:, 0::2]).all())
+
+
+@pytest.mark.parametrize("T,N,K", [(20, 500, 4096), (100, 300, 1000 // 32 * 32), (200, 24000, 256)])
+def test_a_wait_of_w4_tiles_that_gives_up(T, N, K, cuda_device):
+    """As test_a_wait_that_gives_up."""
+    codes, scales, alpha = weights4(N, K, 1)
+    x = rand(T, K, seed=1, dtype=BF)
+    ws = B.new_workspace(w4_bytes(T, N, K, BF))
+    want = B.moe_linear_w4a16(x, codes, scales, alpha, workspace=ws)
+    torch.cuda.synchronize()
+    old = B.set_wait_limit_ns(0)
+    try:
+        for _ in range(2):
+            B.moe_linear_w4a16(x, codes, scales, alpha, workspace=ws)
+            assert B.get_device_status(ws) == B.MOE_ERR_TIMEOUT
+    finally:
+        B.set_wait_limit_ns(old)
+    assert torch.equal(B.moe_linear_w4a16(x, codes, scales, alpha, workspace=ws), want)
+    assert B.get_device_status(ws) == B.MOE_OK
+
+
 def test_w4_rows_agree_with_the_experts(cuda_device):
     """The 4-bit product is the grouped 4-bit product of one expert, whose weights are packed."""
     codes, scales, alpha = weights4(256, 512, 5)
