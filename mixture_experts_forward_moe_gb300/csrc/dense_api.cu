@@ -31,11 +31,11 @@ moe_status_t check_gated(const moe_gated_linear_t* p) {
 // Both parts of a checkpoint, or neither.
 bool both(const void* codes, const void* scales) { return (codes != nullptr) == (scales != nullptr); }
 
-// Few tokens that save nothing: the weights are streamed (dense_rows.cu).  From two tokens on only
-// where there are too few weights for the tiles of dense.cu to fill the SMs (8 x 2048 x 7168: 20.4 us
-// against 26; 8 x 18432 x 7168: 113 against 88).
+// Few tokens that save nothing have the weights as the M side (dense_few.cu), where reading them takes
+// longest: 16 x 2048 x 7168 in 15.5 us against 21, 32 x 18432 x 7168 in 85 against 90, but 128 x 18432 x
+// 7168 in 103 against 92 and 64 x 4096 x 4096 in 21 against 20.
 bool few_rows(const moe_gated_linear_t& p, bool save) {
-  return !save && (p.T == 1 || (p.T <= 16 && 2 * (int64_t)p.F * p.H <= 1 << 26));
+  return !save && (p.T <= 32 || (p.T <= kFewRows && 2 * (int64_t)p.F * p.H < 1 << 25));
 }
 
 size_t gated_bytes(const moe_gated_linear_t& p) {
@@ -155,7 +155,7 @@ moe_status_t moe_gated_linear(const moe_gated_linear_t* p, const void* x, const 
     RowsCall c = {};
     c.T = p->T, c.N = p->F, c.K = p->H, c.dtype = p->dtype, c.gated = 1, c.act = p->activation;
     c.x = x, c.w = w_gate_up, c.out = out, c.status = static_cast<int*>(workspace);
-    return from_cuda(launch_rows(c, s));
+    return from_cuda(p->T == 1 ? launch_rows(c, s) : launch_few(c, s));
   }
   return from_cuda(launch_gated(
       p->dtype, p->activation, p->T, p->F, p->H, x, w_gate_up, out, Ckpt{gate_codes, gate_scales},

@@ -45,7 +45,8 @@ cudaError_t launch_gated_grad(int dtype, int act, int T, int F, int H, const voi
                               const void* d_out, void* d_pre, void* out, float* parts, int* status,
                               cudaStream_t s);
 
-// Few rows of x against 16-bit or 4-bit weights (dense_rows.cu).
+// Few rows of x against 4-bit weights, or one against the 16-bit weights of a gated product
+// (dense_rows.cu).
 struct RowsCall {
   int T, N, K;  // gated: N outputs of 2 N weight rows
   int dtype;
@@ -62,6 +63,9 @@ struct RowsCall {
   int* status;
 };
 cudaError_t launch_rows(const RowsCall& c, cudaStream_t s);
+// The 16-bit gated product of up to kFewRows rows of x (dense_few.cu).
+constexpr int kFewRows = 128;
+cudaError_t launch_few(const RowsCall& c, cudaStream_t s);
 // The same of 4-bit weights, for more rows of x (dense_w4.cu); x16: w4_bytes of workspace.
 constexpr int kFewW4Rows = 16;
 size_t w4_bytes(int dtype, int64_t T, int64_t K);

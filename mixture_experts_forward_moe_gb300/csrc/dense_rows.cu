@@ -1,16 +1,15 @@
-// dense_rows.cu -- up to sixteen rows of x against many weight rows, which are streamed once: 4-bit
-// weights (include/moe.h: moe_linear_w4a16, moe_gated_linear_w4a16) and the 16-bit gated product
-// (moe_gated_linear).  4 bits, 7168 x 7168 at 1, 4, 8 and 16 rows: 13, 14, 15 and 21 us.
+// dense_rows.cu -- up to sixteen rows of x against 4-bit weights, which are streamed once
+// (include/moe.h: moe_linear_w4a16, moe_gated_linear_w4a16), and the 16-bit gated product of one row
+// (moe_gated_linear).  4 bits, 7168 x 7168 at 1, 4, 8 and 16 rows: 13, 14, 15 and 21 us; 16 bits, 4096
+// weight rows of 7168: 12 us.
 //
-// What bounds it is the weights' bytes.  They go into the operand layout of mma.sync m16n8k16 as they
-// lie: 16 weight rows are its M side, eight rows of x its N side.  (One row of x leaves seven of eight
-// columns empty; on the CUDA cores every weight would cost an f32 multiply-add per row of x beside
-// its decoding.)  A lane's 16 bytes of a row are consecutive k, and the k of an MMA are assigned to
-// lanes as they lie there: the order of k within a sum is free as long as x follows it.
-//   16 bits: 8 k of 16 bytes, two MMAs; a block of 64 k is 128 bytes of a row
-//   4 bits: 32 k of 16 bytes, eight MMAs; a block of 256 k.  E2M1 codes times their E4M3 scale are
-//     exact f16, so x is taken in f16 (bf16 x is exact there between 2^-14 and 65504; larger values
-//     are reported)
+// What bounds it is the weights' bytes, and for 4 bits as much the instructions that decode them.
+// They go into the operand layout of mma.sync m16n8k16 as they lie: 16 weight rows are its M side,
+// eight rows of x its N side.  (One row of x leaves seven of eight columns empty; on the CUDA cores
+// every weight would cost an f32 multiply-add per row of x beside its decoding.)  A lane's 16 bytes of
+// a row are 32 consecutive k, eight MMAs, whose k are assigned to lanes as they lie there: the order
+// of k within a sum is free as long as x follows it.  E2M1 codes times their E4M3 scale are exact f16,
+// so x is taken in f16 (bf16 x is exact there between 2^-14 and 65504; larger values are reported).
 // A CTA of four warps has 64 or 128 weight rows, a warp 16 or 32, and a part of K: its x is staged once
 // and read by all warps.  A cluster is the parts of the same rows, whose sums meet in shared memory
 // and are added in the order of the parts.
@@ -19,46 +18,31 @@
 // Gated: an MMA's rows 0-7 are gate rows and 8-15 the up rows that go with them.
 #include "rows.cuh"
 
-#include <type_traits>
-
 namespace gb300moe {
 
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kMaxParts = 8;  // a portable cluster
 
-template <typename T>
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (DT<T>::kIsBF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool kW4>
-struct Block {
-  static constexpr int kLaneK = kW4 ? 32 : 8;  // k of 16 bytes
-  static constexpr int kK = 8 * kLaneK;        // k of a block: two vectors of four lanes, 128 bytes
-  static constexpr int kUnits = kLaneK / 8;    // 16-byte units of x that go with a vector
-};
-// How weights lie: 16 bits; 4 bits, a block's 16 scales of a row on 16 bytes (K a multiple of 256); 4
-// bits with any K, whose scales start on any even byte.
-enum Kind { kBits16, kBits4, kBits4Any };
+constexpr int kLaneK = 32;           // k of 16 bytes
+constexpr int kBlock = 8 * kLaneK;   // k of a block: two vectors of four lanes, 128 bytes of a row
+constexpr int kUnits = kLaneK / 8;   // 16-byte units of x that go with a vector
+// How scales lie: a block's 16 of a row on 16 bytes (K a multiple of 256), or from any even byte.
+enum Kind { kBits4, kBits4Any };
 // Bytes of a row that hold a block's scales, and a warp's stage: two vectors of 16 rows per lane, and
 // the scales.
 template <Kind kKind>
 constexpr int scale_bytes() {
-  return kKind == kBits16 ? 0 : kKind == kBits4 ? 16 : 32;
+  return kKind == kBits4 ? 16 : 32;
 }
 template <Kind kKind, int kMT>
 constexpr int stage_bytes() {
@@ -70,10 +54,7 @@ constexpr int stage_bytes() {
 // bytes more (two rows' reads then touch every bank once), then the rings.
 template <typename T, Kind kKind, int kMT, int kNT, bool kGated, int kStages>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int parts, int chunk) {
-  constexpr bool kW4 = kKind != kBits16;
   constexpr int kScaleBytes = scale_bytes<kKind>();
-  using B = Block<kW4>;
-  using X = typename std::conditional<kW4, __half, T>::type;  // what the MMAs take
   constexpr int kCols = 8 * kNT;
   constexpr int kStageBytes = stage_bytes<kKind, kMT>();
   constexpr int kScaleAt = kMT * 4 * 512;           // in a stage
@@ -86,10 +67,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   const int64_t out0 = (group * kWarps + warp) * kOuts;
   const int64_t t0 = (int64_t)blockIdx.y * kCols;
   const int cols = p.T - t0 < kCols ? (int)(p.T - t0) : kCols;
-  const int all = (p.K - 1) / B::kK + 1;
+  const int all = (p.K - 1) / kBlock + 1;
   const int first = (int)((int64_t)all * part / parts);
   const int last = (int)((int64_t)all * (part + 1) / parts);
-  const int x_pitch = chunk * B::kK * 2 + 64;
+  const int x_pitch = chunk * kBlock * 2 + 64;
   const uint32_t xs = smem_u32(smem);
   const uint32_t ring = xs + (uint32_t)(cols * x_pitch) + (uint32_t)(warp * kStages * kStageBytes);
 
@@ -101,12 +82,12 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   };
   // This lane's place in its two rows, of the block that is loaded next.
   const uint8_t* from[kMT][2];
-  const int64_t pitch = kW4 ? p.K / 2 : (int64_t)p.K * 2;
+  const int64_t pitch = p.K / 2;
 #pragma unroll
   for (int i = 0; i < kMT; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      from[i][h] = (kW4 ? p.codes : static_cast<const uint8_t*>(p.w)) + row_of(i, h * 8 + g) * pitch +
+      from[i][h] = p.codes + row_of(i, h * 8 + g) * pitch +
                    (int64_t)first * 128 + t * 16;
   // 4 bits: lanes 0-15 copy a row's 16 bytes each, or the first half of its 32 and lanes 16-31 the
   // other; `scale_in` is where this lane's first scale lies in them, which is the same in every
@@ -114,25 +95,23 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   const uint8_t* scale_from[kMT];
   int scale_in[kMT][2];
   const uint8_t* scale_end = nullptr;
-  if constexpr (kW4) {
-    scale_end = p.scales + (kGated ? 2 * (int64_t)p.N : p.N) * (p.K / 16);
+  scale_end = p.scales + (kGated ? 2 * (int64_t)p.N : p.N) * (p.K / 16);
 #pragma unroll
-    for (int i = 0; i < kMT; ++i) {
-      const int64_t at = row_of(i, lane & 15) * (p.K / 16) + (int64_t)first * 16;
-      scale_from[i] = p.scales + (at & ~int64_t(15)) + (lane >> 4) * 16;
+  for (int i = 0; i < kMT; ++i) {
+    const int64_t at = row_of(i, lane & 15) * (p.K / 16) + (int64_t)first * 16;
+    scale_from[i] = p.scales + (at & ~int64_t(15)) + (lane >> 4) * 16;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        scale_in[i][h] =
-            (kKind == kBits4 ? 0 : (int)(row_of(i, h * 8 + g) * (p.K / 16) & 15)) + t * 2;
-    }
+    for (int h = 0; h < 2; ++h)
+      scale_in[i][h] =
+          (kKind == kBits4 ? 0 : (int)(row_of(i, h * 8 + g) * (p.K / 16) & 15)) + t * 2;
   }
 
   // Vector (i, h, v) of a lane at ((i * 2 + h) * 2 + v) * 512 of its stage, 16 bytes a lane.
   auto load = [&](int b, int stage) {
     if (b < last) {
       const uint32_t to = ring + (uint32_t)(stage * kStageBytes) + (uint32_t)lane * 16u;
-      const int64_t left = p.K - (int64_t)b * B::kK;  // K is a multiple of a lane's
-      if (kKind == kBits4 || left >= B::kK) {
+      const int64_t left = p.K - (int64_t)b * kBlock;  // K is a multiple of a lane's
+      if (kKind == kBits4 || left >= kBlock) {
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -143,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       } else {
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const bool in = (v * 4 + t) * B::kLaneK < left;
+          const bool in = (v * 4 + t) * kLaneK < left;
 #pragma unroll
           for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -156,22 +135,20 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       for (int i = 0; i < kMT; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) from[i][h] += 128;
-      if constexpr (kW4) {
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-          const uint32_t dst = ring + (uint32_t)(stage * kStageBytes + kScaleAt +
-                                                 (i * 16 + (lane & 15)) * kScaleBytes);
-          if constexpr (kKind == kBits4) {
-            if (lane < 16) copy16(dst, scale_from[i]);
-          } else {
-            // the tensor may end inside the vector, or before it
-            const int64_t rest = scale_end - scale_from[i];
-            const int bytes = rest >= 16 ? 16 : rest > 0 ? (int)rest : 0;
-            copy16_part(dst + (uint32_t)(((lane >> 4) ^ ((lane >> 2) & 1)) * 16),
-                        bytes > 0 ? scale_from[i] : p.scales, bytes);
-          }
-          scale_from[i] += 16;
+      for (int i = 0; i < kMT; ++i) {
+        const uint32_t dst = ring + (uint32_t)(stage * kStageBytes + kScaleAt +
+                                               (i * 16 + (lane & 15)) * kScaleBytes);
+        if constexpr (kKind == kBits4) {
+          if (lane < 16) copy16(dst, scale_from[i]);
+        } else {
+          // the tensor may end inside the vector, or before it
+          const int64_t rest = scale_end - scale_from[i];
+          const int bytes = rest >= 16 ? 16 : rest > 0 ? (int)rest : 0;
+          copy16_part(dst + (uint32_t)(((lane >> 4) ^ ((lane >> 2) & 1)) * 16),
+                      bytes > 0 ? scale_from[i] : p.scales, bytes);
         }
+        scale_from[i] += 16;
       }
     }
     copy_commit();
@@ -180,14 +157,14 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   // x of one chunk: unit u of a block's vector (8 k) of lane t lies at u * 4 + t.
   bool over = false;
   auto stage_x = [&](int b0) {
-    const int units = chunk * B::kK / 8, end = cols * units;
+    const int units = chunk * kBlock / 8, end = cols * units;
     constexpr int kAhead = 4;  // loads that a thread has on their way
     for (int first = threadIdx.x; first < end; first += kAhead * kWarps * 32) {
       uint4 v[kAhead];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         const int i = first + a * kWarps * 32, c = i / units;
-        const int64_t k = (int64_t)b0 * B::kK + (i - c * units) * 8;
+        const int64_t k = (int64_t)b0 * kBlock + (i - c * units) * 8;
         v[a] = i < end && k < p.K
                    ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + (t0 + c) * p.K + k)
                    : zero4();
@@ -196,9 +173,8 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       for (int a = 0; a < kAhead; ++a) {
         const int i = first + a * kWarps * 32, c = i / units, q = i - c * units;
         if (i >= end) break;
-        if constexpr (kW4 && DT<T>::kIsBF16) v[a] = bf16x8_to_f16x8(v[a], over);
-        int at = q;
-        if constexpr (kW4) at = (q & ~15) | ((q & 3) << 2) | ((q >> 2) & 3);
+        if constexpr (DT<T>::kIsBF16) v[a] = bf16x8_to_f16x8(v[a], over);
+        const int at = (q & ~15) | ((q & 3) << 2) | ((q >> 2) & 3);
         *reinterpret_cast<uint4*>(smem + c * x_pitch + at * 16) = v[a];
       }
     }
@@ -213,49 +189,41 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
     const uint32_t at_s = ring + (uint32_t)(stage * kStageBytes + kScaleAt);
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      uint4 xv[kNT][B::kUnits];
+      uint4 xv[kNT][kUnits];
 #pragma unroll
       for (int j = 0; j < kNT; ++j)
 #pragma unroll
-        for (int c = 0; c < B::kUnits; ++c)
+        for (int c = 0; c < kUnits; ++c)
           xv[j][c] = j * 8 + g < cols
-                         ? lds16(xb + (uint32_t)(j * 8 * x_pitch + (v * B::kUnits + c) * 64))
+                         ? lds16(xb + (uint32_t)(j * 8 * x_pitch + (v * kUnits + c) * 64))
                          : zero4();
 #pragma unroll
       for (int i = 0; i < kMT; ++i) {
         uint4 w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) w[h] = lds16(at + (uint32_t)(((i * 2 + h) * 2 + v) * 512));
-        if constexpr (kW4) {
-          uint32_t s[2][2];  // scales of the lane's first and second 16 k, in both halves
+        uint32_t s[2][2];  // scales of the lane's first and second 16 k, in both halves
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t row = at_s + (uint32_t)((i * 16 + h * 8 + g) * kScaleBytes);
-            uint32_t two;
-            if constexpr (kKind == kBits4)
-              two = lds2(row + (uint32_t)(t * 2 + v * 8));
-            else  // behind K lie the next row's, which could be NaN
-              two = (v * 4 + t) * B::kLaneK < left
-                        ? lds2(row + (uint32_t)((scale_in[i][h] + v * 8) ^ ((g & 4) << 2)))
-                        : 0u;
-            two_scales(two, s[h]);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t row = at_s + (uint32_t)((i * 16 + h * 8 + g) * kScaleBytes);
+          uint32_t two;
+          if constexpr (kKind == kBits4)
+            two = lds2(row + (uint32_t)(t * 2 + v * 8));
+          else  // behind K lie the next row's, which could be NaN
+            two = (v * 4 + t) * kLaneK < left
+                      ? lds2(row + (uint32_t)((scale_in[i][h] + v * 8) ^ ((g & 4) << 2)))
+                      : 0u;
+          two_scales(two, s[h]);
+        }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t q0[4], q1[4];
-            nvfp4_decode8(word_of(w[0], c), s[0][c >> 1], q0);
-            nvfp4_decode8(word_of(w[1], c), s[1][c >> 1], q1);
-#pragma unroll
-            for (int j = 0; j < kNT; ++j) {
-              mma_16816<X>(acc[0][i][j], q0[0], q1[0], q0[1], q1[1], xv[j][c].x, xv[j][c].y);
-              mma_16816<X>(acc[kAccs - 1][i][j], q0[2], q1[2], q0[3], q1[3], xv[j][c].z, xv[j][c].w);
-            }
-          }
-        } else {
+        for (int c = 0; c < 4; ++c) {
+          uint32_t q0[4], q1[4];
+          nvfp4_decode8(word_of(w[0], c), s[0][c >> 1], q0);
+          nvfp4_decode8(word_of(w[1], c), s[1][c >> 1], q1);
 #pragma unroll
           for (int j = 0; j < kNT; ++j) {
-            mma_16816<X>(acc[0][i][j], w[0].x, w[1].x, w[0].y, w[1].y, xv[j][0].x, xv[j][0].y);
-            mma_16816<X>(acc[kAccs - 1][i][j], w[0].z, w[1].z, w[0].w, w[1].w, xv[j][0].z, xv[j][0].w);
+            mma_16816(acc[0][i][j], q0[0], q1[0], q0[1], q1[1], xv[j][c].x, xv[j][c].y);
+            mma_16816(acc[kAccs - 1][i][j], q0[2], q1[2], q0[3], q1[3], xv[j][c].z, xv[j][c].w);
           }
         }
       }
@@ -282,20 +250,20 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
     const int end = last - b0 < chunk ? last - b0 : chunk;
     for (int b = 0; b < end; ++b) {
       copy_wait<kStages - 2>();
-      if (kW4) __syncwarp();  // the scales are other lanes' copies
+      __syncwarp();  // the scales are other lanes' copies
       // into the stage that the block before this one has left
       load(b0 + b + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
-      multiply(stage, xs + (uint32_t)(g * x_pitch + b * B::kK * 2 + t * 16),
-               b0 + b + 1 < all ? B::kK : p.K - (all - 1) * B::kK);
+      multiply(stage, xs + (uint32_t)(g * x_pitch + b * kBlock * 2 + t * 16),
+               b0 + b + 1 < all ? kBlock : p.K - (all - 1) * kBlock);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
   }
-  if (kW4 && over) set_status(p.status, MOE_ERR_F16_RANGE);
+  if (over) set_status(p.status, MOE_ERR_F16_RANGE);
   copy_wait<0>();
 
   // Sums [cols][kAll]: the weight rows of the CTA, a gated product's gate rows before its up rows.
   constexpr int kAll = kWarps * 16 * kMT, kUp = kWarps * kOuts;
-  const float alpha = kW4 ? *p.alpha : 1.0f;
+  const float alpha = *p.alpha;
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -422,7 +390,6 @@ int parts_of(int64_t groups, int blocks) {
 
 template <typename T, Kind kKind, bool kGated, int kMT, int kNT>
 cudaError_t go(const RowsCall& c, cudaStream_t s) {
-  using B = Block<kKind != kBits16>;
   constexpr int kStages = kMT == 1 ? 4 : 3;
   constexpr auto kern = rows_kernel<T, kKind, kMT, kNT, kGated, kStages>;
   constexpr int kRing = kWarps * kStages * stage_bytes<kKind, kMT>();
@@ -431,14 +398,14 @@ cudaError_t go(const RowsCall& c, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t outs = (kGated ? 8 : 16) * kMT * kWarps;
   const int64_t groups = (c.N + outs - 1) / outs, tall = (c.T - 1) / (8 * kNT) + 1;
-  const int all = (c.K - 1) / B::kK + 1;
+  const int all = (c.K - 1) / kBlock + 1;
   const int parts = parts_of(groups * tall, all);
   const int cols = c.T < 8 * kNT ? c.T : 8 * kNT;
   // All of a part's x, or as much at a time as leaves room for three CTAs per SM (two).
   int chunk = (all + parts - 1) / parts;
-  const int fit = (((kMT == 1 ? 75 : 112) * 1024 - kRing) / cols - 64) / (B::kK * 2);
+  const int fit = (((kMT == 1 ? 75 : 112) * 1024 - kRing) / cols - 64) / (kBlock * 2);
   if (chunk > fit) chunk = fit > 0 ? fit : 1;
-  const int smem = kRing + cols * (chunk * B::kK * 2 + 64);
+  const int smem = kRing + cols * (chunk * kBlock * 2 + 64);
   if (smem > kSmemLimit) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * parts), (unsigned)tall);
@@ -468,14 +435,13 @@ cudaError_t pick(const RowsCall& c, cudaStream_t s) {
 
 template <typename T>
 cudaError_t typed(const RowsCall& c, cudaStream_t s) {
-  if (!c.codes && c.T == 1) {
+  if (!c.codes) {
     int wpr = 1;  // enough for about sixteen warps per SM
     while (wpr < kGemvWarps && (int64_t)c.N * wpr < (int64_t)num_sms() * 16 && c.K / 8 >= wpr * 2 * 32)
       wpr *= 2;
     return launch_k(gated_gemv_kernel<T>, dim3((unsigned)((c.N - 1) / (kGemvWarps / wpr) + 1)),
                     dim3(kGemvWarps * 32), 0, s, true, c, wpr);
   }
-  if (!c.codes) return pick<T, kBits16, true>(c, s);
   if (c.K % 256 == 0)
     return c.gated ? pick<T, kBits4, true>(c, s) : pick<T, kBits4, false>(c, s);
   return c.gated ? pick<T, kBits4Any, true>(c, s) : pick<T, kBits4Any, false>(c, s);

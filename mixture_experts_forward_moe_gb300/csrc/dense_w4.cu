@@ -27,7 +27,6 @@ constexpr int kStageK = 128;                   // k of a stage: two 64-k tiles o
 constexpr int kWBytes = kRows * kStageK * 2;
 constexpr int kSlots = 3;                      // stages of a warp's 16 rows on their way
 constexpr int kSlotBytes = 16 * 64 + 16 * 32;  // codes, and 32 bytes that hold a row's 8 scales
-constexpr int kMaxParts = 8;                   // a portable cluster
 
 template <int kN>
 struct Shape {
@@ -275,27 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
   else
     __syncthreads();
-  // This CTA's share of the outputs: consecutive threads, consecutive columns of out.
-  const int64_t n0 = group * kOuts;
-  const int end = (part + 1) * kOuts * cols / parts;
-  for (int i = part * kOuts * cols / parts + (int)threadIdx.x; i < end; i += kThreads) {
-    const int c = i / kOuts, r = i % kOuts;
-    if (n0 + r >= p.N) continue;  // (every read of a peer is waited for by its output)
-    float z = 0.0f, up = 0.0f;
-    if (parts > 1) {
-      const uint32_t at = base + (uint32_t)((c * kRows + r) * 4);
-#pragma unroll 4
-      for (int q = 0; q < parts; ++q) {
-        const uint32_t peer = cluster_map(at, (uint32_t)q);
-        z += ld_cluster(peer);
-        if (kGated) up += ld_cluster(peer + kOuts * 4u);
-      }
-    } else {
-      z = sums[c * kRows + r];
-      if (kGated) up = sums[c * kRows + kOuts + r];
-    }
-    finish<T, kGated>(p, t0 + c, n0 + r, z * alpha, up * alpha);
-  }
+  finish_tile<T, kGated, kOuts, kThreads>(p, base, sums, kRows, group, part, parts, t0, cols, alpha);
   if (parts > 1) cluster_leave();  // a peer may still read this CTA's sums
   if (warp == kDecodeWarps + 1) {
     tc_fence_after();
@@ -314,33 +293,6 @@ __global__ void __launch_bounds__(256)
   if (over) set_status(status, MOE_ERR_F16_RANGE);
 }
 
-// Clusters of `parts` CTAs that the GPU holds at a time, asked for once per device.
-template <auto Kernel>
-int max_clusters(int parts, int smem) {
-  static std::once_flag once[64];
-  static int most[64][kMaxParts + 1];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::call_once(once[dev], [dev, smem] {
-    for (int q = 1; q <= kMaxParts; ++q) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)q);
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = (size_t)smem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = (unsigned)q;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int n = 0;
-      most[dev][q] = cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) == cudaSuccess ? n : 0;
-    }
-  });
-  return most[dev][parts];
-}
-
 template <typename T, bool kGated, int kN>
 cudaError_t go(const RowsCall& c, void* x16, cudaStream_t s) {
   constexpr auto kern = w4_kernel<T, kGated, kN>;
@@ -349,16 +301,7 @@ cudaError_t go(const RowsCall& c, void* x16, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t groups = (c.N - 1) / kOuts + 1, tall = (c.T - 1) / kN + 1;
   const int all = (c.K - 1) / kBlock + 1;
-  // Parts of K that take the least time, in blocks, of which a CTA is taken to cost six beside its own
-  // (its start, the first block and the join).
-  int64_t best = 0;
-  int parts = 0;
-  for (int q = 1; q <= kMaxParts && q <= all; ++q) {
-    const int64_t most = max_clusters<kern>(q, kSmem);
-    if (most <= 0) continue;
-    const int64_t t = ((groups * tall + most - 1) / most) * ((all + q - 1) / q + 6);
-    if (parts == 0 || t < best) best = t, parts = q;
-  }
+  const int parts = parts_of<kern>(groups * tall, all, 6, kThreads, kSmem);
   if (parts == 0) return cudaErrorInvalidConfiguration;
   const bool prepare = c.dtype == MOE_BF16;
   const int x_rows = c.T < kN ? (c.T + 7) / 8 * 8 : kN;

@@ -1,5 +1,5 @@
-// rows.cuh -- what the products that decode or stream weight rows share (dense_rows.cu, dense_w4.cu):
-// copies into shared memory, E4M3 scales, and the end of an output.
+// rows.cuh -- what the products of few rows of x share (dense_rows.cu, dense_w4.cu, dense_few.cu):
+// copies into shared memory, E4M3 scales, the end of a tile, and in how many parts K is split.
 #pragma once
 
 #include "activation.cuh"
@@ -75,6 +75,81 @@ __device__ __forceinline__ void finish(const RowsCall& p, int64_t row, int64_t n
     if (p.res) z += DT<T>::to_f(static_cast<const T*>(p.res)[o]);
   }
   static_cast<T*>(p.out)[o] = DT<T>::from_f(z);
+}
+
+// A tile's share of its outputs, once the CTAs of its cluster (`parts` of K, this one the part-th) have
+// written their sums [columns][pitch]: kOuts of them, a gated product's up rows kOuts further.
+// Consecutive threads have consecutive columns of out; the parts are added in their order.
+template <typename T, bool kGated, int kOuts, int kThreads>
+__device__ __forceinline__ void finish_tile(const RowsCall& p, uint32_t base, const float* sums,
+                                            int pitch, int64_t group, int part, int parts,
+                                            int64_t t0, int cols, float alpha) {
+  const int64_t n0 = group * kOuts;
+  const int end = (part + 1) * kOuts * cols / parts;
+  for (int i = part * kOuts * cols / parts + (int)threadIdx.x; i < end; i += kThreads) {
+    const int c = i / kOuts, r = i % kOuts;
+    if (n0 + r >= p.N) continue;  // (every read of a peer is waited for by its output)
+    float z = 0.0f, up = 0.0f;
+    if (parts > 1) {
+      const uint32_t at = base + (uint32_t)((c * pitch + r) * 4);
+#pragma unroll 4
+      for (int q = 0; q < parts; ++q) {
+        const uint32_t peer = cluster_map(at, (uint32_t)q);
+        z += ld_cluster(peer);
+        if (kGated) up += ld_cluster(peer + kOuts * 4u);
+      }
+    } else {
+      z = sums[c * pitch + r];
+      if (kGated) up = sums[c * pitch + kOuts + r];
+    }
+    finish<T, kGated>(p, t0 + c, n0 + r, z * alpha, up * alpha);
+  }
+}
+
+// ---- host side ---------------------------------------------------------------------------------
+constexpr int kMaxParts = 8;  // a portable cluster
+
+// Clusters of `parts` CTAs that the GPU holds at a time, asked for once per device.
+template <auto Kernel>
+inline int max_clusters(int parts, int threads, int smem) {
+  static std::once_flag once[64];
+  static int most[64][kMaxParts + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::call_once(once[dev], [dev, threads, smem] {
+    for (int q = 1; q <= kMaxParts; ++q) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)q);
+      cfg.blockDim = dim3((unsigned)threads);
+      cfg.dynamicSmemBytes = (size_t)smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)q;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      most[dev][q] = cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) == cudaSuccess ? n : 0;
+    }
+  });
+  return most[dev][parts];
+}
+
+// Parts of K in which `tiles` tiles of `all` blocks take the least time, in blocks, of which a CTA is
+// taken to cost `start` beside its own (its start, the first block and the join); 0: no launch is
+// possible.
+template <auto Kernel>
+inline int parts_of(int64_t tiles, int all, int start, int threads, int smem) {
+  int64_t best = 0;
+  int parts = 0;
+  for (int q = 1; q <= kMaxParts && q <= all; ++q) {
+    const int64_t most = max_clusters<Kernel>(q, threads, smem);
+    if (most <= 0) continue;
+    const int64_t t = ((tiles + most - 1) / most) * ((all + q - 1) / q + start);
+    if (parts == 0 || t < best) best = t, parts = q;
+  }
+  return parts;
 }
 
 }  // namespace gb300moe

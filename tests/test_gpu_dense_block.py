@@ -88,6 +88,24 @@ def test_gated_linear_bwd(T, H, F, dtype, act, saved, cuda_device):
         R.assert_within(got[k], want, bound, k)
 
 
+# Up to 128 rows of x: tiles of 16, 32, 64 and 128 of them, outputs that end inside a tile, K of one block
+# and of several parts, more tiles than SMs, and both sides of the rule on the weights' size.
+@pytest.mark.parametrize("T,H,F,dtype,act", [
+    (2, 8, 8, BF, "silu"), (2, 7168, 72, HF, "silu"), (16, 64, 20000, BF, "gelu_tanh"),
+    (31, 5000, 136, BF, "silu"), (32, 4096, 4096, HF, "silu"), (48, 2056, 1000, BF, "silu"),
+    (64, 4096, 4088, HF, "gelu_tanh"), (64, 4096, 4096, BF, "silu"), (65, 1032, 3080, BF, "silu"),
+    (127, 96, 64, HF, "silu"), (128, 7168, 520, BF, "gelu_tanh"),
+])
+def test_gated_linear_of_few_rows(T, H, F, dtype, act, cuda_device):
+    x = rand(T, H, seed=1, dtype=dtype)
+    w = rand(2 * F, H, seed=2, std=1.5 * H ** -0.5, dtype=dtype)
+    ref, err, *_ = D.gated64(d64(x), d64(w), act)
+    out = B.moe_gated_linear(x, w, activation=act)
+    assert out.dtype == dtype and torch.equal(out, B.moe_gated_linear(x, w, activation=act))
+    assert status(cuda_device) == B.MOE_OK
+    R.assert_within(out, ref, D.rounded(ref, err, dtype), "out")
+
+
 # T, N, K
 LINEAR_BWD = [
     (1, 8, 8, BF), (1, 4099, 264, HF), (5, 3, 16, BF), (64, 2048, 768, BF), (100, 4099, 520, HF),

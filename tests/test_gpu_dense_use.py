@@ -416,6 +416,32 @@ def test_checkpoints_are_the_rows_of_the_fp8_grouped_product(cuda_device):
     R.assert_within(out, ref, D.rounded(ref, 2 * off, BF), "fp8")
 
 
+@pytest.mark.parametrize("T,H,F", [(7, 4096, 136), (30, 520, 20000), (100, 1032, 3080)])
+def test_a_wait_of_few_rows_that_gives_up(T, H, F, cuda_device):
+    """As test_a_wait_that_gives_up; and a captured graph with a row of NaN in its second input."""
+    x, w, _ = block(T, H, F, HF)
+    ws = B.new_workspace(gated_bytes(T, H, F, "moe_gated_linear"))
+    want = B.moe_gated_linear(x, w, workspace=ws)
+    torch.cuda.synchronize()
+    old = B.set_wait_limit_ns(0)
+    try:
+        for _ in range(2):
+            B.moe_gated_linear(x, w, workspace=ws)
+            assert B.get_device_status(ws) == B.MOE_ERR_TIMEOUT
+    finally:
+        B.set_wait_limit_ns(old)
+    assert torch.equal(B.moe_gated_linear(x, w, workspace=ws), want)
+    assert B.get_device_status(ws) == B.MOE_OK
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = B.moe_gated_linear(x, w)
+    x[2] = float("nan")
+    graph.replay()
+    torch.cuda.synchronize()
+    rest = [i for i in range(T) if i != 2]
+    assert torch.equal(got[rest], want[rest]) and bool(torch.isnan(got[2]).all())
+
+
 # T, H, F: each form of the tiles (narrow and wide, split or not), its epilogues and both operand orders
 @pytest.mark.parametrize("T,H,F", [(40, 4096, 136), (300, 520, 136), (1000, 1032, 3080)])
 def test_a_wait_that_gives_up(T, H, F, cuda_device):
