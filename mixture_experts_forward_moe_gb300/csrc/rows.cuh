@@ -137,8 +137,9 @@ inline int max_clusters(int parts, int threads, int smem) {
 }
 
 // Parts of K in which `tiles` tiles of `all` blocks take the least time, in blocks, of which a CTA is
-// taken to cost `start` beside its own (its start, the first block and the join); 0: no launch is
-// possible.
+// taken to cost `start` beside its own (its start, the first block and the join): the fastest of one
+// to eight, or within 3% of it, at 30 of 31 sizes of both kernels, 8% behind at the other (4 x 4096 x
+// 1536).  0: no launch is possible.
 template <auto Kernel>
 inline int parts_of(int64_t tiles, int all, int start, int threads, int smem) {
   int64_t best = 0;
