@@ -56,9 +56,17 @@ struct Plan {
 // The tensor cores add to an accumulator with truncation, and 448 additions (K = 7168) move a sum by
 // 1e-5 of its terms: nothing in 16 bits, but one value in a thousand of a checkpoint becomes its
 // neighbour.  Where pre-activations are saved the accumulators are added, rounded, to sums in
-// registers after as many 64-k blocks; 0: never.
+// registers after every few 64-k blocks.
 template <int kEpi>
-constexpr int kDrainBlocks = kEpi == kGatedSave ? 8 : 0;
+constexpr bool kDrains = kEpi == kGatedSave;
+// A sum of f32 on the CUDA cores is off by less the shorter K is, so a short K is drained more often.
+// Of 5.3 million codes 45 fall on their neighbours at K = 512, 83 at 2056 and 88 at 7168 (plain f32:
+// 26, 57 and 139); with eight blocks 85 at 512, with two 31.  4096 x 4096 x 512 takes 76 us so, with
+// eight blocks 71, with two 83.
+inline int drain_blocks(int64_t K) {
+  const int64_t blocks = ceil_div(K, kBlockK);
+  return blocks <= 32 ? 4 : 8;
+}
 
 struct Maps {
   CUtensorMap a[2], b[2], o0[2];  // of each product; o0: h, gated
@@ -85,6 +93,7 @@ struct Args {
   // more, and all take `rounds` of the second's
   int64_t own, more, rounds;
   int want_out;      // kGradient: h too
+  int drain;         // kGatedSave: blocks between two roundings of the sums
   Ckpt gate, up;     // kGatedSave (codes by TMA)
   int* status;
   uint64_t limit_ns;
@@ -226,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using P = Plan<kEpi, kBN>;
   constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes;
   constexpr int kHalf = kBN / 2;  // columns of a half of the warps; gated: gate columns of a tile
-  constexpr int kDrain = kDrainBlocks<kEpi>;
+  constexpr bool kDrain = kDrains<kEpi>;
   constexpr bool kBMn = kEpi == kPlain;
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[kStages];
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t u;
       for (int64_t s = 0; ok && (u = unit_at<kEpi>(p, s)) >= 0; ++s) {
         const Unit q = unit_of<kEpi>(p, u);
-        const int pass = kDrain > 0 ? kDrain : q.kb1 - q.kb0;  // blocks of one accumulator
+        const int pass = kDrain ? p.drain : q.kb1 - q.kb0;  // blocks of one accumulator
         const bool a_mn = kEpi == kPlain && p.q[q.prod].a_mn;
         const uint32_t idesc = idesc_b | (a_mn ? 1u << 15 : 0u);
         const uint64_t a_step = k16_step(a_mn);
@@ -435,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // Passes of an accumulator over `blocks` k blocks.
-    auto passes = [&](int blocks) { return kDrain > 0 ? (blocks - 1) / kDrain + 1 : 1; };
+    auto passes = [&](int blocks) { return kDrain ? (blocks - 1) / p.drain + 1 : 1; };
     // The accumulator has been read; `left` passes of the s-th unit follow.  Where no later pass takes
     // this buffer nobody waits for the arrival, and the even CTA may leave before it comes.
     auto free_buffer = [&](int left, int64_t s) {
@@ -468,11 +477,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       bool got = true;
-      float sums[kDrain > 0 ? 2 : 1][kDrain > 0 ? 64 : 1];  // gate and up
-      if constexpr (kDrain > 0) {
+      float sums[kDrain ? 2 : 1][kDrain ? 64 : 1];  // gate and up
+      if constexpr (kDrain) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) sums[0][i] = sums[1][i] = 0.0f;
-        for (int kc = q.kb0; kc < q.kb1 && got; kc += kDrain) {
+        for (int kc = q.kb0; kc < q.kb1 && got; kc += p.drain) {
           got = __all_sync(kAll, wait(&tfull_bar[buf], buf_phase));
           tc_fence_after();
           if (!got) break;
@@ -503,12 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4 && live; ++c) {
           int col = half * 128 + c * 32;
           float v[32];
-          if constexpr (kDrain > 0) {
+          if constexpr (kDrain) {
             col = (c >> 1) * kHalf + half * 64 + (c & 1) * 32;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               v[i] = c < 2 ? (c == 0 ? sums[0][i] : sums[0][32 + i])
-                           : (c == 2 ? sums[kDrain > 0][i] : sums[kDrain > 0][32 + i]);
+                           : (c == 2 ? sums[kDrain ? 1 : 0][i] : sums[kDrain ? 1 : 0][32 + i]);
           } else {
             tmem_ld_x32(d + (uint32_t)col, v);
           }
@@ -646,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if constexpr (kDrain == 0) free_buffer(0, s);
+      if constexpr (!kDrain) free_buffer(0, s);
     }
     if (leader) {
       store_wait_read<0>();  // the writes themselves end with the kernel
@@ -1059,6 +1068,7 @@ cudaError_t run_tiles(const Problem& q, const Choice& ch, cudaStream_t s) {
              unit_cost(ceil_div(p.q[1].num_kb, p.q[1].split), kBN)},
             grid, &p.rounds);
   p.want_out = q.h != nullptr;
+  p.drain = drain_blocks(q.K);
   p.gate = q.gate;
   p.up = q.up;
   p.status = q.status;
