@@ -57,8 +57,10 @@ struct Plan {
 // 1e-5 of its terms: nothing in 16 bits, but one value in a thousand of a checkpoint becomes its
 // neighbour.  Where pre-activations are saved the accumulators are added, rounded, to sums in
 // registers after every few 64-k blocks.
-template <int kEpi>
-constexpr bool kDrains = kEpi == kGatedSave;
+// What truncation takes off grows with K, which is the rows of x where d_w is made: past kChainK of it
+// (kLong) accumulators are added to sums in registers as well.  4096 x 7168 x 18432, both gradients: 1257
+// us, 1234 in one accumulator.
+constexpr int kChainBlocks = kChainK / kBlockK;
 // A sum of f32 on the CUDA cores is off by less the shorter K is, so a short K is drained more often:
 // no more codes fall on their neighbours than those of an f32 product.  Of 84 million codes at K = 136,
 // 264 and 512, and 42 million at 2056 and 7168, it has 518, 358, 505, 532 and 1245 (its 264 of 84
@@ -95,7 +97,7 @@ struct Args {
   // more, and all take `rounds` of the second's
   int64_t own, more, rounds;
   int want_out;      // kGradient: h too
-  int drain;         // kGatedSave: blocks between two roundings of the sums
+  int drain;         // kGatedSave, kLong: blocks between two roundings of the sums
   Ckpt gate, up;     // kGatedSave (codes by TMA)
   int* status;
   uint64_t limit_ns;
@@ -231,13 +233,14 @@ __device__ __forceinline__ int64_t unit_at(const Args& p, int64_t s) {
 // columns.  (One half for all: 4096 x 2048 x 7168 saved in 145 us.)  Every wait is bounded
 // (MOE_ERR_TIMEOUT in the status word); a pair in which one gave up waits for its copies, MMAs and
 // stores in flight before it leaves.
-template <typename T, int kEpi, int kAct, int kBN>
+template <typename T, int kEpi, int kAct, int kBN, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_kernel(const __grid_constant__ Maps maps, const Args p) {
   using P = Plan<kEpi, kBN>;
   constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes;
   constexpr int kHalf = kBN / 2;  // columns of a half of the warps; gated: gate columns of a tile
-  constexpr bool kDrain = kDrains<kEpi>;
+  constexpr bool kDrain = kEpi == kGatedSave || kLong;
+  static_assert(!kDrain || kBN == kTile, "a thread's 128 sums");
   constexpr bool kBMn = kEpi == kPlain;
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[kStages];
@@ -479,7 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       bool got = true;
-      float sums[kDrain ? 2 : 1][kDrain ? 64 : 1];  // gate and up
+      float sums[kDrain ? 2 : 1][kDrain ? 64 : 1];  // gate and up, or the half's 128 columns
+      auto sum_col = [&](int h) {  // where 32 of them lie in an accumulator
+        return gated(kEpi) ? (h >> 1) * kHalf + half * 64 + (h & 1) * 32 : half * kHalf + h * 32;
+      };
       if constexpr (kDrain) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) sums[0][i] = sums[1][i] = 0.0f;
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             float v[32];
-            tmem_ld_x32(tb + (uint32_t)(buf * kBN + (h >> 1) * kHalf + half * 64 + (h & 1) * 32), v);
+            tmem_ld_x32(tb + (uint32_t)(buf * kBN + sum_col(h)), v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) sums[h >> 1][(h & 1) * 32 + i] += v[i];
           }
@@ -510,12 +516,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       // gated: this warp's 32-column pieces of the gate columns, and where they lie in the box
       constexpr int kPieces = kHalf / 64;
       const int col0 = half * (kHalf / 2), piece0 = P::kShared ? half : 0;
+      auto pre_activations = [&](int h, float(&g)[32], float(&v)[32]) {
+        if constexpr (kDrain) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            g[i] = h == 0 ? sums[0][i] : sums[0][32 + i];
+            v[i] = h == 0 ? sums[1][i] : sums[1][32 + i];
+          }
+        } else {
+          tmem_ld_x32(d + (uint32_t)(col0 + h * 32), g);
+          tmem_ld_x32(d + (uint32_t)(kHalf + col0 + h * 32), v);
+        }
+      };
       if (kBN == kTile && part) {
         for (int c = 0; c < 4 && live; ++c) {
           int col = half * 128 + c * 32;
           float v[32];
           if constexpr (kDrain) {
-            col = (c >> 1) * kHalf + half * 64 + (c & 1) * 32;
+            col = sum_col(c);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               v[i] = c < 2 ? (c == 0 ? sums[0][i] : sums[0][32 + i])
@@ -535,7 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = half * kHalf + c * 64, to = q.at.n * kBN + col;
           if (to >= N) break;
           float v[64];
-          tmem_ld_x64(d + (uint32_t)col, v);
+          if constexpr (kDrain) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] = c == 0 ? sums[0][i] : sums[1][i];
+          } else {
+            tmem_ld_x64(d + (uint32_t)col, v);
+          }
           uint8_t* b = next_box();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -552,8 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < kPieces; ++h) {
             float g[32], v[32];
-            tmem_ld_x32(d + (uint32_t)(col0 + h * 32), g);
-            tmem_ld_x32(d + (uint32_t)(kHalf + col0 + h * 32), v);
+            pre_activations(h, g, v);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float w[8];
@@ -625,8 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < kPieces; ++h) {
             float g[32], v[32];
-            tmem_ld_x32(d + (uint32_t)(col0 + h * 32), g);
-            tmem_ld_x32(d + (uint32_t)(kHalf + col0 + h * 32), v);
+            pre_activations(h, g, v);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               float dh[8], dg[8], du[8], hv[8];
@@ -859,9 +880,10 @@ int64_t tiles_n(int64_t N, bool gate, int bn) { return ceil_div(N, gate ? bn / 2
 
 // Tiles of 128 columns where those of 256 leave pairs idle.  In units of a 64-k block of a 256-column
 // tile: a narrow one costs 0.65 (the loads of a, which it shares with fewer columns), a tile's start
-// and epilogue about 16 and 12.
+// and epilogue about 16 and 12.  (More than kChainBlocks are added up in tiles of 256 alone.)
 bool narrow(int64_t M, int64_t N, int64_t K, bool gate) {
   const int64_t pairs = num_sms() / 2, mt = ceil_div(M, kTile), num_kb = ceil_div(K, kBlockK);
+  if (num_kb > kChainBlocks) return false;
   const int64_t wide_tiles = mt * tiles_n(N, gate, kTile);
   const Split sp = split_of(wide_tiles, K);
   double wide = (double)(sp.whole / pairs) * (num_kb + 16);
@@ -953,7 +975,9 @@ Choice choose(const Product* q, int n) {
     return r;
   }
   double best = 0.0;
+  const bool may_narrow = ceil_div(q[0].K > q[1].K ? q[0].K : q[1].K, kBlockK) <= kChainBlocks;
   for (const int bn : {kTile, 128}) {
+    if (bn != kTile && !may_narrow) break;
     Choice t = {};
     t.bn = bn;
     int64_t tiles[2], kb[2];
@@ -1004,11 +1028,11 @@ Choice choose(const Product* q, int n) {
   return r;
 }
 
-template <typename T, int kEpi, int kAct, int kBN>
+template <typename T, int kEpi, int kAct, int kBN, bool kLong>
 cudaError_t run_tiles(const Problem& q, const Choice& ch, cudaStream_t s) {
   constexpr bool kGate = gated(kEpi);
   using P = Plan<kEpi, kBN>;
-  constexpr auto kern = dense_kernel<T, kEpi, kAct, kBN>;
+  constexpr auto kern = dense_kernel<T, kEpi, kAct, kBN, kLong>;
   Args p = {};
   Maps maps = {};
   bool ok = true;
@@ -1070,7 +1094,7 @@ cudaError_t run_tiles(const Problem& q, const Choice& ch, cudaStream_t s) {
              unit_cost(ceil_div(p.q[1].num_kb, p.q[1].split), kBN)},
             grid, &p.rounds);
   p.want_out = q.h != nullptr;
-  p.drain = drain_blocks(q.K);
+  p.drain = kLong ? kChainBlocks : drain_blocks(q.K);
   p.gate = q.gate;
   p.up = q.up;
   p.status = q.status;
@@ -1116,6 +1140,12 @@ cudaError_t run_tiles(const Problem& q, const Choice& ch, cudaStream_t s) {
   return e;
 }
 
+// Whether a unit has more blocks than an accumulator may take.
+bool long_units(int64_t K, const Split& sp) {
+  const int64_t blocks = ceil_div(K, kBlockK);
+  return (sp.whole > 0 ? blocks : ceil_div(blocks, sp.split)) > kChainBlocks;
+}
+
 template <typename T, int kEpi, int kAct>
 cudaError_t run(const Problem& q, cudaStream_t s) {
   Choice ch = {};
@@ -1123,17 +1153,23 @@ cudaError_t run(const Problem& q, cudaStream_t s) {
   if constexpr (kEpi != kGatedSave) {  // whose checkpoints have 128 channels to a scale
     if (narrow(q.M, q.N, q.K, true)) {
       ch.sp[0] = Split{mt * tiles_n(q.N, true, 128), 0, 1};
-      return run_tiles<T, kEpi, kAct, 128>(q, ch, s);
+      return run_tiles<T, kEpi, kAct, 128, false>(q, ch, s);
     }
   }
   ch.sp[0] = split_of(mt * tiles_n(q.N, true, kTile), q.K);
-  return run_tiles<T, kEpi, kAct, kTile>(q, ch, s);
+  if constexpr (kEpi != kGatedSave) {
+    if (long_units(q.K, ch.sp[0])) return run_tiles<T, kEpi, kAct, kTile, true>(q, ch, s);
+  }
+  return run_tiles<T, kEpi, kAct, kTile, false>(q, ch, s);
 }
 
 template <typename T>
 cudaError_t run_products(const Problem& q, const Choice& ch, cudaStream_t s) {
-  return ch.bn == kTile ? run_tiles<T, kPlain, 0, kTile>(q, ch, s)
-                        : run_tiles<T, kPlain, 0, 128>(q, ch, s);
+  bool any = false;
+  for (int i = 0; i < q.n; ++i) any = any || long_units(q.list[i]->K, ch.sp[i]);
+  if (any) return run_tiles<T, kPlain, 0, kTile, true>(q, ch, s);
+  return ch.bn == kTile ? run_tiles<T, kPlain, 0, kTile, false>(q, ch, s)
+                        : run_tiles<T, kPlain, 0, 128, false>(q, ch, s);
 }
 
 template <int kEpi>

@@ -26,6 +26,7 @@ struct Shape {
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(kStages * kStageBytes >= 2 * kOuts * kN * (int)sizeof(float), "the sums");
 };
+constexpr int kAccs = 4;  // accumulators of a part of K that is longer than one may take
 
 // grid.x: groups of outputs, each `parts` CTAs side by side (the cluster).  x_rows: rows of x that a
 // copy brings; the columns of D behind them hold anything, and nothing reads them.
@@ -51,6 +52,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = (int)((int64_t)all * part / parts);
   const int last = (int)((int64_t)all * (part + 1) / parts);
   const int n0 = (int)(group * kOuts);
+  const int chain = chain_of<kAccs>(last - first, kChainK / kBlock);  // blocks of an accumulator
+  const uint32_t tmem_cols = last - first > chain ? kAccs * kCols : kCols;
   volatile int* abort_flag = &s_abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return wait_bar(bar, parity, abort_flag, limit_ns, p.status);
@@ -77,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    tmem_alloc(&s_tmem, kCols);
+    tmem_alloc(&s_tmem, tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -108,7 +111,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       Ring r(full_bar, kStages, 0u);
       const uint32_t idesc = idesc_f16_m128(kN, DT<T>::kIsBF16);
-      for (int b = first; b < last; ++b) {
+      uint32_t d = tmem;
+      for (int b = first, in = 0; b < last; ++b, ++in) {
+        if (in == chain) in = 0, d += (uint32_t)kCols;
         if (!r.ready && !wait(r.bar(), r.parity)) break;
         tc_fence_after();
         uint64_t* empty = &empty_bar[r.stage];
@@ -116,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.next();
 #pragma unroll
         for (int k = 0; k < kBlock / 16; ++k)
-          umma_f16(tmem, sw128_kmajor_desc(a + (uint32_t)(k * 32)),
-                   sw128_kmajor_desc(x + (uint32_t)(k * 32)), idesc, b > first || k > 0 ? 1u : 0u);
+          umma_f16(d, sw128_kmajor_desc(a + (uint32_t)(k * 32)),
+                   sw128_kmajor_desc(x + (uint32_t)(k * 32)), idesc, in > 0 || k > 0 ? 1u : 0u);
         umma_commit(empty);
       }
       umma_commit(&done_bar);  // also where a wait gave up: the MMAs in flight
@@ -138,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c0 >= p.T) break;
         float v[16];
         tmem_ld_x16(ta + (uint32_t)c0, v);
+        add_accumulators(ta + (uint32_t)c0, kCols, (last - first - 1) / chain, v);
 #pragma unroll
         for (int c = 0; c < 16; ++c) sums[(c0 + c) * 2 * kOuts + row] = v[c];
       }
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (parts > 1) cluster_leave();  // a peer may still read this CTA's sums
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    tmem_dealloc(tmem, tmem_cols);
   }
 }
 

@@ -182,7 +182,17 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
 
   // Consecutive MMAs of one accumulator wait for one another: a single tile has two.
   constexpr int kAccs = kMT * kNT == 1 ? 2 : 1;
-  float acc[kAccs][kMT][kNT][4] = {};
+  float acc[kAccs][kMT][kNT][4];
+  // Of the chunks before this one: an accumulator takes no more than a chunk (kChainK at most).
+  float total[kMT][kNT][4] = {};
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kMT; ++i)
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f(i, j, c);
+  };
   // `xb`: this lane's first unit of the block's x, for row g
   auto multiply = [&](int stage, uint32_t xb, int left) {
     const uint32_t at = ring + (uint32_t)(stage * kStageBytes) + (uint32_t)lane * 16u;
@@ -246,6 +256,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   for (int b0 = first; b0 < last; b0 += chunk) {
     if (b0 > first) __syncthreads();  // the last chunk's x has been read
     stage_x(b0);
+    each([&](int i, int j, int c) { acc[0][i][j][c] = acc[kAccs - 1][i][j][c] = 0.0f; });
     __syncthreads();
     const int end = last - b0 < chunk ? last - b0 : chunk;
     for (int b = 0; b < end; ++b) {
@@ -257,6 +268,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
                b0 + b + 1 < all ? kBlock : p.K - (all - 1) * kBlock);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    each([&](int i, int j, int c) {
+      total[i][j][c] += kAccs == 1 ? acc[0][i][j][c] : acc[0][i][j][c] + acc[kAccs - 1][i][j][c];
+    });
   }
   if (over) set_status(p.status, MOE_ERR_F16_RANGE);
   copy_wait<0>();
@@ -266,17 +280,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   const float alpha = *p.alpha;
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int i = 0; i < kMT; ++i)
-#pragma unroll
-    for (int j = 0; j < kNT; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int w = warp * kOuts;
-        const int r = kGated ? (c >> 1) * kUp + w + i * 8 + g : w + i * 16 + (c >> 1) * 8 + g;
-        sums[(j * 8 + 2 * t + (c & 1)) * kAll + r] =
-            kAccs == 1 ? acc[0][i][j][c] : acc[0][i][j][c] + acc[kAccs - 1][i][j][c];
-      }
+  each([&](int i, int j, int c) {
+    const int w = warp * kOuts;
+    const int r = kGated ? (c >> 1) * kUp + w + i * 8 + g : w + i * 16 + (c >> 1) * 8 + g;
+    sums[(j * 8 + 2 * t + (c & 1)) * kAll + r] = total[i][j][c];
+  });
   if (parts > 1)
     cluster_sync();
   else
@@ -403,6 +411,8 @@ cudaError_t go(const RowsCall& c, cudaStream_t s) {
   const int cols = c.T < 8 * kNT ? c.T : 8 * kNT;
   // All of a part's x, or as much at a time as leaves room for three CTAs per SM (two).
   int chunk = (all + parts - 1) / parts;
+  constexpr int kMost = (kMT * kNT == 1 ? 2 : 1) * kChainK / kBlock;  // two accumulators share a chunk
+  if (chunk > kMost) chunk = kMost;
   const int fit = (((kMT == 1 ? 75 : 112) * 1024 - kRing) / cols - 64) / (kBlock * 2);
   if (chunk > fit) chunk = fit > 0 ? fit : 1;
   const int smem = kRing + cols * (chunk * kBlock * 2 + 64);

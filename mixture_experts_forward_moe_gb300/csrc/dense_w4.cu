@@ -37,6 +37,7 @@ struct Shape {
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(kStages * kStageBytes >= kRows * kN * (int)sizeof(float), "the sums");
 };
+constexpr int kAccs = 4;  // accumulators of a part of K that is longer than one may take
 
 __device__ __forceinline__ void sts16(uint32_t a, const uint32_t (&v)[4]) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -72,6 +73,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = (int)((int64_t)all * part / parts);
   const int last = (int)((int64_t)all * (part + 1) / parts);
   const int steps = 2 * (last - first);
+  const int chain = chain_of<kAccs>(steps, kChainK / kStageK);  // steps of an accumulator
+  const uint32_t tmem_cols = steps > chain ? kAccs * kN : kN;
   volatile int* abort_flag = &s_abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return wait_bar(bar, parity, abort_flag, limit_ns, p.status);
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_shared();  // the barriers, to the copies
     }
     __syncwarp();
-    tmem_alloc(&s_tmem, kN);
+    tmem_alloc(&s_tmem, tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -226,7 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       Ring r(full_bar, kStages, 0u);
       const uint32_t idesc = idesc_f16_m128(kN, 0);
-      for (int i = 0; i < steps; ++i) {
+      uint32_t d = tmem;
+      for (int i = 0, in = 0; i < steps; ++i, ++in) {
+        if (in == chain) in = 0, d += (uint32_t)kN;
         if (!r.ready && !wait(r.bar(), r.parity)) break;
         if (!wait(&x_bar[r.stage], r.parity)) break;
         tc_fence_after();
@@ -235,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.next();
 #pragma unroll
         for (int k = 0; k < kStageK / 16; ++k)
-          umma_f16(tmem,
+          umma_f16(d,
                    sw128_kmajor_desc(a + (uint32_t)((k >> 2) * (kWBytes / 2) + (k & 3) * 32)),
                    sw128_kmajor_desc(b + (uint32_t)((k >> 2) * (kN * 128) + (k & 3) * 32)), idesc,
-                   i > 0 || k > 0 ? 1u : 0u);
+                   in > 0 || k > 0 ? 1u : 0u);
         umma_commit(&empty_bar[stage]);
       }
       umma_commit(&done_bar);  // also where a wait gave up: the MMAs in flight
@@ -258,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c0 >= cols) break;
         float v[16];
         tmem_ld_x16(ta + (uint32_t)c0, v);
+        add_accumulators(ta + (uint32_t)c0, kN, (steps - 1) / chain, v);
 #pragma unroll
         for (int c = 0; c < 16; ++c) sums[(c0 + c) * kRows + warp * 32 + lane] = v[c];
       }
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (parts > 1) cluster_leave();  // a peer may still read this CTA's sums
   if (warp == kDecodeWarps + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kN);
+    tmem_dealloc(tmem, tmem_cols);
   }
 }
 

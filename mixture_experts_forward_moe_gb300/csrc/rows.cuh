@@ -63,6 +63,23 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int c) {
   return c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
 }
 
+// Blocks of K that one of kAccs accumulators takes, of `all` in a part: `most` (kChainK), or more where
+// the accumulators are not enough for that.
+template <int kAccs>
+__device__ __forceinline__ int chain_of(int all, int most) {
+  const int least = (all - 1) / kAccs + 1;
+  return least > most ? least : most;
+}
+// Adds `more` further accumulators, `cols` columns apart, to 16 columns of the first.
+__device__ __forceinline__ void add_accumulators(uint32_t t, int cols, int more, float (&v)[16]) {
+  for (int a = 1; a <= more; ++a) {
+    float u[16];
+    tmem_ld_x16(t + (uint32_t)(a * cols), u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += u[i];
+  }
+}
+
 // One output from its f32 sum (or sums, gated).
 template <typename T, bool kGated>
 __device__ __forceinline__ void finish(const RowsCall& p, int64_t row, int64_t n, float z, float up) {
