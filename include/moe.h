@@ -712,10 +712,13 @@ moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void
  *   K (H) a multiple of 32, T at most 2^20; 16-bit results (out_f32 0).  bias, residual and out as
  *   for moe_linear; out may be the residual itself.
  *   e2m1 * e4m3 is exact in f16, in which the products are taken, with f32 accumulation.  bf16 x
- *   is converted: exact between 2^-14 and 65504 in magnitude, at most 2^-25 off below, and a larger
- *   value sets MOE_ERR_F16_RANGE in the status word.
+ *   is converted: in a row whose largest magnitude lies in [0.5, 65504] exactly from 2^-14 on and at
+ *   most 2^-25 off below; another row times a power of two that its sums are divided by, at most
+ *   2^-39 of its largest value off.  So all of bf16's range is taken.  A value past 65504 is also
+ *   noted as MOE_ERR_F16_RANGE in the status word: the experts of the same model
+ *   (fused_moe_fwd_w4a16) do not take it.
  *   workspace  moe_linear_w4a16_workspace_size(g), moe_gated_linear_w4a16_workspace_size(p) bytes
- *              (more than sixteen rows of bf16 x: also x in f16).
+ *              (more than sixteen rows of bf16 x: also x in f16 and its rows' scales).
  */
 size_t moe_linear_w4a16_workspace_size(const moe_linear_t* g);
 size_t moe_gated_linear_w4a16_workspace_size(const moe_gated_linear_t* p);

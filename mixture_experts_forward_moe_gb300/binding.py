@@ -1057,8 +1057,9 @@ def moe_linear_w4a16(x, codes, scales, alpha, bias=None, activation="none", resi
                      out=None, workspace=None, stream=None):
     """moe_linear with NVFP4 weights, for the few rows of decoding (include/moe.h:
     moe_linear_w4a16).  x [T, K] in bf16 or f16; codes [N, K/2] and scales [N, K/16] uint8, alpha
-    [1] f32: as pack_nvfp4_weights takes them, one matrix, not packed.  The status word of the
-    workspace (call_workspace) tells of x past the f16 range."""
+    [1] f32: as pack_nvfp4_weights takes them, one matrix, not packed.  All of bf16's range is taken;
+    the status word of the workspace (call_workspace) tells of x past f16's, which the experts' 4-bit
+    calls do not take."""
     act = _LINEAR_ACTS.get(activation)
     if act is None:
         raise ValueError(f"unsupported activation {activation}")

@@ -99,7 +99,7 @@ struct LinearBwd {
 
 constexpr int32_t kMaxW4Rows = 1 << 20;
 
-// status | x in f16
+// status | x in f16, its rows' scales
 size_t w4_workspace(int dtype, int64_t T, int64_t K) {
   return kHeaderBytes + align256(w4_bytes(dtype, T, K));
 }

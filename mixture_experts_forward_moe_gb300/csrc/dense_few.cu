@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
   else
     __syncthreads();
-  finish_tile<T, true, kOuts, kThreads>(p, base, sums, 2 * kOuts, group, part, parts, 0, p.T, 1.0f);
+  finish_tile<T, true, kOuts, kThreads>(p, base, sums, 2 * kOuts, group, part, parts, 0, p.T, 1.0f,
+                                           nullptr);
   if (parts > 1) cluster_leave();  // a peer may still read this CTA's sums
   if (warp == 1) {
     tc_fence_after();

@@ -66,7 +66,8 @@ cudaError_t launch_rows(const RowsCall& c, cudaStream_t s);
 // The 16-bit gated product of up to kFewRows rows of x (dense_few.cu).
 constexpr int kFewRows = 128;
 cudaError_t launch_few(const RowsCall& c, cudaStream_t s);
-// The same of 4-bit weights, for more rows of x (dense_w4.cu); x16: w4_bytes of workspace.
+// The same of 4-bit weights, for more rows of x (dense_w4.cu); x16: w4_bytes of workspace, for x in f16
+// and a scale per row.
 constexpr int kFewW4Rows = 16;
 size_t w4_bytes(int dtype, int64_t T, int64_t K);
 cudaError_t launch_w4(const RowsCall& c, void* x16, cudaStream_t s);

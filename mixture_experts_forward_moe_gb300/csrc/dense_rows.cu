@@ -9,7 +9,7 @@
 // every weight would cost an f32 multiply-add per row of x beside its decoding.)  A lane's 16 bytes of
 // a row are 32 consecutive k, eight MMAs, whose k are assigned to lanes as they lie there: the order
 // of k within a sum is free as long as x follows it.  E2M1 codes times their E4M3 scale are exact f16,
-// so x is taken in f16 (bf16 x is exact there between 2^-14 and 65504; larger values are reported).
+// so x is taken in f16, bf16 x times a power of two per row and chunk of K where it needs one (rows.cuh).
 // A CTA of four warps has 64 or 128 weight rows, a warp 16 or 32, and a part of K: its x is staged once
 // and read by all warps.  A cluster is the parts of the same rows, whose sums meet in shared memory
 // and are added in the order of the parts.
@@ -17,6 +17,8 @@
 // ahead and without any barrier.
 // Gated: an MMA's rows 0-7 are gate rows and 8-15 the up rows that go with them.
 #include "rows.cuh"
+
+#include <type_traits>
 
 namespace gb300moe {
 
@@ -59,7 +61,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   constexpr int kStageBytes = stage_bytes<kKind, kMT>();
   constexpr int kScaleAt = kMT * 4 * 512;           // in a stage
   constexpr int kOuts = kGated ? 8 * kMT : 16 * kMT;  // outputs of a warp
+  constexpr bool kBf16 = DT<T>::kIsBF16;
   extern __shared__ __align__(16) uint8_t smem[];
+  // bf16 x: the largest of each row, of up to four warps that staged it
+  __shared__ uint32_t s_top[kWarps][kBf16 ? 16 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int part = blockIdx.x % (unsigned)parts;
@@ -154,36 +159,57 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
     copy_commit();
   };
 
-  // x of one chunk: unit u of a block's vector (8 k) of lane t lies at u * 4 + t.
+  // x of one chunk: unit u of a block's vector (8 k) of lane t lies at u * 4 + t.  Eight threads or more
+  // have a row, x_per of them, so that its largest value stays in registers until they meet.
+  // kScaled: again, times a power of two.
+  const int x_per = kWarps * 32 / (cols <= 1 ? 1 : cols <= 2 ? 2 : cols <= 4 ? 4 : cols <= 8 ? 8 : 16);
+  const int x_row = threadIdx.x / (unsigned)x_per, x_first = threadIdx.x % (unsigned)x_per;
   bool over = false;
-  auto stage_x = [&](int b0) {
-    const int units = chunk * kBlock / 8, end = cols * units;
+  auto stage_x = [&](int b0, auto scaled, float scale) {
+    constexpr bool kScaled = decltype(scaled)::value;
+    const uint4* const from = static_cast<const uint4*>(p.x) + ((t0 + x_row) * p.K + (int64_t)b0 * kBlock) / 8;
+    const int64_t left = (p.K - (int64_t)b0 * kBlock) / 8;
+    const int units = x_row < cols ? chunk * kBlock / 8 : 0;
+    const uint32_t to = xs + (uint32_t)(x_row * x_pitch);
+    uint32_t top = 0u;
     constexpr int kAhead = 4;  // loads that a thread has on their way
-    for (int first = threadIdx.x; first < end; first += kAhead * kWarps * 32) {
+    for (int u0 = x_first; u0 < units; u0 += kAhead * x_per) {
       uint4 v[kAhead];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        const int i = first + a * kWarps * 32, c = i / units;
-        const int64_t k = (int64_t)b0 * kBlock + (i - c * units) * 8;
-        v[a] = i < end && k < p.K
-                   ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + (t0 + c) * p.K + k)
-                   : zero4();
+        const int u = u0 + a * x_per;
+        v[a] = u < units && u < left ? from[u] : zero4();
       }
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        const int i = first + a * kWarps * 32, c = i / units, q = i - c * units;
-        if (i >= end) break;
-        if constexpr (DT<T>::kIsBF16) v[a] = bf16x8_to_f16x8(v[a], over);
-        const int at = (q & ~15) | ((q & 3) << 2) | ((q >> 2) & 3);
-        *reinterpret_cast<uint4*>(smem + c * x_pitch + at * 16) = v[a];
+        const int u = u0 + a * x_per;
+        if (u >= units) break;
+        if constexpr (kBf16 && !kScaled) {
+          top = max(top, top_bits(v[a]));
+          bool past = false;  // is seen by the row's largest
+          v[a] = bf16x8_to_f16x8(v[a], past);
+        } else if constexpr (kBf16) {
+          v[a] = bf16x8_times(v[a], scale, over);
+        }
+        sts16(to + (uint32_t)((u & ~15) | ((u & 3) << 2) | ((u >> 2) & 3)) * 16u, v[a]);
       }
+    }
+    if constexpr (kBf16 && !kScaled) {
+      if (x_per >= 32) {
+        top = __reduce_max_sync(0xffffffffu, top);
+      } else {
+        for (int o = x_per / 2; o > 0; o >>= 1)
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      if (x_first % 32 == 0) s_top[x_first / 32][x_row] = top;
     }
   };
 
   // Consecutive MMAs of one accumulator wait for one another: a single tile has two.
   constexpr int kAccs = kMT * kNT == 1 ? 2 : 1;
   float acc[kAccs][kMT][kNT][4];
-  // Of the chunks before this one: an accumulator takes no more than a chunk (kChainK at most).
+  // Times alpha, of the chunks before this one: an accumulator takes no more than a chunk (kChainK at
+  // most), which has its own scales of x.
   float total[kMT][kNT][4] = {};
   auto each = [&](auto f) {
 #pragma unroll
@@ -252,12 +278,26 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   pdl_trigger();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load(first + s, s);
+  const float alpha = *p.alpha;
   int stage = 0;
   for (int b0 = first; b0 < last; b0 += chunk) {
     if (b0 > first) __syncthreads();  // the last chunk's x has been read
-    stage_x(b0);
+    stage_x(b0, std::false_type{}, 1.0f);
     each([&](int i, int j, int c) { acc[0][i][j][c] = acc[kAccs - 1][i][j][c] = 0.0f; });
     __syncthreads();
+    RowScale scale = {1.0f, 1.0f};  // lane c's: of row c
+    bool scaled = false;
+    if constexpr (kBf16) {
+      uint32_t top = 0u;
+      if (lane < cols)
+        for (int q = 0; q < x_per; q += 32) top = max(top, s_top[q / 32][lane]);
+      scaled = __any_sync(0xffffffffu, needs_scale(top));
+      if (scaled) {  // the same in all warps
+        scale = row_scale(top);
+        stage_x(b0, std::true_type{}, __shfl_sync(0xffffffffu, scale.down, x_row));
+        __syncthreads();
+      }
+    }
     const int end = last - b0 < chunk ? last - b0 : chunk;
     for (int b = 0; b < end; ++b) {
       copy_wait<kStages - 2>();
@@ -269,7 +309,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     each([&](int i, int j, int c) {
-      total[i][j][c] += kAccs == 1 ? acc[0][i][j][c] : acc[0][i][j][c] + acc[kAccs - 1][i][j][c];
+      float z = kAccs == 1 ? acc[0][i][j][c] : acc[0][i][j][c] + acc[kAccs - 1][i][j][c];
+      z *= alpha;
+      if (kBf16 && scaled) z *= __shfl_sync(0xffffffffu, scale.up, j * 8 + 2 * t + (c & 1));
+      total[i][j][c] += z;
     });
   }
   if (over) set_status(p.status, MOE_ERR_F16_RANGE);
@@ -277,7 +320,6 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
 
   // Sums [cols][kAll]: the weight rows of the CTA, a gated product's gate rows before its up rows.
   constexpr int kAll = kWarps * 16 * kMT, kUp = kWarps * kOuts;
-  const float alpha = *p.alpha;
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
   each([&](int i, int j, int c) {
@@ -308,7 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       z = sums[c * kAll + r];
       if (kGated) up = sums[c * kAll + kUp + r];
     }
-    finish<T, kGated>(p, t0 + c, n0 + r, z * alpha, up * alpha);
+    finish<T, kGated>(p, t0 + c, n0 + r, z, up);
   }
   if (parts > 1) cluster_leave();  // a peer may still read this CTA's sums
 }

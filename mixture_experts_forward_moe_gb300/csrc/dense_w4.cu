@@ -3,8 +3,8 @@
 //
 // D[r, t] = sum_k W(r, k) x(t, k): 128 weight rows are the M side, 32 to 128 rows of x the N side.  The
 // weights are decoded once for all of them, as they come: E2M1 codes times their E4M3 scale are exact
-// f16, written into the swizzled tile that the MMAs read.  x is taken in f16 (bf16 x is exact there
-// between 2^-14 and 65504; larger values are reported).
+// f16, written into the swizzled tile that the MMAs read.  x is taken in f16, bf16 x times a power of two
+// per row where it needs one (rows.cuh).
 // bf16 x is converted by a small kernel before: done in this one, by every CTA for itself, it cost
 // more than the decoding (64 rows of 7168 x 7168: 51 us, now 29; dense_rows.cu took 70).
 // What bounds it is the issue of the decoding, about three instructions of a lane per weight with the
@@ -39,18 +39,13 @@ struct Shape {
 };
 constexpr int kAccs = 4;  // accumulators of a part of K that is longer than one may take
 
-__device__ __forceinline__ void sts16(uint32_t a, const uint32_t (&v)[4]) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3])
-               : "memory");
-}
-
 // grid.x: groups of weight rows, each `parts` CTAs side by side (the cluster); grid.y: kN rows of x.
-// x_rows: rows of x that a copy brings; prepared: the kernel before this one made x16 and nothing else.
+// x_rows: rows of x that a copy brings; x_scale: of its rows, not null where the kernel before this one
+// made x16 and it and nothing else.
 template <typename T, bool kGated, int kN>
 __global__ void __launch_bounds__(kThreads, 1)
-    w4_kernel(const __grid_constant__ CUtensorMap x16, const RowsCall p, int parts, int x_rows,
-              int prepared, uint64_t limit_ns) {
+    w4_kernel(const __grid_constant__ CUtensorMap x16, const RowsCall p, const float* x_scale,
+              int parts, int x_rows, uint64_t limit_ns) {
   using S = Shape<kN>;
   constexpr int kStages = S::kStages;
   constexpr int kOuts = kGated ? kRows / 2 : kRows;
@@ -137,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (t == 0 && odd == 0)  // into L2 while the kernel before this one ends
       for (int b = 0; b < kSlots - 1 && first + b < last; ++b)
         for (int h = 0; h < 2; ++h) prefetch_l2(from[h] + b * 128);
-    if (!prepared) pdl_wait();
+    if (!x_scale) pdl_wait();
     // Vector h of a lane at h * 512 of its slot, 16 bytes a lane.
     const int blocks = last - first;
     auto load = [&](int b, int slot) {
@@ -195,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
           uint32_t q[4];
           nvfp4_decode8(word_of(w[h], c), s[h][c >> 1], q);
-          sts16(to + (uint32_t)(h * 1024) + chunk, q);
+          sts16(to + (uint32_t)(h * 1024) + chunk, make_uint4(q[0], q[1], q[2], q[3]));
         }
       }
       fence_async_shared();  // to the MMAs
@@ -275,12 +270,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (issued > 0) land_copies(x_bar, issued, kStages);
     if (threadIdx.x == 0) land_mmas(&done_bar);
   }
+  pdl_wait();  // the decoders have not waited for x_scale
   const float alpha = *p.alpha;
   if (parts > 1)
     cluster_sync();
   else
     __syncthreads();
-  finish_tile<T, kGated, kOuts, kThreads>(p, base, sums, kRows, group, part, parts, t0, cols, alpha);
+  finish_tile<T, kGated, kOuts, kThreads>(p, base, sums, kRows, group, part, parts, t0, cols, alpha,
+                                           x_scale);
   if (parts > 1) cluster_leave();  // a peer may still read this CTA's sums
   if (warp == kDecodeWarps + 1) {
     tc_fence_after();
@@ -288,14 +285,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// bf16 -> f16, `n` values (a multiple of 8).
-__global__ void __launch_bounds__(256)
-    to_f16_kernel(const uint4* x, uint4* out, int64_t n, int* status) {
+// bf16 -> f16, a CTA a row of `vecs` vectors: its largest magnitude first, with up to kHold vectors of a
+// thread kept for the second step.
+constexpr int kRowThreads = 512, kHold = 4;  // at most
+__global__ void __launch_bounds__(kRowThreads)
+    to_f16_kernel(const uint4* x, uint4* out, float* scales, int vecs, int* status) {
+  __shared__ uint32_t s_top[kRowThreads / 32];
+  const int threads = blockDim.x;
   pdl_wait();
   pdl_trigger();
+  const uint4* const from = x + (int64_t)blockIdx.x * vecs;
+  uint4* const to = out + (int64_t)blockIdx.x * vecs;
+  const int lane = threadIdx.x & 31;
+  uint4 v[kHold];
+  uint32_t top = 0u;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    const int i = threadIdx.x + k * threads;
+    v[k] = i < vecs ? from[i] : zero4();
+  }
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) top = max(top, top_bits(v[k]));
+  for (int i = threadIdx.x + kHold * threads; i < vecs; i += threads)
+    top = max(top, top_bits(from[i]));
+  top = __reduce_max_sync(kAll, top);
+  if (lane == 0) s_top[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = __reduce_max_sync(kAll, lane < threads / 32 ? s_top[lane] : 0u);
+  const RowScale s = row_scale(top);
+  if (threadIdx.x == 0) scales[blockIdx.x] = s.up;
   bool over = false;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n / 8; i += (int64_t)gridDim.x * 256)
-    out[i] = bf16x8_to_f16x8(x[i], over);
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    const int i = threadIdx.x + k * threads;
+    if (i < vecs) to[i] = bf16x8_times(v[k], s.down, over);
+  }
+  for (int i = threadIdx.x + kHold * threads; i < vecs; i += threads)
+    to[i] = bf16x8_times(from[i], s.down, over);
   if (over) set_status(status, MOE_ERR_F16_RANGE);
 }
 
@@ -315,11 +341,13 @@ cudaError_t go(const RowsCall& c, void* x16, cudaStream_t s) {
   if (!rows_map(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, prepare ? x16 : c.x,
                 (uint64_t)c.K, (uint64_t)c.T, (uint64_t)c.K * 2, (uint32_t)x_rows))
     return cudaErrorInvalidValue;
+  float* const x_scale =
+      prepare ? reinterpret_cast<float*>(static_cast<char*>(x16) + (size_t)c.T * c.K * 2) : nullptr;
   if (prepare) {
-    const int64_t n = (int64_t)c.T * c.K, ctas = (n / 8 + 255) / 256;
+    const int vecs = c.K / 8, warps = (vecs - 1) / (kHold * 32) + 1;
     const cudaError_t f = launch_k(
-        to_f16_kernel, dim3((unsigned)(ctas < 8 * num_sms() ? ctas : 8 * num_sms())), dim3(256), 0, s,
-        true, static_cast<const uint4*>(c.x), static_cast<uint4*>(x16), n, c.status);
+        to_f16_kernel, dim3((unsigned)c.T), dim3(warps * 32 < kRowThreads ? warps * 32 : kRowThreads), 0,
+        s, true, static_cast<const uint4*>(c.x), static_cast<uint4*>(x16), x_scale, vecs, c.status);
     if (f != cudaSuccess) return f;
   }
   cudaLaunchConfig_t cfg = {};
@@ -336,7 +364,8 @@ cudaError_t go(const RowsCall& c, void* x16, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, map, c, parts, x_rows, (int)prepare, wait_limit_ns());
+  return cudaLaunchKernelEx(&cfg, kern, map, c, (const float*)x_scale, parts, x_rows,
+                            wait_limit_ns());
 }
 
 template <typename T, bool kGated>
@@ -349,7 +378,7 @@ cudaError_t pick(const RowsCall& c, void* x16, cudaStream_t s) {
 }  // namespace
 
 size_t w4_bytes(int dtype, int64_t T, int64_t K) {
-  return dtype == MOE_BF16 && T > kFewW4Rows ? (size_t)T * (size_t)K * 2 : 0;
+  return dtype == MOE_BF16 && T > kFewW4Rows ? (size_t)T * ((size_t)K * 2 + sizeof(float)) : 0;
 }
 
 cudaError_t launch_w4(const RowsCall& c, void* x16, cudaStream_t s) {

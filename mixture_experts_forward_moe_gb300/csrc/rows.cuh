@@ -40,6 +40,11 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t lds2(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
@@ -61,6 +66,44 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int c) {
   return c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+}
+
+// bf16 x in f16.  A row whose largest magnitude lies in [0.5, 65504] is taken as it is: exact down to
+// 2^-14, at most 2^-25 off below, which is 2^-24 of its largest at most, as f32 sums are.  Another is
+// taken times a power of two that brings the largest to [2^14, 2^15), and its sums times the inverse:
+// 2^-39 of its largest at most, over all of bf16's range.
+struct RowScale {
+  float down, up;  // of x, of the sums
+};
+// The largest magnitude of eight values as its bits; NaN does not count (its row is NaN).
+__device__ __forceinline__ uint32_t top_bits(const uint4& v) {
+  const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+  uint32_t zero = 0u;
+  __nv_bfloat162 top = *reinterpret_cast<const __nv_bfloat162*>(&zero);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = __hmax2(top, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+  const uint32_t t = *reinterpret_cast<const uint32_t*>(&top);
+  return max(t & 0xffffu, t >> 16);
+}
+__device__ __forceinline__ bool needs_scale(uint32_t top) {
+  return top != 0u && (top < 0x3f00u || top >= 0x4780u);  // 0.5, 65536
+}
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  if (!needs_scale(top)) return RowScale{1.0f, 1.0f};
+  const int k = max((int)min(top >> 7, 254u) - 127 - 14, -126);  // both powers are normal f32
+  return RowScale{__uint_as_float((uint32_t)(127 - k) << 23), __uint_as_float((uint32_t)(127 + k) << 23)};
+}
+__device__ __forceinline__ uint4 bf16x8_times(const uint4& v, float scale, bool& over) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    over |= fabsf(f.x) >= kF16Overflow || fabsf(f.y) >= kF16Overflow;
+    const __half2 h = __floats2half2_rn(f.x * scale, f.y * scale);
+    r[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Blocks of K that one of kAccs accumulators takes, of `all` in a part: `most` (kChainK), or more where
@@ -97,10 +140,12 @@ __device__ __forceinline__ void finish(const RowsCall& p, int64_t row, int64_t n
 // A tile's share of its outputs, once the CTAs of its cluster (`parts` of K, this one the part-th) have
 // written their sums [columns][pitch]: kOuts of them, a gated product's up rows kOuts further.
 // Consecutive threads have consecutive columns of out; the parts are added in their order.
+// x_scale: of the sums of each row of x, or null.
 template <typename T, bool kGated, int kOuts, int kThreads>
 __device__ __forceinline__ void finish_tile(const RowsCall& p, uint32_t base, const float* sums,
                                             int pitch, int64_t group, int part, int parts,
-                                            int64_t t0, int cols, float alpha) {
+                                            int64_t t0, int cols, float alpha,
+                                            const float* x_scale) {
   const int64_t n0 = group * kOuts;
   const int end = (part + 1) * kOuts * cols / parts;
   for (int i = part * kOuts * cols / parts + (int)threadIdx.x; i < end; i += kThreads) {
@@ -119,7 +164,12 @@ __device__ __forceinline__ void finish_tile(const RowsCall& p, uint32_t base, co
       z = sums[c * pitch + r];
       if (kGated) up = sums[c * pitch + kOuts + r];
     }
-    finish<T, kGated>(p, t0 + c, n0 + r, z * alpha, up * alpha);
+    z *= alpha, up *= alpha;
+    if (x_scale) {  // behind alpha, so that what is not past f32 at the end is not before
+      const float s = x_scale[t0 + c];
+      z *= s, up *= s;
+    }
+    finish<T, kGated>(p, t0 + c, n0 + r, z, up);
   }
 }
 
