@@ -556,9 +556,10 @@ PyObject* call_gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return THPVariable_Wrap(std::move(out));
   }
   const Saved gate(x, p.T, p.F), up(x, p.T, p.F);
-  if (p.T > 0 && failed(moe_gated_linear(&p, ptr(x), ptr(w), ptr(out), gate.c(), gate.s(), up.c(),
-                                         up.s(), ptr(ws), (size_t)ws.numel(), s.stream()),
-                        "moe_gated_linear"))
+  // (without rows the checkpoints have no memory, and the call checks its arguments)
+  if (failed(moe_gated_linear(&p, ptr(x), ptr(w), ptr(out), gate.c(), gate.s(), up.c(), up.s(),
+                              ptr(ws), (size_t)ws.numel(), s.stream()),
+             "moe_gated_linear"))
     return nullptr;
   return tuple_of({out, gate.codes, gate.scales, up.codes, up.scales});
   CALL_END
