@@ -677,9 +677,11 @@ moe_status_t moe_gated_linear(const moe_gated_linear_t* p, const void* x, const 
  *   d_out [T, F]; x [T, H], or its checkpoint (x_codes, x_scales; x NULL): needed for d_w, and
  *   without the checkpoints of gate and up; d_x, d_w and out may each be NULL (not wanted).  With
  *   T = 0 d_w is 0.  out may be d_out itself; outputs overlap nothing else.
- *   workspace  moe_gated_linear_bwd_workspace_size(p) bytes.
+ *   workspace  moe_gated_linear_bwd_workspace_size(p) bytes, of which x in 16 bits is a part; where
+ *   no checkpoint of x is restored moe_gated_linear_bwd_workspace_size_x16(p) are enough.
  */
 size_t moe_gated_linear_bwd_workspace_size(const moe_gated_linear_t* p);
+size_t moe_gated_linear_bwd_workspace_size_x16(const moe_gated_linear_t* p);
 moe_status_t moe_gated_linear_bwd(const moe_gated_linear_t* p, const void* d_out, const void* x,
                                   const uint8_t* x_codes, const float* x_scales,
                                   const void* w_gate_up, const uint8_t* gate_codes,
@@ -695,9 +697,11 @@ moe_status_t moe_gated_linear_bwd(const moe_gated_linear_t* p, const void* d_out
  *   multiple of 8.  d_out [T, N]; x [T, K] or its checkpoint (x_codes, x_scales; x NULL), for d_w;
  *   w [N, K], for d_x; d_x, d_w and d_bias may each be NULL (not wanted).  With T = 0 d_w and
  *   d_bias are 0.  Outputs overlap nothing.
- *   workspace  moe_linear_bwd_workspace_size(g) bytes.
+ *   workspace  moe_linear_bwd_workspace_size(g) bytes; where no checkpoint of x is restored
+ *   moe_linear_bwd_workspace_size_x16(g), without a place for x, are enough.
  */
 size_t moe_linear_bwd_workspace_size(const moe_linear_t* g);
+size_t moe_linear_bwd_workspace_size_x16(const moe_linear_t* g);
 moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void* x,
                             const uint8_t* x_codes, const float* x_scales, const void* w, void* d_x,
                             void* d_w, void* d_bias, void* workspace, size_t workspace_bytes,

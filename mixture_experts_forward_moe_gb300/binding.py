@@ -53,6 +53,7 @@ EXPORTED = (
     "moe_block_norm_bwd_workspace_size", "moe_block_norm_bwd", "moe_balance_loss_workspace_size",
     "moe_balance_loss_fwd", "moe_router_bwd", "moe_checkpoint", "moe_checkpoint_restore",
     "moe_gated_linear_workspace_size", "moe_gated_linear", "moe_gated_linear_bwd_workspace_size",
+    "moe_gated_linear_bwd_workspace_size_x16", "moe_linear_bwd_workspace_size_x16",
     "moe_gated_linear_bwd", "moe_linear_bwd_workspace_size", "moe_linear_bwd", "moe_linear_w4a16",
     "moe_linear_w4a16_workspace_size", "moe_gated_linear_w4a16",
     "moe_gated_linear_w4a16_workspace_size",
@@ -193,6 +194,9 @@ def lib():
                              ("moe_linear_bwd", PL), ("moe_linear_w4a16", PL),
                              ("moe_gated_linear_w4a16", PG)):
                 size = getattr(L, fn + "_workspace_size")
+                size.restype, size.argtypes = sz, [desc]
+            for fn, desc in (("moe_gated_linear_bwd", PG), ("moe_linear_bwd", PL)):
+                size = getattr(L, fn + "_workspace_size_x16")
                 size.restype, size.argtypes = sz, [desc]
             L.moe_gated_linear.argtypes = [PG] + [P] * 8 + [sz, P]
             L.moe_gated_linear_bwd.argtypes = [PG] + [P] * 13 + [sz, P]
@@ -889,6 +893,12 @@ def call_workspace(device=None, stream=None) -> torch.Tensor:
     index = None if device is None else torch.device(device).index
     return _call("scratch", stream,
                  (256, torch.cuda.current_device() if index is None else index))
+
+
+def release_call_workspaces():
+    """Gives the scratch of all streams back to torch's allocator, which reuses it in the stream's
+    order; what their status words hold is lost.  The next call of a stream takes what it needs."""
+    _call("release", None, ())
 
 
 def moe_linear(x, w, bias=None, activation="none", residual=None, out_dtype=None, out=None,

@@ -137,17 +137,20 @@ at::Tensor fresh_workspace(int64_t bytes, const c10::cuda::CUDAStream& s) {
 }
 
 // Scratch of the current stream: one per stream, since calls on other streams may run at the same
-// time, and never freed while a call may still use it (a larger one replaces it, with what was
-// reported so far; torch's allocator reuses the memory in the stream's order).  Host threads share it: a call holds the interpreter's
-// lock from here to its last launch, so the launches of two calls do not mix.  A captured call gets
-// its own, which lives in the graph's memory.
+// time, and kept until release() (a larger one replaces it, with what was reported so far; torch's
+// allocator reuses the memory in the stream's order, behind the calls that use it).  Host threads share
+// it: a call holds the interpreter's lock from here to its last launch, so the launches of two calls do
+// not mix.  A captured call gets its own, which lives in the graph's memory.
+using Scratch = std::map<std::pair<int, int64_t>, at::Tensor>;
+Scratch& scratches() {
+  // leaked on purpose: a destructor at the process' end may find no CUDA context
+  static auto* all = new Scratch();
+  return *all;
+}
 at::Tensor scratch(int64_t bytes, const c10::cuda::CUDAStream& s) {
   if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
     return fresh_workspace(bytes, s);
-  using Key = std::pair<int, int64_t>;
-  // leaked on purpose: a destructor at the process' end may find no CUDA context
-  static auto* cache = new std::map<Key, at::Tensor>();
-  at::Tensor& t = (*cache)[Key(s.device_index(), (int64_t)(intptr_t)s.stream())];
+  at::Tensor& t = scratches()[{s.device_index(), (int64_t)(intptr_t)s.stream()}];
   if (!t.defined() || t.numel() < bytes) {
     at::Tensor larger = fresh_workspace(bytes, s);
     if (t.defined()) larger.narrow(0, 0, kHeader).copy_(t.narrow(0, 0, kHeader));
@@ -180,6 +183,16 @@ PyObject* call_scratch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const c10::DeviceIndex dev = (c10::DeviceIndex)as_int(a[1]);
   c10::cuda::CUDAGuard guard(dev);
   return THPVariable_Wrap(scratch(as_int(a[0]), c10::cuda::getCurrentCUDAStream(dev)));
+  CALL_END
+}
+
+// release(): gives the scratch of all streams back to torch's allocator, status words with it.
+PyObject* call_release(PyObject*, PyObject* const*, Py_ssize_t n) {
+  CALL_BEGIN
+  arguments(n, 0);
+  Scratch all;
+  all.swap(scratches());
+  Py_RETURN_NONE;
   CALL_END
 }
 
@@ -592,7 +605,9 @@ PyObject* call_gated_linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (want_x) dx = fresh(dy, {p.T, p.H}, dt);
   if (want_w) dw = fresh(w);
   if (want_out) out = fresh(dy);
-  const at::Tensor ws = workspace(a[16], (int64_t)moe_gated_linear_bwd_workspace_size(&p), s);
+  const size_t bytes = x8.defined() ? moe_gated_linear_bwd_workspace_size(&p)
+                                    : moe_gated_linear_bwd_workspace_size_x16(&p);
+  const at::Tensor ws = workspace(a[16], (int64_t)bytes, s);
   if (failed(moe_gated_linear_bwd(&p, ptr(dy), ptr(x), x8.c(), x8.s(), ptr(w), gate.c(), gate.s(),
                                   up.c(), up.s(), ptr(dx), ptr(dw), ptr(out), ptr(ws),
                                   (size_t)ws.numel(), s.stream()),
@@ -636,7 +651,9 @@ PyObject* call_linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (want_x) dx = fresh(dy, {g.T, g.K}, dt);
   if (want_w) dw = fresh(w);
   if (want_bias) db = fresh(dy, {g.N}, dt);
-  const at::Tensor ws = workspace(a[9], (int64_t)moe_linear_bwd_workspace_size(&g), s);
+  const size_t bytes = x8.defined() ? moe_linear_bwd_workspace_size(&g)
+                                    : moe_linear_bwd_workspace_size_x16(&g);
+  const at::Tensor ws = workspace(a[9], (int64_t)bytes, s);
   if (failed(moe_linear_bwd(&g, ptr(dy), ptr(x), x8.c(), x8.s(), ptr(w), ptr(dx), ptr(dw), ptr(db),
                             ptr(ws), (size_t)ws.numel(), s.stream()),
              "moe_linear_bwd"))
@@ -745,6 +762,7 @@ PyMethodDef method(const char* name) {
 }
 PyMethodDef g_methods[] = {
     method<call_scratch>("scratch"),
+    method<call_release>("release"),
     method<call_linear>("linear"),
     method<call_block_norm>("block_norm"),
     method<call_block_norm_bwd>("block_norm_bwd"),

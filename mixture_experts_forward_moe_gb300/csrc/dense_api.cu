@@ -62,17 +62,25 @@ cudaError_t launch_gradients(int dtype, const Gradients& g, float* parts, int* s
   return launch_products(dtype, g.list + (x ? 0 : 1), x && w ? 2 : 1, parts, status, s);
 }
 
-// moe_gated_linear_bwd: status | d_pre [T, 2F] | x [T, H] | parts of K
+// The last part of a workspace, x restored from its checkpoint: needed where it is one, and up to a
+// megabyte always, so that small calls have one size.
+constexpr size_t kSmallX = 1 << 20;
+struct Restored {
+  size_t x, bytes;  // where it begins, and the whole workspace
+  Restored(size_t at, size_t size) : x(at), bytes(at + align256(size)) {}
+  size_t without() const { return bytes - x <= kSmallX ? bytes : x; }
+  size_t need(bool restored) const { return restored ? bytes : without(); }
+};
+
+// moe_gated_linear_bwd: status | d_pre [T, 2F] | parts of K | x [T, H]
 struct GatedBwd {
-  size_t d_pre, x, parts, bytes;
-  explicit GatedBwd(const moe_gated_linear_t& p) {
-    const size_t T = (size_t)p.T;
-    d_pre = kHeaderBytes;
-    x = d_pre + align256(T * 2 * p.F * 2);
-    parts = x + align256(T * p.H * 2);
-    bytes = parts + align256(larger(gated_split_bytes(p.T, p.F, p.H),
-                                    gradient_bytes(p.T, 2 * p.F, p.H)));
-  }
+  size_t d_pre, parts;
+  Restored x;
+  explicit GatedBwd(const moe_gated_linear_t& p)
+      : d_pre(kHeaderBytes), parts(d_pre + align256((size_t)p.T * 2 * p.F * 2)),
+        x(parts + align256(larger(gated_split_bytes(p.T, p.F, p.H),
+                                  gradient_bytes(p.T, 2 * p.F, p.H))),
+          (size_t)p.T * p.H * 2) {}
 };
 
 moe_status_t check_linear_bwd(const moe_linear_t* g) {
@@ -83,18 +91,15 @@ moe_status_t check_linear_bwd(const moe_linear_t* g) {
   return MOE_OK;
 }
 
-// moe_linear_bwd: status | d_out with rows of a multiple of 8 | x [T, K] | parts of K
+// moe_linear_bwd: status | d_out with rows of a multiple of 8 | parts of K | x [T, K]
 struct LinearBwd {
   int64_t pitch;
-  size_t d_out, x, parts, bytes;
-  explicit LinearBwd(const moe_linear_t& g) {
-    const size_t T = (size_t)g.T;
-    pitch = ((int64_t)g.N + 7) / 8 * 8;
-    d_out = kHeaderBytes;
-    x = d_out + (pitch != g.N ? align256(T * (size_t)pitch * 2) : 0);
-    parts = x + align256(T * g.K * 2);
-    bytes = parts + align256(gradient_bytes(g.T, g.N, g.K));
-  }
+  size_t d_out, parts;
+  Restored x;
+  explicit LinearBwd(const moe_linear_t& g)
+      : pitch(((int64_t)g.N + 7) / 8 * 8), d_out(kHeaderBytes),
+        parts(d_out + (pitch != g.N ? align256((size_t)g.T * (size_t)pitch * 2) : 0)),
+        x(parts + align256(gradient_bytes(g.T, g.N, g.K)), (size_t)g.T * g.K * 2) {}
 };
 
 constexpr int32_t kMaxW4Rows = 1 << 20;
@@ -165,7 +170,10 @@ moe_status_t moe_gated_linear(const moe_gated_linear_t* p, const void* x, const 
 }
 
 size_t moe_gated_linear_bwd_workspace_size(const moe_gated_linear_t* p) {
-  return check_gated(p) == MOE_OK ? GatedBwd(*p).bytes : 0;
+  return check_gated(p) == MOE_OK ? GatedBwd(*p).x.bytes : 0;
+}
+size_t moe_gated_linear_bwd_workspace_size_x16(const moe_gated_linear_t* p) {
+  return check_gated(p) == MOE_OK ? GatedBwd(*p).x.without() : 0;
 }
 
 moe_status_t moe_gated_linear_bwd(const moe_gated_linear_t* p, const void* d_out, const void* x,
@@ -187,7 +195,8 @@ moe_status_t moe_gated_linear_bwd(const moe_gated_linear_t* p, const void* d_out
                d_x, d_w, out, workspace))
     return MOE_ERR_INVALID_ARG;
   const GatedBwd at(*p);
-  if (workspace_bytes < at.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const bool restored = need_x && x_codes;
+  if (workspace_bytes < at.x.need(restored)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const cudaStream_t s = (cudaStream_t)stream;
   if (p->T == 0)
     return d_w ? from_cuda(cudaMemsetAsync(d_w, 0, (size_t)2 * p->F * p->H * 2, s)) : MOE_OK;
@@ -196,11 +205,11 @@ moe_status_t moe_gated_linear_bwd(const moe_gated_linear_t* p, const void* d_out
   int* status = static_cast<int*>(workspace);
   float* parts = reinterpret_cast<float*>(ws + at.parts);
   void* d_pre = ws + at.d_pre;
-  if (need_x && x_codes) {
+  if (restored) {
     if (const cudaError_t e = launch_restore(p->dtype, p->T, p->H, CkptIn{x_codes, x_scales},
-                                             ws + at.x, s))
+                                             ws + at.x.x, s))
       return from_cuda(e);
-    x = ws + at.x;
+    x = ws + at.x.x;
   }
   const cudaError_t e =
       saved ? launch_gated_grad_saved(p->dtype, p->activation, p->T, p->F, d_out,
@@ -215,7 +224,10 @@ moe_status_t moe_gated_linear_bwd(const moe_gated_linear_t* p, const void* d_out
 }
 
 size_t moe_linear_bwd_workspace_size(const moe_linear_t* g) {
-  return check_linear_bwd(g) == MOE_OK ? LinearBwd(*g).bytes : 0;
+  return check_linear_bwd(g) == MOE_OK ? LinearBwd(*g).x.bytes : 0;
+}
+size_t moe_linear_bwd_workspace_size_x16(const moe_linear_t* g) {
+  return check_linear_bwd(g) == MOE_OK ? LinearBwd(*g).x.without() : 0;
 }
 
 moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void* x,
@@ -229,7 +241,8 @@ moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void
   if (!aligned(d_out, x, x_codes, x_scales, w, d_x, d_w, d_bias, workspace))
     return MOE_ERR_INVALID_ARG;
   const LinearBwd at(*g);
-  if (workspace_bytes < at.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const bool restored = d_w && x_codes;
+  if (workspace_bytes < at.x.need(restored)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const cudaStream_t s = (cudaStream_t)stream;
   if (g->T == 0) {
     cudaError_t e = cudaSuccess;
@@ -252,11 +265,11 @@ moe_status_t moe_linear_bwd(const moe_linear_t* g, const void* d_out, const void
       return from_cuda(e);
   }
   if (pad) d_out = ws + at.d_out;
-  if (d_w && x_codes) {
+  if (restored) {
     if (const cudaError_t e = launch_restore(g->dtype, g->T, g->K, CkptIn{x_codes, x_scales},
-                                             ws + at.x, s))
+                                             ws + at.x.x, s))
       return from_cuda(e);
-    x = ws + at.x;
+    x = ws + at.x.x;
   }
   return from_cuda(launch_gradients(
       g->dtype, Gradients(g->T, g->N, g->K, d_out, at.pitch, x, w, d_x, d_w), parts, status, s));
