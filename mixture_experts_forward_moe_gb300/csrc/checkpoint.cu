@@ -280,8 +280,9 @@ __device__ __forceinline__ uint4 load8(const void* tensor, int64_t i, int64_t by
 
 // A CTA adds 64 columns, eight threads side by side and 32 rows at a time; a cluster of `parts` CTAs
 // shares the rows of the same columns, and its first CTA adds their sums.  The order depends on T
-// alone.  (One CTA for all of 4096 rows: 39 us for 4096 columns.)  kPad: the rows start anywhere, `pitch` = N; they are copied to `out`, whose rows lie
-// out_pitch apart, with anything behind N.
+// alone.  (One CTA for all of 4096 rows: 39 us for 4096 columns.)
+// kPad: the rows start anywhere, `pitch` = N; they are copied to `out`, whose rows lie out_pitch apart,
+// with anything behind N.
 template <typename T, bool kPad>
 __global__ void __launch_bounds__(kThreads)
     column_sum_kernel(int T_, int N, int parts, int64_t pitch, int64_t out_pitch,

@@ -1,7 +1,7 @@
 // dense_rows.cu -- up to sixteen rows of x against 4-bit weights, which are streamed once
 // (include/moe.h: moe_linear_w4a16, moe_gated_linear_w4a16), and the 16-bit gated product of one row
-// (moe_gated_linear).  4 bits, 7168 x 7168 at 1, 4, 8 and 16 rows: 13, 14, 15 and 21 us; 16 bits, 4096
-// weight rows of 7168: 12 us.
+// (moe_gated_linear).  4 bits, 7168 x 7168 at 1, 4, 8 and 16 rows of bf16 x: 11.5, 11, 14 and 16.5 us;
+// 16 bits, 4096 weight rows of 7168: 11.5 us.
 //
 // What bounds it is the weights' bytes, and for 4 bits as much the instructions that decode them.
 // They go into the operand layout of mma.sync m16n8k16 as they lie: 16 weight rows are its M side,
@@ -51,7 +51,7 @@ constexpr int stage_bytes() {
   return kMT * (2 * 2 * 32 * 16 + 16 * scale_bytes<kKind>());
 }
 
-// grid.x: groups of weight rows, each `parts` CTAs side by side (the cluster); grid.y: of rows of x.
+// The grid: groups of weight rows, each `parts` CTAs side by side (the cluster).
 // chunk: blocks of K whose x is staged at a time.  Shared memory: x, rows of chunk * kK values and 64
 // bytes more (two rows' reads then touch every bank once), then the rings.
 template <typename T, Kind kKind, int kMT, int kNT, bool kGated, int kStages>
@@ -70,8 +70,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   const int part = blockIdx.x % (unsigned)parts;
   const int64_t group = blockIdx.x / (unsigned)parts;
   const int64_t out0 = (group * kWarps + warp) * kOuts;
-  const int64_t t0 = (int64_t)blockIdx.y * kCols;
-  const int cols = p.T - t0 < kCols ? (int)(p.T - t0) : kCols;
+  const int cols = p.T;  // at most kCols
   const int all = (p.K - 1) / kBlock + 1;
   const int first = (int)((int64_t)all * part / parts);
   const int last = (int)((int64_t)all * (part + 1) / parts);
@@ -99,8 +98,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   // block.  (Rows 4-7 and 12-15 have their halves swapped: eight rows' reads touch different banks.)
   const uint8_t* scale_from[kMT];
   int scale_in[kMT][2];
-  const uint8_t* scale_end = nullptr;
-  scale_end = p.scales + (kGated ? 2 * (int64_t)p.N : p.N) * (p.K / 16);
+  const uint8_t* const scale_end = p.scales + (kGated ? 2 * (int64_t)p.N : p.N) * (p.K / 16);
 #pragma unroll
   for (int i = 0; i < kMT; ++i) {
     const int64_t at = row_of(i, lane & 15) * (p.K / 16) + (int64_t)first * 16;
@@ -167,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   bool over = false;
   auto stage_x = [&](int b0, auto scaled, float scale) {
     constexpr bool kScaled = decltype(scaled)::value;
-    const uint4* const from = static_cast<const uint4*>(p.x) + ((t0 + x_row) * p.K + (int64_t)b0 * kBlock) / 8;
+    const uint4* const from = static_cast<const uint4*>(p.x) + ((int64_t)x_row * p.K + (int64_t)b0 * kBlock) / 8;
     const int64_t left = (p.K - (int64_t)b0 * kBlock) / 8;
     const int units = x_row < cols ? chunk * kBlock / 8 : 0;
     const uint32_t to = xs + (uint32_t)(x_row * x_pitch);
@@ -331,33 +329,13 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
     cluster_sync();
   else
     __syncthreads();
-  // This CTA's share of the outputs: consecutive threads, consecutive columns of out.
-  const int64_t n0 = group * kUp;
-  const int end = (part + 1) * kUp * cols / parts;
-  for (int i = part * kUp * cols / parts + threadIdx.x; i < end; i += kWarps * 32) {
-    const int c = i / kUp, r = i % kUp;
-    if (n0 + r >= p.N) continue;  // (every read of a peer is waited for by its output)
-    float z = 0.0f, up = 0.0f;
-    if (parts > 1) {
-      const uint32_t at = xs + (uint32_t)((c * kAll + r) * 4);
-#pragma unroll 8
-      for (int q = 0; q < parts; ++q) {
-        const uint32_t peer = cluster_map(at, (uint32_t)q);
-        z += ld_cluster(peer);
-        if (kGated) up += ld_cluster(peer + kUp * 4u);
-      }
-    } else {
-      z = sums[c * kAll + r];
-      if (kGated) up = sums[c * kAll + kUp + r];
-    }
-    finish<T, kGated>(p, t0 + c, n0 + r, z, up);
-  }
+  finish_tile<T, kGated, kUp, kWarps * 32>(p, xs, sums, kAll, group, part, parts, 0, cols, 1.0f, nullptr);
   if (parts > 1) cluster_leave();  // a peer may still read this CTA's sums
 }
 
 // ---- 16-bit weights, one row of x: on the CUDA cores --------------------------------------------
-// A gate row and its up row by `wpr` warps (a power of two) of the CTA's.  Small CTAs even out the SMs
-// (eight warps: 2048 x 7168 in 17.4 us, four 16.5), and each lane has 128 bytes on their way (64: 18.3).
+// A gate row and its up row by `wpr` warps (a power of two) of the CTA's.  2 x 2048 rows of 7168 with 128
+// bytes of a lane on their way: 11.5 us in CTAs of four warps or eight, 11.9 of two; 64 bytes 13.2.
 constexpr int kGemvWarps = 4;
 template <typename T>
 __global__ void __launch_bounds__(kGemvWarps * 32) gated_gemv_kernel(const RowsCall p, int wpr) {
@@ -426,7 +404,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32) gated_gemv_kernel(const RowsC
 
 // Parts of K: those that leave the busiest SM the least time, in blocks.  A CTA costs about four
 // blocks beside its own, and one alone on its SM has too few bytes on their way.
-int parts_of(int64_t groups, int blocks) {
+int even_parts(int64_t groups, int blocks) {
   const int64_t sms = num_sms();
   int64_t best = 0;
   int parts = 1;
@@ -447,10 +425,9 @@ cudaError_t go(const RowsCall& c, cudaStream_t s) {
   const cudaError_t e = set_smem_limit<kern>(kSmemLimit);
   if (e != cudaSuccess) return e;
   const int64_t outs = (kGated ? 8 : 16) * kMT * kWarps;
-  const int64_t groups = (c.N + outs - 1) / outs, tall = (c.T - 1) / (8 * kNT) + 1;
+  const int64_t groups = (c.N + outs - 1) / outs;
   const int all = (c.K - 1) / kBlock + 1;
-  const int parts = parts_of(groups * tall, all);
-  const int cols = c.T < 8 * kNT ? c.T : 8 * kNT;
+  const int parts = even_parts(groups, all), cols = c.T;
   // All of a part's x, or as much at a time as leaves room for three CTAs per SM (two).
   int chunk = (all + parts - 1) / parts;
   constexpr int kMost = (kMT * kNT == 1 ? 2 : 1) * kChainK / kBlock;  // two accumulators share a chunk
@@ -460,7 +437,7 @@ cudaError_t go(const RowsCall& c, cudaStream_t s) {
   const int smem = kRing + cols * (chunk * kBlock * 2 + 64);
   if (smem > kSmemLimit) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * parts), (unsigned)tall);
+  cfg.gridDim = dim3((unsigned)(groups * parts));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -494,6 +471,7 @@ cudaError_t typed(const RowsCall& c, cudaStream_t s) {
     return launch_k(gated_gemv_kernel<T>, dim3((unsigned)((c.N - 1) / (kGemvWarps / wpr) + 1)),
                     dim3(kGemvWarps * 32), 0, s, true, c, wpr);
   }
+  if (c.T > kFewW4Rows) return cudaErrorInvalidValue;
   if (c.K % 256 == 0)
     return c.gated ? pick<T, kBits4, true>(c, s) : pick<T, kBits4, false>(c, s);
   return c.gated ? pick<T, kBits4Any, true>(c, s) : pick<T, kBits4Any, false>(c, s);
