@@ -42,11 +42,11 @@ __device__ __forceinline__ float gate_value(float g) {
 template <int kAct>
 __device__ __forceinline__ void gate_slope(float g, float& value, float& slope) {
   if constexpr (kAct == MOE_ACT_SILU) {
-    // past +-80, where t would leave f32, the slope is 1 or 0 to within 2e-33
+    // past +-80, where t would leave f32, value and slope are those of 1 or 0 to within 2e-33
     const float c = fminf(fmaxf(g, -80.0f), 80.0f);
     const float t = __expf(-c);
     const float s = __fdividef(1.0f, 1.0f + t);
-    value = g < -80.0f ? gate_value<kAct>(g) : g * s;
+    value = g * (g < -80.0f ? 0.0f : s);
     slope = fmaf(c * t * s, s, s) + (g - g);  // NaN where g has no slope
   } else {
     // the same past v = +-80; g = +-9.6 there, and 12 keeps its powers small
@@ -55,7 +55,7 @@ __device__ __forceinline__ void gate_slope(float g, float& value, float& slope) 
     const float v = 1.5957691216057308f * c * fmaf(0.044715f, g2, 1.0f);
     const float t = __expf(-fminf(fmaxf(v, -80.0f), 80.0f));
     const float s = __fdividef(1.0f, 1.0f + t);
-    value = v < -80.0f ? gate_value<kAct>(g) : g * s;
+    value = g * (v < -80.0f ? 0.0f : s);
     slope = fmaf(c * t * s * 1.5957691216057308f * fmaf(0.134145f, g2, 1.0f), s, s) + (g - g);
   }
 }
