@@ -958,8 +958,8 @@ double unit_cost(int64_t blocks, int bn) {
 }
 
 // Two gradients share a launch, which fills the pairs that the first one's last tiles leave idle and
-// starts once: 243 rows of 416 x 1784 take 8 us, in two launches 14, and 4096 rows of 4096 x 4096
-// 157, in two 178.  Its units are whole, though, where a launch for each splits its last tiles: 6943
+// starts once: 243 rows of 416 x 1784 take 9 us, in two launches 17, and 4096 rows of 4096 x 4096
+// 155, in two 181.  Its units are whole, though, where a launch for each splits its last tiles: 6943
 // rows of 12360 x 680 take 237 us in one and 210 in two.  The busiest pairs' blocks foretell that to
 // about a tenth (3051 rows of 2960 x 6136: two should gain 7% and lose 4%), which is what a gain has
 // to be.

@@ -1,5 +1,6 @@
-// dense_few.cu -- the gated product of a few to 128 rows of x (include/moe.h: moe_gated_linear without
-// checkpoints), on the tensor cores with the weights as the M side.
+// dense_few.cu -- the gated product of two to 32 rows of x, and up to 128 where the weights are few
+// (few_rows in dense_api.cu; include/moe.h: moe_gated_linear without checkpoints), on the tensor cores with
+// the weights as the M side.
 //
 // D[r, t] = sum_k W(r, k) x(t, k): a tile is 64 gate rows of the weights and the 64 up rows that go
 // with them, against all rows of x (16 to 128 columns of D), so that none of the MMAs' rows are empty
