@@ -18,8 +18,6 @@
 // Gated: an MMA's rows 0-7 are gate rows and 8-15 the up rows that go with them.
 #include "rows.cuh"
 
-#include <type_traits>
-
 namespace gb300moe {
 
 namespace {
@@ -158,13 +156,11 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   };
 
   // x of one chunk: unit u of a block's vector (8 k) of lane t lies at u * 4 + t.  Eight threads or more
-  // have a row, x_per of them, so that its largest value stays in registers until they meet.
-  // kScaled: again, times a power of two.
+  // have a row, x_per of them, so that its largest value stays in registers until they meet.  bf16 x is
+  // staged as it is first, and `again` times a power of two where a row needs one.
   const int x_per = kWarps * 32 / (cols <= 1 ? 1 : cols <= 2 ? 2 : cols <= 4 ? 4 : cols <= 8 ? 8 : 16);
   const int x_row = threadIdx.x / (unsigned)x_per, x_first = threadIdx.x % (unsigned)x_per;
-  bool over = false;
-  auto stage_x = [&](int b0, auto scaled, float scale) {
-    constexpr bool kScaled = decltype(scaled)::value;
+  auto stage_x = [&](int b0, bool again, float scale) {
     const uint4* const from = static_cast<const uint4*>(p.x) + ((int64_t)x_row * p.K + (int64_t)b0 * kBlock) / 8;
     const int64_t left = (p.K - (int64_t)b0 * kBlock) / 8;
     const int units = x_row < cols ? chunk * kBlock / 8 : 0;
@@ -182,17 +178,14 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       for (int a = 0; a < kAhead; ++a) {
         const int u = u0 + a * x_per;
         if (u >= units) break;
-        if constexpr (kBf16 && !kScaled) {
+        if constexpr (kBf16) {
           top = max(top, top_bits(v[a]));
-          bool past = false;  // is seen by the row's largest
-          v[a] = bf16x8_to_f16x8(v[a], past);
-        } else if constexpr (kBf16) {
-          v[a] = bf16x8_times(v[a], scale, over);
+          v[a] = bf16x8_times(v[a], scale);
         }
         sts16(to + (uint32_t)((u & ~15) | ((u & 3) << 2) | ((u >> 2) & 3)) * 16u, v[a]);
       }
     }
-    if constexpr (kBf16 && !kScaled) {
+    if (kBf16 && !again) {
       if (x_per >= 32) {
         top = __reduce_max_sync(0xffffffffu, top);
       } else {
@@ -280,21 +273,20 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
   int stage = 0;
   for (int b0 = first; b0 < last; b0 += chunk) {
     if (b0 > first) __syncthreads();  // the last chunk's x has been read
-    stage_x(b0, std::false_type{}, 1.0f);
     each([&](int i, int j, int c) { acc[0][i][j][c] = acc[kAccs - 1][i][j][c] = 0.0f; });
-    __syncthreads();
     RowScale scale = {1.0f, 1.0f};  // lane c's: of row c
-    bool scaled = false;
-    if constexpr (kBf16) {
+    bool scaled = false;            // the same in all warps
+    for (;;) {
+      stage_x(b0, scaled, kBf16 ? __shfl_sync(0xffffffffu, scale.down, x_row) : 1.0f);
+      __syncthreads();
+      if (!kBf16 || scaled) break;
       uint32_t top = 0u;
       if (lane < cols)
         for (int q = 0; q < x_per; q += 32) top = max(top, s_top[q / 32][lane]);
       scaled = __any_sync(0xffffffffu, needs_scale(top));
-      if (scaled) {  // the same in all warps
-        scale = row_scale(top);
-        stage_x(b0, std::true_type{}, __shfl_sync(0xffffffffu, scale.down, x_row));
-        __syncthreads();
-      }
+      if (!scaled) break;
+      scale = row_scale(top);
+      if (past_f16(top)) set_status(p.status, MOE_ERR_F16_RANGE);
     }
     const int end = last - b0 < chunk ? last - b0 : chunk;
     for (int b = 0; b < end; ++b) {
@@ -313,7 +305,6 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsCall p, int
       total[i][j][c] += z;
     });
   }
-  if (over) set_status(p.status, MOE_ERR_F16_RANGE);
   copy_wait<0>();
 
   // Sums [cols][kAll]: the weight rows of the CTA, a gated product's gate rows before its up rows.

@@ -313,16 +313,17 @@ __global__ void __launch_bounds__(kRowThreads)
   __syncthreads();
   top = __reduce_max_sync(kAll, lane < threads / 32 ? s_top[lane] : 0u);
   const RowScale s = row_scale(top);
-  if (threadIdx.x == 0) scales[blockIdx.x] = s.up;
-  bool over = false;
+  if (threadIdx.x == 0) {
+    scales[blockIdx.x] = s.up;
+    if (past_f16(top)) set_status(status, MOE_ERR_F16_RANGE);
+  }
 #pragma unroll
   for (int k = 0; k < kHold; ++k) {
     const int i = threadIdx.x + k * threads;
-    if (i < vecs) to[i] = bf16x8_times(v[k], s.down, over);
+    if (i < vecs) to[i] = bf16x8_times(v[k], s.down);
   }
   for (int i = threadIdx.x + kHold * threads; i < vecs; i += threads)
-    to[i] = bf16x8_times(from[i], s.down, over);
-  if (over) set_status(status, MOE_ERR_F16_RANGE);
+    to[i] = bf16x8_times(from[i], s.down);
 }
 
 template <typename T, bool kGated, int kN>

@@ -85,21 +85,21 @@ __device__ __forceinline__ uint32_t top_bits(const uint4& v) {
   const uint32_t t = *reinterpret_cast<const uint32_t*>(&top);
   return max(t & 0xffffu, t >> 16);
 }
+__device__ __forceinline__ bool past_f16(uint32_t top) { return top >= 0x4780u; }  // 65536
 __device__ __forceinline__ bool needs_scale(uint32_t top) {
-  return top != 0u && (top < 0x3f00u || top >= 0x4780u);  // 0.5, 65536
+  return top != 0u && (top < 0x3f00u || past_f16(top));  // 0.5
 }
 __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   if (!needs_scale(top)) return RowScale{1.0f, 1.0f};
   const int k = max((int)min(top >> 7, 254u) - 127 - 14, -126);  // both powers are normal f32
   return RowScale{__uint_as_float((uint32_t)(127 - k) << 23), __uint_as_float((uint32_t)(127 + k) << 23)};
 }
-__device__ __forceinline__ uint4 bf16x8_times(const uint4& v, float scale, bool& over) {
+__device__ __forceinline__ uint4 bf16x8_times(const uint4& v, float scale) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    over |= fabsf(f.x) >= kF16Overflow || fabsf(f.y) >= kF16Overflow;
     const __half2 h = __floats2half2_rn(f.x * scale, f.y * scale);
     r[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
@@ -122,6 +122,8 @@ __device__ __forceinline__ void add_accumulators(uint32_t t, int cols, int more,
     for (int i = 0; i < 16; ++i) v[i] += u[i];
   }
 }
+
+constexpr int kMaxParts = 8;  // of K: a portable cluster
 
 // One output from its f32 sum (or sums, gated).
 template <typename T, bool kGated>
@@ -154,12 +156,15 @@ __device__ __forceinline__ void finish_tile(const RowsCall& p, uint32_t base, co
     float z = 0.0f, up = 0.0f;
     if (parts > 1) {
       const uint32_t at = base + (uint32_t)((c * pitch + r) * 4);
-#pragma unroll 4
-      for (int q = 0; q < parts; ++q) {
-        const uint32_t peer = cluster_map(at, (uint32_t)q);
-        z += ld_cluster(peer);
-        if (kGated) up += ld_cluster(peer + kOuts * 4u);
+      float a[kMaxParts], b[kMaxParts];  // all asked for before the first is added
+#pragma unroll
+      for (int q = 0; q < kMaxParts; ++q) {
+        const uint32_t peer = cluster_map(at, (uint32_t)(q < parts ? q : 0));
+        a[q] = q < parts ? ld_cluster(peer) : 0.0f;
+        b[q] = kGated && q < parts ? ld_cluster(peer + kOuts * 4u) : 0.0f;
       }
+#pragma unroll
+      for (int q = 0; q < kMaxParts; ++q) z += a[q], up += b[q];
     } else {
       z = sums[c * pitch + r];
       if (kGated) up = sums[c * pitch + kOuts + r];
@@ -174,8 +179,6 @@ __device__ __forceinline__ void finish_tile(const RowsCall& p, uint32_t base, co
 }
 
 // ---- host side ---------------------------------------------------------------------------------
-constexpr int kMaxParts = 8;  // a portable cluster
-
 // Clusters of `parts` CTAs that the GPU holds at a time, asked for once per device.
 template <auto Kernel>
 inline int max_clusters(int parts, int threads, int smem) {
