@@ -6,8 +6,8 @@
 // with them, against all rows of x (16 to 128 columns of D), so that none of the MMAs' rows are empty
 // and every weight is read once.  What bounds it is the weights' bytes: a CTA has up to 200 KB of
 // them and of x on their way.  K is split over a cluster, whose sums meet in shared memory and are
-// added in the order of the parts.  7168 x 2048 at 2, 16, 64 and 128 rows: 14, 15.5, 18 and 20 us (4.1
-// to 2.8 TB/s: the start and the join show); 7168 x 18432 at 2 and 32 rows 82 and 85 us (6.4, 6.2).
+// added in the order of the parts.  7168 x 2048 at 2, 16, 64 and 128 rows: 13, 13, 15 and 17.5 us (4.5
+// to 3.4 TB/s: the start and the join show); 7168 x 18432 at 2 and 32 rows 80 and 83 us (6.6, 6.3).
 #include "rows.cuh"
 
 namespace gb300moe {

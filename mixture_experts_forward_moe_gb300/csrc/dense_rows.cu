@@ -1,6 +1,6 @@
 // dense_rows.cu -- up to sixteen rows of x against 4-bit weights, which are streamed once
 // (include/moe.h: moe_linear_w4a16, moe_gated_linear_w4a16), and the 16-bit gated product of one row
-// (moe_gated_linear).  4 bits, 7168 x 7168 at 1, 4, 8 and 16 rows of bf16 x: 11.5, 11, 14 and 16.5 us;
+// (moe_gated_linear).  4 bits, 7168 x 7168 at 1, 4, 8 and 16 rows of bf16 x: 12, 11, 12 and 16 us;
 // 16 bits, 4096 weight rows of 7168: 11.5 us.
 //
 // What bounds it is the weights' bytes, and for 4 bits as much the instructions that decode them.

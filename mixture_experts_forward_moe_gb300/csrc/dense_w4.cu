@@ -6,10 +6,10 @@
 // f16, written into the swizzled tile that the MMAs read.  x is taken in f16, bf16 x times a power of two
 // per row where it needs one (rows.cuh).
 // bf16 x is converted by a small kernel before: done in this one, by every CTA for itself, it cost
-// more than the decoding (64 rows of 7168 x 7168: 51 us, now 26).
+// more than the decoding (64 rows of 7168 x 7168: 51 us, now 23).
 // What bounds it is the issue of the decoding, about three instructions of a lane per weight with the
 // stores and waits, on as many SMs as the tiles and parts of K fill.  7168 x 7168 at 17, 32, 64, 128
-// and 256 rows: 22, 23, 26, 32 and 46 us.
+// and 256 rows: 20, 21, 23, 29 and 45 us.
 // Gated: 64 gate rows and the 64 up rows that go with them.
 // A cluster is parts of K of the same rows, whose sums meet in shared memory and are added in the
 // order of the parts.
