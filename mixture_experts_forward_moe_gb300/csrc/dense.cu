@@ -62,11 +62,11 @@ struct Plan {
 // us, 1234 in one accumulator.
 constexpr int kChainBlocks = kChainK / kBlockK;
 // A sum of f32 on the CUDA cores is off by less the shorter K is, so a short K is drained more often:
-// no more codes fall on their neighbours than those of an f32 product.  Of 84 million codes at K = 136,
-// 264 and 512, and 42 million at 2056 and 7168, it has 518, 358, 505, 532 and 1245 (its 264 of 84
-// million too).  Drained every block 483, 258, 322, 239 and 364, every two 652, 313, 445, 247 and 307,
-// every four 659, 560, 712, 398 and 441, every eight 659, 564, 1240, 784 and 825.  A pass costs time
-// where the products are short: 16384 x 5120 x 512 takes 129 us with two blocks, 108 with four.
+// no more codes fall on their neighbours than those of an f32 product.  That has 518 of 168 million there
+// at K = 136, 358 and 505 of 84 million at 264 and 512, 532 and 1245 of 42 million at 2056 and 7168.
+// Drained every block 483, 258, 322, 239 and 364, every two 652, 313, 445, 247 and 307, every four 659,
+// 560, 712, 398 and 441, every eight 659, 564, 1240, 784 and 825.  A pass costs time where the products
+// are short: 16384 x 5120 x 512 takes 129 us with two blocks, 108 with four.
 inline int drain_blocks(int64_t K) {
   const int64_t blocks = ceil_div(K, kBlockK);
   return blocks <= 4 ? 1 : blocks <= 12 ? 2 : blocks <= 64 ? 4 : 8;
